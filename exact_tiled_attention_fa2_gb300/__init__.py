@@ -24,7 +24,9 @@ FA2_ERR_CUDA = 4
 FA2_ERR_DEVICE_TIMEOUT = 5
 FA2_ERR_SCRATCH_LIMIT = 6
 FA2_ERR_DEVICE_SEQLENS = 7
+FA2_ERR_DEVICE_PAGES = 8
 FA2_DECODE_MAX_Q = 8
+FA2_PAGED_PLAN_MAX_BATCH = 16384
 FA2_NOALLOC_SCRATCH_BYTES = 32 << 20
 
 _lib = None
@@ -55,6 +57,55 @@ class Fa2BwdParams(ctypes.Structure):
         ("fwd", Fa2FwdParams),
         ("dout", ctypes.c_void_p), ("dq", ctypes.c_void_p), ("dk", ctypes.c_void_p), ("dv", ctypes.c_void_p),
         ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class Fa2PagedCache(ctypes.Structure):
+    """Mirror of ``fa2_paged_cache`` in include/fa2.h."""
+
+    _fields_ = [
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("k_strides", ctypes.c_int64 * 3), ("v_strides", ctypes.c_int64 * 3),
+        ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("heads", ctypes.c_int),
+        ("head_dim", ctypes.c_int), ("dtype", ctypes.c_int),
+    ]
+
+
+class Fa2PagedParams(ctypes.Structure):
+    """Mirror of ``fa2_paged_params`` in include/fa2.h (checked against the library's sizeof)."""
+
+    _fields_ = [
+        ("cache", Fa2PagedCache),
+        ("q", ctypes.c_void_p), ("o", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+        ("block_table", ctypes.c_void_p), ("cu_seqlens_q", ctypes.c_void_p), ("seqlens_k", ctypes.c_void_p),
+        ("table_stride", ctypes.c_int64), ("q_strides", ctypes.c_int64 * 2), ("o_strides", ctypes.c_int64 * 2),
+        ("lse_stride", ctypes.c_int64),
+        ("batch", ctypes.c_int), ("heads", ctypes.c_int), ("total_q", ctypes.c_int), ("max_seqlen_q", ctypes.c_int),
+        ("max_pages", ctypes.c_int), ("window_left", ctypes.c_int), ("window_right", ctypes.c_int),
+        ("prefix_len", ctypes.c_int), ("scale", ctypes.c_float),
+    ]
+
+
+class Fa2PagedAppendParams(ctypes.Structure):
+    """Mirror of ``fa2_paged_append_params`` in include/fa2.h."""
+
+    _fields_ = [
+        ("cache", Fa2PagedCache),
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("slots", ctypes.c_void_p),
+        ("k_strides", ctypes.c_int64 * 2), ("v_strides", ctypes.c_int64 * 2), ("total", ctypes.c_int),
+    ]
+
+
+class Fa2PagedPlanParams(ctypes.Structure):
+    """Mirror of ``fa2_paged_plan_params`` in include/fa2.h."""
+
+    _fields_ = [
+        ("context_lens", ctypes.c_void_p), ("query_lens", ctypes.c_void_p), ("free_pages", ctypes.c_void_p),
+        ("free_count", ctypes.c_void_p), ("block_table", ctypes.c_void_p), ("cu_seqlens_q", ctypes.c_void_p),
+        ("seqlens_k", ctypes.c_void_p), ("slots", ctypes.c_void_p), ("free_left", ctypes.c_void_p),
+        ("table_stride", ctypes.c_int64),
+        ("batch", ctypes.c_int), ("max_pages", ctypes.c_int), ("num_pages", ctypes.c_int),
+        ("page_size", ctypes.c_int), ("total_q", ctypes.c_int), ("num_free", ctypes.c_int),
     ]
 
 
@@ -108,6 +159,19 @@ def load_library():
     lib.fa2_bwd_ex.restype = ci
     lib.fa2_bwd_ex_workspace_bytes.argtypes = [ctypes.POINTER(Fa2FwdParams)]
     lib.fa2_bwd_ex_workspace_bytes.restype = sz
+    lib.fa2_paged_plan.argtypes = [ctypes.POINTER(Fa2PagedPlanParams), vp]
+    lib.fa2_paged_plan.restype = ci
+    lib.fa2_paged_append.argtypes = [ctypes.POINTER(Fa2PagedAppendParams), vp]
+    lib.fa2_paged_append.restype = ci
+    lib.fa2_paged_fwd.argtypes = [ctypes.POINTER(Fa2PagedParams), vp, sz, vp]
+    lib.fa2_paged_fwd.restype = ci
+    lib.fa2_paged_fwd_workspace_bytes.argtypes = [ctypes.POINTER(Fa2PagedParams)]
+    lib.fa2_paged_fwd_workspace_bytes.restype = sz
+    lib.fa2_paged_params_size.argtypes = []
+    lib.fa2_paged_params_size.restype = sz
+    if lib.fa2_paged_params_size() != ctypes.sizeof(Fa2PagedParams):
+        raise RuntimeError("fa2_paged_params layout mismatch: library %d bytes, binding %d bytes"
+                           % (lib.fa2_paged_params_size(), ctypes.sizeof(Fa2PagedParams)))
     if lib.fa2_fwd_params_size() != ctypes.sizeof(Fa2FwdParams):
         raise RuntimeError("fa2_fwd_params layout mismatch: library %d bytes, binding %d bytes"
                            % (lib.fa2_fwd_params_size(), ctypes.sizeof(Fa2FwdParams)))
@@ -354,6 +418,224 @@ def fa2_bwd_ex(q, k, v, o, lse, dout, dq=None, dk=None, dv=None, workspace=None,
     if rc:
         raise Fa2Error(rc, "fa2_bwd_ex")
     return dq, dk, dv
+
+
+class _on_device:
+    """Makes ``tensor``'s device current and ``stream`` (None: that device's
+    current stream) the one new tensors are allocated for, so that a result or
+    a workspace allocated here is not handed out again before the kernels of
+    ``stream`` are done with it.  ``handle``: the stream for the library."""
+
+    def __init__(self, tensor, stream):
+        import torch
+        device = tensor.device
+        guards = []
+        if device.index != torch.cuda.current_device():
+            guards.append(torch.cuda.device(device))
+        if stream is None:
+            stream = torch.cuda.current_stream(device)
+        elif stream.device != device:
+            raise ValueError("stream must belong to the tensors' device %s" % device)
+        elif stream != torch.cuda.current_stream(device):
+            guards.append(torch.cuda.stream(stream))
+        self._guards = guards
+        self.handle = ctypes.c_void_p(int(stream.cuda_stream))
+
+    def __enter__(self):
+        for g in self._guards:
+            g.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        for g in reversed(self._guards):
+            g.__exit__(*exc)
+        return False
+
+
+def _int32(t, name, device, dims, shape=None):
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.device != device or t.dim() != dims:
+        raise ValueError("%s must be an int32 tensor with %d dimension%s on %s"
+                         % (name, dims, "" if dims == 1 else "s", device))
+    if t.numel() and t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError("%s must have a contiguous last dimension" % name)
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    return t
+
+
+def _paged_cache(k_cache, v_cache):
+    """Marshal cache tensors [num_pages, H_kv, page_size, d] into an Fa2PagedCache."""
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must share one [num_pages, H_kv, page_size, d] shape")
+    for t in (k_cache, v_cache):
+        if not t.is_cuda or t.stride(-1) != 1:
+            raise ValueError("k_cache and v_cache must be CUDA tensors with a contiguous last dimension")
+    if v_cache.dtype != k_cache.dtype:
+        raise TypeError("k_cache and v_cache must share one dtype")
+    if v_cache.device != k_cache.device:
+        raise ValueError("k_cache and v_cache must be on one device")
+    c = Fa2PagedCache()
+    c.k, c.v = k_cache.data_ptr(), v_cache.data_ptr()
+    c.k_strides[:], c.v_strides[:] = k_cache.stride()[:3], v_cache.stride()[:3]
+    c.num_pages, c.heads, c.page_size, c.head_dim = k_cache.shape
+    c.dtype = _dtype_code(k_cache)
+    return c
+
+
+def fa2_paged_plan(context_lens, query_lens, block_table, free_pages, free_count, num_pages, page_size, total_q,
+                   cu_seqlens_q=None, seqlens_k=None, slots=None, free_left=None, stream=None):
+    """Block tables and slot map of one serving step from its request lengths (fa2_paged_plan).
+
+    ``context_lens`` and ``query_lens`` (int32 CUDA [B]): each request's cached
+    tokens and new ones.  ``block_table`` (int32 CUDA [B, max_pages]) holds the
+    cached tokens' pages and gets the new tokens', taken from the top of the
+    stack ``free_pages[:free_count]`` (int32 CUDA [F] and [1]).  ``total_q``:
+    rows of the step, its tokens or more (padding).  Returns (cu_seqlens_q
+    [B + 1], seqlens_k [B], slots [total_q], free_left [1]); slots is -1 on
+    padding.  ``free_count`` is not written: pass free_left to the next step.
+
+    A step that cannot be placed (lengths out of range, not enough free pages)
+    is refused whole: empty outputs, the table as it was, and
+    FA2_ERR_DEVICE_PAGES from the next fa2_get_device_status.
+    """
+    import torch
+    if not context_lens.is_cuda:
+        raise ValueError("fa2_paged_plan takes CUDA tensors")
+    dev = context_lens.device
+    B = context_lens.shape[0] if context_lens.dim() == 1 else 0
+    _int32(context_lens, "context_lens", dev, 1)
+    _int32(query_lens, "query_lens", dev, 1, (B,))
+    _int32(block_table, "block_table", dev, 2)
+    if block_table.shape[0] != B:
+        raise ValueError("block_table must have one row per request")
+    _int32(free_pages, "free_pages", dev, 1)
+    _int32(free_count, "free_count", dev, 1, (1,))
+    total_q = int(total_q)
+    with _on_device(context_lens, stream) as on:
+        new = lambda n: torch.empty(n, dtype=torch.int32, device=dev)
+        cu_seqlens_q = new(B + 1) if cu_seqlens_q is None else _int32(cu_seqlens_q, "cu_seqlens_q", dev, 1, (B + 1,))
+        seqlens_k = new(B) if seqlens_k is None else _int32(seqlens_k, "seqlens_k", dev, 1, (B,))
+        slots = new(max(total_q, 0)) if slots is None else _int32(slots, "slots", dev, 1, (total_q,))
+        free_left = new(1) if free_left is None else _int32(free_left, "free_left", dev, 1, (1,))
+        p = Fa2PagedPlanParams()
+        p.context_lens, p.query_lens = context_lens.data_ptr(), query_lens.data_ptr()
+        p.free_pages, p.free_count = free_pages.data_ptr(), free_count.data_ptr()
+        p.block_table, p.table_stride = block_table.data_ptr(), block_table.stride(0)
+        p.cu_seqlens_q, p.seqlens_k = cu_seqlens_q.data_ptr(), seqlens_k.data_ptr()
+        p.slots, p.free_left = slots.data_ptr(), free_left.data_ptr()
+        p.batch, p.max_pages, p.num_pages, p.page_size = B, block_table.shape[1], int(num_pages), int(page_size)
+        p.total_q, p.num_free = total_q, free_pages.shape[0]
+        rc = load_library().fa2_paged_plan(ctypes.byref(p), on.handle)
+    if rc:
+        raise Fa2Error(rc, "fa2_paged_plan")
+    return cu_seqlens_q, seqlens_k, slots, free_left
+
+
+def fa2_paged_append(k, v, slots, k_cache, v_cache, stream=None):
+    """Write new key/value rows to their slots of a paged cache (fa2_paged_append).
+
+    k, v [total, H_kv, d] (views with a contiguous last dimension, e.g. parts
+    of a fused projection); ``slots`` int32 CUDA [total], negative: skipped;
+    the others distinct.  Caches [num_pages, H_kv, page_size, d], any views
+    with a contiguous last dimension (a [num_pages, page_size, H_kv, d] cache
+    as ``x.transpose(1, 2)``); slot s is row s % page_size of page s // page_size.
+    """
+    p = Fa2PagedAppendParams()
+    p.cache = _paged_cache(k_cache, v_cache)
+    dev = k_cache.device
+    if k.dim() != 3 or v.shape != k.shape or k.shape[1] != k_cache.shape[1] or k.shape[2] != k_cache.shape[3]:
+        raise ValueError("k and v must be [total, H_kv, d] with the cache's heads and head dim")
+    for t in (k, v):
+        if t.device != dev or t.stride(-1) != 1:
+            raise ValueError("k and v must be on the cache's device with a contiguous last dimension")
+        if t.dtype != k_cache.dtype:
+            raise TypeError("k, v and the cache must share one dtype")
+    _int32(slots, "slots", dev, 1, (k.shape[0],))
+    p.k, p.v, p.slots, p.total = k.data_ptr(), v.data_ptr(), slots.data_ptr(), k.shape[0]
+    p.k_strides[:], p.v_strides[:] = k.stride()[:2], v.stride()[:2]
+    with _on_device(k_cache, stream) as on:
+        rc = load_library().fa2_paged_append(ctypes.byref(p), on.handle)
+    if rc:
+        raise Fa2Error(rc, "fa2_paged_append")
+
+
+def _paged_params(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, scale, window_left, window_right,
+                  prefix_len, max_seqlen_q):
+    """Marshal a paged forward's inputs into an Fa2PagedParams (o and lse are set by the caller)."""
+    p = Fa2PagedParams()
+    p.cache = _paged_cache(k_cache, v_cache)
+    dev = k_cache.device
+    if q.dim() != 3 or q.shape[2] != k_cache.shape[3]:
+        raise ValueError("q must be [total_q, H, d] with the cache's head dim")
+    if q.device != dev or q.stride(-1) != 1:
+        raise ValueError("q must be on the cache's device with a contiguous last dimension")
+    if q.dtype != k_cache.dtype:
+        raise TypeError("q and the cache must share one dtype")
+    _int32(seqlens_k, "seqlens_k", dev, 1)
+    B = seqlens_k.shape[0]
+    _int32(cu_seqlens_q, "cu_seqlens_q", dev, 1, (B + 1,))
+    _int32(block_table, "block_table", dev, 2)
+    if block_table.shape[0] != B:
+        raise ValueError("block_table must have one row per sequence")
+    p.q, p.block_table = q.data_ptr(), block_table.data_ptr()
+    p.cu_seqlens_q, p.seqlens_k = cu_seqlens_q.data_ptr(), seqlens_k.data_ptr()
+    p.table_stride, p.max_pages = block_table.stride(0), block_table.shape[1]
+    p.q_strides[:] = q.stride()[:2]
+    p.batch, p.heads, p.total_q = B, q.shape[1], q.shape[0]
+    p.max_seqlen_q = q.shape[0] if max_seqlen_q is None else int(max_seqlen_q)
+    p.window_left, p.window_right, p.prefix_len = int(window_left), int(window_right), int(prefix_len)
+    p.scale = 1.0 / float(q.shape[2]) ** 0.5 if scale is None else float(scale)
+    return p
+
+
+def fa2_paged_fwd_workspace_bytes(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, max_seqlen_q=None) -> int:
+    """Workspace fa2_paged_fwd needs for these tensors; it depends on their shapes only."""
+    p = _paged_params(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, None, -1, -1, 0, max_seqlen_q)
+    return int(load_library().fa2_paged_fwd_workspace_bytes(ctypes.byref(p)))
+
+
+def fa2_paged_fwd(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, o=None, lse=None, workspace=None,
+                  scale=None, window_left=-1, window_right=-1, prefix_len=0, max_seqlen_q=None, stream=None):
+    """Attention of each sequence's query tokens over its keys in a paged cache (fa2_paged_fwd).
+
+    q [total_q, H, d] (packed: sequence b's tokens are rows cu_seqlens_q[b] ..
+    cu_seqlens_q[b+1] - 1), caches [num_pages, H_kv, page_size, d] (views as in
+    fa2_paged_append; H a multiple of H_kv: query head i reads K/V head
+    i // (H // H_kv)), ``block_table`` int32 CUDA [B, max_pages],
+    ``cu_seqlens_q`` [B + 1] and ``seqlens_k`` [B] int32 CUDA: keys of each
+    sequence, its new tokens' own (already appended) among them.  Masks as
+    fa2_fwd_ex: causal is window (-1, 0).  ``max_seqlen_q`` (default: total_q)
+    bounds every sequence's query count; give it while decoding, it sizes the
+    grid and the workspace.  Returns (o [total_q, H, d], lse [H, total_q]);
+    rows outside every sequence are not written.
+    """
+    import torch
+    p = _paged_params(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, scale, window_left, window_right,
+                      prefix_len, max_seqlen_q)
+    lib = load_library()
+    with _on_device(q, stream) as on:
+        if o is None:
+            o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        elif o.shape != q.shape or o.dtype != q.dtype or o.device != q.device or o.stride(-1) != 1:
+            raise ValueError("o must have q's shape, dtype and device with a contiguous last dimension")
+        if lse is None:
+            lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=q.device)
+        elif (tuple(lse.shape) != (q.shape[1], q.shape[0]) or lse.dtype != torch.float32 or lse.device != q.device
+              or (lse.stride(-1) != 1 and lse.shape[-1] > 1)):
+            raise ValueError("lse must be float32 [H, total_q] on q's device with a contiguous last dimension")
+        p.o, p.lse, p.lse_stride = o.data_ptr(), lse.data_ptr(), lse.stride(0)
+        p.o_strides[:] = o.stride()[:2]
+        if workspace is None:
+            need = int(lib.fa2_paged_fwd_workspace_bytes(ctypes.byref(p)))
+            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+        elif workspace.device != q.device or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on q's device")
+        rc = lib.fa2_paged_fwd(ctypes.byref(p), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                               on.handle)
+    if rc:
+        raise Fa2Error(rc, "fa2_paged_fwd")
+    return o, lse
 
 
 def _check_host_tensors(q, k, v, o, lse, where):

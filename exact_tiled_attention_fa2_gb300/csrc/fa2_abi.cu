@@ -16,6 +16,7 @@
 #include "fa2_common.cuh"
 #include "fa2_decode.cuh"
 #include "fa2_internal.h"
+#include "fa2_paged.h"
 
 namespace fa2 {
 
@@ -1032,6 +1033,35 @@ extern "C" int fa2_selftest_wait_timeout(int limit_us, void* stream) {
   return cudaGetLastError() == cudaSuccess ? FA2_OK : FA2_ERR_CUDA;
 }
 
+namespace fa2 {
+
+int paged_device_status(uint32_t** status) {
+  DeviceState* ds = nullptr;
+  const int rc = device_state(&ds);
+  if (rc == FA2_OK) *status = ds->status;
+  return rc;
+}
+
+// The strides of dimensions of size 1 address nothing and are replaced by a
+// valid placeholder.
+int encode_map_4d(CUtensorMap* m, const void* base, const long long dims[4], const long long strides[3],
+                  const int box[4], bool bf16) {
+  cuuint64_t d[4], st[3];
+  cuuint32_t b[4], estr[4] = {1, 1, 1, 1};
+  for (int i = 0; i < 4; ++i) {
+    d[i] = (cuuint64_t)dims[i];
+    b[i] = (cuuint32_t)box[i];
+  }
+  for (int i = 0; i < 3; ++i) st[i] = (cuuint64_t)(dims[i + 1] > 1 ? strides[i] : dims[0]) * 2;
+  const CUresult r = g_encode(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+                              const_cast<void*>(base), d, st, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? FA2_OK : FA2_ERR_CUDA;
+}
+
+}  // namespace fa2
+
 extern "C" int fa2_get_device_status(void* stream, uint32_t* detail) {
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return FA2_ERR_CUDA;
   DeviceState* ds = nullptr;
@@ -1044,6 +1074,7 @@ extern "C" int fa2_get_device_status(void* stream, uint32_t* detail) {
   if (detail) *detail = word;
   if (word & kStatusTimeout) return FA2_ERR_DEVICE_TIMEOUT;
   if (word & kStatusBadSeqlens) return FA2_ERR_DEVICE_SEQLENS;
+  if (word & kStatusBadPages) return FA2_ERR_DEVICE_PAGES;
   return word ? FA2_ERR_DEVICE_TIMEOUT : FA2_OK;
 }
 
@@ -1057,6 +1088,7 @@ extern "C" const char* fa2_status_string(int status) {
     case FA2_ERR_DEVICE_TIMEOUT: return "a kernel wait timed out; the tile was abandoned";
     case FA2_ERR_SCRATCH_LIMIT: return "problem exceeds the static device scratch of fa2_fwd_host_noalloc";
     case FA2_ERR_DEVICE_SEQLENS: return "packed-batch row offsets out of range; those sequences were not written";
+    case FA2_ERR_DEVICE_PAGES: return "paged cache: a step's lengths, a slot or a page of a block table out of range";
     default: return "unknown status";
   }
 }

@@ -1,0 +1,110 @@
+// fa2_paged.h -- declarations shared by the paged-cache translation units: the
+// parameters their kernels read and the launchers.  Not part of the public
+// interface.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace fa2 {
+
+// Bit of the device status word a paged kernel sets when a step's lengths, a
+// slot or a page of a block table is out of range.
+constexpr uint32_t kStatusBadPages = 4u;
+
+// Largest batch of fa2_paged_plan: its kernel keeps two prefix sums of it in
+// shared memory (128 KB).
+constexpr int kPagedPlanMaxBatch = 16384;
+
+// Rows of one query tile: group (query heads of one K/V head) x tokens.
+constexpr int kPagedTileRows = 128;
+constexpr int kPagedKeyTile = 64;
+
+struct PagedParams {
+  void* o;                // 16-bit output [total_q][heads_q][d] by strides
+  float* lse;             // [heads_q][total_q], head stride lse_hs
+  uint32_t* status;       // device status word (library-owned)
+  const int* table;       // block table, rows of max_pages entries, table_stride apart
+  const int* cu_q;        // [batch + 1] row offsets of the sequences' queries
+  const int* lens_k;      // [batch] key counts
+  long long table_stride, o_rs, o_hs, lse_hs;
+  int batch, heads_kv, group;
+  int tile_tokens;        // tokens of a query tile: 128 / group
+  int box_tokens;         // tokens of a Q load: min(tile_tokens, max_q)
+  int total_q, max_q;
+  int num_pages, page_size, max_pages;
+  int window_left, window_right, prefix;   // as KernelParams
+  float scale_log2_mag;   // as KernelParams
+  uint32_t qk_negate;     // as KernelParams
+  // Key splits: a query tile's visited key tiles are cut into chunks of at
+  // most C = max(min_chunk, ceil(work / target_units)) tiles, `work` the
+  // batch's sum over (sequence, K/V head, query tile).
+  int target_units, min_chunk;
+  int max_slots;          // partial states the workspace holds
+  int slot_rows;          // rows of a partial state: group * box_tokens
+  float* ws_o;            // [slot][slot_rows][d] partial O~
+  float* ws_ml;           // [slot][slot_rows][2] partial (m, l), exp2 domain
+};
+
+struct PagedLaunchArgs {
+  CUtensorMap tm_q;       // (d, group, heads_kv, total_q), boxes of 64 columns x group x 1 x box_tokens
+  CUtensorMap tm_k, tm_v; // (d, page_size, heads_kv, num_pages), boxes of 64 columns x min(page_size, 64) rows
+  PagedParams p;
+  long long grid;         // upper bound of the units
+  long long merge_tiles;  // upper bound of the split (query tile, K/V head) pairs
+  bool bf16;
+  bool band;              // window_left >= 0 or prefix > 0
+  cudaStream_t stream;
+};
+
+int launch_paged_d64(const PagedLaunchArgs& a);
+int launch_paged_d128(const PagedLaunchArgs& a);
+int launch_paged_d256(const PagedLaunchArgs& a);
+
+struct PagedPlanArgs {
+  const int* context_lens;
+  const int* query_lens;
+  const int* free_pages;
+  const int* free_count;
+  int* table;
+  int* cu_q;
+  int* lens_k;
+  int* slots;
+  int* free_left;
+  uint32_t* status;
+  long long table_stride;
+  int batch, max_pages, num_pages, page_size, total_q, num_free;
+};
+
+int launch_paged_plan(const PagedPlanArgs& a, cudaStream_t stream);
+
+// One of K and V: new rows [total][heads][d] and cache [page][head][row][d],
+// strides in 16-byte units.
+struct PagedAppendSide {
+  const uint4* src;
+  uint4* dst;
+  long long src_rs, src_hs;          // token, head
+  long long dst_ps, dst_hs, dst_rs;  // page, head, row of a page
+};
+
+struct PagedAppendArgs {
+  PagedAppendSide k, v;
+  const int* slots;
+  uint32_t* status;
+  int total, heads, num_slots, page_size;
+  int row_chunks_log2;    // 16-byte chunks of a head's row: d / 8 = 1 << row_chunks_log2
+};
+
+int launch_paged_append(const PagedAppendArgs& a, cudaStream_t stream);
+
+// Services of the C-ABI translation unit: the current device's status word
+// (checks the device), and an rank-4 tensor map of a 16-bit tensor whose
+// innermost dimension is contiguous (strides of dimensions 1 .. 3 in
+// elements; boxes of 64 columns, 128-byte swizzle).
+int paged_device_status(uint32_t** status);
+int encode_map_4d(CUtensorMap* m, const void* base, const long long dims[4], const long long strides[3],
+                  const int box[4], bool bf16);
+
+}  // namespace fa2

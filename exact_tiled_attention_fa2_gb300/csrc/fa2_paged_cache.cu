@@ -1,0 +1,215 @@
+// fa2_paged_cache.cu -- the kernels that fill a paged key/value cache: one
+// step's block tables and slot map from its request lengths, and new
+// key/value rows written to their slots.
+#include "fa2_paged.h"
+
+#include <atomic>
+
+#include "fa2_internal.h"
+
+namespace fa2 {
+namespace {
+
+constexpr int kPlanThreads = 1024;
+
+// Exclusive prefix sums of (a, b) over the block's threads and their totals.
+__device__ __forceinline__ void block_scan2(long long& a, long long& b, long long& total_a, long long& total_b,
+                                            long long* scratch) {
+  const int lane = (int)threadIdx.x & 31, w = (int)threadIdx.x >> 5;
+  long long ia = a, ib = b;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long va = __shfl_up_sync(0xffffffffu, ia, o), vb = __shfl_up_sync(0xffffffffu, ib, o);
+    if (lane >= o) {
+      ia += va;
+      ib += vb;
+    }
+  }
+  if (lane == 31) {
+    scratch[2 * w] = ia;
+    scratch[2 * w + 1] = ib;
+  }
+  __syncthreads();
+  long long before_a = 0, before_b = 0;
+  total_a = total_b = 0;
+  for (int j = 0; j < (int)(blockDim.x >> 5); ++j) {
+    if (j == w) {
+      before_a = total_a;
+      before_b = total_b;
+    }
+    total_a += scratch[2 * j];
+    total_b += scratch[2 * j + 1];
+  }
+  a = before_a + ia - a;
+  b = before_b + ib - b;
+}
+
+// Last index i in [0, n) with x[i] <= v (x non-decreasing, x[0] <= v).
+__device__ __forceinline__ int last_at_most(const int* x, int n, int v) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (x[mid] <= v)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
+// Every block sums all requests' new tokens and new pages (8 bytes a request,
+// from L2 after the first block), so the blocks need nothing from each other:
+// then each writes its part of the tokens' slots and of the new pages' table
+// entries, finding an item's request by bisection in shared memory.  A slot
+// in a new page comes from the free list itself, not from the table entry
+// another block may still be writing.
+__global__ void __launch_bounds__(kPlanThreads) fa2_paged_plan_kernel(const PagedPlanArgs a) {
+  extern __shared__ int sums[];             // [batch + 1] first token, [batch + 1] first new page
+  __shared__ long long scratch[2 * kPlanThreads / 32];
+  __shared__ int bad_any;
+  int* tok = sums;
+  int* pag = sums + a.batch + 1;
+  const int tid = (int)threadIdx.x;
+  const unsigned ps = (unsigned)a.page_size;
+  const int per = (a.batch + kPlanThreads - 1) / kPlanThreads;
+  const int i0 = min(tid * per, a.batch), i1 = min(i0 + per, a.batch);
+  if (tid == 0) bad_any = 0;
+  __syncthreads();
+  long long n_tok = 0, n_pag = 0;
+  bool bad = false;
+  for (int i = i0; i < i1; ++i) {
+    const long long c = a.context_lens[i], n = a.query_lens[i];
+    if (c < 0 || n < 0 || c + n > (long long)a.max_pages * ps) {
+      bad = true;
+    } else {
+      n_tok += n;
+      n_pag += ((unsigned)(c + n) + ps - 1) / ps - ((unsigned)c + ps - 1) / ps;
+    }
+  }
+  if (bad) bad_any = 1;
+  long long at_tok = n_tok, at_pag = n_pag, all_tok, all_pag;
+  block_scan2(at_tok, at_pag, all_tok, all_pag, scratch);   // its barrier also publishes bad_any
+  const int count = *a.free_count;
+  if (bad_any || all_tok > a.total_q || count < 0 || count > a.num_free || all_pag > count) {
+    // refused: an empty step, the table and the free list as they were
+    for (int i = (int)blockIdx.x * kPlanThreads + tid; i < max(a.total_q, a.batch + 1);
+         i += (int)gridDim.x * kPlanThreads) {
+      if (i < a.total_q) a.slots[i] = -1;
+      if (i <= a.batch) a.cu_q[i] = 0;
+      if (i < a.batch) a.lens_k[i] = 0;
+    }
+    if (blockIdx.x == 0 && tid == 0) {
+      *a.free_left = count;
+      atomicOr(a.status, kStatusBadPages);
+    }
+    return;
+  }
+  for (int i = i0; i < i1; ++i) {
+    const unsigned c = (unsigned)a.context_lens[i], n = (unsigned)a.query_lens[i];
+    tok[i] = (int)at_tok;
+    pag[i] = (int)at_pag;
+    if (blockIdx.x == 0) {
+      a.cu_q[i] = (int)at_tok;
+      a.lens_k[i] = (int)(c + n);
+    }
+    at_tok += n;
+    at_pag += (c + n + ps - 1) / ps - (c + ps - 1) / ps;
+  }
+  if (tid == 0) {
+    tok[a.batch] = (int)all_tok;
+    pag[a.batch] = (int)all_pag;
+    if (blockIdx.x == 0) {
+      a.cu_q[a.batch] = (int)all_tok;
+      *a.free_left = count - (int)all_pag;
+    }
+  }
+  __syncthreads();
+  bool bad_page = false;
+  const int stride = (int)gridDim.x * kPlanThreads;
+  for (long long tl = (long long)blockIdx.x * kPlanThreads + tid; tl < a.total_q; tl += stride) {
+    const int t = (int)tl;
+    int slot = -1;
+    if (t < (int)all_tok) {
+      const int b = last_at_most(tok, a.batch, t);
+      const unsigned c = (unsigned)a.context_lens[b], pos = c + (unsigned)(t - tok[b]);
+      const unsigned held = (c + ps - 1) / ps, page_at = pos / ps;
+      const int page = page_at < held ? a.table[(long long)b * a.table_stride + page_at]
+                                      : a.free_pages[count - 1 - (pag[b] + (int)(page_at - held))];
+      if (page >= 0 && page < a.num_pages)
+        slot = page * (int)ps + (int)(pos - page_at * ps);
+      else
+        bad_page = true;
+    }
+    a.slots[t] = slot;
+  }
+  for (long long nl = (long long)blockIdx.x * kPlanThreads + tid; nl < all_pag; nl += stride) {
+    const int n = (int)nl;
+    const int b = last_at_most(pag, a.batch, n);
+    const unsigned held = ((unsigned)a.context_lens[b] + ps - 1) / ps;
+    const int page = a.free_pages[count - 1 - n];
+    if (page < 0 || page >= a.num_pages) bad_page = true;
+    a.table[(long long)b * a.table_stride + held + (unsigned)(n - pag[b])] = page;
+  }
+  if (bad_page) atomicOr(a.status, kStatusBadPages);
+}
+
+// One 16-byte chunk of K and of V per thread and token: threads x walk the
+// chunks of a token's heads (a head's row is contiguous on both sides),
+// threads y the tokens.
+__global__ void __launch_bounds__(256) fa2_paged_append_kernel(const PagedAppendArgs a) {
+  const int items = a.heads << a.row_chunks_log2;
+  const int mask = (1 << a.row_chunks_log2) - 1;
+  bool bad = false;
+  for (long long tl = (long long)blockIdx.x * blockDim.y + threadIdx.y; tl < a.total;
+       tl += (long long)gridDim.x * blockDim.y) {
+    const int slot = __ldg(a.slots + tl);
+    if (slot < 0) continue;
+    if (slot >= a.num_slots) {
+      bad = true;
+      continue;
+    }
+    const long long page = slot / a.page_size, at = slot % a.page_size;
+    const uint4* ks = a.k.src + tl * a.k.src_rs;
+    const uint4* vs = a.v.src + tl * a.v.src_rs;
+    uint4* kd = a.k.dst + page * a.k.dst_ps + at * a.k.dst_rs;
+    uint4* vd = a.v.dst + page * a.v.dst_ps + at * a.v.dst_rs;
+    for (int i = (int)threadIdx.x; i < items; i += (int)blockDim.x) {
+      const long long h = i >> a.row_chunks_log2;
+      const int c = i & mask;
+      const uint4 x = ks[h * a.k.src_hs + c];
+      const uint4 y = vs[h * a.v.src_hs + c];
+      kd[h * a.k.dst_hs + c] = x;
+      vd[h * a.v.dst_hs + c] = y;
+    }
+  }
+  if (bad) atomicOr(a.status, kStatusBadPages);
+}
+
+}  // namespace
+
+int launch_paged_plan(const PagedPlanArgs& a, cudaStream_t stream) {
+  static std::atomic<unsigned long long> configured{0};
+  const int e = once_per_device(configured, [&]() -> int {
+    return (int)cudaFuncSetAttribute(fa2_paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     2 * (kPagedPlanMaxBatch + 1) * (int)sizeof(int));
+  });
+  if (e != 0) return e;
+  long long blocks = ((long long)a.total_q + kPlanThreads - 1) / kPlanThreads;
+  if (blocks > 152) blocks = 152;
+  const size_t smem = 2 * ((size_t)a.batch + 1) * sizeof(int);
+  fa2_paged_plan_kernel<<<(unsigned)blocks, kPlanThreads, smem, stream>>>(a);
+  return (int)cudaGetLastError();
+}
+
+int launch_paged_append(const PagedAppendArgs& a, cudaStream_t stream) {
+  const int items = a.heads << a.row_chunks_log2;
+  int x = 8;
+  while (x < 256 && x < items) x *= 2;
+  const dim3 block(x, 256 / x);
+  long long blocks = ((long long)a.total + block.y - 1) / block.y;
+  if (blocks > 152 * 64) blocks = 152 * 64;
+  fa2_paged_append_kernel<<<(unsigned)blocks, block, 0, stream>>>(a);
+  return (int)cudaGetLastError();
+}
+
+}  // namespace fa2

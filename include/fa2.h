@@ -22,13 +22,18 @@
  *                            packed variable-length batches (fa2_fwd_params);
  *   fa2_decode               up to FA2_DECODE_MAX_Q query rows per sequence
  *                            against long key sequences (fa2_fwd_params);
- *   fa2_fwd_host[_noalloc]   the forward on host buffers, end to end.
+ *   fa2_fwd_host[_noalloc]   the forward on host buffers, end to end;
+ *   fa2_paged_plan / fa2_paged_append / fa2_paged_fwd
+ *                            a serving step on a paged key/value cache: block
+ *                            tables and slots from request lengths, new rows
+ *                            written to their slots, attention of each
+ *                            request's new tokens (grouped query heads).
  *
  * Ownership: the caller owns every buffer.  fa2_fwd and fa2_fwd_ex allocate
- * no device memory; fa2_bwd, fa2_bwd_ex and fa2_decode take a caller
- * workspace.  The library keeps one small device status word per device for
- * reporting kernel-side wait timeouts and rejected packed offsets (see
- * fa2_get_device_status).
+ * no device memory; fa2_bwd, fa2_bwd_ex, fa2_decode and fa2_paged_fwd take a
+ * caller workspace.  The library keeps one small device status word per device
+ * for reporting kernel-side wait timeouts, rejected packed offsets and
+ * out-of-range pages (see fa2_get_device_status).
  *
  * No C++ exception crosses this interface: every entry point returns an
  * fa2_status code.
@@ -54,7 +59,8 @@ typedef enum {
   FA2_ERR_CUDA = 4,           /* a CUDA runtime/driver call failed */
   FA2_ERR_DEVICE_TIMEOUT = 5, /* a kernel wait ran out of time (fa2_get_device_status) */
   FA2_ERR_SCRATCH_LIMIT = 6,  /* problem too large for fa2_fwd_host_noalloc's static scratch */
-  FA2_ERR_DEVICE_SEQLENS = 7  /* packed-batch offsets out of range (fa2_get_device_status) */
+  FA2_ERR_DEVICE_SEQLENS = 7, /* packed-batch offsets out of range (fa2_get_device_status) */
+  FA2_ERR_DEVICE_PAGES = 8    /* paged cache: lengths, slots or pages out of range (fa2_get_device_status) */
 } fa2_status;
 
 /*
@@ -266,7 +272,9 @@ int fa2_fwd_host_noalloc(const void* q_host, const void* k_host, const void* v_h
  * current device's status word: FA2_OK, FA2_ERR_DEVICE_TIMEOUT if some
  * kernel's bounded wait on an mbarrier gave up (the kernel then abandoned its
  * tile, released its tensor memory and returned instead of hanging), else
- * FA2_ERR_DEVICE_SEQLENS if fa2_fwd_ex met out-of-range packed offsets.
+ * FA2_ERR_DEVICE_SEQLENS if fa2_fwd_ex met out-of-range packed offsets, else
+ * FA2_ERR_DEVICE_PAGES if a paged-cache call met lengths, a slot or a page out
+ * of range.
  * `detail` (may be NULL) receives the raw status bits (role and wait site).
  */
 int fa2_get_device_status(void* stream, uint32_t* detail);
@@ -335,6 +343,168 @@ typedef struct fa2_bwd_params {
 
 size_t fa2_bwd_ex_workspace_bytes(const fa2_fwd_params* fwd);
 int fa2_bwd_ex(const fa2_bwd_params* params, void* stream);
+
+/*
+ * fa2_paged_cache -- a key/value cache in pages of page_size rows, shared by
+ * the requests of a server: element (page, head, row, c) of k is at
+ *   k + page*k_strides[0] + head*k_strides[1] + row*k_strides[2] + c
+ * elements, v likewise.  So [num_pages, heads, page_size, d] and [num_pages,
+ * page_size, heads, d] storage both fit, and k and v may interleave in one
+ * allocation (fa2_paged_append: their elements are distinct).  Row r of page p
+ * is slot p * page_size + r.  Strides of dimensions larger than 1 are positive
+ * multiples of 8 elements below 2^39.
+ */
+typedef struct fa2_paged_cache {
+  void* k;                /* device, `dtype`, 16-byte aligned; written by fa2_paged_append only */
+  void* v;                /* device, `dtype`, 16-byte aligned; written by fa2_paged_append only */
+  int64_t k_strides[3];   /* page, head, row strides in elements */
+  int64_t v_strides[3];
+  int num_pages;          /* >= 1; num_pages * page_size < 2^31 (FA2_ERR_UNSUPPORTED) */
+  int page_size;          /* 8, 16, 32 or a multiple of 64 (FA2_ERR_UNSUPPORTED otherwise) */
+  int heads;              /* K/V heads >= 1 */
+  int head_dim;           /* d: 64, 128 or 256 */
+  int dtype;              /* FA2_FP16 or FA2_BF16 */
+} fa2_paged_cache;
+
+/*
+ * fa2_paged_plan -- block tables and the slot map of one serving step, built
+ * on the GPU from the requests' lengths.  Request b holds context_lens[b]
+ * cached tokens, on the first ceil(context / page_size) entries of its block
+ * table row, and gets query_lens[b] new ones (0: idle).  The call
+ *   - sets cu_seqlens_q (exclusive prefix sums of query_lens, batch + 1) and
+ *     seqlens_k[b] = context_lens[b] + query_lens[b];
+ *   - takes the pages the new tokens need beyond those held from the top of
+ *     the stack free_pages[0 .. *free_count), in order of the requests and of
+ *     each request's pages (the first page taken is free_pages[*free_count -
+ *     1]), and writes them to the table rows; other entries are left;
+ *   - sets slots[t] of new token t (packed order) to its slot, and to -1 for
+ *     the rows of slots behind the last token (padding);
+ *   - sets *free_left to what remains of the stack.
+ * free_count is read, not written, so the call may be repeated; the next step
+ * passes free_left as its free_count.
+ *
+ * A step that cannot be placed -- a negative length, a request past max_pages
+ * pages, more tokens than total_q, more pages than *free_count, *free_count
+ * outside [0, num_free] -- is refused whole: cu_seqlens_q = seqlens_k = 0,
+ * slots = -1, *free_left = *free_count, the table as it was (so an append and
+ * a forward of that step write nothing), and the next fa2_get_device_status
+ * returns FA2_ERR_DEVICE_PAGES.  The same status reports a page outside [0,
+ * num_pages) met in the free list or in a held entry; its tokens get slot -1.
+ *
+ * One kernel, asynchronous on `stream`, deterministic, no workspace.  Outputs
+ * overlap neither each other nor an input (FA2_ERR_INVALID_ARG).  Checks as
+ * fa2_fwd_ex; batch <= FA2_PAGED_PLAN_MAX_BATCH (FA2_ERR_UNSUPPORTED).
+ */
+#define FA2_PAGED_PLAN_MAX_BATCH 16384
+
+typedef struct fa2_paged_plan_params {
+  const int* context_lens; /* device, [batch] int32 */
+  const int* query_lens;   /* device, [batch] int32 */
+  const int* free_pages;   /* device, [num_free] int32 (may be NULL when num_free = 0) */
+  const int* free_count;   /* device, one int32 */
+  int* block_table;        /* device, [batch][max_pages] int32, rows table_stride apart; updated */
+  int* cu_seqlens_q;       /* device, [batch + 1] int32; written */
+  int* seqlens_k;          /* device, [batch] int32; written */
+  int* slots;              /* device, [total_q] int32; written */
+  int* free_left;          /* device, one int32; written */
+  int64_t table_stride;    /* elements; >= max_pages unless batch = 1 */
+  int batch;               /* >= 1 */
+  int max_pages;           /* table entries per request >= 1; max_pages * page_size < 2^31 */
+  int num_pages;           /* pages of the cache >= 1; num_pages * page_size < 2^31 */
+  int page_size;           /* >= 1 */
+  int total_q;             /* rows of slots >= 1: the step's tokens, with padding */
+  int num_free;            /* entries of free_pages >= 0 */
+} fa2_paged_plan_params;
+
+int fa2_paged_plan(const fa2_paged_plan_params* params, void* stream);
+
+/*
+ * fa2_paged_append -- new key/value rows into a paged cache: row t of k and v
+ * ([total, heads, d] by strides: token, head) goes to slot slots[t] of every
+ * head, bit for bit.  A negative slot is skipped (padding); a slot past the
+ * cache is skipped and reported (FA2_ERR_DEVICE_PAGES).  The slots >= 0 of one
+ * call are distinct (as fa2_paged_plan's are): which of two rows with one slot
+ * remains is not determined, per 16 bytes.  Other rows of the cache are not
+ * touched.  k, v and slots overlap neither cache tensor.  One kernel,
+ * asynchronous on `stream`.
+ */
+typedef struct fa2_paged_append_params {
+  fa2_paged_cache cache;
+  const void* k;           /* device, cache.dtype, 16-byte aligned; read only */
+  const void* v;           /* device, cache.dtype, 16-byte aligned; read only */
+  const int* slots;        /* device, [total] int32 */
+  int64_t k_strides[2];    /* token, head strides in elements; multiples of 8 */
+  int64_t v_strides[2];
+  int total;               /* rows >= 1 */
+} fa2_paged_append_params;
+
+int fa2_paged_append(const fa2_paged_append_params* params, void* stream);
+
+/*
+ * fa2_paged_fwd -- attention of each sequence's query tokens (one while
+ * decoding, a chunk of a prompt, or any mix over the batch) over its keys in a
+ * paged cache.  Sequence b's queries are rows cu_seqlens_q[b] <= r <
+ * cu_seqlens_q[b+1] of q / o ([total_q, heads, d] by strides: token, head) and
+ * of lse ([heads, total_q], head stride lse_stride); its seqlens_k[b] keys --
+ * the new tokens' own among them, already appended -- are rows j % page_size
+ * of pages block_table[b][j / page_size].  Query head i reads K/V head i /
+ * (heads / cache.heads); heads is a multiple of cache.heads, at most 128 times
+ * it (FA2_ERR_UNSUPPORTED).  Masks, scale, rows that see no key (O = 0, LSE =
+ * -inf) and rounding as fa2_fwd_ex: causal attention is window (-1, 0), a
+ * sliding window with sink keys (w, 0) with prefix_len.
+ *
+ * Rows of q / o / lse outside every sequence are left as they were.  Keys no
+ * query row of a sequence sees (rows past its length, keys before a window)
+ * may hold anything, NaN included, and their table entries are not read;
+ * visible keys and values are finite.
+ *
+ * Lengths, offsets and tables live on the device and are checked by the
+ * kernel: a sequence with cu_seqlens_q[b] > cu_seqlens_q[b+1], an offset
+ * outside [0, total_q], more than max_seqlen_q queries, or seqlens_k[b]
+ * outside [0, max_pages * page_size] is left unwritten and reported as
+ * FA2_ERR_DEVICE_SEQLENS (sequences whose query rows overlap: as fa2_fwd_ex).
+ * A needed page outside [0, num_pages) reads as zero keys and values and is
+ * reported as FA2_ERR_DEVICE_PAGES.
+ *
+ * `workspace`: device, >= fa2_paged_fwd_workspace_bytes(params) bytes, 256-byte
+ * aligned, overlapping no tensor: fp32 partial states, written before they
+ * are read (calls that overlap on the GPU each need their own).  o, lse and
+ * the workspace overlap nothing else.  Asynchronous on `stream`, two kernels;
+ * the host reads no length, so a captured call replays with new lengths,
+ * tables and slots in the same buffers.  Deterministic.  The first call on a
+ * device comes before any stream capture.
+ */
+typedef struct fa2_paged_params {
+  fa2_paged_cache cache;
+  const void* q;           /* device, cache.dtype, 16-byte aligned; read only */
+  void* o;                 /* device, cache.dtype, 16-byte aligned; written */
+  float* lse;              /* device, float32; written (natural log) */
+  const int* block_table;  /* device, [batch][max_pages] int32, rows table_stride apart */
+  const int* cu_seqlens_q; /* device, [batch + 1] int32 */
+  const int* seqlens_k;    /* device, [batch] int32 */
+  int64_t table_stride;    /* elements; >= 0 (0: one row for all sequences) */
+  int64_t q_strides[2];    /* token, head strides in elements; multiples of 8 */
+  int64_t o_strides[2];
+  int64_t lse_stride;      /* head stride in elements (token stride 1); >= total_q unless heads = 1 */
+  int batch;               /* sequences >= 1 */
+  int heads;               /* query heads >= 1 */
+  int total_q;             /* rows of q, o and lse >= 1 */
+  int max_seqlen_q;        /* longest sequence's query count >= 1 (sizes grid and workspace) */
+  int max_pages;           /* table entries per sequence >= 1; max_pages * page_size < 2^31 */
+  int window_left;         /* >= 0, or -1 = unbounded */
+  int window_right;        /* >= 0, or -1 = unbounded */
+  int prefix_len;          /* >= 0 */
+  float scale;             /* any finite value */
+} fa2_paged_params;
+
+/* sizeof(fa2_paged_params) as compiled into the library (binding check). */
+size_t fa2_paged_params_size(void);
+
+/* Workspace fa2_paged_fwd needs for these sizes (0 if they are invalid); it
+ * depends on no length and not on the device. */
+size_t fa2_paged_fwd_workspace_bytes(const fa2_paged_params* params);
+
+int fa2_paged_fwd(const fa2_paged_params* params, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * fa2_selftest_wait_timeout -- exercises the kernels' failure path without a
