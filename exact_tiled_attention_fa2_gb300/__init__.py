@@ -8,8 +8,10 @@ There is no CPU fallback: if the library is missing, calls raise.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
+import struct
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libfa2_gb300.so")
@@ -159,16 +161,20 @@ def load_library():
     lib.fa2_bwd_ex.restype = ci
     lib.fa2_bwd_ex_workspace_bytes.argtypes = [ctypes.POINTER(Fa2FwdParams)]
     lib.fa2_bwd_ex_workspace_bytes.restype = sz
-    lib.fa2_paged_plan.argtypes = [ctypes.POINTER(Fa2PagedPlanParams), vp]
+    lib.fa2_paged_plan.argtypes = [vp, vp]   # the parameter struct, by reference or packed
     lib.fa2_paged_plan.restype = ci
-    lib.fa2_paged_append.argtypes = [ctypes.POINTER(Fa2PagedAppendParams), vp]
+    lib.fa2_paged_append.argtypes = [vp, vp]
     lib.fa2_paged_append.restype = ci
-    lib.fa2_paged_fwd.argtypes = [ctypes.POINTER(Fa2PagedParams), vp, sz, vp]
+    lib.fa2_paged_fwd.argtypes = [vp, vp, sz, vp]
     lib.fa2_paged_fwd.restype = ci
-    lib.fa2_paged_fwd_workspace_bytes.argtypes = [ctypes.POINTER(Fa2PagedParams)]
+    lib.fa2_paged_fwd_workspace_bytes.argtypes = [vp]
     lib.fa2_paged_fwd_workspace_bytes.restype = sz
     lib.fa2_paged_params_size.argtypes = []
     lib.fa2_paged_params_size.restype = sz
+    for pack, mirror in ((_PAGED_PACK, Fa2PagedParams), (_PAGED_APPEND_PACK, Fa2PagedAppendParams),
+                         (_PAGED_PLAN_PACK, Fa2PagedPlanParams)):
+        if pack.size != ctypes.sizeof(mirror):
+            raise RuntimeError("%s layout mismatch: packed %d bytes" % (mirror.__name__, pack.size))
     if lib.fa2_paged_params_size() != ctypes.sizeof(Fa2PagedParams):
         raise RuntimeError("fa2_paged_params layout mismatch: library %d bytes, binding %d bytes"
                            % (lib.fa2_paged_params_size(), ctypes.sizeof(Fa2PagedParams)))
@@ -420,67 +426,76 @@ def fa2_bwd_ex(q, k, v, o, lse, dout, dq=None, dk=None, dv=None, workspace=None,
     return dq, dk, dv
 
 
-class _on_device:
-    """Makes ``tensor``'s device current and ``stream`` (None: that device's
-    current stream) the one new tensors are allocated for, so that a result or
-    a workspace allocated here is not handed out again before the kernels of
-    ``stream`` are done with it.  ``handle``: the stream for the library."""
-
-    def __init__(self, tensor, stream):
-        import torch
-        device = tensor.device
-        guards = []
-        if device.index != torch.cuda.current_device():
-            guards.append(torch.cuda.device(device))
-        if stream is None:
-            stream = torch.cuda.current_stream(device)
-        elif stream.device != device:
-            raise ValueError("stream must belong to the tensors' device %s" % device)
-        elif stream != torch.cuda.current_stream(device):
-            guards.append(torch.cuda.stream(stream))
-        self._guards = guards
-        self.handle = ctypes.c_void_p(int(stream.cuda_stream))
-
-    def __enter__(self):
-        for g in self._guards:
-            g.__enter__()
-        return self
-
-    def __exit__(self, *exc):
-        for g in reversed(self._guards):
-            g.__exit__(*exc)
-        return False
+# The paged calls run once per layer of a serving step on small tensors, so the
+# binding's own time shows: parameters are packed in one go (the formats mirror
+# the Structures above field by field; load_library checks their sizes) and
+# results come from the tensors' own allocators.
+_PAGED_PACK = struct.Struct("@PP3q3q5i4x3P3Pq2q2qq8if4x")
+_PAGED_APPEND_PACK = struct.Struct("@PP3q3q5i4x3P2q2qi4x")
+_PAGED_PLAN_PACK = struct.Struct("@9Pq6i")
+_torch = None   # torch, its 16-bit dtypes' codes, int32, raw-stream and device getters (set on first use)
 
 
-def _int32(t, name, device, dims, shape=None):
+def _torch_facts():
+    global _torch
     import torch
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.device != device or t.dim() != dims:
-        raise ValueError("%s must be an int32 tensor with %d dimension%s on %s"
-                         % (name, dims, "" if dims == 1 else "s", device))
-    if t.numel() and t.stride(-1) != 1 and t.shape[-1] > 1:
-        raise ValueError("%s must have a contiguous last dimension" % name)
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    return t
+    _torch = (torch, {torch.float16: FA2_FP16, torch.bfloat16: FA2_BF16}, torch.int32,
+              torch._C._cuda_getCurrentRawStream, torch.cuda.current_device)
+    return _torch
+
+
+@contextlib.contextmanager
+def _on_device(device, stream):
+    """``device`` current, and ``stream`` (if given) the current stream there:
+    tensors allocated inside are not handed out again before its kernels are
+    done with them."""
+    import torch
+    with torch.cuda.device(device):
+        if stream is None:
+            yield
+        elif stream.device.index != device:
+            raise ValueError("stream must belong to the tensors' device (cuda:%d)" % device)
+        else:
+            with torch.cuda.stream(stream):
+                yield
+
+
+def _int32_1d(t, name, dev, n):
+    if t.dtype != _torch[2] or t.get_device() != dev or t.dim() != 1 or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous int32 tensor [n] on the call's CUDA device" % name)
+    if t.numel() != n:
+        raise ValueError("%s must have %d elements, has %d" % (name, n, t.numel()))
+    return t.data_ptr()
+
+
+def _block_table(t, dev, rows):
+    """(pointer, row stride, columns) of a block table."""
+    shape, st = t.shape, t.stride()
+    if t.dtype != _torch[2] or t.get_device() != dev or len(shape) != 2 or shape[0] != rows:
+        raise ValueError("block_table must be an int32 tensor [%d, max_pages] on the call's CUDA device" % rows)
+    if st[1] != 1 and shape[1] > 1:
+        raise ValueError("block_table must have a contiguous last dimension")
+    return t.data_ptr(), st[0], shape[1]
 
 
 def _paged_cache(k_cache, v_cache):
-    """Marshal cache tensors [num_pages, H_kv, page_size, d] into an Fa2PagedCache."""
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+    """(device, shape, dtype, Fa2PagedCache fields) of cache tensors [num_pages, H_kv, page_size, d]."""
+    facts = _torch or _torch_facts()
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must share one [num_pages, H_kv, page_size, d] shape")
-    for t in (k_cache, v_cache):
-        if not t.is_cuda or t.stride(-1) != 1:
-            raise ValueError("k_cache and v_cache must be CUDA tensors with a contiguous last dimension")
-    if v_cache.dtype != k_cache.dtype:
-        raise TypeError("k_cache and v_cache must share one dtype")
-    if v_cache.device != k_cache.device:
-        raise ValueError("k_cache and v_cache must be on one device")
-    c = Fa2PagedCache()
-    c.k, c.v = k_cache.data_ptr(), v_cache.data_ptr()
-    c.k_strides[:], c.v_strides[:] = k_cache.stride()[:3], v_cache.stride()[:3]
-    c.num_pages, c.heads, c.page_size, c.head_dim = k_cache.shape
-    c.dtype = _dtype_code(k_cache)
-    return c
+    dev, dtype = k_cache.get_device(), k_cache.dtype
+    if dev < 0 or v_cache.get_device() != dev:
+        raise ValueError("k_cache and v_cache must be CUDA tensors on one device")
+    code = facts[1].get(dtype)
+    if code is None or v_cache.dtype != dtype:
+        raise TypeError("k_cache and v_cache must share one dtype, float16 or bfloat16")
+    ks, vs = k_cache.stride(), v_cache.stride()
+    pages, heads, page_size, d = shape
+    if (ks[3] != 1 or vs[3] != 1) and d > 1:
+        raise ValueError("k_cache and v_cache must have a contiguous last dimension")
+    return dev, shape, dtype, (k_cache.data_ptr(), v_cache.data_ptr(), ks[0], ks[1], ks[2], vs[0], vs[1], vs[2],
+                               pages, page_size, heads, d, code)
 
 
 def fa2_paged_plan(context_lens, query_lens, block_table, free_pages, free_count, num_pages, page_size, total_q,
@@ -499,34 +514,35 @@ def fa2_paged_plan(context_lens, query_lens, block_table, free_pages, free_count
     is refused whole: empty outputs, the table as it was, and
     FA2_ERR_DEVICE_PAGES from the next fa2_get_device_status.
     """
-    import torch
-    if not context_lens.is_cuda:
-        raise ValueError("fa2_paged_plan takes CUDA tensors")
-    dev = context_lens.device
-    B = context_lens.shape[0] if context_lens.dim() == 1 else 0
-    _int32(context_lens, "context_lens", dev, 1)
-    _int32(query_lens, "query_lens", dev, 1, (B,))
-    _int32(block_table, "block_table", dev, 2)
-    if block_table.shape[0] != B:
-        raise ValueError("block_table must have one row per request")
-    _int32(free_pages, "free_pages", dev, 1)
-    _int32(free_count, "free_count", dev, 1, (1,))
-    total_q = int(total_q)
-    with _on_device(context_lens, stream) as on:
-        new = lambda n: torch.empty(n, dtype=torch.int32, device=dev)
-        cu_seqlens_q = new(B + 1) if cu_seqlens_q is None else _int32(cu_seqlens_q, "cu_seqlens_q", dev, 1, (B + 1,))
-        seqlens_k = new(B) if seqlens_k is None else _int32(seqlens_k, "seqlens_k", dev, 1, (B,))
-        slots = new(max(total_q, 0)) if slots is None else _int32(slots, "slots", dev, 1, (total_q,))
-        free_left = new(1) if free_left is None else _int32(free_left, "free_left", dev, 1, (1,))
-        p = Fa2PagedPlanParams()
-        p.context_lens, p.query_lens = context_lens.data_ptr(), query_lens.data_ptr()
-        p.free_pages, p.free_count = free_pages.data_ptr(), free_count.data_ptr()
-        p.block_table, p.table_stride = block_table.data_ptr(), block_table.stride(0)
-        p.cu_seqlens_q, p.seqlens_k = cu_seqlens_q.data_ptr(), seqlens_k.data_ptr()
-        p.slots, p.free_left = slots.data_ptr(), free_left.data_ptr()
-        p.batch, p.max_pages, p.num_pages, p.page_size = B, block_table.shape[1], int(num_pages), int(page_size)
-        p.total_q, p.num_free = total_q, free_pages.shape[0]
-        rc = load_library().fa2_paged_plan(ctypes.byref(p), on.handle)
+    facts = _torch or _torch_facts()
+    dev = context_lens.get_device()
+    if dev < 0 or context_lens.dim() != 1:
+        raise ValueError("context_lens must be an int32 CUDA tensor [B]")
+    if stream is not None or dev != facts[4]():
+        with _on_device(dev, stream):
+            return fa2_paged_plan(context_lens, query_lens, block_table, free_pages, free_count, num_pages,
+                                  page_size, total_q, cu_seqlens_q, seqlens_k, slots, free_left)
+    B, total_q, num_free = context_lens.numel(), int(total_q), free_pages.numel()
+    ctx = _int32_1d(context_lens, "context_lens", dev, B)
+    new = _int32_1d(query_lens, "query_lens", dev, B)
+    table, table_stride, max_pages = _block_table(block_table, dev, B)
+    free = _int32_1d(free_pages, "free_pages", dev, num_free)
+    count = _int32_1d(free_count, "free_count", dev, 1)
+    if total_q < 1:
+        raise ValueError("total_q must be at least 1")
+    if cu_seqlens_q is None:
+        cu_seqlens_q = context_lens.new_empty(B + 1)
+    if seqlens_k is None:
+        seqlens_k = context_lens.new_empty(B)
+    if slots is None:
+        slots = context_lens.new_empty(total_q)
+    if free_left is None:
+        free_left = context_lens.new_empty(1)
+    params = _PAGED_PLAN_PACK.pack(
+        ctx, new, free, count, table, _int32_1d(cu_seqlens_q, "cu_seqlens_q", dev, B + 1),
+        _int32_1d(seqlens_k, "seqlens_k", dev, B), _int32_1d(slots, "slots", dev, total_q),
+        _int32_1d(free_left, "free_left", dev, 1), table_stride, B, max_pages, num_pages, page_size, total_q, num_free)
+    rc = (_lib or load_library()).fa2_paged_plan(params, facts[3](dev))
     if rc:
         raise Fa2Error(rc, "fa2_paged_plan")
     return cu_seqlens_q, seqlens_k, slots, free_left
@@ -541,58 +557,55 @@ def fa2_paged_append(k, v, slots, k_cache, v_cache, stream=None):
     with a contiguous last dimension (a [num_pages, page_size, H_kv, d] cache
     as ``x.transpose(1, 2)``); slot s is row s % page_size of page s // page_size.
     """
-    p = Fa2PagedAppendParams()
-    p.cache = _paged_cache(k_cache, v_cache)
-    dev = k_cache.device
-    if k.dim() != 3 or v.shape != k.shape or k.shape[1] != k_cache.shape[1] or k.shape[2] != k_cache.shape[3]:
+    dev, shape, dtype, cache = _paged_cache(k_cache, v_cache)
+    facts = _torch
+    if stream is not None or dev != facts[4]():
+        with _on_device(dev, stream):
+            return fa2_paged_append(k, v, slots, k_cache, v_cache)
+    rows = k.shape
+    if len(rows) != 3 or v.shape != rows or rows[1] != shape[1] or rows[2] != shape[3]:
         raise ValueError("k and v must be [total, H_kv, d] with the cache's heads and head dim")
-    for t in (k, v):
-        if t.device != dev or t.stride(-1) != 1:
-            raise ValueError("k and v must be on the cache's device with a contiguous last dimension")
-        if t.dtype != k_cache.dtype:
-            raise TypeError("k, v and the cache must share one dtype")
-    _int32(slots, "slots", dev, 1, (k.shape[0],))
-    p.k, p.v, p.slots, p.total = k.data_ptr(), v.data_ptr(), slots.data_ptr(), k.shape[0]
-    p.k_strides[:], p.v_strides[:] = k.stride()[:2], v.stride()[:2]
-    with _on_device(k_cache, stream) as on:
-        rc = load_library().fa2_paged_append(ctypes.byref(p), on.handle)
+    ks, vs = k.stride(), v.stride()
+    if k.get_device() != dev or v.get_device() != dev or ks[2] != 1 or vs[2] != 1:
+        raise ValueError("k and v must be on the cache's device with a contiguous last dimension")
+    if k.dtype != dtype or v.dtype != dtype:
+        raise TypeError("k, v and the cache must share one dtype")
+    total = rows[0]
+    params = _PAGED_APPEND_PACK.pack(*cache, k.data_ptr(), v.data_ptr(), _int32_1d(slots, "slots", dev, total),
+                                     ks[0], ks[1], vs[0], vs[1], total)
+    rc = (_lib or load_library()).fa2_paged_append(params, facts[3](dev))
     if rc:
         raise Fa2Error(rc, "fa2_paged_append")
 
 
-def _paged_params(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, scale, window_left, window_right,
-                  prefix_len, max_seqlen_q):
-    """Marshal a paged forward's inputs into an Fa2PagedParams (o and lse are set by the caller)."""
-    p = Fa2PagedParams()
-    p.cache = _paged_cache(k_cache, v_cache)
-    dev = k_cache.device
-    if q.dim() != 3 or q.shape[2] != k_cache.shape[3]:
+def _paged_inputs(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, max_seqlen_q):
+    """A paged forward's inputs, checked: (device, function packing the call's parameters)."""
+    dev, shape, dtype, cache = _paged_cache(k_cache, v_cache)
+    q_shape, qs = q.shape, q.stride()
+    if len(q_shape) != 3 or q_shape[2] != shape[3]:
         raise ValueError("q must be [total_q, H, d] with the cache's head dim")
-    if q.device != dev or q.stride(-1) != 1:
+    if q.get_device() != dev or qs[2] != 1:
         raise ValueError("q must be on the cache's device with a contiguous last dimension")
-    if q.dtype != k_cache.dtype:
+    if q.dtype != dtype:
         raise TypeError("q and the cache must share one dtype")
-    _int32(seqlens_k, "seqlens_k", dev, 1)
-    B = seqlens_k.shape[0]
-    _int32(cu_seqlens_q, "cu_seqlens_q", dev, 1, (B + 1,))
-    _int32(block_table, "block_table", dev, 2)
-    if block_table.shape[0] != B:
-        raise ValueError("block_table must have one row per sequence")
-    p.q, p.block_table = q.data_ptr(), block_table.data_ptr()
-    p.cu_seqlens_q, p.seqlens_k = cu_seqlens_q.data_ptr(), seqlens_k.data_ptr()
-    p.table_stride, p.max_pages = block_table.stride(0), block_table.shape[1]
-    p.q_strides[:] = q.stride()[:2]
-    p.batch, p.heads, p.total_q = B, q.shape[1], q.shape[0]
-    p.max_seqlen_q = q.shape[0] if max_seqlen_q is None else int(max_seqlen_q)
-    p.window_left, p.window_right, p.prefix_len = int(window_left), int(window_right), int(prefix_len)
-    p.scale = 1.0 / float(q.shape[2]) ** 0.5 if scale is None else float(scale)
-    return p
+    B = seqlens_k.numel()
+    lens = _int32_1d(seqlens_k, "seqlens_k", dev, B)
+    cu = _int32_1d(cu_seqlens_q, "cu_seqlens_q", dev, B + 1)
+    table, table_stride, max_pages = _block_table(block_table, dev, B)
+    total, heads, d = q_shape
+    longest = total if max_seqlen_q is None else int(max_seqlen_q)
+
+    def pack(o, lse, os, lse_stride, scale=0.0, window_left=-1, window_right=-1, prefix_len=0):
+        return _PAGED_PACK.pack(*cache, q.data_ptr(), o, lse, table, cu, lens, table_stride, qs[0], qs[1], os[0],
+                                os[1], lse_stride, B, heads, total, longest, max_pages, window_left, window_right,
+                                prefix_len, scale)
+    return dev, pack
 
 
 def fa2_paged_fwd_workspace_bytes(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, max_seqlen_q=None) -> int:
     """Workspace fa2_paged_fwd needs for these tensors; it depends on their shapes only."""
-    p = _paged_params(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, None, -1, -1, 0, max_seqlen_q)
-    return int(load_library().fa2_paged_fwd_workspace_bytes(ctypes.byref(p)))
+    _, pack = _paged_inputs(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, max_seqlen_q)
+    return int(load_library().fa2_paged_fwd_workspace_bytes(pack(0, 0, (0, 0), 0)))
 
 
 def fa2_paged_fwd(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, o=None, lse=None, workspace=None,
@@ -610,29 +623,31 @@ def fa2_paged_fwd(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, o=N
     grid and the workspace.  Returns (o [total_q, H, d], lse [H, total_q]);
     rows outside every sequence are not written.
     """
-    import torch
-    p = _paged_params(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, scale, window_left, window_right,
-                      prefix_len, max_seqlen_q)
-    lib = load_library()
-    with _on_device(q, stream) as on:
-        if o is None:
-            o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        elif o.shape != q.shape or o.dtype != q.dtype or o.device != q.device or o.stride(-1) != 1:
-            raise ValueError("o must have q's shape, dtype and device with a contiguous last dimension")
-        if lse is None:
-            lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=q.device)
-        elif (tuple(lse.shape) != (q.shape[1], q.shape[0]) or lse.dtype != torch.float32 or lse.device != q.device
-              or (lse.stride(-1) != 1 and lse.shape[-1] > 1)):
-            raise ValueError("lse must be float32 [H, total_q] on q's device with a contiguous last dimension")
-        p.o, p.lse, p.lse_stride = o.data_ptr(), lse.data_ptr(), lse.stride(0)
-        p.o_strides[:] = o.stride()[:2]
-        if workspace is None:
-            need = int(lib.fa2_paged_fwd_workspace_bytes(ctypes.byref(p)))
-            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
-        elif workspace.device != q.device or not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous tensor on q's device")
-        rc = lib.fa2_paged_fwd(ctypes.byref(p), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                               on.handle)
+    dev, pack = _paged_inputs(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, max_seqlen_q)
+    facts = _torch
+    if stream is not None or dev != facts[4]():
+        with _on_device(dev, stream):
+            return fa2_paged_fwd(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, o, lse, workspace, scale,
+                                 window_left, window_right, prefix_len, max_seqlen_q)
+    torch = facts[0]
+    total, heads, d = q.shape
+    if o is None:
+        o = q.new_empty((total, heads, d))
+    elif o.shape != q.shape or o.dtype != q.dtype or o.get_device() != dev or o.stride(2) != 1:
+        raise ValueError("o must have q's shape, dtype and device with a contiguous last dimension")
+    if lse is None:
+        lse = q.new_empty((heads, total), dtype=torch.float32)
+    elif (lse.shape != (heads, total) or lse.dtype != torch.float32 or lse.get_device() != dev
+          or (lse.stride(1) != 1 and total > 1)):
+        raise ValueError("lse must be float32 [H, total_q] on q's device with a contiguous last dimension")
+    params = pack(o.data_ptr(), lse.data_ptr(), o.stride(), lse.stride(0),
+                  1.0 / float(d) ** 0.5 if scale is None else float(scale), window_left, window_right, prefix_len)
+    lib = _lib or load_library()
+    if workspace is None:
+        workspace = q.new_empty(max(lib.fa2_paged_fwd_workspace_bytes(params), 256), dtype=torch.uint8)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on q's device")
+    rc = lib.fa2_paged_fwd(params, workspace.data_ptr(), workspace.numel() * workspace.element_size(), facts[3](dev))
     if rc:
         raise Fa2Error(rc, "fa2_paged_fwd")
     return o, lse

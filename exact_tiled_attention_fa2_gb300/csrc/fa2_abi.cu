@@ -1044,19 +1044,19 @@ int paged_device_status(uint32_t** status) {
 
 // The strides of dimensions of size 1 address nothing and are replaced by a
 // valid placeholder.
-int encode_map_4d(CUtensorMap* m, const void* base, const long long dims[4], const long long strides[3],
-                  const int box[4], bool bf16) {
-  cuuint64_t d[4], st[3];
-  cuuint32_t b[4], estr[4] = {1, 1, 1, 1};
-  for (int i = 0; i < 4; ++i) {
+int encode_map_nd(CUtensorMap* m, const void* base, int rank, const long long* dims, const long long* strides,
+                  const int* box, bool bf16) {
+  cuuint64_t d[5], st[4];
+  cuuint32_t b[5], estr[5] = {1, 1, 1, 1, 1};
+  for (int i = 0; i < rank; ++i) {
     d[i] = (cuuint64_t)dims[i];
     b[i] = (cuuint32_t)box[i];
   }
-  for (int i = 0; i < 3; ++i) st[i] = (cuuint64_t)(dims[i + 1] > 1 ? strides[i] : dims[0]) * 2;
-  const CUresult r = g_encode(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
-                              const_cast<void*>(base), d, st, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  for (int i = 0; i + 1 < rank; ++i) st[i] = (cuuint64_t)(dims[i + 1] > 1 ? strides[i] : dims[0]) * 2;
+  const CUresult r = g_encode(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                              (cuuint32_t)rank, const_cast<void*>(base), d, st, b, estr,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? FA2_OK : FA2_ERR_CUDA;
 }
 

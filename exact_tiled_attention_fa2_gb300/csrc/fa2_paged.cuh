@@ -12,55 +12,115 @@
 // cores.  Row r of the tile is token r / group, query head h * group +
 // r % group, the order in which a TMA box (64 columns x group x tokens) lands.
 //
-// The tile loop is the double-buffered forward kernel's (fa2_fwd_dbuf.cuh: its
-// MMA role, barriers, tensor-memory layout and two-CTA size classes).  What
-// differs: a 64-key tile arrives as one box per page (pages of 8 .. 32 rows)
-// or as one box (pages of 64 k rows); the TMA warp's lanes each read their
-// box's page from the block table three tiles ahead and issue their own box,
-// so the table's latency stays off the pipeline.  Pages none of the tile's
+// Schedule.  The lengths are on the device, so the CTAs lay the batch's work
+// out themselves: every (query tile, K/V head) pair is a span of keys, the
+// spans of all pairs make one line, and each of the p.ctas CTAs (two per SM,
+// one at d = 256) takes an equal piece of it, whatever the lengths are.  A
+// piece is a run of fragments: the end of one pair, whole pairs, the start of
+// another.  Whole pairs write O and L; the others leave fp32 partials (m, l,
+// O~) in the CTA's two slots, which a second kernel, launched as a programmatic
+// dependent, merges.  Batches of many query tiles (a long prompt from its
+// start, where equal pieces of the line would lose the CTAs' walking of the
+// same keys) run one pair per CTA instead, in the hardware's order.
+//
+// One CTA, 192 threads, as the double-buffered forward kernel
+// (fa2_fwd_dbuf.cuh: tensor-memory layout, two S buffers, 2-stage K and V
+// rings, one softmax thread per row), with the rings' and barriers' phases
+// counted across its fragments: while the softmax warps finish a fragment, the
+// TMA warp already loads the next one's K, V and Q and the MMA thread issues
+// its first S products.
+//
+// A 64-key tile lands as [8-row group][64-column block][8 rows][128 bytes]
+// (128-byte swizzle), so that rows of any page size follow each other with one
+// stride: one 5-D box per page and tile (pages of 8 .. 32 rows: 8 .. 2 boxes, of
+// 64 k rows: one), issued by one lane of the TMA warp per page, which reads
+// its page from the block table three tiles ahead.  Pages none of the tile's
 // rows see are not loaded, and key tiles between a prefix and the band are not
 // visited.  V rows no row of the tile sees (the last page's tail, keys before
 // a window) may hold anything: they are zeroed in shared memory before the
 // product, since 0 x NaN would reach the sums.
-//
-// Key splits: the lengths are on the device, so every CTA sums the batch's
-// work (the visited key tiles of all query tiles), derives the split size that
-// cuts it into about target_units equal units, and finds its own unit by a
-// prefix sum over the sequences.  A tile cut into several units leaves fp32
-// partials (m, l, O~) that a second kernel, launched as a programmatic
-// dependent, merges; other tiles write O and L directly.
 #pragma once
 
-#include <cstring>
+#include <climits>
 
 #include "fa2_fwd_dbuf.cuh"
 #include "fa2_paged.h"
 
 namespace fa2 {
 
+// Barriers (8 bytes each).  Phases count key tiles g (K, V, S, P, O) or
+// fragments f of the CTA (the others).
+enum : int {
+  PG_Q = 0,        // + f & 1: the fragment's description and Q are in shared memory
+  PG_QEMPTY = 2,   // the fragment's last S product is done with Q
+  PG_KFULL = 3,    // + stage
+  PG_KEMPTY = 5,   // + stage
+  PG_VFULL = 7,    // + stage
+  PG_VEMPTY = 9,   // + stage
+  PG_S = 11,       // + buffer
+  PG_P = 13,       // + buffer (four softmax warps)
+  PG_O = 15,       // after every PV product
+  PG_OLAST = 16,   // after a fragment's last PV product
+  PG_ODONE = 17,   // + f & 1: the softmax warps are done with O~ and the description
+  PG_EXIT = 19,
+  PG_BARS = 20,
+};
+
+// Everything the softmax warps and the MMA thread need of a fragment: written
+// by the TMA warp, two in flight.
+struct PagedFrag {
+  int n;           // key tiles (0: the pair has no visible key; -1: no more fragments)
+  int j0;          // first of them, as a visited index of the pair
+  int row;         // first token's row of q / o / lse
+  int q0;          // first token within its sequence
+  int rows;        // live rows: group x tokens
+  int h;           // K/V head
+  int slot;        // partial slot, or -1: write O and L
+  int few_keys;    // N_k <= 2 key tiles: every bf16 P is split
+  TileMask tm;     // key tiles every row sees, by index from j0
+  KeyMask km;
+  int npre, skip;  // visited index j is key tile j + (j >= npre ? skip : 0)
+  int lo, end;     // the band's keys (the prefix's: km.pre_end)
+  __device__ __forceinline__ int tile(int j) const { return j + (j >= npre ? skip : 0); }
+};
+
 template <int D_>
-struct PagedConfig : DbufConfig<D_> {
-  using Base = DbufConfig<D_>;
-  static constexpr bool TMA_GATES_P = false;
-  static constexpr uint32_t MISC_BYTES = 512;   // TMEM address, abort flag, unit; scan scratch
-  static constexpr uint32_t SMEM_BYTES = Base::OFF_MISC + MISC_BYTES + 1024;
+struct PagedConfig {
+  static constexpr int D = D_;
+  static constexpr int BR = kPagedTileRows;
+  static constexpr int BC = kPagedKeyTile;
+  static constexpr int KSTAGES = 2;
+  static constexpr int VSTAGES = 2;
+  static constexpr int THREADS = 192;
+  static constexpr int MMA_WARP = 4;
+  static constexpr int TMA_WARP = 5;
+  static constexpr int BLOCKS = D / 64;                 // 64-column blocks of a row
+  static constexpr uint32_t GROUP_BYTES = BLOCKS * 1024;   // 8 key rows
+  static constexpr uint32_t Q_BYTES = BR * D * 2;
+  static constexpr uint32_t KV_BYTES = BC * D * 2;
+  static constexpr uint32_t OFF_Q = 0;
+  static constexpr uint32_t OFF_K = OFF_Q + Q_BYTES;
+  static constexpr uint32_t OFF_V = OFF_K + KSTAGES * KV_BYTES;
+  static constexpr uint32_t OFF_BAR = OFF_V + VSTAGES * KV_BYTES;
+  static constexpr uint32_t OFF_MISC = OFF_BAR + PG_BARS * 8;   // TMEM address, abort flag
+  static constexpr uint32_t OFF_FRAG = OFF_MISC + 16;
+  static constexpr uint32_t OFF_SCAN = OFF_FRAG + 256;
+  static constexpr uint32_t SMEM_BYTES = OFF_SCAN + 256 + 1024;
+  static constexpr uint32_t TMEM_S = 0;   // + 64 * buffer
+  static constexpr uint32_t TMEM_O = 128;
+  static constexpr uint32_t TMEM_COLS = D == 256 ? 512 : 256;
+  static constexpr int CTAS_PER_SM = D == 256 ? 1 : 2;
+  static_assert(2 * sizeof(PagedFrag) <= 256, "fragment descriptions");
   static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
-  static_assert(Base::CTAS_PER_SM * (SMEM_BYTES + 1024) <= 233472, "shared memory per SM");
+  static_assert(CTAS_PER_SM * (SMEM_BYTES + 1024) <= 233472, "shared memory per SM");
 };
 
-// One sequence's part in the schedule.
-struct PagedSeq {
-  int row0, n_q, n_k;
-  int tiles;   // query tiles
-  int nv;      // most key tiles one of them visits
-};
+// ---------------------------------------------------------------- the line of work
 
-// The key tiles a query tile visits: visited index j is key tile j + (j >=
-// npre ? skip : 0).  lo / end: the band's keys; pre_end (KeyMask): the prefix.
+// The key tiles a query tile visits (PagedFrag::tile), and its band's keys.
 struct TileWalk {
   int npre, skip, n;
   int lo, end;
-  __device__ __forceinline__ int tile(int j) const { return j + (j >= npre ? skip : 0); }
 };
 
 __device__ __forceinline__ TileWalk tile_walk(const KeyMask& km, int first, int last) {
@@ -96,6 +156,26 @@ __device__ __forceinline__ KeyMask paged_mask(const PagedParams& p, int n_q, int
   return km;
 }
 
+// One sequence's part of the line: `tiles` query tiles x heads_kv pairs, in
+// order of the tiles, heads fastest.
+struct PagedSeq {
+  int row0, n_q, n_k;
+  int tiles;
+  int keys;      // a pair's span in keys, or -1: a causal chunk, whose spans
+                 // grow by tile_tokens from tile to tile and end at N_k
+  __device__ __forceinline__ int width(const PagedParams& p, int t) const {
+    return p.overhead + (keys >= 0 ? keys : n_k - n_q + min((t + 1) * p.tile_tokens, n_q));
+  }
+  // spans of the tiles before t (one head's)
+  __device__ __forceinline__ long long before(const PagedParams& p, int t) const {
+    return keys >= 0 ? (long long)t * (p.overhead + keys)
+                     : (long long)t * (p.overhead + n_k - n_q) + (long long)p.tile_tokens * t * (t + 1) / 2;
+  }
+  __device__ __forceinline__ long long span(const PagedParams& p) const {
+    return tiles == 0 ? 0 : (before(p, tiles - 1) + width(p, tiles - 1)) * p.heads_kv;
+  }
+};
+
 // Sequence i; no tiles (and the bad-offsets bit, if `report`) when its row
 // offsets or its length are out of range.
 __device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int i, bool report) {
@@ -105,7 +185,7 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int i, bool 
   s.n_q = b - a;
   s.n_k = k;
   s.tiles = 0;
-  s.nv = 0;
+  s.keys = 0;
   if (!(0 <= a && a <= b && b <= p.total_q && b - a <= p.max_q && 0 <= k &&
         (long long)k <= (long long)p.max_pages * p.page_size)) {
     if (report) atomicOr(p.status, kStatusBadSeqlens);
@@ -114,264 +194,488 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int i, bool 
   if (s.n_q == 0) return s;
   s.tiles = (s.n_q + p.tile_tokens - 1) / p.tile_tokens;
   const KeyMask km = paged_mask(p, s.n_q, s.n_k);
-  if (p.window_left < 0 || s.tiles == 1) {
-    // without a left window the last tile visits the most
-    s.nv = tile_walk(km, (s.tiles - 1) * p.tile_tokens, s.n_q - 1).n;
+  int nv;   // most key tiles one of the query tiles visits
+  if (s.tiles == 1) {
+    nv = tile_walk(km, 0, s.n_q - 1).n;
+  } else if (p.window_left < 0) {
+    if (p.window_right == 0 && km.off + p.tile_tokens >= max(km.pre_end, 1)) {
+      s.keys = -1;
+      return s;
+    }
+    nv = tile_walk(km, (s.tiles - 1) * p.tile_tokens, s.n_q - 1).n;   // the last tile visits the most
   } else {
     const long long band = (long long)p.window_left + (p.window_right < 0 ? s.n_k : p.window_right) + p.tile_tokens;
     const long long all = (s.n_k + kPagedKeyTile - 1) / kPagedKeyTile;
     const long long n = (km.pre_end + kPagedKeyTile - 1) / kPagedKeyTile + band / kPagedKeyTile + 2;
-    s.nv = (int)(n < all ? n : all);
+    nv = (int)(n < all ? n : all);
   }
+  s.keys = max(nv, 1) * kPagedKeyTile;
   return s;
 }
 
-// What a CTA works on: a query tile of one K/V head of one sequence, and the
-// split size that its units follow.
-struct PagedUnit {
-  int seq, row0, n_q, n_k;
-  int h, tile;
-  int split;        // this unit's chunk
-  int splits;       // chunks the sequence's tiles are cut into at most
-  int chunk;        // the split size C in key tiles
-  int slot0;        // first partial slot of the sequence (splits > 1)
+// Where a CTA (or a merge block) starts, and the pieces' size.
+struct PagedPlace {
+  long long at;      // the sequence's start on the line
+  long long share;   // keys of a piece; 0: one pair per CTA
+  long long total;   // the line's length
+  int seq;           // the sequence holding the position, or -1: past the end
+  int rank;          // one pair per CTA: the pair's index in its sequence
 };
-
-// Chunks a tile of n visited key tiles is cut into, given the split size.
-__device__ __forceinline__ int tile_splits(int n, int chunk) { return n > chunk ? (n + chunk - 1) / chunk : 1; }
-
-// Slot of a tile's chunk `s`: the sequence's units in launch order.
-__device__ __forceinline__ int unit_slot(const PagedUnit& u, int tiles, int heads, int s) {
-  return u.slot0 + ((tiles - 1 - u.tile) * u.splits + s) * heads + u.h;
-}
 
 struct PagedScan {
-  long long warp_a[8], warp_b[8];
-  PagedUnit unit;
-  int found;
+  long long warp_sum[3][8];
+  PagedPlace place;
 };
 
+// Finds the sequence that holds piece `piece`'s start (or, where the batch
+// runs one pair per CTA, pair `piece`).  Every thread sums a run of sequences;
+// every thread returns the same.
 template <int THREADS>
-__device__ __forceinline__ long long block_sum(long long x, long long* scratch) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = x;
-  __syncthreads();
-  long long sum = 0;
-#pragma unroll
-  for (int j = 0; j < THREADS / 32; ++j) sum += scratch[j];
-  return sum;
-}
-
-// Places `index` in the batch: unit `index` (MERGE = false) or split (query
-// tile, K/V head) pair `index` (MERGE = true).  Every thread takes a run of
-// sequences and returns the same answer; false if there is no such unit.
-// Inside a sequence units run over K/V heads fastest, then chunks, then query
-// tiles from the last (under a causal mask the one with the most keys), so
-// the CTAs resident at a time walk the same keys.
-template <int THREADS, bool MERGE>
-__device__ __forceinline__ bool find_unit(const PagedParams& p, long long index, PagedScan* sh, PagedUnit& out) {
+__device__ __forceinline__ PagedPlace find_place(const PagedParams& p, int piece, PagedScan* sh, bool report) {
+  constexpr int NW = THREADS / 32;
   const int tid = (int)threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int per = (p.batch + THREADS - 1) / THREADS;
   const int i0 = min(tid * per, p.batch), i1 = min(i0 + per, p.batch);
-  const bool report = !MERGE && blockIdx.x == 0;
+  long long span = 0, pairs = 0, chunks = 0;   // chunks: the line's part in sequences of several query tiles
   PagedSeq s;
-  s.tiles = s.nv = 0;
-  long long work = 0;
+  s.tiles = s.keys = s.n_q = s.n_k = s.row0 = 0;
   for (int i = i0; i < i1; ++i) {
     s = paged_seq(p, i, report);
-    work += (long long)s.tiles * s.nv;
+    const long long x = s.span(p);
+    span += x;
+    pairs += (long long)s.tiles * p.heads_kv;
+    if (s.tiles > 1) chunks += x;
   }
-  if (tid == 0) sh->found = 0;
-  work = block_sum<THREADS>(work, sh->warp_a) * p.heads_kv;
-  const long long want = (work + p.target_units - 1) / p.target_units;
-  const int chunk = (int)(want > p.min_chunk ? (want < INT_MAX ? want : INT_MAX) : p.min_chunk);
-  // units (or split pairs) and slots before this thread's sequences
-  long long n = 0, slots = 0;
-  for (int i = i0; i < i1; ++i) {
-    if (per > 1) s = paged_seq(p, i, false);
-    const long long pairs = (long long)s.tiles * p.heads_kv;
-    const int splits = tile_splits(s.nv, chunk);
-    n += MERGE ? (splits > 1 ? pairs : 0) : pairs * splits;
-    if (splits > 1) slots += pairs * splits;
-  }
-  long long in = n, is = slots;
+  long long a = span, b = pairs, c = chunks;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long a = __shfl_up_sync(0xffffffffu, in, o), b = __shfl_up_sync(0xffffffffu, is, o);
+    const long long va = __shfl_up_sync(0xffffffffu, a, o), vb = __shfl_up_sync(0xffffffffu, b, o),
+                    vc = __shfl_up_sync(0xffffffffu, c, o);
     if (lane >= o) {
-      in += a;
-      is += b;
+      a += va;
+      b += vb;
+      c += vc;
     }
   }
-  __syncthreads();   // block_sum's reads of warp_a
   if (lane == 31) {
-    sh->warp_a[w] = in;
-    sh->warp_b[w] = is;
+    sh->warp_sum[0][w] = a;
+    sh->warp_sum[1][w] = b;
+    sh->warp_sum[2][w] = c;
   }
+  if (tid == 0) sh->place.seq = -1;
   __syncthreads();
-  long long at = in - n, slot = is - slots;
-  for (int j = 0; j < w; ++j) {
-    at += sh->warp_a[j];
-    slot += sh->warp_b[j];
+  a -= span;
+  b -= pairs;
+  long long total = 0, all_pairs = 0, all_chunks = 0;
+#pragma unroll
+  for (int j = 0; j < NW; ++j) {
+    if (j == w) {
+      a += total;
+      b += all_pairs;
+    }
+    total += sh->warp_sum[0][j];
+    all_pairs += sh->warp_sum[1][j];
+    all_chunks += sh->warp_sum[2][j];
   }
-  if (index >= at && index < at + n) {
+  long long share = (total + p.ctas - 1) / p.ctas;
+  if (share < p.min_share) share = p.min_share;
+  const bool whole = p.pair_ctas > 0 && all_pairs >= 4ll * p.ctas && 2 * all_chunks > total;
+  const long long pos = whole ? piece : piece * share;
+  const long long mine = whole ? b : a, size = whole ? pairs : span;
+  if (pos >= mine && pos < mine + size) {
+    long long x = a, n = b;
     for (int i = i0; i < i1; ++i) {
       if (per > 1) s = paged_seq(p, i, false);
-      const long long pairs = (long long)s.tiles * p.heads_kv;
-      const int splits = tile_splits(s.nv, chunk);
-      const long long mine = MERGE ? (splits > 1 ? pairs : 0) : pairs * splits;
-      if (index < at + mine) {
-        const int r = (int)(index - at);
-        PagedUnit u;
-        u.seq = i;
-        u.row0 = s.row0;
-        u.n_q = s.n_q;
-        u.n_k = s.n_k;
-        u.h = r % p.heads_kv;
-        const int rest = r / p.heads_kv;
-        u.split = MERGE ? 0 : rest % splits;
-        u.tile = s.tiles - 1 - (MERGE ? rest : rest / splits);
-        u.splits = splits;
-        u.chunk = chunk;
-        u.slot0 = (int)slot;
-        // more slots than the workspace: only offsets that overlap lead here
-        if (splits > 1 && slot + pairs * splits > p.max_slots) {
-          if (!MERGE) atomicOr(p.status, kStatusBadSeqlens);
-        } else {
-          sh->unit = u;
-          sh->found = 1;
-        }
+      const long long sx = s.span(p), sn = (long long)s.tiles * p.heads_kv;
+      if (whole ? pos < n + sn : pos < x + sx) {
+        sh->place.at = x;
+        sh->place.seq = i;
+        sh->place.rank = whole ? (int)(pos - n) : 0;
         break;
       }
-      at += mine;
-      if (splits > 1) slot += pairs * splits;
+      x += sx;
+      n += sn;
     }
   }
   __syncthreads();
-  out = sh->unit;
-  return sh->found != 0;
+  PagedPlace r = sh->place;
+  r.share = whole ? 0 : share;
+  r.total = total;
+  return r;
 }
 
-// A unit's place in its tile, beside DbufCtx (whose q0 / kv0 are not used).
-struct PagedTile {
-  int seq, h, row0;
-  int q0;            // first token of the tile
-  int rows;          // live rows: group x tokens
-  int j0;            // first visited index of the unit
-  TileWalk walk;
-  int slot;          // partial slot, or -1: write O and L
+// The pair of sequence s that holds offset y of the sequence's span: query
+// tile, head, and the pair's start within the span.
+__device__ __forceinline__ long long pair_at(const PagedParams& p, const PagedSeq& s, long long y, int& tile, int& h) {
+  int lo = 0, hi = s.tiles;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (s.before(p, mid) * p.heads_kv <= y)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  tile = lo;
+  const long long base = s.before(p, lo) * p.heads_kv;
+  const int w = s.width(p, lo);
+  h = (int)((y - base) / w);
+  return base + (long long)h * w;
+}
+
+// First visited key tile at or after offset y of a pair's span, of n.
+__device__ __forceinline__ int span_tile(const PagedParams& p, long long y, int n) {
+  const long long k = y - p.overhead;
+  const long long j = k <= 0 ? 0 : (k + kPagedKeyTile - 1) / kPagedKeyTile;
+  return (int)(j < n ? j : n);
+}
+
+// Walks the fragments of one CTA's piece; every lane of the TMA warp in step.
+struct FragWalk {
+  PagedSeq s;
+  long long x, end;   // the pair's start on the line, the piece's end
+  long long share;
+  int cta, seq, tile, h;
+  bool more;
+
+  __device__ __forceinline__ void start(const PagedParams& p, const PagedPlace& pl, int piece) {
+    cta = piece;
+    share = pl.share;
+    seq = pl.seq;
+    s = paged_seq(p, seq, false);
+    more = true;
+    if (share == 0) {   // one pair: the query tiles from the last (the most keys) to the first
+      h = pl.rank % p.heads_kv;
+      tile = s.tiles - 1 - pl.rank / p.heads_kv;
+      x = 0;
+      end = s.width(p, tile);
+    } else {
+      const long long pos = piece * share;
+      end = min(pos + share, pl.total);
+      x = pl.at + pair_at(p, s, pos - pl.at, tile, h);
+    }
+  }
+
+  // The next fragment and its block-table row; false when the piece is done.
+  template <bool BAND>
+  __device__ __forceinline__ bool next(const PagedParams& p, PagedFrag& f, const int*& table) {
+    while (more) {
+      const int w = s.width(p, tile);
+      const long long begin = share == 0 ? 0 : cta * share;
+      const long long y0 = begin > x ? begin - x : 0, y1 = min(end - x, (long long)w);
+      const bool whole = y0 == 0 && y1 == w;
+      const int q0 = tile * p.tile_tokens, last = min(q0 + p.tile_tokens, s.n_q) - 1;
+      f.km = paged_mask(p, s.n_q, s.n_k);
+      const TileWalk walk = tile_walk(f.km, q0, last);
+      f.j0 = span_tile(p, y0, walk.n);
+      f.n = (whole ? walk.n : span_tile(p, y1, walk.n)) - f.j0;
+      f.row = s.row0 + q0;
+      f.q0 = q0;
+      f.rows = (last + 1 - q0) * p.group;
+      f.h = h;
+      f.slot = whole ? -1 : 2 * cta + (y0 == 0 ? 1 : 0);
+      f.few_keys = s.n_k <= 2 * kPagedKeyTile;
+      f.npre = walk.npre;
+      f.skip = walk.skip;
+      f.lo = walk.lo;
+      f.end = walk.end;
+      f.tm = tile_mask<BAND>(f.km, q0, last, kPagedKeyTile);
+      if (walk.npre == 0) f.tm.pre -= walk.skip;
+      f.tm.lo -= walk.skip;
+      f.tm.hi -= walk.skip;
+      f.tm = f.tm.from(f.j0);
+      table = p.table + (long long)seq * p.table_stride;
+      // on to the next pair
+      x += w;
+      if (share == 0 || x >= end) {
+        more = false;
+      } else if (++h == p.heads_kv) {
+        h = 0;
+        if (++tile == s.tiles) {
+          tile = 0;
+          do {
+            if (++seq >= p.batch) {
+              more = false;
+              break;
+            }
+            s = paged_seq(p, seq, false);
+          } while (s.tiles == 0);
+        }
+      }
+      if (f.n > 0 || whole) return true;   // else: nothing of this pair falls here (its merge sees the same)
+    }
+    return false;
+  }
 };
 
-// The TMA warp.  Lane l holds box l of a key tile: rows of page l % sub of the
-// tile's `sub` pages, columns 64 (l / sub) ..
-template <class C>
-__device__ __forceinline__ void pg_producer(const DbufCtx& t, const PagedTile& u, const PagedParams& p,
-                                            const CUtensorMap* tm_q, const CUtensorMap* tm_k,
-                                            const CUtensorMap* tm_v, int lane) {
+// ---------------------------------------------------------------- the warps' roles
+
+struct PagedCtx {
+  uint32_t bar0, sQ, sK, sV, tmem;
+  volatile int* abort_flag;
+  uint32_t* status;
+  PagedFrag* frags;   // two, by fragment parity
+  __device__ __forceinline__ uint32_t bar(int i) const { return bar0 + 8u * (uint32_t)i; }
+  // One warp waits through lane 0 (the others only need its answer).
+  __device__ __forceinline__ bool warp_wait(int i, int phase, uint32_t site, int lane) const {
+    bool ok = true;
+    if (lane == 0) ok = wait_or_abort(bar(i), (uint32_t)phase & 1, abort_flag, status, site);
+    return __all_sync(0xffffffffu, ok);
+  }
+};
+
+// 5-D tiled load (see tma_load_4d).
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, int c3, int c4,
+                                            uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(bar)
+      : "memory");
+}
+
+// One lane's box of one tensor: coordinates 1, 3 and 4, or none (c4 = -1).
+struct BoxAt {
+  int c1, c3, c4;
+};
+
+// The TMA warp.  Lane l holds box l of a key tile (rows l * box_rows ..).
+template <class C, bool BAND>
+__device__ __forceinline__ void pg_producer(const PagedCtx& t, const PagedParams& p, const CUtensorMap* tm_q,
+                                            const CUtensorMap* tm_k, const CUtensorMap* tm_v, const PagedPlace& place,
+                                            int piece, int lane) {
   const int ps = p.page_size;
-  const int box_rows = min(ps, C::BC);
-  const int sub = C::BC / box_rows;                 // pages per key tile, or 1
-  const int tpp = ps > C::BC ? ps / C::BC : 1;      // key tiles per page, or 1
-  const int my_sub = lane % sub, my_kb = lane / sub;
-  const bool has_box = my_kb < C::D / 64;
-  const int* row = p.table + (long long)u.seq * p.table_stride;
+  const int box_rows = p.box_rows;
+  const int boxes = C::BC / box_rows;
+  FragWalk walk;
+  walk.start(p, place, piece);
+  PagedFrag f;
+  const int* table = nullptr;
   bool bad = false;
-  // Page of this lane's box of visited tile j: -1 when no row of the query
-  // tile sees a key of it; an out-of-range page is reported and read as zeros
-  // (num_pages lies outside the map).
-  auto fetch = [&](int j) -> int {
-    if (j >= t.nkv || !has_box) return -1;
-    const int kt = u.walk.tile(u.j0 + j);
-    const int k0 = kt * C::BC + my_sub * box_rows, k1 = k0 + box_rows;   // the box's keys
-    if (!(k0 < t.km.pre_end || (k0 < u.walk.end && k1 > u.walk.lo))) return -1;
-    const int page = __ldg(row + (sub > 1 ? kt * sub + my_sub : kt / tpp));
+  // The page of this lane's box of the fragment's tile j (-1: no row of the
+  // query tile sees a key of it; num_pages: out of range, to be read as
+  // zeros), and the box's first row within the page.
+  auto fetch = [&](int j, int& row) -> int {
+    if (j >= f.n || lane >= boxes) return -1;
+    const int k0 = f.tile(f.j0 + j) * C::BC + lane * box_rows, k1 = k0 + box_rows;   // the box's keys
+    if (!(k0 < f.km.pre_end || (k0 < f.end && k1 > f.lo))) return -1;
+    const int at = k0 / ps;
+    row = k0 - at * ps;
+    const int page = __ldg(table + at);
     if (page < 0 || page >= p.num_pages) {
       bad = true;
       return p.num_pages;
     }
     return page;
   };
-  auto load = [&](uint32_t s_tile, uint32_t bar, const CUtensorMap* tm, int page, int j) {
-    const unsigned boxes = __popc(__ballot_sync(0xffffffffu, page >= 0));
-    if (lane == 0) mbar_arrive_expect_tx(bar, boxes * (uint32_t)box_rows * 128u);
+  auto load = [&](uint32_t s_tile, uint32_t bar, const CUtensorMap* tm, const PagedSide& side, int page, int row) {
+    const unsigned n = __popc(__ballot_sync(0xffffffffu, page >= 0));
+    if (lane == 0) mbar_arrive_expect_tx(bar, n * (uint32_t)box_rows * (uint32_t)(C::D * 2));
     __syncwarp();
     if (page >= 0) {
-      const int kt = u.walk.tile(u.j0 + j);
-      tma_load_4d(s_tile + (uint32_t)my_kb * (C::BC * 128) + (uint32_t)(my_sub * box_rows) * 128u, tm, my_kb * 64,
-                  tpp > 1 ? (kt % tpp) * C::BC : 0, u.h, page, bar);
+      const uint32_t dst = s_tile + (uint32_t)(lane * box_rows) * (uint32_t)(C::D * 2);
+      // merged (page, head) coordinate, or (head, page) apart; num_pages lies outside either map
+      if (side.ratio > 0)
+        tma_load_5d(dst, tm, 0, 0, 0, row >> 3, page < p.num_pages ? page * side.ratio + f.h : side.extent, bar);
+      else
+        tma_load_5d(dst, tm, 0, row, 0, f.h, page, bar);
     }
     __syncwarp();
   };
-  int pg0 = fetch(0), pg1 = fetch(1), pg2 = fetch(2), pg3 = fetch(3);
-  if (lane == 0) {
-    mbar_arrive_expect_tx(t.bar(DB_Q), (uint32_t)(C::D / 64) * (uint32_t)p.slot_rows * 128u);
-    for (int kb = 0; kb < C::D / 64; ++kb)
-      tma_load_4d(t.sQ + kb * (C::BR * 128), tm_q, kb * 64, 0, u.h, u.row0 + u.q0, t.bar(DB_Q));
+  bool ok = true;
+  int g = 0;     // key tiles loaded (K)
+  int gv = 0;    // (V)
+  int nf = 0;    // fragments published
+  bool have = walk.next<BAND>(p, f, table);
+  int r0 = 0, r1 = 0, r2 = 0;
+  int p0 = -1, p1 = -1, p2 = -1;
+  if (have) {
+    p0 = fetch(0, r0);
+    p1 = fetch(1, r1);
+    p2 = fetch(2, r2);
   }
-  __syncwarp();
-  // K_j is needed two products before V_j, and a K stage frees at S(j), before
-  // PV(j) frees V's: K_0 V_0 K_1 V_1 K_2 (K_3 V_2) (K_4 V_3) ..
-  load(t.sK, t.bar(DB_KFULL), tm_k, pg0, 0);
-  load(t.sV, t.bar(DB_VFULL), tm_v, pg0, 0);
-  int jk = 1, jv = 1;
-  if (t.nkv > 1) {
-    load(t.sK + C::KV_BYTES, t.bar(DB_KFULL + 1), tm_k, pg1, 1);
-    load(t.sV + C::KV_BYTES, t.bar(DB_VFULL + 1), tm_v, pg1, 1);
-    jk = jv = 2;
-  }
-  int prev = pg1;   // pages of tile j - 1
-  pg0 = pg2;
-  pg1 = pg3;
-  pg2 = fetch(4);
-  auto wait = [&](int bar, int phase) -> bool {
-    bool ok = true;
-    if (lane == 0)
-      ok = wait_or_abort(t.bar(bar), (uint32_t)phase & 1, t.abort_flag, t.status, kSiteProducerEmpty);
-    return __all_sync(0xffffffffu, ok);
+  // The fragment's description (and Q) to the other warps, once its slot's and
+  // Q's last users are done.
+  auto publish = [&](int n) -> bool {
+    if (nf >= 1 && !t.warp_wait(PG_QEMPTY, nf - 1, kSiteProducerEmpty, lane)) return false;
+    if (nf >= 2 && !t.warp_wait(PG_ODONE + (nf & 1), (nf - 2) >> 1, kSiteProducerEmpty, lane)) return false;
+    if (lane == 0) {
+      const uint32_t bar = t.bar(PG_Q + (nf & 1));
+      PagedFrag* dst = t.frags + (nf & 1);
+      *dst = f;
+      dst->n = n;
+      if (n > 0) {
+        mbar_arrive_expect_tx(bar, (uint32_t)C::BLOCKS * (uint32_t)p.slot_rows * 128u);
+        for (int kb = 0; kb < C::BLOCKS; ++kb)
+          tma_load_4d(t.sQ + kb * (C::BR * 128), tm_q, kb * 64, 0, f.h, f.row, bar);
+      } else {
+        mbar_arrive(bar);
+      }
+    }
+    ++nf;
+    __syncwarp();
+    return true;
   };
-  for (int j = 2; j <= t.nkv; ++j) {   // pg0: pages of tile j
-    const int ahead = fetch(j + 3);
-    if (j < t.nkv) {
-      const int s = j % C::KSTAGES, n = j / C::KSTAGES;
-      if (!wait(DB_KEMPTY + s, n - 1)) break;
-      load(t.sK + s * C::KV_BYTES, t.bar(DB_KFULL + s), tm_k, pg0, j);
-      jk = j + 1;
+  while (ok && have) {
+    if (f.n == 0) {
+      ok = publish(0);
+    } else {
+      int pv = -1, rv = 0;   // tile j - 1's pages
+      for (int j = 0; j < f.n; ++j) {
+        int r3 = 0;
+        const int p3 = fetch(j + 3, r3);
+        const int s = g % C::KSTAGES;
+        if (g >= C::KSTAGES && !t.warp_wait(PG_KEMPTY + s, g / C::KSTAGES - 1, kSiteProducerEmpty, lane)) {
+          ok = false;
+          break;
+        }
+        load(t.sK + s * C::KV_BYTES, t.bar(PG_KFULL + s), tm_k, p.k_side, p0, r0);
+        ++g;
+        if (j == 0) {
+          if (!(ok = publish(f.n))) break;
+        } else {
+          const int sv = gv % C::VSTAGES;
+          if (gv >= C::VSTAGES && !t.warp_wait(PG_VEMPTY + sv, gv / C::VSTAGES - 1, kSiteProducerEmpty, lane)) {
+            ok = false;
+            break;
+          }
+          load(t.sV + sv * C::KV_BYTES, t.bar(PG_VFULL + sv), tm_v, p.v_side, pv, rv);
+          ++gv;
+        }
+        pv = p0;
+        rv = r0;
+        p0 = p1;
+        r0 = r1;
+        p1 = p2;
+        r1 = r2;
+        p2 = p3;
+        r2 = r3;
+      }
+      if (!ok) break;
+      // the last V tile, behind the next fragment's table reads
+      const int h = f.h;
+      have = walk.next<BAND>(p, f, table);
+      if (have) {
+        p0 = fetch(0, r0);
+        p1 = fetch(1, r1);
+        p2 = fetch(2, r2);
+      }
+      const int sv = gv % C::VSTAGES;
+      if (gv >= C::VSTAGES && !t.warp_wait(PG_VEMPTY + sv, gv / C::VSTAGES - 1, kSiteProducerEmpty, lane)) {
+        ok = false;
+        break;
+      }
+      const int next_h = f.h;
+      f.h = h;
+      load(t.sV + sv * C::KV_BYTES, t.bar(PG_VFULL + sv), tm_v, p.v_side, pv, rv);
+      f.h = next_h;
+      ++gv;
+      continue;
     }
-    if (j > 2) {
-      const int jj = j - 1, s = jj % C::VSTAGES, n = jj / C::VSTAGES;
-      if (!wait(DB_VEMPTY + s, n - 1)) break;
-      load(t.sV + s * C::KV_BYTES, t.bar(DB_VFULL + s), tm_v, prev, jj);
-      jv = jj + 1;
+    have = walk.next<BAND>(p, f, table);
+    if (have) {
+      p0 = fetch(0, r0);
+      p1 = fetch(1, r1);
+      p2 = fetch(2, r2);
     }
-    prev = pg0;
-    pg0 = pg1;
-    pg1 = pg2;
-    pg2 = ahead;
   }
+  if (ok) publish(-1);
   if (bad) atomicOr(p.status, kStatusBadPages);
   // own copies in flight land before the CTA may exit
   if (lane == 0) {
-    wait_drain(t.bar(DB_Q), 0, t.status);
+    for (int i = 0; i < 2; ++i)
+      if (nf > i) wait_drain(t.bar(PG_Q + i), (uint32_t)((nf - 1 - i) / 2) & 1, t.status);
     for (int s = 0; s < C::KSTAGES; ++s)
-      if (jk > s) wait_drain(t.bar(DB_KFULL + s), (uint32_t)((jk - 1 - s) / C::KSTAGES) & 1, t.status);
+      if (g > s) wait_drain(t.bar(PG_KFULL + s), (uint32_t)((g - 1 - s) / C::KSTAGES) & 1, t.status);
     for (int s = 0; s < C::VSTAGES; ++s)
-      if (jv > s) wait_drain(t.bar(DB_VFULL + s), (uint32_t)((jv - 1 - s) / C::VSTAGES) & 1, t.status);
+      if (gv > s) wait_drain(t.bar(PG_VFULL + s), (uint32_t)((gv - 1 - s) / C::VSTAGES) & 1, t.status);
   }
 }
 
-// Zeroes the rows of V tile `kt` (shared memory, 64 rows x D, 64-column blocks)
-// whose keys no row of the query tile sees; 128 threads, thread `tid`.
+// The MMA thread: per fragment S(0), S(1), then O~ += P(j) V_j and S(j+2) for
+// each key tile, as db_mma.  O~ of the fragment before must have been read
+// (PG_ODONE) before the first PV product; the S products run ahead of that.
+template <class C, bool BF16>
+__device__ __forceinline__ void pg_mma(const PagedCtx& t, const PagedParams& p) {
+  const uint32_t idesc_qk = make_idesc_f16(C::BR, C::BC, BF16, false, false) | p.qk_negate;
+  constexpr uint32_t idesc_pv = make_idesc_f16(C::BR, C::D, BF16, false, true);
+  const uint64_t dq0 = make_sdesc_sw128(t.sQ, 16, 1024);
+  const uint64_t dk0 = make_sdesc_sw128(t.sK, 16, C::GROUP_BYTES);
+  const uint64_t dv0 = make_sdesc_sw128(t.sV, 1024, C::GROUP_BYTES);
+  auto wait = [&](int bar, int phase, uint32_t site) -> bool {
+    return wait_or_abort(t.bar(bar), (uint32_t)phase & 1, t.abort_flag, t.status, site);
+  };
+  auto issue_s = [&](int g, bool last) -> bool {
+    const int sk = g % C::KSTAGES;
+    if (!wait(PG_KFULL + sk, g / C::KSTAGES, kSiteMmaK)) return false;
+    tc_fence_after();
+    const uint64_t b0 = dk0 + (uint64_t)((sk * C::KV_BYTES) >> 4);
+    const uint32_t tS = t.tmem + C::TMEM_S + 64 * (g & 1);
+#pragma unroll
+    for (int k = 0; k < C::D / 16; ++k)
+      umma_ss(tS, dq0 + (uint64_t)(((k >> 2) * (C::BR * 128) + (k & 3) * 32) >> 4),
+              b0 + (uint64_t)(((k >> 2) * 1024 + (k & 3) * 32) >> 4), idesc_qk, k > 0 ? 1u : 0u);
+    umma_commit(t.bar(PG_S + (g & 1)));
+    umma_commit(t.bar(PG_KEMPTY + sk));
+    if (last) umma_commit(t.bar(PG_QEMPTY));
+    return true;
+  };
+  bool ok = true;
+  int g = 0;
+  for (int nf = 0; ok; ++nf) {
+    if (!wait(PG_Q + (nf & 1), nf >> 1, kSiteMmaQ)) break;
+    const PagedFrag* f = t.frags + (nf & 1);
+    const int n = f->n;
+    if (n < 0) break;
+    if (n == 0) {
+      mbar_arrive(t.bar(PG_QEMPTY));
+      continue;
+    }
+    const TileMask tm = f->tm;
+    const bool few_keys = f->few_keys != 0;
+    tc_fence_after();
+    ok = issue_s(g, n == 1);
+    if (ok && n > 1) ok = issue_s(g + 1, n == 2);
+    for (int j = 0; j < n && ok; ++j, ++g) {
+      const int sv = g % C::VSTAGES;
+      if (j == 0 && nf > 0) ok = wait(PG_ODONE + ((nf - 1) & 1), (nf - 1) >> 1, kSiteMmaO);
+      ok = ok && wait(PG_P + (g & 1), g >> 1, kSiteMmaP) && wait(PG_VFULL + sv, g / C::VSTAGES, kSiteMmaV);
+      if (!ok) break;
+      tc_fence_after();
+      const uint64_t b0 = dv0 + (uint64_t)((sv * C::KV_BYTES) >> 4);
+      const uint32_t tS = t.tmem + C::TMEM_S + 64 * (g & 1);
+      const uint32_t tO = t.tmem + C::TMEM_O;
+      if (split_tile<BF16>(!tm.full(j), few_keys)) {
+#pragma unroll
+        for (int k = 0; k < C::BC / 16; ++k) {
+          const uint64_t b = b0 + (uint64_t)((k * 2 * C::GROUP_BYTES) >> 4);
+          umma_ts(tO, tS + k * 8, b, idesc_pv, (j > 0 || k > 0) ? 1u : 0u);
+          umma_ts(tO, tS + C::BC / 2 + k * 8, b, idesc_pv, 1u);
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < C::BC / 16; ++k)
+          umma_ts(tO, tS + k * 8, b0 + (uint64_t)((k * 2 * C::GROUP_BYTES) >> 4), idesc_pv,
+                  (j > 0 || k > 0) ? 1u : 0u);
+      }
+      umma_commit(t.bar(PG_O));
+      umma_commit(t.bar(PG_VEMPTY + sv));
+      if (j + 1 == n) umma_commit(t.bar(PG_OLAST));
+      if (j + 2 < n) ok = issue_s(g + 2, j + 3 == n);
+    }
+  }
+  umma_commit(t.bar(PG_EXIT));
+  wait_drain(t.bar(PG_EXIT), 0, t.status);
+}
+
+// Zeroes the rows of V tile `kt` (shared memory) whose keys no row of the
+// query tile sees; 128 threads, thread `tid`.
 template <class C>
-__device__ __forceinline__ void zero_hidden_rows(uint32_t sV, int kt, const TileWalk& w, int pre_end, int tid) {
+__device__ __forceinline__ void zero_hidden_rows(uint32_t sV, int kt, const PagedFrag* f, int tid) {
+  const int lo = f->lo, end = f->end, pre = f->km.pre_end;
   for (int c = tid; c < C::BC * (C::D / 8); c += 128) {
-    const int r = (c / 8) % C::BC, kb = c / (8 * C::BC);   // 16-byte chunk c % 8 of row r, column block kb
-    const int key = kt * C::BC + r;
-    if (key < pre_end || (key >= w.lo && key < w.end)) continue;
-    asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(sV + (uint32_t)kb * (C::BC * 128) +
-                                                                   (uint32_t)r * 128u + (uint32_t)(c % 8) * 16u),
-                 "r"(0u)
-                 : "memory");
+    // 16-byte chunk c % 8 of row (c / 8) % 8, column block, 8-row group
+    const int key = kt * C::BC + c / (64 * C::BLOCKS) * 8 + (c / 8) % 8;
+    if (key < pre || (key >= lo && key < end)) continue;
+    asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(sV + (uint32_t)c * 16u), "r"(0u) : "memory");
   }
 }
 
@@ -381,189 +685,148 @@ __device__ __forceinline__ uint8_t* paged_o_row(const PagedParams& p, int row, i
 }
 
 template <class C, bool BF16, bool BAND>
-__device__ __forceinline__ void pg_softmax(const DbufCtx& t, const PagedTile& u, const PagedParams& p, int warp,
-                                           int lane) {
+__device__ __forceinline__ void pg_softmax(const PagedCtx& t, const PagedParams& p, int warp, int lane) {
   const int quad = warp & 3;
   const int r = quad * 32 + lane;
-  const bool live = r < u.rows;
-  const bool warp_live = quad * 32 < u.rows;
   const int tok = r / p.group;
-  const int row = u.q0 + tok;                        // token of the sequence
-  const int head = u.h * p.group + (r - tok * p.group);
   const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
   const uint32_t tO = t.tmem + lane_off + C::TMEM_O;
   const float sl2 = p.scale_log2_mag;
-  const TileMask tmask = t.tm;
-  const bool few_keys = t.few_keys;
-  float m_run = -INFINITY;
-  float l_run = 0.f;
-  bool ok = true;
-  if constexpr (C::Q_IN_TMEM) {
-    // row r of Q_i into TMEM lane r, as in fa2_fwd_dbuf.cuh; rows past the
-    // loaded box hold whatever was there, and reach only their own lanes
-    ok = wait_or_abort(t.bar(DB_Q), 0, t.abort_flag, t.status, kSiteMmaQ);
-    ok = __all_sync(0xffffffffu, ok);
-    if (ok) {
+  auto wait = [&](int bar, int phase, uint32_t site) -> bool {
+    const bool ok = wait_or_abort(t.bar(bar), (uint32_t)phase & 1, t.abort_flag, t.status, site);
+    return __all_sync(0xffffffffu, ok);
+  };
+  int g = 0, products = 0;   // key tiles; fragments that had some
+  for (int nf = 0;; ++nf) {
+    if (!wait(PG_Q + (nf & 1), nf >> 1, kSiteMmaQ)) return;
+    const PagedFrag* f = t.frags + (nf & 1);
+    const int n = f->n;
+    if (n < 0) return;
+    const int rows = f->rows;
+    const bool live = r < rows;
+    const bool warp_live = quad * 32 < rows;
+    const int head = f->h * p.group + (r - tok * p.group);
+    const TileMask tmask = f->tm;
+    const bool few_keys = f->few_keys != 0;
+    float m_run = -INFINITY;
+    float l_run = 0.f;
+    for (int j = 0; j < n; ++j, ++g) {
+      const uint32_t tS = t.tmem + lane_off + C::TMEM_S + 64 * (g & 1);
+      if (!wait(PG_S + (g & 1), g >> 1, kSiteSoftmaxS)) return;
+      tc_fence_after();
+      const bool masked = !tmask.full(j);
       if (warp_live) {
-#pragma unroll 1
-        for (int kb = 0; kb < C::D / 64; ++kb) {
-          const uint32_t src = t.sQ + kb * (C::BR * 128) + r * 128;
-          uint32_t w[32];
+        uint32_t sr[C::BC];
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            const uint4 x = lds128(src + ((c ^ (r & 7)) << 4));
-            w[4 * c] = x.x;
-            w[4 * c + 1] = x.y;
-            w[4 * c + 2] = x.z;
-            w[4 * c + 3] = x.w;
+        for (int c = 0; c < C::BC; c += 32) tmem_ld_32x32b_x32(tS + c, sr + c);
+#pragma unroll
+        for (int c = 0; c < C::BC; c += 32) tmem_ld_wait_x32(sr + c);
+        if (masked) mask_scores<C::BC, BAND>(sr, f->km, f->q0 + tok, f->tile(f->j0 + j) * C::BC);
+        float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < C::BC; c += 8) {
+          mx0 = fmax3(mx0, __uint_as_float(sr[c + 0]), __uint_as_float(sr[c + 1]));
+          mx1 = fmax3(mx1, __uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3]));
+          mx2 = fmax3(mx2, __uint_as_float(sr[c + 4]), __uint_as_float(sr[c + 5]));
+          mx3 = fmax3(mx3, __uint_as_float(sr[c + 6]), __uint_as_float(sr[c + 7]));
+        }
+        const float m_tile = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * sl2;
+        const bool raise = live && m_tile > m_run + kRescaleLog2;
+        const float m_new = raise ? m_tile : m_run;
+        const float m_use = (m_new == -INFINITY) ? 0.f : m_new;
+        const float alpha = raise ? ex2_approx(m_run - m_use) : 1.f;
+        const float2 scale2 = make_float2(sl2, sl2);
+        const float2 neg_m2 = make_float2(-m_use, -m_use);
+        float2 sum0 = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
+        if (split_tile<BF16>(masked, few_keys)) {
+#pragma unroll
+          for (int ch = 0; ch < C::BC / 32; ++ch)
+            softmax_p_chunk<C, BF16, true>(sr, ch, tS, scale2, neg_m2, sum0, sum1);
+        } else {
+#pragma unroll
+          for (int ch = 0; ch < C::BC / 32; ++ch)
+            softmax_p_chunk<C, BF16, false>(sr, ch, tS, scale2, neg_m2, sum0, sum1);
+        }
+        const float2 sum2 = __fadd2_rn(sum0, sum1);
+        l_run = l_run * alpha + (sum2.x + sum2.y);
+        if (j > 0 && __any_sync(0xffffffffu, raise)) {
+          // S(g) was issued before PV(g-1): wait for that product before rescaling
+          if (!wait(PG_O, g - 1, kSiteSoftmaxO)) return;
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < C::D; c += 32) {
+            uint32_t o[32];
+            tmem_ld_32x32b_x32(tO + c, o);
+            tmem_ld_wait_x32(o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+            tmem_st_32x32b_x32(tO + c, o);
           }
-          tmem_st_32x32b_x32(t.tmem + lane_off + C::TMEM_Q + kb * 32, w);
         }
         tmem_st_wait();
+        m_run = m_new;
+      }
+      if (masked) {
+        const int kt = f->tile(f->j0 + j);
+        if (!((kt + 1) * C::BC <= f->km.pre_end || (kt * C::BC >= f->lo && (kt + 1) * C::BC <= f->end))) {
+          // some key of the tile is hidden from every row: its V row may be anything
+          const int sv = g % C::VSTAGES;
+          if (!wait(PG_VFULL + sv, g / C::VSTAGES, kSiteMmaV)) return;
+          zero_hidden_rows<C>(t.sV + sv * C::KV_BYTES, kt, f, r);
+          fence_proxy_async_smem();
+        }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(t.bar(DB_QT));
+      if (lane == 0) mbar_arrive(t.bar(PG_P + (g & 1)));
     }
-  }
-  for (int j = 0; ok && j < t.nkv; ++j) {
-    const uint32_t tS = t.tmem + lane_off + C::TMEM_S + 64 * (j & 1);
-    ok = wait_or_abort(t.bar(DB_S + (j & 1)), (uint32_t)(j >> 1) & 1, t.abort_flag, t.status, kSiteSoftmaxS);
-    ok = __all_sync(0xffffffffu, ok);
-    if (!ok) break;
-    tc_fence_after();
-    const bool masked = !tmask.full(j);
-    const int kt = u.walk.tile(u.j0 + j);
-    if (warp_live) {
-      uint32_t sr[C::BC];
-#pragma unroll
-      for (int c = 0; c < C::BC; c += 32) tmem_ld_32x32b_x32(tS + c, sr + c);
-#pragma unroll
-      for (int c = 0; c < C::BC; c += 32) tmem_ld_wait_x32(sr + c);
-      if (masked) mask_scores<C::BC, BAND>(sr, t.km, row, kt * C::BC);
-      float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
-#pragma unroll
-      for (int c = 0; c < C::BC; c += 8) {
-        mx0 = fmax3(mx0, __uint_as_float(sr[c + 0]), __uint_as_float(sr[c + 1]));
-        mx1 = fmax3(mx1, __uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3]));
-        mx2 = fmax3(mx2, __uint_as_float(sr[c + 4]), __uint_as_float(sr[c + 5]));
-        mx3 = fmax3(mx3, __uint_as_float(sr[c + 6]), __uint_as_float(sr[c + 7]));
-      }
-      const float m_tile = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * sl2;
-      const bool raise = live && m_tile > m_run + kRescaleLog2;
-      const float m_new = raise ? m_tile : m_run;
-      const float m_use = (m_new == -INFINITY) ? 0.f : m_new;
-      const float alpha = raise ? ex2_approx(m_run - m_use) : 1.f;
-      const float2 scale2 = make_float2(sl2, sl2);
-      const float2 neg_m2 = make_float2(-m_use, -m_use);
-      float2 sum0 = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
-      if (split_tile<BF16>(masked, few_keys)) {
-#pragma unroll
-        for (int ch = 0; ch < C::BC / 32; ++ch)
-          softmax_p_chunk<C, BF16, true>(sr, ch, tS, scale2, neg_m2, sum0, sum1);
-      } else {
-#pragma unroll
-        for (int ch = 0; ch < C::BC / 32; ++ch)
-          softmax_p_chunk<C, BF16, false>(sr, ch, tS, scale2, neg_m2, sum0, sum1);
-      }
-      const float2 sum2 = __fadd2_rn(sum0, sum1);
-      l_run = l_run * alpha + (sum2.x + sum2.y);
-      if (j > 0 && __any_sync(0xffffffffu, raise)) {
-        // S(j) was issued before PV(j-1): wait for that product before rescaling
-        bool ok2 = wait_or_abort(t.bar(DB_O), (uint32_t)(j - 1) & 1, t.abort_flag, t.status, kSiteSoftmaxO);
-        ok2 = __all_sync(0xffffffffu, ok2);
-        if (!ok2) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
+    if (n > 0) {
+      if (!wait(PG_OLAST, products++, kSiteEpilogueO)) return;
+      tc_fence_after();
+    }
+    const int slot_at = f->slot;
+    const int row = f->row + tok;
+    if (warp_live && slot_at >= 0) {
+      const size_t slot = (size_t)slot_at * (size_t)p.slot_rows + (size_t)r;
+      float4* dst = reinterpret_cast<float4*>(p.ws_o + slot * C::D);
 #pragma unroll 1
-        for (int c = 0; c < C::D; c += 32) {
-          uint32_t o[32];
-          tmem_ld_32x32b_x32(tO + c, o);
-          tmem_ld_wait_x32(o);
+      for (int c = 0; c < C::D; c += 32) {
+        uint32_t o[32];
+        tmem_ld_32x32b_x32(tO + c, o);
+        tmem_ld_wait_x32(o);
+        if (live) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-          tmem_st_32x32b_x32(tO + c, o);
+          for (int i = 0; i < 8; ++i)
+            dst[c / 4 + i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                         __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
         }
       }
-      tmem_st_wait();
-      m_run = m_new;
-    }
-    if (masked && !((kt + 1) * C::BC <= t.km.pre_end ||
-                    (kt * C::BC >= u.walk.lo && (kt + 1) * C::BC <= u.walk.end))) {
-      // some key of the tile is hidden from every row: its V row may be anything
-      const int sv = j % C::VSTAGES;
-      ok = wait_or_abort(t.bar(DB_VFULL + sv), (uint32_t)(j / C::VSTAGES) & 1, t.abort_flag, t.status, kSiteMmaV);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      zero_hidden_rows<C>(t.sV + sv * C::KV_BYTES, kt, u.walk, t.km.pre_end, r);
-      fence_proxy_async_smem();
+      if (live) *reinterpret_cast<float2*>(p.ws_ml + slot * 2) = make_float2(m_run, l_run);
+    } else if (warp_live) {
+      const bool empty = !(l_run > 0.f);
+      const float inv_l = empty ? 0.f : 1.f / l_run;
+      uint8_t* o_row = paged_o_row(p, row, head);
+#pragma unroll 1
+      for (int c = 0; c < C::D; c += 32) {
+        uint32_t o[32];
+        tmem_ld_32x32b_x32(tO + c, o);   // n = 0: not used
+        tmem_ld_wait_x32(o);
+        if (live) {
+          uint4* dst = reinterpret_cast<uint4*>(o_row + c * 2);
+          uint32_t w[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            w[i] = empty ? 0u : pack2<BF16>(__uint_as_float(o[2 * i]) * inv_l, __uint_as_float(o[2 * i + 1]) * inv_l);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        }
+      }
+      if (live)
+        p.lse[(long long)head * p.lse_hs + row] = empty ? -INFINITY : (m_run + log2f(l_run)) * 0.6931471805599453f;
     }
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive(t.bar(DB_P + (j & 1)));
-  }
-  if (ok) {
-    ok = wait_or_abort(t.bar(DB_OLAST), 0, t.abort_flag, t.status, kSiteEpilogueO);
-    ok = __all_sync(0xffffffffu, ok);
-  }
-  if (!ok || !warp_live) return;
-  tc_fence_after();
-  if (u.slot >= 0) {
-    const size_t slot = (size_t)u.slot * (size_t)p.slot_rows + (size_t)r;
-    float4* dst = reinterpret_cast<float4*>(p.ws_o + slot * C::D);
-#pragma unroll 1
-    for (int c = 0; c < C::D; c += 32) {
-      uint32_t o[32];
-      tmem_ld_32x32b_x32(tO + c, o);
-      tmem_ld_wait_x32(o);
-      if (live) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          dst[c / 4 + i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
-                                       __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
-      }
-    }
-    if (live) *reinterpret_cast<float2*>(p.ws_ml + slot * 2) = make_float2(m_run, l_run);
-    return;
-  }
-  const bool empty = !(l_run > 0.f);
-  const float inv_l = empty ? 0.f : 1.f / l_run;
-  uint8_t* o_row = paged_o_row(p, u.row0 + row, head);
-#pragma unroll 1
-  for (int c = 0; c < C::D; c += 32) {
-    uint32_t o[32];
-    tmem_ld_32x32b_x32(tO + c, o);
-    tmem_ld_wait_x32(o);
-    if (live) {
-      uint4* dst = reinterpret_cast<uint4*>(o_row + c * 2);
-      uint32_t w[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        w[i] = empty ? 0u : pack2<BF16>(__uint_as_float(o[2 * i]) * inv_l, __uint_as_float(o[2 * i + 1]) * inv_l);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-    }
-  }
-  if (live)
-    p.lse[(long long)head * p.lse_hs + u.row0 + row] =
-        empty ? -INFINITY : (m_run + log2f(l_run)) * 0.6931471805599453f;
-}
-
-// A unit without a key: O = 0 and L = -inf (whole tiles only: a split tile's
-// chunks all have keys).
-template <class C>
-__device__ __forceinline__ void pg_store_empty(const PagedTile& u, const PagedParams& p, int tid) {
-  constexpr int CH = C::D / 8;
-  for (int i = tid; i < u.rows * CH; i += C::THREADS) {
-    const int r = i / CH, tok = r / p.group;
-    uint8_t* o_row = paged_o_row(p, u.row0 + u.q0 + tok, u.h * p.group + r - tok * p.group);
-    reinterpret_cast<uint4*>(o_row)[i % CH] = make_uint4(0u, 0u, 0u, 0u);
-  }
-  for (int r = tid; r < u.rows; r += C::THREADS) {
-    const int tok = r / p.group;
-    p.lse[(long long)(u.h * p.group + r - tok * p.group) * p.lse_hs + u.row0 + u.q0 + tok] = -INFINITY;
+    if (lane == 0) mbar_arrive(t.bar(PG_ODONE + (nf & 1)));
   }
 }
 
@@ -578,75 +841,29 @@ __global__ void __launch_bounds__(192, PagedConfig<D>::CTAS_PER_SM)
   const uint32_t sbase = smem_u32(smem);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
-  PagedScan* scan = reinterpret_cast<PagedScan*>(smem + C::OFF_MISC + 16);
-  static_assert(16 + sizeof(PagedScan) <= C::MISC_BYTES, "shared-memory misc area");
-  static_assert(C::OFF_MISC % 8 == 0, "scan alignment");
+  PagedScan* scan = reinterpret_cast<PagedScan*>(smem + C::OFF_SCAN);
+  static_assert(sizeof(PagedScan) <= 256 && C::OFF_SCAN % 8 == 0, "scan area");
   const int warp = (int)(threadIdx.x >> 5);
   const int lane = (int)(threadIdx.x & 31);
-  grid_launch_dependents();   // the merge may be scheduled once every unit has started; it waits for the partials
+  grid_launch_dependents();   // the merge may be scheduled once every CTA has started; it waits for the partials
 
   // The whole CTA leaves together, before any barrier or TMEM set-up, when it
-  // has no unit.
-  PagedUnit un;
-  if (!find_unit<C::THREADS, false>(p, (long long)blockIdx.x, scan, un)) return;
-  DbufCtx t;
-  PagedTile u;
-  u.seq = un.seq;
-  u.h = un.h;
-  u.row0 = un.row0;
-  u.q0 = un.tile * p.tile_tokens;
-  const int last = min(u.q0 + p.tile_tokens, un.n_q) - 1;
-  u.rows = (last + 1 - u.q0) * p.group;
-  t.km = paged_mask(p, un.n_q, un.n_k);
-  u.walk = tile_walk(t.km, u.q0, last);
-  const int splits = tile_splits(u.walk.n, un.chunk);   // this tile's; at most the sequence's
-  if (un.split >= splits) return;
-  // equal chunks: the tile's n key tiles over its splits, none of them empty
-  // (splits - 1 chunks of at most C tiles hold fewer than n)
-  const int size = (u.walk.n + splits - 1) / splits;
-  u.j0 = un.split * size;
-  t.nkv = min(size, u.walk.n - u.j0);
-  u.slot = -1;
-  if (splits > 1) {
-    const int tiles = (un.n_q + p.tile_tokens - 1) / p.tile_tokens;
-    u.slot = unit_slot(un, tiles, p.heads_kv, un.split);
-  }
-  if (t.nkv == 0) {   // no row of the tile sees a key (a split tile's chunks all have some)
-    pg_store_empty<C>(u, p, (int)threadIdx.x);
-    return;
-  }
+  // has no piece.
+  const int piece = (int)blockIdx.x;
+  const PagedPlace place = find_place<C::THREADS>(p, piece, scan, blockIdx.x == 0);
+  if (place.seq < 0) return;
+  PagedCtx t;
   t.bar0 = sbase + C::OFF_BAR;
   t.sQ = sbase + C::OFF_Q;
   t.sK = sbase + C::OFF_K;
   t.sV = sbase + C::OFF_V;
   t.abort_flag = abort_flag;
   t.status = p.status;
-  // key tiles every row sees, by visited index of this unit
-  TileMask tm = tile_mask<BAND>(t.km, u.q0, last, C::BC);
-  if (u.walk.npre == 0) tm.pre -= u.walk.skip;
-  tm.lo -= u.walk.skip;
-  tm.hi -= u.walk.skip;
-  t.tm = tm.from(u.j0);
-  t.few_keys = t.km.n_k <= 2 * C::BC;
+  t.frags = reinterpret_cast<PagedFrag*>(smem + C::OFF_FRAG);
 
   if (warp == C::TMA_WARP && lane == 0) {
-    mbar_init(t.bar(DB_Q), 1);
-    for (int s = 0; s < C::KSTAGES; ++s) {
-      mbar_init(t.bar(DB_KFULL + s), 1);
-      mbar_init(t.bar(DB_KEMPTY + s), 1);
-    }
-    for (int s = 0; s < C::VSTAGES; ++s) {
-      mbar_init(t.bar(DB_VFULL + s), 1);
-      mbar_init(t.bar(DB_VEMPTY + s), 1);
-    }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(t.bar(DB_S + s), 1);
-      mbar_init(t.bar(DB_P + s), 4);
-    }
-    mbar_init(t.bar(DB_O), 1);
-    mbar_init(t.bar(DB_OLAST), 1);
-    mbar_init(t.bar(DB_EXIT), 1);
-    mbar_init(t.bar(DB_QT), 4);
+    for (int i = 0; i < PG_BARS; ++i)
+      mbar_init(t.bar(i), (i == PG_P || i == PG_P + 1 || i == PG_ODONE || i == PG_ODONE + 1) ? 4 : 1);
     *abort_flag = 0;
     fence_mbar_init();
     fence_proxy_async_smem();
@@ -664,14 +881,12 @@ __global__ void __launch_bounds__(192, PagedConfig<D>::CTAS_PER_SM)
   t.tmem = *tmem_slot;
 
   if (warp == C::TMA_WARP) {
-    pg_producer<C>(t, u, p, &tm_q, &tm_k, &tm_v, lane);
+    pg_producer<C, BAND>(t, p, &tm_q, &tm_k, &tm_v, place, piece, lane);
   } else if (warp == C::MMA_WARP) {
-    KernelParams kp;
-    kp.qk_negate = p.qk_negate;
-    if (lane == 0) db_mma<C, BF16>(t, kp);
+    if (lane == 0) pg_mma<C, BF16>(t, p);
     __syncwarp();
   } else {
-    pg_softmax<C, BF16, BAND>(t, u, p, warp, lane);
+    pg_softmax<C, BF16, BAND>(t, p, warp, lane);
   }
   tc_fence_before();
   __syncthreads();
@@ -681,72 +896,125 @@ __global__ void __launch_bounds__(192, PagedConfig<D>::CTAS_PER_SM)
   }
 }
 
-constexpr int kPagedMergeThreads = 128;
-constexpr int kPagedMergeRows = 16;   // rows a block merges, four a warp
+// ---------------------------------------------------------------- the merge
 
-// One block per split (query tile, K/V head) and 16 of its rows: a warp per
-// row, a lane per D / 32 columns, the chunks' states added in chunk order with
-// the online softmax's rescaling.  The place of the block in the batch is
-// found before the wait for the partials.
+constexpr int kPagedMergeThreads = 256;
+constexpr int kPagedMergeRows = 32;   // rows of a block, eight at a time
+
+// Block (m, y): the pair that piece m + 1's start falls inside, if that is the
+// pair's first such boundary; rows 32 y .. of it.  A warp takes a row, a lane D / 32
+// columns; fewer than eight rows share the eight warps, whose sums are joined
+// through shared memory in a fixed order.  The
+// place of the block on the line is found before the wait for the partials.
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kPagedMergeThreads) fa2_paged_merge_kernel(const PagedParams p) {
-  __shared__ PagedScan scan;
-  PagedUnit u;
-  const bool any = find_unit<kPagedMergeThreads, true>(p, (long long)blockIdx.x, &scan, u);
-  grid_dependency_wait();   // the partials are complete and visible
-  if (!any) return;
-  const int q0 = u.tile * p.tile_tokens;
-  const int last = min(q0 + p.tile_tokens, u.n_q) - 1;
-  const int rows = (last + 1 - q0) * p.group;
-  const KeyMask km = paged_mask(p, u.n_q, u.n_k);
-  const int splits = tile_splits(tile_walk(km, q0, last).n, u.chunk);
-  if (splits <= 1) return;   // its one unit has written O and L
-  const int tiles = (u.n_q + p.tile_tokens - 1) / p.tile_tokens;
-  const int slot0 = unit_slot(u, tiles, p.heads_kv, 0);
-  const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31;
+  constexpr int NW = kPagedMergeThreads / 32;
   constexpr int E = D / 32;   // columns of a lane
-  const int r1 = min(((int)blockIdx.y + 1) * kPagedMergeRows, rows);
-  for (int r = (int)blockIdx.y * kPagedMergeRows + warp; r < r1; r += kPagedMergeThreads / 32) {
-    float M = -INFINITY;
-    for (int s = lane; s < splits; s += 32)
-      M = fmaxf(M, p.ws_ml[((size_t)(slot0 + s * p.heads_kv) * p.slot_rows + r) * 2]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float L = 0.f, acc[E];
+  __shared__ PagedScan scan;
+  __shared__ float part_o[NW][D];
+  __shared__ float part_ml[NW][2];
+  const int piece = (int)blockIdx.x + 1;
+  const PagedPlace place = find_place<kPagedMergeThreads>(p, piece, &scan, false);
+  grid_dependency_wait();   // the partials are complete and visible
+  if (place.share == 0 || place.seq < 0) return;
+  const PagedSeq s = paged_seq(p, place.seq, false);
+  const long long pos = piece * place.share;
+  int tile, h;
+  const long long x = place.at + pair_at(p, s, pos - place.at, tile, h);
+  if (x == pos || x / place.share != piece - 1) return;
+  const int w = s.width(p, tile);
+  const int last_piece = (int)((x + w - 1) / place.share);
+  const int q0 = tile * p.tile_tokens, last = min(q0 + p.tile_tokens, s.n_q) - 1;
+  const int rows = (last + 1 - q0) * p.group;
+  const int n = tile_walk(paged_mask(p, s.n_q, s.n_k), q0, last).n;
+  const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31;
+  // state of piece c's fragment of the pair: its slot, or none
+  auto slot_of = [&](int c) -> int {
+    const long long begin = c * place.share;
+    const int j0 = span_tile(p, begin > x ? begin - x : 0, n);
+    const long long y1 = begin + place.share - x;
+    const int j1 = y1 >= w ? n : span_tile(p, y1, n);
+    return j1 > j0 ? 2 * c + (begin <= x ? 1 : 0) : -1;
+  };
+  const int r_end = min(rows, ((int)blockIdx.y + 1) * kPagedMergeRows);
+  for (int r0 = (int)blockIdx.y * kPagedMergeRows; r0 < r_end; r0 += NW) {
+    const int here = min(r_end - r0, NW);
+    const int wide = here <= 1 ? 1 : here <= 2 ? 2 : here <= 4 ? 4 : 8;   // rows side by side
+    const int team = NW / wide;                                           // warps of a row
+    const int my_row = warp % wide, member = warp / wide;
+    const int r = r0 + my_row;
+    float M = -INFINITY, L = 0.f, acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
-#pragma unroll 4
-    for (int s = 0; s < splits; ++s) {
-      const size_t slot = (size_t)(slot0 + s * p.heads_kv) * p.slot_rows + r;
-      const float2 ml = *reinterpret_cast<const float2*>(p.ws_ml + slot * 2);
-      if (ml.x == -INFINITY) continue;   // a chunk that shows the row nothing: O~ is not read
-      const float f = ex2_approx(ml.x - M);
-      L = fmaf(f, ml.y, L);
-      const float* src = p.ws_o + slot * D + lane * E;
-      if constexpr (E == 2) {
-        const float2 x = *reinterpret_cast<const float2*>(src);
-        acc[0] = fmaf(f, x.x, acc[0]);
-        acc[1] = fmaf(f, x.y, acc[1]);
-      } else {
+    for (int c0 = piece - 1 + member; my_row < here && c0 <= last_piece; c0 += 32 * team) {
+      // a lane per partial: its (m, l)
+      const int c = c0 + lane * team;
+      const int slot = c <= last_piece ? slot_of(c) : -1;
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (slot >= 0) ml = *reinterpret_cast<const float2*>(p.ws_ml + ((size_t)slot * p.slot_rows + r) * 2);
+      float top = ml.x;
 #pragma unroll
-        for (int e = 0; e < E; e += 4) {
-          const float4 x = *reinterpret_cast<const float4*>(src + e);
-          acc[e] = fmaf(f, x.x, acc[e]);
-          acc[e + 1] = fmaf(f, x.y, acc[e + 1]);
-          acc[e + 2] = fmaf(f, x.z, acc[e + 2]);
-          acc[e + 3] = fmaf(f, x.w, acc[e + 3]);
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const float M2 = fmaxf(M, top);
+      if (M2 == -INFINITY) continue;
+      const float f0 = M == -INFINITY ? 0.f : ex2_approx(M - M2);
+      M = M2;
+      const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
+      float l = f * ml.y;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+      L = L * f0 + l;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] *= f0;
+      const int count = min(32, (last_piece - c0) / team + 1);
+#pragma unroll 8
+      for (int k = 0; k < count; ++k) {
+        const float fk = __shfl_sync(0xffffffffu, f, k);
+        const int at = __shfl_sync(0xffffffffu, slot, k);
+        if (at < 0) continue;
+        const float* src = p.ws_o + ((size_t)at * p.slot_rows + r) * D + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+          const float2 v = *reinterpret_cast<const float2*>(src + e);
+          acc[e] = fmaf(fk, v.x, acc[e]);
+          acc[e + 1] = fmaf(fk, v.y, acc[e + 1]);
         }
       }
     }
+    if (team > 1) {   // the block's last rows only
+#pragma unroll
+      for (int e = 0; e < E; ++e) part_o[warp][lane * E + e] = acc[e];
+      if (lane == 0) {
+        part_ml[warp][0] = M;
+        part_ml[warp][1] = L;
+      }
+      __syncthreads();
+      if (member > 0) return;
+      float top = M;
+      for (int k = 1; k < team; ++k) top = fmaxf(top, part_ml[warp + k * wide][0]);
+      const float f0 = M == -INFINITY ? 0.f : ex2_approx(M - top);
+      L *= f0;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] *= f0;
+      M = top;
+      for (int k = 1; k < team; ++k) {
+        const float mk = part_ml[warp + k * wide][0];
+        if (mk == -INFINITY) continue;
+        const float fk = ex2_approx(mk - M);
+        L = fmaf(fk, part_ml[warp + k * wide][1], L);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(fk, part_o[warp + k * wide][lane * E + e], acc[e]);
+      }
+    }
+    if (my_row >= here) continue;
     const bool empty = !(L > 0.f);
     const float inv_l = empty ? 0.f : 1.f / L;
-    const int tok = r / p.group, head = u.h * p.group + r - tok * p.group;
-    uint32_t* dst = reinterpret_cast<uint32_t*>(paged_o_row(p, u.row0 + q0 + tok, head)) + lane * (E / 2);
+    const int tok = r / p.group, head = h * p.group + r - tok * p.group;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(paged_o_row(p, s.row0 + q0 + tok, head)) + lane * (E / 2);
 #pragma unroll
     for (int e = 0; e < E; e += 2) dst[e / 2] = empty ? 0u : pack2<BF16>(acc[e] * inv_l, acc[e + 1] * inv_l);
     if (lane == 0)
-      p.lse[(long long)head * p.lse_hs + u.row0 + q0 + tok] =
-          empty ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+      p.lse[(long long)head * p.lse_hs + s.row0 + q0 + tok] = empty ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
   }
 }
 
@@ -759,11 +1027,12 @@ int launch_paged_kernels(const PagedLaunchArgs& a) {
     return (int)cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM_BYTES);
   });
   if (e != 0) return e;
-  kern<<<(unsigned)a.grid, C::THREADS, C::SMEM_BYTES, a.stream>>>(a.tm_q, a.tm_k, a.tm_v, a.p);
+  const int grid = a.p.pair_ctas > a.p.ctas ? a.p.pair_ctas : a.p.ctas;
+  kern<<<(unsigned)grid, C::THREADS, C::SMEM_BYTES, a.stream>>>(a.tm_q, a.tm_k, a.tm_v, a.p);
   const cudaError_t r = cudaGetLastError();
   if (r != cudaSuccess) return (int)r;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)a.merge_tiles, (unsigned)((a.p.slot_rows + kPagedMergeRows - 1) / kPagedMergeRows));
+  cfg.gridDim = dim3((unsigned)(a.p.ctas - 1), (unsigned)((a.p.slot_rows + kPagedMergeRows - 1) / kPagedMergeRows));
   cfg.blockDim = dim3(kPagedMergeThreads);
   cfg.stream = a.stream;
   cudaLaunchAttribute attr[1];

@@ -22,6 +22,14 @@ constexpr int kPagedPlanMaxBatch = 16384;
 constexpr int kPagedTileRows = 128;
 constexpr int kPagedKeyTile = 64;
 
+// Where a cache tensor's boxes lie in its 5-D map (64 columns, 8 rows, d / 64
+// column blocks, then): ratio > 0: 8-row groups of a page, and page * ratio +
+// head (the page stride is `ratio` head strides); ratio = 0: heads, pages.
+struct PagedSide {
+  int ratio;
+  int extent;   // ratio > 0: the last coordinate's extent (out of range: zeros)
+};
+
 struct PagedParams {
   void* o;                // 16-bit output [total_q][heads_q][d] by strides
   float* lse;             // [heads_q][total_q], head stride lse_hs
@@ -32,28 +40,27 @@ struct PagedParams {
   long long table_stride, o_rs, o_hs, lse_hs;
   int batch, heads_kv, group;
   int tile_tokens;        // tokens of a query tile: 128 / group
-  int box_tokens;         // tokens of a Q load: min(tile_tokens, max_q)
   int total_q, max_q;
   int num_pages, page_size, max_pages;
+  int box_rows;           // key rows of a box: 8, 16, 32 or 64
+  PagedSide k_side, v_side;
   int window_left, window_right, prefix;   // as KernelParams
   float scale_log2_mag;   // as KernelParams
   uint32_t qk_negate;     // as KernelParams
-  // Key splits: a query tile's visited key tiles are cut into chunks of at
-  // most C = max(min_chunk, ceil(work / target_units)) tiles, `work` the
-  // batch's sum over (sequence, K/V head, query tile).
-  int target_units, min_chunk;
-  int max_slots;          // partial states the workspace holds
-  int slot_rows;          // rows of a partial state: group * box_tokens
-  float* ws_o;            // [slot][slot_rows][d] partial O~
-  float* ws_ml;           // [slot][slot_rows][2] partial (m, l), exp2 domain
+  int ctas;               // pieces the line of work is cut into
+  int pair_ctas;          // CTAs for one (query tile, K/V head) pair each where
+                          // the batch may have that many, or 0
+  int overhead;           // a pair's fixed cost on the line, in keys
+  int min_share;          // keys of a piece at least
+  int slot_rows;          // rows of a Q load and of a partial state: group x tokens
+  float* ws_o;            // [2 * ctas][slot_rows][d] partial O~
+  float* ws_ml;           // [2 * ctas][slot_rows][2] partial (m, l), exp2 domain
 };
 
 struct PagedLaunchArgs {
-  CUtensorMap tm_q;       // (d, group, heads_kv, total_q), boxes of 64 columns x group x 1 x box_tokens
-  CUtensorMap tm_k, tm_v; // (d, page_size, heads_kv, num_pages), boxes of 64 columns x min(page_size, 64) rows
+  CUtensorMap tm_q;       // (d, group, heads_kv, total_q), boxes of 64 columns x group x 1 x tokens
+  CUtensorMap tm_k, tm_v; // see PagedSide; boxes of 64 columns x 8 rows x d / 64 x (box_rows / 8 groups)
   PagedParams p;
-  long long grid;         // upper bound of the units
-  long long merge_tiles;  // upper bound of the split (query tile, K/V head) pairs
   bool bf16;
   bool band;              // window_left >= 0 or prefix > 0
   cudaStream_t stream;
@@ -100,11 +107,11 @@ struct PagedAppendArgs {
 int launch_paged_append(const PagedAppendArgs& a, cudaStream_t stream);
 
 // Services of the C-ABI translation unit: the current device's status word
-// (checks the device), and an rank-4 tensor map of a 16-bit tensor whose
-// innermost dimension is contiguous (strides of dimensions 1 .. 3 in
-// elements; boxes of 64 columns, 128-byte swizzle).
+// (checks the device), and a tensor map of a 16-bit tensor whose innermost
+// dimension is contiguous (strides of the others in elements; 128-byte
+// swizzle, rank <= 5).
 int paged_device_status(uint32_t** status);
-int encode_map_4d(CUtensorMap* m, const void* base, const long long dims[4], const long long strides[3],
-                  const int box[4], bool bf16);
+int encode_map_nd(CUtensorMap* m, const void* base, int rank, const long long* dims, const long long* strides,
+                  const int* box, bool bf16);
 
 }  // namespace fa2

@@ -15,11 +15,15 @@ namespace {
 
 constexpr long long kMaxStride = 1ll << 39;   // elements: 16-bit strides stay below the TMA limit of 2^40 bytes
 
-// Split units aimed at: one wave of the resident CTAs of a GB300's 152 SMs
-// (two per SM, one at head dim 256).  Fixed, so that neither the workspace nor
-// the result depends on the device.
-constexpr int target_units(int d) { return d == 256 ? 152 : 304; }
-constexpr int kPagedMinChunk = 4;   // key tiles: no chunk below 256 keys
+// Pieces the work is cut into: one wave of the resident CTAs of a GB300's 152
+// SMs (two per SM, one at head dim 256).  Fixed, so that neither the workspace
+// nor the result depends on the device.
+constexpr int paged_ctas(int d) { return d == 256 ? 152 : 304; }
+// A pair's fixed cost (Q, the first products, the epilogue) in keys, and the
+// shortest piece worth a CTA and a share of the merge.
+constexpr int kPagedOverhead = 128;
+constexpr int kPagedMinShare = 256;
+constexpr long long kPagedMaxKeys = (1ll << 31) - 4096;   // keys of a sequence, rounded up to tiles, stay below 2^31
 
 struct Range {
   uintptr_t at;
@@ -85,12 +89,11 @@ int check_cache(const fa2_paged_cache& c, CacheView& k, CacheView& v) {
 
 struct PagedShape {
   int group, tile_tokens, box_tokens, max_q;
-  long long grid, merge_tiles, slots;
+  int ctas, pair_ctas;
   size_t ws_o_bytes, ws_ml_bytes;
 };
 
-// Sizes of a paged forward call, and the bounds that size its grid and its
-// workspace from what the host knows.
+// Sizes of a paged forward call that follow from what the host knows.
 int paged_shape(const fa2_paged_params& a, PagedShape& s) {
   const fa2_paged_cache& c = a.cache;
   if (a.batch < 1 || a.heads < 1 || a.total_q < 1 || a.max_seqlen_q < 1 || a.max_pages < 1) return FA2_ERR_INVALID_ARG;
@@ -99,7 +102,7 @@ int paged_shape(const fa2_paged_params& a, PagedShape& s) {
   if (a.heads % c.heads) return FA2_ERR_INVALID_ARG;
   s.group = a.heads / c.heads;
   if (s.group > kPagedTileRows) return FA2_ERR_UNSUPPORTED;
-  if ((long long)a.max_pages * c.page_size > INT_MAX) return FA2_ERR_UNSUPPORTED;
+  if ((long long)a.max_pages * c.page_size > kPagedMaxKeys) return FA2_ERR_UNSUPPORTED;
   s.max_q = a.max_seqlen_q < a.total_q ? a.max_seqlen_q : a.total_q;
   const long long T = s.tile_tokens = kPagedTileRows / s.group;
   s.box_tokens = (int)(T < s.max_q ? T : s.max_q);
@@ -108,17 +111,47 @@ int paged_shape(const fa2_paged_params& a, PagedShape& s) {
   const long long each = (s.max_q + T - 1) / T;
   if (tiles > a.batch * each) tiles = a.batch * each;
   if (tiles > a.total_q) tiles = a.total_q;
-  const long long pairs = tiles * c.heads, target = target_units(c.head_dim);
-  // sum of ceil(n / C) over the pairs, with C >= work / target: at most target
-  // + pairs units; pairs with n > C number fewer than target
-  s.grid = target + pairs;
-  s.merge_tiles = pairs < target ? pairs : target;
-  s.slots = target + s.merge_tiles;
-  if (s.grid > INT_MAX) return FA2_ERR_UNSUPPORTED;
-  const size_t rows = (size_t)s.slots * (size_t)(s.group * s.box_tokens);
+  const long long pairs = tiles * c.heads;
+  if (pairs > INT_MAX) return FA2_ERR_UNSUPPORTED;
+  s.ctas = paged_ctas(c.head_dim);
+  s.pair_ctas = pairs >= 4 * s.ctas ? (int)pairs : 0;
+  const size_t rows = 2 * (size_t)s.ctas * (size_t)(s.group * s.box_tokens);
   s.ws_o_bytes = align256(rows * (size_t)c.head_dim * 4);
   s.ws_ml_bytes = align256(rows * 2 * 4);
   return FA2_OK;
+}
+
+// Map of one cache tensor: a page's 8-row groups, with pages and heads as one
+// coordinate where the page stride is a whole number of head strides (as in
+// [pages, heads, rows, d] and [pages, rows, heads, d], also with K and V
+// interleaved); otherwise pages and heads apart, in boxes of 8 rows.
+bool merged_side(const CacheView& x, PagedSide& side) {
+  const long long pages = x.dims[0], heads = x.dims[1];
+  long long ratio = 1;
+  if (pages > 1 && heads > 1) {
+    if (x.st[0] % x.st[1]) return false;
+    ratio = x.st[0] / x.st[1];
+  }
+  const long long extent = (pages - 1) * ratio + heads;
+  if (extent > INT_MAX) return false;
+  side.ratio = (int)ratio;
+  side.extent = (int)extent;
+  return true;
+}
+
+int cache_map(CUtensorMap* m, const void* at, const CacheView& x, const PagedSide& side, int d, int box_rows,
+              bool bf16) {
+  const long long rows = x.dims[2], rs = x.st[2];
+  if (side.ratio > 0) {
+    const long long dims[5] = {64, 8, d / 64, rows / 8, side.extent};
+    const long long st[4] = {rs, 64, 8 * rs, x.dims[1] > 1 ? x.st[1] : x.st[0]};
+    const int box[5] = {64, 8, d / 64, box_rows / 8, 1};
+    return encode_map_nd(m, at, 5, dims, st, box, bf16);
+  }
+  const long long dims[5] = {64, rows, d / 64, x.dims[1], x.dims[0]};
+  const long long st[4] = {rs, 64, x.st[1], x.st[0]};
+  const int box[5] = {64, 8, d / 64, 1, 1};
+  return encode_map_nd(m, at, 5, dims, st, box, bf16);
 }
 
 int paged_forward(const fa2_paged_params& a, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
@@ -171,20 +204,16 @@ int paged_forward(const fa2_paged_params& a, void* workspace, size_t workspace_b
     const long long dims[4] = {c.head_dim, s.group, c.heads, a.total_q};
     const long long st[3] = {qs[1], qs[1] * s.group, qs[0]};
     const int box[4] = {64, s.group, 1, s.box_tokens};
-    rc = encode_map_4d(&la.tm_q, a.q, dims, st, box, la.bf16);
+    rc = encode_map_nd(&la.tm_q, a.q, 4, dims, st, box, la.bf16);
     if (rc) return rc;
   }
-  const CacheView* views[2] = {&kc, &vc};
-  const void* at[2] = {c.k, c.v};
-  CUtensorMap* maps[2] = {&la.tm_k, &la.tm_v};
-  for (int i = 0; i < 2; ++i) {
-    const CacheView& x = *views[i];
-    const long long dims[4] = {c.head_dim, x.dims[2], x.dims[1], x.dims[0]};
-    const long long st[3] = {x.st[2], x.st[1], x.st[0]};
-    const int box[4] = {64, c.page_size < kPagedKeyTile ? c.page_size : kPagedKeyTile, 1, 1};
-    rc = encode_map_4d(maps[i], at[i], dims, st, box, la.bf16);
-    if (rc) return rc;
-  }
+  p.box_rows = c.page_size < kPagedKeyTile ? c.page_size : kPagedKeyTile;
+  const bool merged_k = merged_side(kc, p.k_side), merged_v = merged_side(vc, p.v_side);
+  if (!merged_k || !merged_v) p.box_rows = 8;
+  rc = cache_map(&la.tm_k, c.k, kc, p.k_side, c.head_dim, p.box_rows, la.bf16);
+  if (rc) return rc;
+  rc = cache_map(&la.tm_v, c.v, vc, p.v_side, c.head_dim, p.box_rows, la.bf16);
+  if (rc) return rc;
   p.o = a.o;
   p.lse = a.lse;
   p.table = a.block_table;
@@ -198,7 +227,6 @@ int paged_forward(const fa2_paged_params& a, void* workspace, size_t workspace_b
   p.heads_kv = c.heads;
   p.group = s.group;
   p.tile_tokens = s.tile_tokens;
-  p.box_tokens = s.box_tokens;
   p.total_q = a.total_q;
   p.max_q = s.max_q;
   p.num_pages = c.num_pages;
@@ -210,14 +238,13 @@ int paged_forward(const fa2_paged_params& a, void* workspace, size_t workspace_b
   const float scale_log2 = a.scale * 1.4426950408889634f;
   p.scale_log2_mag = std::fmax(std::fabs(scale_log2), FLT_MIN);
   p.qk_negate = scale_log2 < 0.f ? 1u << 13 : 0u;   // the negate-A bit of the S product's descriptor
-  p.target_units = target_units(c.head_dim);
-  p.min_chunk = kPagedMinChunk;
-  p.max_slots = (int)s.slots;
+  p.ctas = s.ctas;
+  p.pair_ctas = s.pair_ctas;
+  p.overhead = kPagedOverhead;
+  p.min_share = kPagedMinShare;
   p.slot_rows = s.group * s.box_tokens;
   p.ws_o = static_cast<float*>(workspace);
   p.ws_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + s.ws_o_bytes);
-  la.grid = s.grid;
-  la.merge_tiles = s.merge_tiles;
   la.band = a.window_left >= 0 || a.prefix_len > 0;
   la.stream = stream;
   int e = 0;
@@ -269,7 +296,7 @@ int paged_plan(const fa2_paged_plan_params& a, cudaStream_t stream) {
   if (a.batch < 1 || a.max_pages < 1 || a.num_pages < 1 || a.page_size < 1 || a.total_q < 1 || a.num_free < 0)
     return FA2_ERR_INVALID_ARG;
   if (a.batch > FA2_PAGED_PLAN_MAX_BATCH) return FA2_ERR_UNSUPPORTED;
-  if ((long long)a.num_pages * a.page_size > INT_MAX || (long long)a.max_pages * a.page_size > INT_MAX)
+  if ((long long)a.num_pages * a.page_size > INT_MAX || (long long)a.max_pages * a.page_size > kPagedMaxKeys)
     return FA2_ERR_UNSUPPORTED;
   if (!a.free_pages && a.num_free > 0) return FA2_ERR_INVALID_ARG;
   const void* all[8] = {a.context_lens, a.query_lens, a.free_count, a.block_table,

@@ -409,7 +409,7 @@ typedef struct fa2_paged_plan_params {
   int* free_left;          /* device, one int32; written */
   int64_t table_stride;    /* elements; >= max_pages unless batch = 1 */
   int batch;               /* >= 1 */
-  int max_pages;           /* table entries per request >= 1; max_pages * page_size < 2^31 */
+  int max_pages;           /* table entries per request >= 1; max_pages * page_size <= 2^31 - 4096 */
   int num_pages;           /* pages of the cache >= 1; num_pages * page_size < 2^31 */
   int page_size;           /* >= 1 */
   int total_q;             /* rows of slots >= 1: the step's tokens, with padding */
@@ -490,7 +490,7 @@ typedef struct fa2_paged_params {
   int heads;               /* query heads >= 1 */
   int total_q;             /* rows of q, o and lse >= 1 */
   int max_seqlen_q;        /* longest sequence's query count >= 1 (sizes grid and workspace) */
-  int max_pages;           /* table entries per sequence >= 1; max_pages * page_size < 2^31 */
+  int max_pages;           /* table entries per sequence >= 1; max_pages * page_size <= 2^31 - 4096 */
   int window_left;         /* >= 0, or -1 = unbounded */
   int window_right;        /* >= 0, or -1 = unbounded */
   int prefix_len;          /* >= 0 */

@@ -95,14 +95,14 @@ def test_fwd_refusals(lib, kw, code):
 
 def test_fwd_workspace_follows_shapes(lib):
     size = lambda **kw: lib.fa2_paged_fwd_workspace_bytes(ctypes.byref(_fwd(**kw)))
-    # 5 tokens in 3 sequences of at most 2: at most 3 tiles of 64 tokens x 2 heads, 6 pairs; 304 + 6 slots of
-    # 2 x 2 rows, (64 + 2) floats each
-    assert size() == 310 * 4 * 64 * 4 + (310 * 4 * 2 * 4 + 255) // 256 * 256
+    # two partial states for each of 304 CTAs (152 at head dim 256): 2 x 2 rows (tokens x heads of a K/V head), d + 2
+    # floats each
+    assert size() == 608 * 4 * 64 * 4 + 608 * 4 * 2 * 4
+    assert size(head_dim=256) == 304 * 4 * 256 * 4 + 304 * 4 * 2 * 4
     assert size(heads=5) == 0 and size(head_dim=80) == 0 and size(total_q=0) == 0
     assert lib.fa2_paged_fwd_workspace_bytes(None) == 0
-    # bounded whatever the batch holds: 2 x 304 slots of 128 rows
-    big = size(total_q=1 << 20, max_seqlen_q=1 << 20, batch=64)
-    assert big == 608 * 128 * 64 * 4 + 608 * 128 * 2 * 4
+    # bounded whatever the batch holds: 128 rows
+    assert size(total_q=1 << 20, max_seqlen_q=1 << 20, batch=64) == 608 * 128 * 64 * 4 + 608 * 128 * 2 * 4
 
 
 def _append(**kw):
@@ -173,3 +173,25 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
         fa2.fa2_paged_append(q[:, :2], q[:, 2:], i32(5), cache, cache.clone())
     with pytest.raises(ValueError):
         fa2.fa2_paged_plan(i32(3), i32(3), i32(3, 8), i32(4), i32(1), 4, 16, 5)
+
+
+def test_packed_parameters_equal_the_structures(lib):
+    """The binding's packed parameters field by field against the ctypes mirrors (distinct values)."""
+    def fields(struct):
+        out = []
+        for name, _ in struct._fields_:
+            val = getattr(struct, name)
+            if isinstance(val, ctypes.Structure):
+                out += fields(val)
+            elif isinstance(val, ctypes.Array):
+                out += list(val)
+            else:
+                out.append(val)
+        return out
+
+    for pack, mirror in ((fa2._PAGED_PACK, fa2.Fa2PagedParams), (fa2._PAGED_APPEND_PACK, fa2.Fa2PagedAppendParams),
+                         (fa2._PAGED_PLAN_PACK, fa2.Fa2PagedPlanParams)):
+        n = len(fields(mirror()))
+        values = list(range(101, 101 + n))
+        data = pack.pack(*values)
+        assert fields(mirror.from_buffer_copy(data)) == values

@@ -200,6 +200,19 @@ def test_many_sequences():
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
+def test_many_query_tiles():
+    """Prompts from their start: enough (query tile, K/V head) pairs for one CTA each, beside short sequences."""
+    lens_q = [2500, 1, 1300, 7, 0, 900]
+    lens_k = [2500, 900, 1300, 7, 5, 1000]
+    p = Problem(lens_q, lens_k, 32, 8, 64, "fp16", 64, seed=13, fill=float("nan"))
+    o, lse = p.run(window_right=0)
+    assert status() == fa2.FA2_OK
+    p.check(o, lse, window_right=0)
+    o, lse = p.run(window_left=300, window_right=0, prefix_len=10)
+    assert status() == fa2.FA2_OK
+    p.check(o, lse, window_left=300, window_right=0, prefix_len=10)
+
+
 def test_layouts_equal_contiguous():
     """[page, row, head] caches, K and V interleaved, q and o as parts of wider rows, a sliced table."""
     p = Problem([3, 1, 70], [400, 33, 200], 8, 2, 128, "bf16", 16, seed=21)
@@ -220,6 +233,22 @@ def test_layouts_equal_contiguous():
     assert torch.equal(out[:, 4:12], o) and torch.equal(lse_wide[:, 20:94], lse)
     assert (out[:, :4] == 7).all() and (out[:, 12:] == 7).all()
     assert (lse_wide[:, :20] == 7).all() and (lse_wide[:, 94:] == 7).all()
+
+
+def test_padded_pages():
+    """Page strides that are no whole number of head strides (pages padded apart), in K, in V and in both."""
+    p = Problem([3, 1, 70], [400, 33, 200], 6, 3, 64, "fp16", 32, seed=22)
+    o, lse = p.run(window_right=0)
+    for which in ("k", "v", "kv"):
+        side = {}
+        for name, src in (("k", p.k), ("v", p.v)):
+            n = src[0].numel()
+            wide = torch.full((src.shape[0], n + 8), float("nan"), dtype=src.dtype, device="cuda")
+            wide[:, :n] = src.reshape(src.shape[0], n)
+            side[name] = wide[:, :n].unflatten(1, src.shape[1:]) if name in which else src
+        o2, lse2 = fa2.fa2_paged_fwd(p.q, side["k"], side["v"], p.table, p.cu, p.lens, window_right=0, max_seqlen_q=70)
+        assert status() == fa2.FA2_OK
+        assert torch.equal(o2, o) and torch.equal(lse2, lse)
 
 
 def test_pages_no_query_sees_are_not_read():
