@@ -156,6 +156,12 @@ __device__ __forceinline__ KeyMask paged_mask(const PagedParams& p, int n_q, int
   return km;
 }
 
+// a / b for 0 <= a, 0 < b: a 32-bit division where both fit.
+__device__ __forceinline__ long long line_div(long long a, long long b) {
+  if (((unsigned long long)(a | b) >> 32) == 0) return (long long)((unsigned)a / (unsigned)b);
+  return a / b;
+}
+
 // One sequence's part of the line: `tiles` query tiles x heads_kv pairs, in
 // order of the tiles, heads fastest.
 struct PagedSeq {
@@ -277,7 +283,7 @@ __device__ __forceinline__ PagedPlace find_place(const PagedParams& p, int piece
     all_pairs += sh->warp_sum[1][j];
     all_chunks += sh->warp_sum[2][j];
   }
-  long long share = (total + p.ctas - 1) / p.ctas;
+  long long share = line_div(total + p.ctas - 1, p.ctas);
   if (share < p.min_share) share = p.min_share;
   const bool whole = p.pair_ctas > 0 && all_pairs >= 4ll * p.ctas && 2 * all_chunks > total;
   const long long pos = whole ? piece : piece * share;
@@ -318,7 +324,7 @@ __device__ __forceinline__ long long pair_at(const PagedParams& p, const PagedSe
   tile = lo;
   const long long base = s.before(p, lo) * p.heads_kv;
   const int w = s.width(p, lo);
-  h = (int)((y - base) / w);
+  h = (int)line_div(y - base, w);
   return base + (long long)h * w;
 }
 
@@ -328,6 +334,16 @@ __device__ __forceinline__ int span_tile(const PagedParams& p, long long y, int 
   const long long j = k <= 0 ? 0 : (k + kPagedKeyTile - 1) / kPagedKeyTile;
   return (int)(j < n ? j : n);
 }
+
+// A pair whose partials are to be merged: left by the CTA at whose start the
+// pair is cut for the first time.
+struct PagedMerge {
+  long long x, share;   // the pair's start on the line; keys of a piece
+  int w, n;             // its span; its key tiles
+  int first;            // the piece that holds its start (last: (x + w - 1) / share), or -1: nothing to merge
+  int row, rows, h;     // first row of q / o / lse; live rows; K/V head
+};
+static_assert(sizeof(PagedMerge) == kPagedMergeBytes, "merge description");
 
 // Walks the fragments of one CTA's piece; every lane of the TMA warp in step.
 struct FragWalk {
@@ -357,7 +373,7 @@ struct FragWalk {
 
   // The next fragment and its block-table row; false when the piece is done.
   template <bool BAND>
-  __device__ __forceinline__ bool next(const PagedParams& p, PagedFrag& f, const int*& table) {
+  __device__ __forceinline__ bool next(const PagedParams& p, PagedFrag& f, const int*& table, PagedMerge& merge) {
     while (more) {
       const int w = s.width(p, tile);
       const long long begin = share == 0 ? 0 : cta * share;
@@ -383,6 +399,16 @@ struct FragWalk {
       f.tm.lo -= walk.skip;
       f.tm.hi -= walk.skip;
       f.tm = f.tm.from(f.j0);
+      if (y0 > 0) {   // the piece starts inside this pair
+        merge.first = line_div(x, share) == cta - 1 ? cta - 1 : -1;
+        merge.x = x;
+        merge.share = share;
+        merge.w = w;
+        merge.n = walk.n;
+        merge.row = f.row;
+        merge.rows = f.rows;
+        merge.h = h;
+      }
       table = p.table + (long long)seq * p.table_stride;
       // on to the next pair
       x += w;
@@ -484,7 +510,10 @@ __device__ __forceinline__ void pg_producer(const PagedCtx& t, const PagedParams
   int g = 0;     // key tiles loaded (K)
   int gv = 0;    // (V)
   int nf = 0;    // fragments published
-  bool have = walk.next<BAND>(p, f, table);
+  PagedMerge merge;
+  merge.first = -1;
+  bool have = walk.next<BAND>(p, f, table, merge);
+  if (lane == 0 && piece < p.ctas) p.merges[piece] = merge;   // (one pair per CTA: piece may be larger)
   int r0 = 0, r1 = 0, r2 = 0;
   int p0 = -1, p1 = -1, p2 = -1;
   if (have) {
@@ -552,7 +581,7 @@ __device__ __forceinline__ void pg_producer(const PagedCtx& t, const PagedParams
       if (!ok) break;
       // the last V tile, behind the next fragment's table reads
       const int h = f.h;
-      have = walk.next<BAND>(p, f, table);
+      have = walk.next<BAND>(p, f, table, merge);
       if (have) {
         p0 = fetch(0, r0);
         p1 = fetch(1, r1);
@@ -570,7 +599,7 @@ __device__ __forceinline__ void pg_producer(const PagedCtx& t, const PagedParams
       ++gv;
       continue;
     }
-    have = walk.next<BAND>(p, f, table);
+    have = walk.next<BAND>(p, f, table, merge);
     if (have) {
       p0 = fetch(0, r0);
       p1 = fetch(1, r1);
@@ -787,8 +816,10 @@ __device__ __forceinline__ void pg_softmax(const PagedCtx& t, const PagedParams&
     const int slot_at = f->slot;
     const int row = f->row + tok;
     if (warp_live && slot_at >= 0) {
-      const size_t slot = (size_t)slot_at * (size_t)p.slot_rows + (size_t)r;
-      float4* dst = reinterpret_cast<float4*>(p.ws_o + slot * C::D);
+      // four columns of a row are 16 bytes, the rows of four columns follow
+      // each other: a warp's store is one contiguous run (row-major, its 32
+      // rows would be 32 lines)
+      float4* dst = reinterpret_cast<float4*>(p.ws_o) + (size_t)slot_at * (size_t)(C::D / 4) * (size_t)p.slot_rows + r;
 #pragma unroll 1
       for (int c = 0; c < C::D; c += 32) {
         uint32_t o[32];
@@ -797,11 +828,14 @@ __device__ __forceinline__ void pg_softmax(const PagedCtx& t, const PagedParams&
         if (live) {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            dst[c / 4 + i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
-                                         __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+            dst[(c / 4 + i) * p.slot_rows] =
+                make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]), __uint_as_float(o[4 * i + 2]),
+                            __uint_as_float(o[4 * i + 3]));
         }
       }
-      if (live) *reinterpret_cast<float2*>(p.ws_ml + slot * 2) = make_float2(m_run, l_run);
+      if (live)
+        *reinterpret_cast<float2*>(p.ws_ml + ((size_t)slot_at * (size_t)p.slot_rows + r) * 2) =
+            make_float2(m_run, l_run);
     } else if (warp_live) {
       const bool empty = !(l_run > 0.f);
       const float inv_l = empty ? 0.f : 1.f / l_run;
@@ -851,7 +885,10 @@ __global__ void __launch_bounds__(192, PagedConfig<D>::CTAS_PER_SM)
   // has no piece.
   const int piece = (int)blockIdx.x;
   const PagedPlace place = find_place<C::THREADS>(p, piece, scan, blockIdx.x == 0);
-  if (place.seq < 0) return;
+  if (place.seq < 0) {
+    if (threadIdx.x == 0 && piece < p.ctas) p.merges[piece].first = -1;
+    return;
+  }
   PagedCtx t;
   t.bar0 = sbase + C::OFF_BAR;
   t.sQ = sbase + C::OFF_Q;
@@ -899,122 +936,100 @@ __global__ void __launch_bounds__(192, PagedConfig<D>::CTAS_PER_SM)
 // ---------------------------------------------------------------- the merge
 
 constexpr int kPagedMergeThreads = 256;
-constexpr int kPagedMergeRows = 32;   // rows of a block, eight at a time
+constexpr int kPagedMergeRows = 32;   // rows of a block
 
-// Block (m, y): the pair that piece m + 1's start falls inside, if that is the
-// pair's first such boundary; rows 32 y .. of it.  A warp takes a row, a lane D / 32
-// columns; fewer than eight rows share the eight warps, whose sums are joined
-// through shared memory in a fixed order.  The
-// place of the block on the line is found before the wait for the partials.
+// Block (m, y): rows 32 y .. of the pair that the start of piece m + 1 cuts
+// first.  Each warp takes every eighth run of four columns; its lanes are the
+// rows, or (fewer than 17 rows) rows x partials, whose sums are then joined by
+// shuffles in a fixed order.  The rows go out through shared memory, whole.
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kPagedMergeThreads) fa2_paged_merge_kernel(const PagedParams p) {
   constexpr int NW = kPagedMergeThreads / 32;
-  constexpr int E = D / 32;   // columns of a lane
-  __shared__ PagedScan scan;
-  __shared__ float part_o[NW][D];
-  __shared__ float part_ml[NW][2];
-  const int piece = (int)blockIdx.x + 1;
-  const PagedPlace place = find_place<kPagedMergeThreads>(p, piece, &scan, false);
-  grid_dependency_wait();   // the partials are complete and visible
-  if (place.share == 0 || place.seq < 0) return;
-  const PagedSeq s = paged_seq(p, place.seq, false);
-  const long long pos = piece * place.share;
-  int tile, h;
-  const long long x = place.at + pair_at(p, s, pos - place.at, tile, h);
-  if (x == pos || x / place.share != piece - 1) return;
-  const int w = s.width(p, tile);
-  const int last_piece = (int)((x + w - 1) / place.share);
-  const int q0 = tile * p.tile_tokens, last = min(q0 + p.tile_tokens, s.n_q) - 1;
-  const int rows = (last + 1 - q0) * p.group;
-  const int n = tile_walk(paged_mask(p, s.n_q, s.n_k), q0, last).n;
+  constexpr int E = D / 4 / NW;   // column runs of a warp
+  __shared__ uint2 stage[kPagedMergeRows][D / 4];
+  grid_dependency_wait();   // the partials and descriptions are complete and visible
+  const PagedMerge& mg = p.merges[blockIdx.x + 1];
+  const int first = mg.first;
+  const int r0 = (int)blockIdx.y * kPagedMergeRows;
+  if (first < 0 || r0 >= mg.rows) return;
+  const long long x = mg.x, share = mg.share;
+  const int w = mg.w, n = mg.n, h = mg.h, row0 = mg.row;
+  const int pieces = (int)(line_div(x + w - 1, share) - first) + 1;
+  const int here = min(mg.rows - r0, kPagedMergeRows);
   const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31;
-  // state of piece c's fragment of the pair: its slot, or none
-  auto slot_of = [&](int c) -> int {
-    const long long begin = c * place.share;
+  int width = 1;   // lanes of rows
+  while (width < here) width *= 2;
+  const int r = lane & (width - 1), sub = lane / width, subs = 32 / width;
+  // slot of the k-th piece's fragment of the pair, or -1
+  auto slot_of = [&](int k) -> int {
+    const long long begin = (first + k) * share;
     const int j0 = span_tile(p, begin > x ? begin - x : 0, n);
-    const long long y1 = begin + place.share - x;
+    const long long y1 = begin + share - x;
     const int j1 = y1 >= w ? n : span_tile(p, y1, n);
-    return j1 > j0 ? 2 * c + (begin <= x ? 1 : 0) : -1;
+    return j1 > j0 ? 2 * (first + k) + (begin <= x ? 1 : 0) : -1;
   };
-  const int r_end = min(rows, ((int)blockIdx.y + 1) * kPagedMergeRows);
-  for (int r0 = (int)blockIdx.y * kPagedMergeRows; r0 < r_end; r0 += NW) {
-    const int here = min(r_end - r0, NW);
-    const int wide = here <= 1 ? 1 : here <= 2 ? 2 : here <= 4 ? 4 : 8;   // rows side by side
-    const int team = NW / wide;                                           // warps of a row
-    const int my_row = warp % wide, member = warp / wide;
-    const int r = r0 + my_row;
-    float M = -INFINITY, L = 0.f, acc[E];
+  const float2* ml = reinterpret_cast<const float2*>(p.ws_ml) + r0 + r;
+  const float4* part = reinterpret_cast<const float4*>(p.ws_o) + (size_t)warp * p.slot_rows + r0 + r;
+  float M = -INFINITY;
+  if (r < here) {
+    for (int k = sub; k < pieces; k += subs) {
+      const int slot = slot_of(k);
+      if (slot >= 0) M = fmaxf(M, ml[(size_t)slot * p.slot_rows].x);
+    }
+  }
+  for (int o = width; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  float L = 0.f;
+  float4 acc[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
-    for (int c0 = piece - 1 + member; my_row < here && c0 <= last_piece; c0 += 32 * team) {
-      // a lane per partial: its (m, l)
-      const int c = c0 + lane * team;
-      const int slot = c <= last_piece ? slot_of(c) : -1;
-      float2 ml = make_float2(-INFINITY, 0.f);
-      if (slot >= 0) ml = *reinterpret_cast<const float2*>(p.ws_ml + ((size_t)slot * p.slot_rows + r) * 2);
-      float top = ml.x;
+  for (int e = 0; e < E; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (r < here && M != -INFINITY) {
+#pragma unroll 2
+    for (int k = sub; k < pieces; k += subs) {
+      const int slot = slot_of(k);
+      if (slot < 0) continue;
+      const float2 s = ml[(size_t)slot * p.slot_rows];
+      const float f = s.x == -INFINITY ? 0.f : ex2_approx(s.x - M);
+      L = fmaf(f, s.y, L);
+      const float4* src = part + (size_t)slot * (size_t)(D / 4) * (size_t)p.slot_rows;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const float M2 = fmaxf(M, top);
-      if (M2 == -INFINITY) continue;
-      const float f0 = M == -INFINITY ? 0.f : ex2_approx(M - M2);
-      M = M2;
-      const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
-      float l = f * ml.y;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-      L = L * f0 + l;
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] *= f0;
-      const int count = min(32, (last_piece - c0) / team + 1);
-#pragma unroll 8
-      for (int k = 0; k < count; ++k) {
-        const float fk = __shfl_sync(0xffffffffu, f, k);
-        const int at = __shfl_sync(0xffffffffu, slot, k);
-        if (at < 0) continue;
-        const float* src = p.ws_o + ((size_t)at * p.slot_rows + r) * D + lane * E;
-#pragma unroll
-        for (int e = 0; e < E; e += 2) {
-          const float2 v = *reinterpret_cast<const float2*>(src + e);
-          acc[e] = fmaf(fk, v.x, acc[e]);
-          acc[e + 1] = fmaf(fk, v.y, acc[e + 1]);
-        }
+      for (int e = 0; e < E; ++e) {
+        const float4 v = src[(size_t)(e * NW) * p.slot_rows];
+        acc[e].x = fmaf(f, v.x, acc[e].x);
+        acc[e].y = fmaf(f, v.y, acc[e].y);
+        acc[e].z = fmaf(f, v.z, acc[e].z);
+        acc[e].w = fmaf(f, v.w, acc[e].w);
       }
     }
-    if (team > 1) {   // the block's last rows only
+  }
+  for (int o = width; o < 32; o <<= 1) {
+    L += __shfl_xor_sync(0xffffffffu, L, o);
 #pragma unroll
-      for (int e = 0; e < E; ++e) part_o[warp][lane * E + e] = acc[e];
-      if (lane == 0) {
-        part_ml[warp][0] = M;
-        part_ml[warp][1] = L;
-      }
-      __syncthreads();
-      if (member > 0) return;
-      float top = M;
-      for (int k = 1; k < team; ++k) top = fmaxf(top, part_ml[warp + k * wide][0]);
-      const float f0 = M == -INFINITY ? 0.f : ex2_approx(M - top);
-      L *= f0;
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] *= f0;
-      M = top;
-      for (int k = 1; k < team; ++k) {
-        const float mk = part_ml[warp + k * wide][0];
-        if (mk == -INFINITY) continue;
-        const float fk = ex2_approx(mk - M);
-        L = fmaf(fk, part_ml[warp + k * wide][1], L);
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = fmaf(fk, part_o[warp + k * wide][lane * E + e], acc[e]);
-      }
+    for (int e = 0; e < E; ++e) {
+      acc[e].x += __shfl_xor_sync(0xffffffffu, acc[e].x, o);
+      acc[e].y += __shfl_xor_sync(0xffffffffu, acc[e].y, o);
+      acc[e].z += __shfl_xor_sync(0xffffffffu, acc[e].z, o);
+      acc[e].w += __shfl_xor_sync(0xffffffffu, acc[e].w, o);
     }
-    if (my_row >= here) continue;
-    const bool empty = !(L > 0.f);
-    const float inv_l = empty ? 0.f : 1.f / L;
-    const int tok = r / p.group, head = h * p.group + r - tok * p.group;
-    uint32_t* dst = reinterpret_cast<uint32_t*>(paged_o_row(p, s.row0 + q0 + tok, head)) + lane * (E / 2);
+  }
+  const bool empty = !(L > 0.f);
+  const float inv_l = empty ? 0.f : 1.f / L;
+  if (sub == 0 && r < here) {
 #pragma unroll
-    for (int e = 0; e < E; e += 2) dst[e / 2] = empty ? 0u : pack2<BF16>(acc[e] * inv_l, acc[e + 1] * inv_l);
-    if (lane == 0)
-      p.lse[(long long)head * p.lse_hs + s.row0 + q0 + tok] = empty ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+    for (int e = 0; e < E; ++e)
+      stage[r][warp + e * NW] = empty ? make_uint2(0u, 0u)
+                                      : make_uint2(pack2<BF16>(acc[e].x * inv_l, acc[e].y * inv_l),
+                                                   pack2<BF16>(acc[e].z * inv_l, acc[e].w * inv_l));
+    if (warp == 0) {
+      const int at = r0 + r, tok = at / p.group;
+      p.lse[(long long)(h * p.group + at - tok * p.group) * p.lse_hs + row0 + tok] =
+          empty ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+    }
+  }
+  __syncthreads();
+  for (int i = (int)threadIdx.x; i < here * (D / 8); i += kPagedMergeThreads) {
+    const int at = r0 + i / (D / 8), c = i % (D / 8), tok = at / p.group;
+    reinterpret_cast<uint4*>(paged_o_row(p, row0 + tok, h * p.group + at - tok * p.group))[c] =
+        reinterpret_cast<const uint4*>(stage[at - r0])[c];
   }
 }
 

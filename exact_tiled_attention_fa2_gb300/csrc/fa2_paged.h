@@ -30,6 +30,8 @@ struct PagedSide {
   int extent;   // ratio > 0: the last coordinate's extent (out of range: zeros)
 };
 
+constexpr int kPagedMergeBytes = 40;   // sizeof(PagedMerge)
+
 struct PagedParams {
   void* o;                // 16-bit output [total_q][heads_q][d] by strides
   float* lse;             // [heads_q][total_q], head stride lse_hs
@@ -53,8 +55,9 @@ struct PagedParams {
   int overhead;           // a pair's fixed cost on the line, in keys
   int min_share;          // keys of a piece at least
   int slot_rows;          // rows of a Q load and of a partial state: group x tokens
-  float* ws_o;            // [2 * ctas][slot_rows][d] partial O~
+  float* ws_o;            // [2 * ctas][d / 4][slot_rows][4] partial O~
   float* ws_ml;           // [2 * ctas][slot_rows][2] partial (m, l), exp2 domain
+  struct PagedMerge* merges;   // [ctas] pairs to merge, kPagedMergeBytes each
 };
 
 struct PagedLaunchArgs {

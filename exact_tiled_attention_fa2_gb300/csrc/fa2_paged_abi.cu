@@ -20,7 +20,8 @@ constexpr long long kMaxStride = 1ll << 39;   // elements: 16-bit strides stay b
 // nor the result depends on the device.
 constexpr int paged_ctas(int d) { return d == 256 ? 152 : 304; }
 // A pair's fixed cost (Q, the first products, the epilogue) in keys, and the
-// shortest piece worth a CTA and a share of the merge.
+// shortest piece worth a CTA: 256 keys, or (many rows) the keys whose K and V
+// are as many bytes as a partial's write and read four times over.
 constexpr int kPagedOverhead = 128;
 constexpr int kPagedMinShare = 256;
 constexpr long long kPagedMaxKeys = (1ll << 31) - 4096;   // keys of a sequence, rounded up to tiles, stay below 2^31
@@ -90,7 +91,7 @@ int check_cache(const fa2_paged_cache& c, CacheView& k, CacheView& v) {
 struct PagedShape {
   int group, tile_tokens, box_tokens, max_q;
   int ctas, pair_ctas;
-  size_t ws_o_bytes, ws_ml_bytes;
+  size_t ws_o_bytes, ws_ml_bytes, ws_bytes;   // ws_bytes: all, with the pairs to merge
 };
 
 // Sizes of a paged forward call that follow from what the host knows.
@@ -118,6 +119,7 @@ int paged_shape(const fa2_paged_params& a, PagedShape& s) {
   const size_t rows = 2 * (size_t)s.ctas * (size_t)(s.group * s.box_tokens);
   s.ws_o_bytes = align256(rows * (size_t)c.head_dim * 4);
   s.ws_ml_bytes = align256(rows * 2 * 4);
+  s.ws_bytes = s.ws_o_bytes + s.ws_ml_bytes + align256((size_t)s.ctas * kPagedMergeBytes);
   return FA2_OK;
 }
 
@@ -169,7 +171,7 @@ int paged_forward(const fa2_paged_params& a, void* workspace, size_t workspace_b
   if (misaligned(a.q, 16) || misaligned(a.o, 16) || misaligned(a.lse, 4) || misaligned(a.block_table, 4) ||
       misaligned(a.cu_seqlens_q, 4) || misaligned(a.seqlens_k, 4) || misaligned(workspace, 256))
     return FA2_ERR_MISALIGNED;
-  if (workspace_bytes < s.ws_o_bytes + s.ws_ml_bytes) return FA2_ERR_INVALID_ARG;
+  if (workspace_bytes < s.ws_bytes) return FA2_ERR_INVALID_ARG;
   const long long qd[2] = {a.total_q, a.heads};
   const long long qs[2] = {(long long)a.q_strides[0], (long long)a.q_strides[1]};
   const long long os[2] = {(long long)a.o_strides[0], (long long)a.o_strides[1]};
@@ -182,7 +184,7 @@ int paged_forward(const fa2_paged_params& a, void* workspace, size_t workspace_b
   const long long ld[1] = {a.heads}, ls[1] = {(long long)a.lse_stride};
   if (a.heads > 1 && (ls[0] < a.total_q || ls[0] >= kMaxStride)) return FA2_ERR_INVALID_ARG;
   const Range out[3] = {extent(a.o, qd, os, c.head_dim, 2), extent(a.lse, ld, ls, a.total_q, 4),
-                        range(workspace, s.ws_o_bytes + s.ws_ml_bytes)};
+                        range(workspace, s.ws_bytes)};
   const Range in[6] = {extent(a.q, qd, qs, c.head_dim, 2), kc.bytes, vc.bytes,
                        extent(a.block_table, td, ts, a.max_pages, 4),
                        range(a.cu_seqlens_q, ((size_t)a.batch + 1) * 4), range(a.seqlens_k, (size_t)a.batch * 4)};
@@ -238,13 +240,14 @@ int paged_forward(const fa2_paged_params& a, void* workspace, size_t workspace_b
   const float scale_log2 = a.scale * 1.4426950408889634f;
   p.scale_log2_mag = std::fmax(std::fabs(scale_log2), FLT_MIN);
   p.qk_negate = scale_log2 < 0.f ? 1u << 13 : 0u;   // the negate-A bit of the S product's descriptor
+  p.slot_rows = s.group * s.box_tokens;
+  p.overhead = kPagedOverhead;
   p.ctas = s.ctas;
   p.pair_ctas = s.pair_ctas;
-  p.overhead = kPagedOverhead;
-  p.min_share = kPagedMinShare;
-  p.slot_rows = s.group * s.box_tokens;
+  p.min_share = kPagedMinShare > 8 * p.slot_rows ? kPagedMinShare : 8 * p.slot_rows;
   p.ws_o = static_cast<float*>(workspace);
   p.ws_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + s.ws_o_bytes);
+  p.merges = reinterpret_cast<PagedMerge*>(static_cast<uint8_t*>(workspace) + s.ws_o_bytes + s.ws_ml_bytes);
   la.band = a.window_left >= 0 || a.prefix_len > 0;
   la.stream = stream;
   int e = 0;
@@ -355,7 +358,7 @@ extern "C" size_t fa2_paged_fwd_workspace_bytes(const fa2_paged_params* params) 
   if (!params) return 0;
   PagedShape s;
   if (paged_shape(*params, s)) return 0;
-  return s.ws_o_bytes + s.ws_ml_bytes;
+  return s.ws_bytes;
 }
 
 extern "C" int fa2_paged_fwd(const fa2_paged_params* params, void* workspace, size_t workspace_bytes, void* stream) {
