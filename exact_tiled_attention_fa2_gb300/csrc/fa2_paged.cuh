@@ -52,23 +52,24 @@ namespace fa2 {
 // fragments f of the CTA (the others).
 enum : int {
   PG_Q = 0,        // + f & 1: the fragment's description and Q are in shared memory
-  PG_QEMPTY = 2,   // the fragment's last S product is done with Q
-  PG_KFULL = 3,    // + stage
-  PG_KEMPTY = 5,   // + stage
-  PG_VFULL = 7,    // + stage
-  PG_VEMPTY = 9,   // + stage
-  PG_S = 11,       // + buffer
-  PG_P = 13,       // + buffer (four softmax warps)
-  PG_O = 15,       // after every PV product
-  PG_OLAST = 16,   // after a fragment's last PV product
-  PG_ODONE = 17,   // + f & 1: the softmax warps are done with O~ and the description
-  PG_EXIT = 19,
-  PG_BARS = 20,
+  PG_QEMPTY = 2,   // + f & 1: the fragment's last S product is done with Q
+  PG_S = 4,        // + buffer
+  PG_P = 6,        // + buffer (four softmax warps)
+  PG_ODONE = 8,    // + f & 1: the softmax warps are done with O~ and the description
+  PG_O = 10,       // after every PV product
+  PG_OLAST = 11,   // after a fragment's last PV product
+  PG_EXIT = 12,
+  PG_KFULL = 13,   // + stage
+  PG_KEMPTY = 17,  // + stage
+  PG_VFULL = 21,   // + stage
+  PG_VEMPTY = 25,  // + stage
+  PG_BARS = 29,
 };
 
 // Everything the softmax warps and the MMA thread need of a fragment: written
-// by the TMA warp, two in flight.
+// by the TMA warp, in a ring of four.
 struct PagedFrag {
+  const int* table;   // the sequence's block-table row
   int n;           // key tiles (0: the pair has no visible key; -1: no more fragments)
   int j0;          // first of them, as a visited index of the pair
   int row;         // first token's row of q / o / lse
@@ -76,7 +77,7 @@ struct PagedFrag {
   int rows;        // live rows: group x tokens
   int h;           // K/V head
   int slot;        // partial slot, or -1: write O and L
-  int few_keys;    // N_k <= 2 key tiles: every bf16 P is split
+  int split;       // every bf16 P is split, not the masked tiles' alone
   TileMask tm;     // key tiles every row sees, by index from j0
   KeyMask km;
   int npre, skip;  // visited index j is key tile j + (j >= npre ? skip : 0)
@@ -84,13 +85,15 @@ struct PagedFrag {
   __device__ __forceinline__ int tile(int j) const { return j + (j >= npre ? skip : 0); }
 };
 
-template <int D_>
+// WIDE: query tiles of more than 64 rows (p.slot_rows).
+template <int D_, bool WIDE_>
 struct PagedConfig {
   static constexpr int D = D_;
+  static constexpr bool WIDE = WIDE_;
   static constexpr int BR = kPagedTileRows;
   static constexpr int BC = kPagedKeyTile;
-  static constexpr int KSTAGES = 2;
-  static constexpr int VSTAGES = 2;
+  static constexpr int KSTAGES = D == 64 ? 4 : 2;
+  static constexpr int VSTAGES = D == 64 ? 4 : 2;
   static constexpr int THREADS = 192;
   static constexpr int MMA_WARP = 4;
   static constexpr int TMA_WARP = 5;
@@ -102,15 +105,15 @@ struct PagedConfig {
   static constexpr uint32_t OFF_K = OFF_Q + Q_BYTES;
   static constexpr uint32_t OFF_V = OFF_K + KSTAGES * KV_BYTES;
   static constexpr uint32_t OFF_BAR = OFF_V + VSTAGES * KV_BYTES;
-  static constexpr uint32_t OFF_MISC = OFF_BAR + PG_BARS * 8;   // TMEM address, abort flag
+  static constexpr uint32_t OFF_MISC = OFF_BAR + (PG_BARS + 1) / 2 * 16;   // TMEM address, abort flag
   static constexpr uint32_t OFF_FRAG = OFF_MISC + 16;
-  static constexpr uint32_t OFF_SCAN = OFF_FRAG + 256;
-  static constexpr uint32_t SMEM_BYTES = OFF_SCAN + 256 + 1024;
+  static constexpr uint32_t OFF_SCAN = OFF_FRAG + 512;
+  static constexpr uint32_t SMEM_BYTES = OFF_SCAN + 320 + 1024;
   static constexpr uint32_t TMEM_S = 0;   // + 64 * buffer
   static constexpr uint32_t TMEM_O = 128;
   static constexpr uint32_t TMEM_COLS = D == 256 ? 512 : 256;
   static constexpr int CTAS_PER_SM = D == 256 ? 1 : 2;
-  static_assert(2 * sizeof(PagedFrag) <= 256, "fragment descriptions");
+  static_assert(4 * sizeof(PagedFrag) <= 512, "fragment descriptions");
   static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
   static_assert(CTAS_PER_SM * (SMEM_BYTES + 1024) <= 233472, "shared memory per SM");
 };
@@ -182,11 +185,10 @@ struct PagedSeq {
   }
 };
 
-// Sequence i; no tiles (and the bad-offsets bit, if `report`) when its row
-// offsets or its length are out of range.
-__device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int i, bool report) {
+// The sequence of query rows [a, b) and k keys; no tiles (and the bad-offsets
+// bit, if `report`) when these are out of range.
+static __device__ __noinline__ PagedSeq paged_seq(const PagedParams& p, int a, int b, int k, bool report) {
   PagedSeq s;
-  const int a = __ldg(p.cu_q + i), b = __ldg(p.cu_q + i + 1), k = __ldg(p.lens_k + i);
   s.row0 = a;
   s.n_q = b - a;
   s.n_k = k;
@@ -219,12 +221,17 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int i, bool 
   return s;
 }
 
-// Where a CTA (or a merge block) starts, and the pieces' size.
+__device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int i, bool report) {
+  return paged_seq(p, __ldg(p.cu_q + i), __ldg(p.cu_q + i + 1), __ldg(p.lens_k + i), report);
+}
+
+// Where a CTA starts, and the pieces' size.
 struct PagedPlace {
   long long at;      // the sequence's start on the line
   long long share;   // keys of a piece; 0: one pair per CTA
   long long total;   // the line's length
-  int seq;           // the sequence holding the position, or -1: past the end
+  PagedSeq s;        // the sequence that holds the position
+  int seq;           // its index, or -1: past the end
   int rank;          // one pair per CTA: the pair's index in its sequence
 };
 
@@ -253,7 +260,7 @@ __device__ __forceinline__ PagedPlace find_place(const PagedParams& p, int piece
     if (s.tiles > 1) chunks += x;
   }
   long long a = span, b = pairs, c = chunks;
-#pragma unroll
+#pragma unroll 1
   for (int o = 1; o < 32; o <<= 1) {
     const long long va = __shfl_up_sync(0xffffffffu, a, o), vb = __shfl_up_sync(0xffffffffu, b, o),
                     vc = __shfl_up_sync(0xffffffffu, c, o);
@@ -273,7 +280,7 @@ __device__ __forceinline__ PagedPlace find_place(const PagedParams& p, int piece
   a -= span;
   b -= pairs;
   long long total = 0, all_pairs = 0, all_chunks = 0;
-#pragma unroll
+#pragma unroll 1
   for (int j = 0; j < NW; ++j) {
     if (j == w) {
       a += total;
@@ -295,6 +302,7 @@ __device__ __forceinline__ PagedPlace find_place(const PagedParams& p, int piece
       const long long sx = s.span(p), sn = (long long)s.tiles * p.heads_kv;
       if (whole ? pos < n + sn : pos < x + sx) {
         sh->place.at = x;
+        sh->place.s = s;
         sh->place.seq = i;
         sh->place.rank = whole ? (int)(pos - n) : 0;
         break;
@@ -346,105 +354,169 @@ struct PagedMerge {
 static_assert(sizeof(PagedMerge) == kPagedMergeBytes, "merge description");
 
 // Walks the fragments of one CTA's piece; every lane of the TMA warp in step.
+// What the pairs of one query tile share is worked out once, and the next
+// sequence's lengths are read a sequence ahead.
+template <bool BAND>
 struct FragWalk {
   PagedSeq s;
-  long long x, end;   // the pair's start on the line, the piece's end
-  long long share;
+  PagedFrag base;     // the current query tile's facts, for all of its key tiles
+  int tiles_n;        // its key tiles
+  int w;              // its pairs' span
+  const int* table;   // the sequence's block-table row
+  long long x, begin, end;   // the pair's start on the line; the piece
   int cta, seq, tile, h;
-  bool more;
+  int next_a, next_b, next_k;   // sequence seq + 1
+  bool more, one;     // one: a single pair, whole
+  PagedMerge merge;   // the pair cut by the piece's start
+
+  __device__ __forceinline__ void read_ahead(const PagedParams& p) {
+    if (seq + 1 < p.batch) {
+      next_a = __ldg(p.cu_q + seq + 1);
+      next_b = __ldg(p.cu_q + seq + 2);
+      next_k = __ldg(p.lens_k + seq + 1);
+    }
+  }
+
+  __device__ void start_tile(const PagedParams& p) {
+    const int q0 = tile * p.tile_tokens, last = min(q0 + p.tile_tokens, s.n_q) - 1;
+    base.km = paged_mask(p, s.n_q, s.n_k);
+    const TileWalk walk = tile_walk(base.km, q0, last);
+    tiles_n = walk.n;
+    w = s.width(p, tile);
+    base.row = s.row0 + q0;
+    base.q0 = q0;
+    base.rows = (last + 1 - q0) * p.group;
+    // few keys, or a tile of few rows, where the second PV product hides behind
+    // reading the keys and the masked tiles would otherwise run code that the
+    // others have not brought in (measured: 256 requests of 1..1000 keys, d = 128
+    // bf16, 172 us with the masked tiles alone split)
+    base.split = s.n_k <= 2 * kPagedKeyTile || p.slot_rows <= kPagedTileRows / 2;
+    base.npre = walk.npre;
+    base.skip = walk.skip;
+    base.lo = walk.lo;
+    base.end = walk.end;
+    base.tm = tile_mask<BAND>(base.km, q0, last, kPagedKeyTile);
+    if (walk.npre == 0) base.tm.pre -= walk.skip;
+    base.tm.lo -= walk.skip;
+    base.tm.hi -= walk.skip;
+  }
 
   __device__ __forceinline__ void start(const PagedParams& p, const PagedPlace& pl, int piece) {
     cta = piece;
-    share = pl.share;
     seq = pl.seq;
-    s = paged_seq(p, seq, false);
+    s = pl.s;
     more = true;
-    if (share == 0) {   // one pair: the query tiles from the last (the most keys) to the first
+    one = pl.share == 0;
+    merge.first = -1;
+    table = p.table + (long long)seq * p.table_stride;
+    if (one) {   // the query tiles from the last (the most keys) to the first
       h = pl.rank % p.heads_kv;
       tile = s.tiles - 1 - pl.rank / p.heads_kv;
-      x = 0;
-      end = s.width(p, tile);
-    } else {
-      const long long pos = piece * share;
-      end = min(pos + share, pl.total);
-      x = pl.at + pair_at(p, s, pos - pl.at, tile, h);
+      x = begin = 0;
+      start_tile(p);
+      end = w;
+      return;
+    }
+    begin = piece * pl.share;
+    end = min(begin + pl.share, pl.total);
+    x = pl.at + pair_at(p, s, begin - pl.at, tile, h);
+    start_tile(p);
+    read_ahead(p);
+    if (begin > x) {
+      merge.first = x >= begin - pl.share ? piece - 1 : -1;
+      merge.x = x;
+      merge.share = pl.share;
+      merge.w = w;
+      merge.n = tiles_n;
+      merge.row = base.row;
+      merge.rows = base.rows;
+      merge.h = h;
     }
   }
 
-  // The next fragment and its block-table row; false when the piece is done.
-  template <bool BAND>
-  __device__ __forceinline__ bool next(const PagedParams& p, PagedFrag& f, const int*& table, PagedMerge& merge) {
-    while (more) {
-      const int w = s.width(p, tile);
-      const long long begin = share == 0 ? 0 : cta * share;
-      const long long y0 = begin > x ? begin - x : 0, y1 = min(end - x, (long long)w);
-      const bool whole = y0 == 0 && y1 == w;
-      const int q0 = tile * p.tile_tokens, last = min(q0 + p.tile_tokens, s.n_q) - 1;
-      f.km = paged_mask(p, s.n_q, s.n_k);
-      const TileWalk walk = tile_walk(f.km, q0, last);
-      f.j0 = span_tile(p, y0, walk.n);
-      f.n = (whole ? walk.n : span_tile(p, y1, walk.n)) - f.j0;
-      f.row = s.row0 + q0;
-      f.q0 = q0;
-      f.rows = (last + 1 - q0) * p.group;
-      f.h = h;
-      f.slot = whole ? -1 : 2 * cta + (y0 == 0 ? 1 : 0);
-      f.few_keys = s.n_k <= 2 * kPagedKeyTile;
-      f.npre = walk.npre;
-      f.skip = walk.skip;
-      f.lo = walk.lo;
-      f.end = walk.end;
-      f.tm = tile_mask<BAND>(f.km, q0, last, kPagedKeyTile);
-      if (walk.npre == 0) f.tm.pre -= walk.skip;
-      f.tm.lo -= walk.skip;
-      f.tm.hi -= walk.skip;
-      f.tm = f.tm.from(f.j0);
-      if (y0 > 0) {   // the piece starts inside this pair
-        merge.first = line_div(x, share) == cta - 1 ? cta - 1 : -1;
-        merge.x = x;
-        merge.share = share;
-        merge.w = w;
-        merge.n = walk.n;
-        merge.row = f.row;
-        merge.rows = f.rows;
-        merge.h = h;
-      }
-      table = p.table + (long long)seq * p.table_stride;
-      // on to the next pair
-      x += w;
-      if (share == 0 || x >= end) {
-        more = false;
-      } else if (++h == p.heads_kv) {
-        h = 0;
-        if (++tile == s.tiles) {
-          tile = 0;
-          do {
-            if (++seq >= p.batch) {
-              more = false;
-              break;
-            }
-            s = paged_seq(p, seq, false);
-          } while (s.tiles == 0);
-        }
-      }
-      if (f.n > 0 || whole) return true;   // else: nothing of this pair falls here (its merge sees the same)
-    }
-    return false;
-  }
 };
+
+// The next fragment, to shared memory; false when the piece is done.  Out of
+// line (as the waits' slow path below): once per fragment.
+template <bool BAND>
+static __device__ __noinline__ bool next_fragment(FragWalk<BAND>& k, const PagedParams& p, PagedFrag* dst, int lane) {
+  while (k.more) {
+    const bool from_start = k.begin <= k.x, to_end = k.end - k.x >= k.w, whole = from_start && to_end;
+    const int j0 = from_start ? 0 : span_tile(p, k.begin - k.x, k.tiles_n);
+    const int n = (to_end ? k.tiles_n : span_tile(p, k.end - k.x, k.tiles_n)) - j0;
+    const bool some = n > 0 || whole;   // else: nothing of this pair falls here (its merge sees the same)
+    if (some && lane == 0) {
+      *dst = k.base;
+      dst->table = k.table;
+      dst->h = k.h;
+      dst->j0 = j0;
+      dst->n = n;
+      dst->slot = whole ? -1 : 2 * k.cta + (from_start ? 1 : 0);
+      dst->tm = k.base.tm.from(j0);
+    }
+    // on to the next pair
+    k.x += k.w;
+    if (k.one || k.x >= k.end) {
+      k.more = false;
+    } else if (++k.h == p.heads_kv) {
+      k.h = 0;
+      if (++k.tile == k.s.tiles) {
+        k.tile = 0;
+        do {
+          if (++k.seq >= p.batch) {
+            k.more = false;
+            break;
+          }
+          k.table += p.table_stride;
+          k.s = paged_seq(p, k.next_a, k.next_b, k.next_k, false);
+          k.read_ahead(p);
+        } while (k.s.tiles == 0);
+      }
+      if (k.more) k.start_tile(p);
+    }
+    if (some) {
+      __syncwarp();
+      return true;
+    }
+  }
+  return false;
+}
 
 // ---------------------------------------------------------------- the warps' roles
 
+// Waits as wait_or_abort.  With few rows (C::WIDE false) all but the first look
+// is out of line: such a kernel runs little of its code often, and what each of
+// the many waits carries along is fetched from L2 again and again (256 requests
+// of 1..1000 keys, d = 128: 28 % of the instruction cache's requests missed).
+// With many rows the call itself costs more (prompt chunk of 2048 over 16384
+// keys: 469 against 426 us).
+static __device__ __noinline__ bool paged_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                                    uint32_t* status, uint32_t site) {
+  return wait_or_abort(bar, parity, abort_flag, status, site);
+}
+template <bool WIDE>
+__device__ __forceinline__ bool paged_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint32_t* status,
+                                           uint32_t site) {
+  if constexpr (WIDE)
+    return wait_or_abort(bar, parity, abort_flag, status, site);
+  else
+    return mbar_try_wait(bar, parity) || paged_wait_slow(bar, parity, abort_flag, status, site);
+}
+static __device__ __noinline__ void paged_drain(uint32_t bar, uint32_t parity, uint32_t* status) {
+  wait_drain(bar, parity, status);
+}
+
+template <class C>
 struct PagedCtx {
   uint32_t bar0, sQ, sK, sV, tmem;
   volatile int* abort_flag;
   uint32_t* status;
-  PagedFrag* frags;   // two, by fragment parity
+  PagedFrag* frags;   // four
   __device__ __forceinline__ uint32_t bar(int i) const { return bar0 + 8u * (uint32_t)i; }
   // One warp waits through lane 0 (the others only need its answer).
   __device__ __forceinline__ bool warp_wait(int i, int phase, uint32_t site, int lane) const {
     bool ok = true;
-    if (lane == 0) ok = wait_or_abort(bar(i), (uint32_t)phase & 1, abort_flag, status, site);
+    if (lane == 0) ok = paged_wait<C::WIDE>(bar(i), (uint32_t)phase & 1, abort_flag, status, site);
     return __all_sync(0xffffffffu, ok);
   }
 };
@@ -458,241 +530,262 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
-// One lane's box of one tensor: coordinates 1, 3 and 4, or none (c4 = -1).
-struct BoxAt {
-  int c1, c3, c4;
-};
-
-// The TMA warp.  Lane l holds box l of a key tile (rows l * box_rows ..).
+// The TMA warp: walks the piece's fragments, publishes them (with Q) and loads
+// their key tiles, K_0 K_1 V_0 K_2 V_1 .. (a K stage frees at S(j), just before
+// PV(j - 1) frees a V stage).  The boxes of four tiles are worked out at once,
+// lane 8 q + b holding box b (rows b * box_rows ..) of tile q, and their
+// block-table entries read four tiles ahead (the next fragment's first four
+// while this one is loaded): with two stages, the time from a free stage to its
+// next load is part of the tile loop's period, and between the two stand only a
+// wait and the issue.
 template <class C, bool BAND>
-__device__ __forceinline__ void pg_producer(const PagedCtx& t, const PagedParams& p, const CUtensorMap* tm_q,
-                                            const CUtensorMap* tm_k, const CUtensorMap* tm_v, const PagedPlace& place,
-                                            int piece, int lane) {
-  const int ps = p.page_size;
-  const int box_rows = p.box_rows;
-  const int boxes = C::BC / box_rows;
-  FragWalk walk;
+__device__ __forceinline__ void pg_load(const PagedCtx<C>& t, const PagedParams& p, const CUtensorMap* tm_q,
+                                        const CUtensorMap* tm_k, const CUtensorMap* tm_v, const PagedPlace& place,
+                                        int piece, int lane) {
+  FragWalk<BAND> walk;
   walk.start(p, place, piece);
-  PagedFrag f;
-  const int* table = nullptr;
-  bool bad = false;
-  // The page of this lane's box of the fragment's tile j (-1: no row of the
-  // query tile sees a key of it; num_pages: out of range, to be read as
-  // zeros), and the box's first row within the page.
-  auto fetch = [&](int j, int& row) -> int {
-    if (j >= f.n || lane >= boxes) return -1;
-    const int k0 = f.tile(f.j0 + j) * C::BC + lane * box_rows, k1 = k0 + box_rows;   // the box's keys
-    if (!(k0 < f.km.pre_end || (k0 < f.end && k1 > f.lo))) return -1;
-    const int at = k0 / ps;
-    row = k0 - at * ps;
-    const int page = __ldg(table + at);
-    if (page < 0 || page >= p.num_pages) {
-      bad = true;
-      return p.num_pages;
-    }
-    return page;
+  if (lane == 0 && piece < p.ctas) p.merges[piece] = walk.merge;   // (one pair per CTA: piece may be larger)
+  // Q loads of at most 64 rows leave room for the next fragment's in the other
+  // half of the rows (the products then read 64 rows of whatever follows, which
+  // reach no live row).
+  constexpr bool two_q = !C::WIDE;
+  const int my_tile = lane >> 3, my_box = lane & 7;
+  const bool has_box = my_box < C::BC / p.box_rows;
+  int walked = 0, published = 0;   // fragments
+  bool ok = true, bad = false;
+  // Four tiles' boxes: this lane's page and first row within it (-1: no box,
+  // or no row of the query tile sees a key of it).
+  struct Ahead {
+    int page, row;
   };
-  auto load = [&](uint32_t s_tile, uint32_t bar, const CUtensorMap* tm, const PagedSide& side, int page, int row) {
-    const unsigned n = __popc(__ballot_sync(0xffffffffu, page >= 0));
-    if (lane == 0) mbar_arrive_expect_tx(bar, n * (uint32_t)box_rows * (uint32_t)(C::D * 2));
-    __syncwarp();
-    if (page >= 0) {
-      const uint32_t dst = s_tile + (uint32_t)(lane * box_rows) * (uint32_t)(C::D * 2);
-      // merged (page, head) coordinate, or (head, page) apart; num_pages lies outside either map
-      if (side.ratio > 0)
-        tma_load_5d(dst, tm, 0, 0, 0, row >> 3, page < p.num_pages ? page * side.ratio + f.h : side.extent, bar);
-      else
-        tma_load_5d(dst, tm, 0, row, 0, f.h, page, bar);
-    }
-    __syncwarp();
+  auto fetch = [&](const PagedFrag* f, int j4) -> Ahead {
+    Ahead x;
+    const int k0 = f->tile(f->j0 + j4 + my_tile) * C::BC + my_box * p.box_rows;   // the box's keys [k0, k0 + box_rows)
+    const int at = (int)((__umulhi((unsigned)k0, p.page_magic) + (unsigned)k0) >> p.page_shift);   // k0 / page_size
+    const bool need = j4 + my_tile < f->n && has_box &&
+                      (k0 < f->km.pre_end || (k0 < f->end && k0 + p.box_rows > f->lo));
+    x.page = need ? __ldg(f->table + at) : 0;
+    x.row = need ? k0 - at * p.page_size : -1;
+    return x;
   };
-  bool ok = true;
-  int g = 0;     // key tiles loaded (K)
-  int gv = 0;    // (V)
-  int nf = 0;    // fragments published
-  PagedMerge merge;
-  merge.first = -1;
-  bool have = walk.next<BAND>(p, f, table, merge);
-  if (lane == 0 && piece < p.ctas) p.merges[piece] = merge;   // (one pair per CTA: piece may be larger)
-  int r0 = 0, r1 = 0, r2 = 0;
-  int p0 = -1, p1 = -1, p2 = -1;
-  if (have) {
-    p0 = fetch(0, r0);
-    p1 = fetch(1, r1);
-    p2 = fetch(2, r2);
-  }
-  // The fragment's description (and Q) to the other warps, once its slot's and
-  // Q's last users are done.
-  auto publish = [&](int n) -> bool {
-    if (nf >= 1 && !t.warp_wait(PG_QEMPTY, nf - 1, kSiteProducerEmpty, lane)) return false;
-    if (nf >= 2 && !t.warp_wait(PG_ODONE + (nf & 1), (nf - 2) >> 1, kSiteProducerEmpty, lane)) return false;
+  Ahead next4;    // the fragment's next four tiles
+  Ahead first4;   // the next fragment's first four
+  // The next fragment into its slot (whose last user, four before, is done:
+  // publishing the one before waited for a later one).
+  auto look_ahead = [&]() {
+    PagedFrag* f = t.frags + (walked & 3);
+    if (!next_fragment(walk, p, f, lane)) return;
+    first4 = fetch(f, 0);
+    ++walked;
+  };
+  // The next fragment's description (and Q), or the end of them, to the other
+  // warps, once the last users of its barriers and of Q are done.
+  auto publish = [&]() {
+    const int nf = published, before = two_q ? nf - 2 : nf - 1;   // `before` used this Q
+    ok = (before < 0 || t.warp_wait(PG_QEMPTY + (before & 1), before >> 1, kSiteProducerEmpty, lane)) &&
+         (nf < 2 || t.warp_wait(PG_ODONE + (nf & 1), (nf - 2) >> 1, kSiteProducerEmpty, lane));
+    if (!ok) return;
     if (lane == 0) {
+      PagedFrag* f = t.frags + (nf & 3);
+      if (nf == walked) f->n = -1;
       const uint32_t bar = t.bar(PG_Q + (nf & 1));
-      PagedFrag* dst = t.frags + (nf & 1);
-      *dst = f;
-      dst->n = n;
-      if (n > 0) {
+      if (f->n > 0) {
+        const uint32_t sQ = t.sQ + (two_q && (nf & 1) ? C::BR / 2 * 128u : 0u);
         mbar_arrive_expect_tx(bar, (uint32_t)C::BLOCKS * (uint32_t)p.slot_rows * 128u);
+#pragma unroll 1
         for (int kb = 0; kb < C::BLOCKS; ++kb)
-          tma_load_4d(t.sQ + kb * (C::BR * 128), tm_q, kb * 64, 0, f.h, f.row, bar);
+          tma_load_4d(sQ + kb * (C::BR * 128), tm_q, kb * 64, 0, f->h, f->row, bar);
       } else {
         mbar_arrive(bar);
       }
     }
-    ++nf;
+    ++published;
     __syncwarp();
-    return true;
   };
-  while (ok && have) {
-    if (f.n == 0) {
-      ok = publish(0);
+  // Coordinates of this lane's box in one tensor: merged (page, head), or head
+  // and page apart; an out-of-range page is read as zeros from outside the map.
+  struct At {
+    int c1, c3, c4;
+  };
+  auto place_box = [&](const Ahead& x, const PagedSide& side, int h) -> At {
+    const bool off = x.page < 0 || x.page >= p.num_pages;
+    At c;
+    if (side.ratio > 0) {
+      c.c1 = 0;
+      c.c3 = x.row >> 3;
+      c.c4 = off ? side.extent : x.page * side.ratio + h;
     } else {
-      int pv = -1, rv = 0;   // tile j - 1's pages
-      for (int j = 0; j < f.n; ++j) {
-        int r3 = 0;
-        const int p3 = fetch(j + 3, r3);
-        const int s = g % C::KSTAGES;
-        if (g >= C::KSTAGES && !t.warp_wait(PG_KEMPTY + s, g / C::KSTAGES - 1, kSiteProducerEmpty, lane)) {
-          ok = false;
-          break;
-        }
-        load(t.sK + s * C::KV_BYTES, t.bar(PG_KFULL + s), tm_k, p.k_side, p0, r0);
-        ++g;
-        if (j == 0) {
-          if (!(ok = publish(f.n))) break;
-        } else {
-          const int sv = gv % C::VSTAGES;
-          if (gv >= C::VSTAGES && !t.warp_wait(PG_VEMPTY + sv, gv / C::VSTAGES - 1, kSiteProducerEmpty, lane)) {
-            ok = false;
-            break;
-          }
-          load(t.sV + sv * C::KV_BYTES, t.bar(PG_VFULL + sv), tm_v, p.v_side, pv, rv);
-          ++gv;
-        }
-        pv = p0;
-        rv = r0;
-        p0 = p1;
-        r0 = r1;
-        p1 = p2;
-        r1 = r2;
-        p2 = p3;
-        r2 = r3;
-      }
+      c.c1 = x.row;
+      c.c3 = h;
+      c.c4 = off ? p.num_pages : x.page;
+    }
+    if (x.row >= 0 && off) bad = true;
+    return c;
+  };
+  const uint32_t box_bytes = (uint32_t)p.box_rows * (uint32_t)(C::D * 2);
+  // Tile q of the four whose lanes with a box are `lanes`.
+  auto issue = [&](const At& c, unsigned lanes, int q, const CUtensorMap* tm, uint32_t s_tile, uint32_t bar) {
+    const unsigned mine = lanes & (255u << (8 * q));
+    if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)__popc(mine) * box_bytes);
+    __syncwarp();
+    if ((mine >> lane) & 1u) tma_load_5d(s_tile + (uint32_t)my_box * box_bytes, tm, 0, c.c1, 0, c.c3, c.c4, bar);
+    __syncwarp();
+  };
+  int g = 0, gv = 0;            // key tiles loaded
+  int nf = -1, j = 0, n = 0;    // the fragment, the tile to load next, its tiles
+  At ck, cv, cv_last;           // the four tiles' boxes; V's of the tile before
+  unsigned lanes = 0, lanes_last = 0;
+  int v_left = 0;               // a V tile to load: 1 + its index of four
+  auto load_v = [&]() {
+    if (v_left == 0) return;
+    const int s = gv % C::VSTAGES;
+    if (gv >= C::VSTAGES) ok = t.warp_wait(PG_VEMPTY + s, gv / C::VSTAGES - 1, kSiteProducerEmpty, lane);
+    if (!ok) return;
+    issue(cv_last, lanes_last, v_left - 1, tm_v, t.sV + s * C::KV_BYTES, t.bar(PG_VFULL + s));
+    v_left = 0;
+    ++gv;
+  };
+#pragma unroll 1
+  while (true) {
+    // the next tile, of this fragment or of the next with keys
+    if (++j >= n) {
+      // a fragment's last V goes before anything of the next: what publish waits for may need it
+      load_v();
       if (!ok) break;
-      // the last V tile, behind the next fragment's table reads
-      const int h = f.h;
-      have = walk.next<BAND>(p, f, table, merge);
-      if (have) {
-        p0 = fetch(0, r0);
-        p1 = fetch(1, r1);
-        p2 = fetch(2, r2);
-      }
-      const int sv = gv % C::VSTAGES;
-      if (gv >= C::VSTAGES && !t.warp_wait(PG_VEMPTY + sv, gv / C::VSTAGES - 1, kSiteProducerEmpty, lane)) {
-        ok = false;
-        break;
-      }
-      const int next_h = f.h;
-      f.h = h;
-      load(t.sV + sv * C::KV_BYTES, t.bar(PG_VFULL + sv), tm_v, p.v_side, pv, rv);
-      f.h = next_h;
-      ++gv;
-      continue;
+      j = 0;
+#pragma unroll 1
+      do {
+        ++nf;
+        if (nf == walked) look_ahead();
+        n = nf < walked ? t.frags[nf & 3].n : -1;
+        if (published == nf && n <= 0) publish();   // without keys, or the end
+        if (!ok) n = -1;
+      } while (n == 0);
+      if (n < 0) break;
+      next4 = first4;
     }
-    have = walk.next<BAND>(p, f, table, merge);
-    if (have) {
-      p0 = fetch(0, r0);
-      p1 = fetch(1, r1);
-      p2 = fetch(2, r2);
+    if ((j & 3) == 0) {
+      const PagedFrag* f = t.frags + (nf & 3);
+      const Ahead now = next4;
+      next4 = fetch(f, j + 4);
+      ck = place_box(now, p.k_side, f->h);
+      cv = place_box(now, p.v_side, f->h);
+      lanes = __ballot_sync(0xffffffffu, now.row >= 0);
     }
+    const int s = g % C::KSTAGES;
+    if (g >= C::KSTAGES) ok = t.warp_wait(PG_KEMPTY + s, g / C::KSTAGES - 1, kSiteProducerEmpty, lane);
+    if (!ok) break;
+    issue(ck, lanes, j & 3, tm_k, t.sK + s * C::KV_BYTES, t.bar(PG_KFULL + s));
+    ++g;
+    load_v();
+    if (!ok) break;
+    cv_last = cv;
+    lanes_last = lanes;
+    v_left = 1 + (j & 3);
+    if (j > 0 && j == min(n, 3) - 1 && walked == nf + 1) look_ahead();
+    // this fragment at its first tile; the next one, with room for its Q, once V_j with j = VSTAGES has waited
+    // for PV(0), which followed the epilogue of the fragment before
+    if (published == nf || (two_q && j == C::VSTAGES + 1 && published == nf + 1 && walked > published)) publish();
+    if (!ok) break;
   }
-  if (ok) publish(-1);
   if (bad) atomicOr(p.status, kStatusBadPages);
   // own copies in flight land before the CTA may exit
   if (lane == 0) {
+#pragma unroll 1
     for (int i = 0; i < 2; ++i)
-      if (nf > i) wait_drain(t.bar(PG_Q + i), (uint32_t)((nf - 1 - i) / 2) & 1, t.status);
-    for (int s = 0; s < C::KSTAGES; ++s)
-      if (g > s) wait_drain(t.bar(PG_KFULL + s), (uint32_t)((g - 1 - s) / C::KSTAGES) & 1, t.status);
-    for (int s = 0; s < C::VSTAGES; ++s)
-      if (gv > s) wait_drain(t.bar(PG_VFULL + s), (uint32_t)((gv - 1 - s) / C::VSTAGES) & 1, t.status);
+      if (published > i) paged_drain(t.bar(PG_Q + i), (uint32_t)((published - 1 - i) / 2) & 1, t.status);
+#pragma unroll 1
+    for (int s = 0; s < C::KSTAGES; ++s) {
+      if (g > s) paged_drain(t.bar(PG_KFULL + s), (uint32_t)((g - 1 - s) / C::KSTAGES) & 1, t.status);
+      if (gv > s) paged_drain(t.bar(PG_VFULL + s), (uint32_t)((gv - 1 - s) / C::VSTAGES) & 1, t.status);
+    }
   }
 }
 
-// The MMA thread: per fragment S(0), S(1), then O~ += P(j) V_j and S(j+2) for
-// each key tile, as db_mma.  O~ of the fragment before must have been read
-// (PG_ODONE) before the first PV product; the S products run ahead of that.
+// The MMA thread: per fragment S(0), S(1), PV(0), S(2), PV(1) .. (PV(j): O~ +=
+// P(j) V_j), as db_mma; with few rows, in a loop with one place in the code for
+// each product.  O~ of the fragment before must have been read (PG_ODONE) before PV(0); the S products
+// run ahead of that.  P of keys 32 c .. of a tile lies in the columns its
+// scores had, low parts (split) 16 columns on.
 template <class C, bool BF16>
-__device__ __forceinline__ void pg_mma(const PagedCtx& t, const PagedParams& p) {
+__device__ __forceinline__ void pg_mma(const PagedCtx<C>& t, const PagedParams& p) {
   const uint32_t idesc_qk = make_idesc_f16(C::BR, C::BC, BF16, false, false) | p.qk_negate;
   constexpr uint32_t idesc_pv = make_idesc_f16(C::BR, C::D, BF16, false, true);
   const uint64_t dq0 = make_sdesc_sw128(t.sQ, 16, 1024);
   const uint64_t dk0 = make_sdesc_sw128(t.sK, 16, C::GROUP_BYTES);
   const uint64_t dv0 = make_sdesc_sw128(t.sV, 1024, C::GROUP_BYTES);
+  constexpr bool two_q = !C::WIDE;
   auto wait = [&](int bar, int phase, uint32_t site) -> bool {
-    return wait_or_abort(t.bar(bar), (uint32_t)phase & 1, t.abort_flag, t.status, site);
-  };
-  auto issue_s = [&](int g, bool last) -> bool {
-    const int sk = g % C::KSTAGES;
-    if (!wait(PG_KFULL + sk, g / C::KSTAGES, kSiteMmaK)) return false;
-    tc_fence_after();
-    const uint64_t b0 = dk0 + (uint64_t)((sk * C::KV_BYTES) >> 4);
-    const uint32_t tS = t.tmem + C::TMEM_S + 64 * (g & 1);
-#pragma unroll
-    for (int k = 0; k < C::D / 16; ++k)
-      umma_ss(tS, dq0 + (uint64_t)(((k >> 2) * (C::BR * 128) + (k & 3) * 32) >> 4),
-              b0 + (uint64_t)(((k >> 2) * 1024 + (k & 3) * 32) >> 4), idesc_qk, k > 0 ? 1u : 0u);
-    umma_commit(t.bar(PG_S + (g & 1)));
-    umma_commit(t.bar(PG_KEMPTY + sk));
-    if (last) umma_commit(t.bar(PG_QEMPTY));
-    return true;
+    return paged_wait<C::WIDE>(t.bar(bar), (uint32_t)phase & 1, t.abort_flag, t.status, site);
   };
   bool ok = true;
-  int g = 0;
+  int g0 = 0;   // key tiles of the fragments before
+#pragma unroll 1
   for (int nf = 0; ok; ++nf) {
     if (!wait(PG_Q + (nf & 1), nf >> 1, kSiteMmaQ)) break;
-    const PagedFrag* f = t.frags + (nf & 1);
+    const PagedFrag* f = t.frags + (nf & 3);
     const int n = f->n;
     if (n < 0) break;
     if (n == 0) {
-      mbar_arrive(t.bar(PG_QEMPTY));
+      mbar_arrive(t.bar(PG_QEMPTY + (nf & 1)));
       continue;
     }
     const TileMask tm = f->tm;
-    const bool few_keys = f->few_keys != 0;
-    tc_fence_after();
-    ok = issue_s(g, n == 1);
-    if (ok && n > 1) ok = issue_s(g + 1, n == 2);
-    for (int j = 0; j < n && ok; ++j, ++g) {
-      const int sv = g % C::VSTAGES;
-      if (j == 0 && nf > 0) ok = wait(PG_ODONE + ((nf - 1) & 1), (nf - 1) >> 1, kSiteMmaO);
-      ok = ok && wait(PG_P + (g & 1), g >> 1, kSiteMmaP) && wait(PG_VFULL + sv, g / C::VSTAGES, kSiteMmaV);
-      if (!ok) break;
+    const bool always = f->split != 0;
+    const uint64_t a0 = dq0 + (two_q && (nf & 1) ? (uint64_t)((C::BR / 2 * 128) >> 4) : 0ull);
+    auto issue_s = [&](int i) -> bool {
+      const int g = g0 + i, sk = g % C::KSTAGES;
+      if (!wait(PG_KFULL + sk, g / C::KSTAGES, kSiteMmaK)) return false;
+      tc_fence_after();
+      const uint64_t b0 = dk0 + (uint64_t)((sk * C::KV_BYTES) >> 4);
+      const uint32_t tS = t.tmem + C::TMEM_S + 64 * (g & 1);
+#pragma unroll
+      for (int k = 0; k < C::D / 16; ++k)
+        umma_ss(tS, a0 + (uint64_t)(((k >> 2) * (C::BR * 128) + (k & 3) * 32) >> 4),
+                b0 + (uint64_t)(((k >> 2) * 1024 + (k & 3) * 32) >> 4), idesc_qk, k > 0 ? 1u : 0u);
+      umma_commit(t.bar(PG_S + (g & 1)));
+      umma_commit(t.bar(PG_KEMPTY + sk));
+      if (i + 1 == n) umma_commit(t.bar(PG_QEMPTY + (nf & 1)));
+      return true;
+    };
+    auto issue_pv = [&](int j) -> bool {
+      const int g = g0 + j, sv = g % C::VSTAGES;
+      if (j == 0 && nf > 0 && !wait(PG_ODONE + ((nf - 1) & 1), (nf - 1) >> 1, kSiteMmaO)) return false;
+      if (!wait(PG_P + (g & 1), g >> 1, kSiteMmaP) || !wait(PG_VFULL + sv, g / C::VSTAGES, kSiteMmaV)) return false;
       tc_fence_after();
       const uint64_t b0 = dv0 + (uint64_t)((sv * C::KV_BYTES) >> 4);
       const uint32_t tS = t.tmem + C::TMEM_S + 64 * (g & 1);
       const uint32_t tO = t.tmem + C::TMEM_O;
-      if (split_tile<BF16>(!tm.full(j), few_keys)) {
+      const bool split = split_tile<BF16>(!tm.full(j), always);
+      auto product = [&](bool both) {
 #pragma unroll
         for (int k = 0; k < C::BC / 16; ++k) {
-          const uint64_t b = b0 + (uint64_t)((k * 2 * C::GROUP_BYTES) >> 4);
-          umma_ts(tO, tS + k * 8, b, idesc_pv, (j > 0 || k > 0) ? 1u : 0u);
-          umma_ts(tO, tS + C::BC / 2 + k * 8, b, idesc_pv, 1u);
+          const uint64_t bk = b0 + (uint64_t)((k * 2 * C::GROUP_BYTES) >> 4);
+          const uint32_t pk = tS + (k >> 1) * 32 + (k & 1) * 8;
+          umma_ts(tO, pk, bk, idesc_pv, (j > 0 || k > 0) ? 1u : 0u);
+          if (both) umma_ts(tO, pk + 16, bk, idesc_pv, 1u);
         }
-      } else {
-#pragma unroll
-        for (int k = 0; k < C::BC / 16; ++k)
-          umma_ts(tO, tS + k * 8, b0 + (uint64_t)((k * 2 * C::GROUP_BYTES) >> 4), idesc_pv,
-                  (j > 0 || k > 0) ? 1u : 0u);
-      }
+      };
+      if (C::WIDE && !split)
+        product(false);
+      else
+        product(BF16);   // few rows: bf16 P is always split
       umma_commit(t.bar(PG_O));
       umma_commit(t.bar(PG_VEMPTY + sv));
       if (j + 1 == n) umma_commit(t.bar(PG_OLAST));
-      if (j + 2 < n) ok = issue_s(g + 2, j + 3 == n);
+      return true;
+    };
+    if constexpr (C::WIDE) {
+      ok = issue_s(0) && (n == 1 || issue_s(1));
+      for (int j = 0; j < n && ok; ++j) ok = issue_pv(j) && (j + 2 >= n || issue_s(j + 2));
+    } else {
+#pragma unroll 1
+      for (int i = 0; i <= n && ok; ++i) ok = (i == n || issue_s(i)) && (i == 0 || issue_pv(i - 1));
     }
+    g0 += n;
   }
   umma_commit(t.bar(PG_EXIT));
-  wait_drain(t.bar(PG_EXIT), 0, t.status);
+  paged_drain(t.bar(PG_EXIT), 0, t.status);
 }
 
 // Zeroes the rows of V tile `kt` (shared memory) whose keys no row of the
@@ -708,13 +801,39 @@ __device__ __forceinline__ void zero_hidden_rows(uint32_t sV, int kt, const Page
   }
 }
 
+// P = 2^(s * scale - m) of 32 keys into 16 columns of 16-bit pairs, its low part
+// P - P_hi (SPLIT) into the 16 after them: the columns their scores had.
+template <bool BF16, bool SPLIT>
+__device__ __forceinline__ void paged_p_run(const uint32_t* sr, uint32_t tP, float2 scale2, float2 neg_m2, float2& sum0,
+                                            float2& sum1) {
+  uint32_t ph[16];
+  uint32_t pl[16];
+#pragma unroll
+  for (int c = 0; c < 16; ++c) {
+    float2 x = __ffma2_rn(make_float2(__uint_as_float(sr[2 * c]), __uint_as_float(sr[2 * c + 1])), scale2, neg_m2);
+    x.x = ex2_approx(x.x);
+    x.y = ex2_approx(x.y);
+    if (c & 1)
+      sum1 = __fadd2_rn(sum1, x);
+    else
+      sum0 = __fadd2_rn(sum0, x);
+    ph[c] = pack2<BF16>(x.x, x.y);
+    if constexpr (SPLIT) {
+      const float2 h = unpack2<BF16>(ph[c]);
+      pl[c] = pack2<BF16>(x.x - h.x, x.y - h.y);
+    }
+  }
+  tmem_st_32x32b_x16(tP, ph);
+  if constexpr (SPLIT) tmem_st_32x32b_x16(tP + 16, pl);
+}
+
 // Output row r of a tile: the token's row, the query head's columns.
 __device__ __forceinline__ uint8_t* paged_o_row(const PagedParams& p, int row, int head) {
   return reinterpret_cast<uint8_t*>(p.o) + 2 * ((long long)row * p.o_rs + (long long)head * p.o_hs);
 }
 
 template <class C, bool BF16, bool BAND>
-__device__ __forceinline__ void pg_softmax(const PagedCtx& t, const PagedParams& p, int warp, int lane) {
+__device__ __forceinline__ void pg_softmax(const PagedCtx<C>& t, const PagedParams& p, int warp, int lane) {
   const int quad = warp & 3;
   const int r = quad * 32 + lane;
   const int tok = r / p.group;
@@ -722,13 +841,13 @@ __device__ __forceinline__ void pg_softmax(const PagedCtx& t, const PagedParams&
   const uint32_t tO = t.tmem + lane_off + C::TMEM_O;
   const float sl2 = p.scale_log2_mag;
   auto wait = [&](int bar, int phase, uint32_t site) -> bool {
-    const bool ok = wait_or_abort(t.bar(bar), (uint32_t)phase & 1, t.abort_flag, t.status, site);
+    const bool ok = paged_wait<C::WIDE>(t.bar(bar), (uint32_t)phase & 1, t.abort_flag, t.status, site);
     return __all_sync(0xffffffffu, ok);
   };
   int g = 0, products = 0;   // key tiles; fragments that had some
   for (int nf = 0;; ++nf) {
     if (!wait(PG_Q + (nf & 1), nf >> 1, kSiteMmaQ)) return;
-    const PagedFrag* f = t.frags + (nf & 1);
+    const PagedFrag* f = t.frags + (nf & 3);
     const int n = f->n;
     if (n < 0) return;
     const int rows = f->rows;
@@ -736,7 +855,7 @@ __device__ __forceinline__ void pg_softmax(const PagedCtx& t, const PagedParams&
     const bool warp_live = quad * 32 < rows;
     const int head = f->h * p.group + (r - tok * p.group);
     const TileMask tmask = f->tm;
-    const bool few_keys = f->few_keys != 0;
+    const bool always = f->split != 0;
     float m_run = -INFINITY;
     float l_run = 0.f;
     for (int j = 0; j < n; ++j, ++g) {
@@ -745,21 +864,47 @@ __device__ __forceinline__ void pg_softmax(const PagedCtx& t, const PagedParams&
       tc_fence_after();
       const bool masked = !tmask.full(j);
       if (warp_live) {
-        uint32_t sr[C::BC];
+        const int k0 = f->tile(f->j0 + j) * C::BC, tok_row = f->q0 + tok;
+        const bool split = split_tile<BF16>(masked, always);
+        // The tile's 64 scores: in registers (a warp of live rows, where the
+        // softmax is what bounds the loop), or read from tensor memory twice in
+        // runs of 32, half the code (few rows: the loop waits for the keys, and
+        // code costs more than the second read)
+        uint32_t sr[C::WIDE ? C::BC : 32];
+        auto read = [&](int c) {
+          tmem_ld_32x32b_x32(tS + c, sr + (C::WIDE ? c : 0));
+          tmem_ld_wait_x32(sr + (C::WIDE ? c : 0));
+          if (masked) mask_scores<32, BAND>(sr + (C::WIDE ? c : 0), f->km, tok_row, k0 + c);
+        };
+        float m_tile = -INFINITY;
+        auto top = [&](int c) {
+          const uint32_t* x = sr + (C::WIDE ? c : 0);
+          float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < C::BC; c += 32) tmem_ld_32x32b_x32(tS + c, sr + c);
-#pragma unroll
-        for (int c = 0; c < C::BC; c += 32) tmem_ld_wait_x32(sr + c);
-        if (masked) mask_scores<C::BC, BAND>(sr, f->km, f->q0 + tok, f->tile(f->j0 + j) * C::BC);
-        float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < C::BC; c += 8) {
-          mx0 = fmax3(mx0, __uint_as_float(sr[c + 0]), __uint_as_float(sr[c + 1]));
-          mx1 = fmax3(mx1, __uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3]));
-          mx2 = fmax3(mx2, __uint_as_float(sr[c + 4]), __uint_as_float(sr[c + 5]));
-          mx3 = fmax3(mx3, __uint_as_float(sr[c + 6]), __uint_as_float(sr[c + 7]));
+          for (int i = 0; i < 32; i += 8) {
+            mx0 = fmax3(mx0, __uint_as_float(x[i + 0]), __uint_as_float(x[i + 1]));
+            mx1 = fmax3(mx1, __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
+            mx2 = fmax3(mx2, __uint_as_float(x[i + 4]), __uint_as_float(x[i + 5]));
+            mx3 = fmax3(mx3, __uint_as_float(x[i + 6]), __uint_as_float(x[i + 7]));
+          }
+          m_tile = fmaxf(m_tile, fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)));
+        };
+        if constexpr (C::WIDE) {
+          tmem_ld_32x32b_x32(tS, sr);
+          tmem_ld_32x32b_x32(tS + 32, sr + 32);
+          tmem_ld_wait_x32(sr);
+          tmem_ld_wait_x32(sr + 32);
+          if (masked) mask_scores<C::BC, BAND>(sr, f->km, tok_row, k0);
+          top(0);
+          top(32);
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < C::BC; c += 32) {
+            read(c);
+            top(c);
+          }
         }
-        const float m_tile = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * sl2;
+        m_tile *= sl2;
         const bool raise = live && m_tile > m_run + kRescaleLog2;
         const float m_new = raise ? m_tile : m_run;
         const float m_use = (m_new == -INFINITY) ? 0.f : m_new;
@@ -767,14 +912,20 @@ __device__ __forceinline__ void pg_softmax(const PagedCtx& t, const PagedParams&
         const float2 scale2 = make_float2(sl2, sl2);
         const float2 neg_m2 = make_float2(-m_use, -m_use);
         float2 sum0 = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
-        if (split_tile<BF16>(masked, few_keys)) {
-#pragma unroll
-          for (int ch = 0; ch < C::BC / 32; ++ch)
-            softmax_p_chunk<C, BF16, true>(sr, ch, tS, scale2, neg_m2, sum0, sum1);
+        if constexpr (C::WIDE) {
+          if (BF16 && split) {
+            paged_p_run<BF16, true>(sr, tS, scale2, neg_m2, sum0, sum1);
+            paged_p_run<BF16, true>(sr + 32, tS + 32, scale2, neg_m2, sum0, sum1);
+          } else {
+            paged_p_run<BF16, false>(sr, tS, scale2, neg_m2, sum0, sum1);
+            paged_p_run<BF16, false>(sr + 32, tS + 32, scale2, neg_m2, sum0, sum1);
+          }
         } else {
-#pragma unroll
-          for (int ch = 0; ch < C::BC / 32; ++ch)
-            softmax_p_chunk<C, BF16, false>(sr, ch, tS, scale2, neg_m2, sum0, sum1);
+#pragma unroll 1
+          for (int c = 0; c < C::BC; c += 32) {
+            read(c);
+            paged_p_run<BF16, BF16>(sr, tS + c, scale2, neg_m2, sum0, sum1);
+          }
         }
         const float2 sum2 = __fadd2_rn(sum0, sum1);
         l_run = l_run * alpha + (sum2.x + sum2.y);
@@ -864,11 +1015,11 @@ __device__ __forceinline__ void pg_softmax(const PagedCtx& t, const PagedParams&
   }
 }
 
-template <int D, bool BF16, bool BAND>
-__global__ void __launch_bounds__(192, PagedConfig<D>::CTAS_PER_SM)
+template <int D, bool BF16, bool BAND, bool WIDE>
+__global__ void __launch_bounds__(PagedConfig<D, WIDE>::THREADS, PagedConfig<D, WIDE>::CTAS_PER_SM)
     fa2_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                     const __grid_constant__ CUtensorMap tm_v, const PagedParams p) {
-  using C = PagedConfig<D>;
+                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PagedParams p) {
+  using C = PagedConfig<D, WIDE>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
@@ -876,7 +1027,7 @@ __global__ void __launch_bounds__(192, PagedConfig<D>::CTAS_PER_SM)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
   PagedScan* scan = reinterpret_cast<PagedScan*>(smem + C::OFF_SCAN);
-  static_assert(sizeof(PagedScan) <= 256 && C::OFF_SCAN % 8 == 0, "scan area");
+  static_assert(sizeof(PagedScan) <= 320 && C::OFF_SCAN % 8 == 0, "scan area");
   const int warp = (int)(threadIdx.x >> 5);
   const int lane = (int)(threadIdx.x & 31);
   grid_launch_dependents();   // the merge may be scheduled once every CTA has started; it waits for the partials
@@ -889,7 +1040,7 @@ __global__ void __launch_bounds__(192, PagedConfig<D>::CTAS_PER_SM)
     if (threadIdx.x == 0 && piece < p.ctas) p.merges[piece].first = -1;
     return;
   }
-  PagedCtx t;
+  PagedCtx<C> t;
   t.bar0 = sbase + C::OFF_BAR;
   t.sQ = sbase + C::OFF_Q;
   t.sK = sbase + C::OFF_K;
@@ -918,7 +1069,7 @@ __global__ void __launch_bounds__(192, PagedConfig<D>::CTAS_PER_SM)
   t.tmem = *tmem_slot;
 
   if (warp == C::TMA_WARP) {
-    pg_producer<C, BAND>(t, p, &tm_q, &tm_k, &tm_v, place, piece, lane);
+    pg_load<C, BAND>(t, p, &tm_q, &tm_k, &tm_v, place, piece, lane);
   } else if (warp == C::MMA_WARP) {
     if (lane == 0) pg_mma<C, BF16>(t, p);
     __syncwarp();
@@ -943,7 +1094,7 @@ constexpr int kPagedMergeRows = 32;   // rows of a block
 // rows, or (fewer than 17 rows) rows x partials, whose sums are then joined by
 // shuffles in a fixed order.  The rows go out through shared memory, whole.
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kPagedMergeThreads) fa2_paged_merge_kernel(const PagedParams p) {
+__global__ void __launch_bounds__(kPagedMergeThreads) fa2_paged_merge_kernel(const __grid_constant__ PagedParams p) {
   constexpr int NW = kPagedMergeThreads / 32;
   constexpr int E = D / 4 / NW;   // column runs of a warp
   __shared__ uint2 stage[kPagedMergeRows][D / 4];
@@ -1033,10 +1184,10 @@ __global__ void __launch_bounds__(kPagedMergeThreads) fa2_paged_merge_kernel(con
   }
 }
 
-template <int D, bool BF16, bool BAND>
+template <int D, bool BF16, bool BAND, bool WIDE>
 int launch_paged_kernels(const PagedLaunchArgs& a) {
-  using C = PagedConfig<D>;
-  auto kern = fa2_paged_kernel<D, BF16, BAND>;
+  using C = PagedConfig<D, WIDE>;
+  auto kern = fa2_paged_kernel<D, BF16, BAND, WIDE>;
   static std::atomic<unsigned long long> configured{0};
   const int e = once_per_device(configured, [&]() -> int {
     return (int)cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM_BYTES);
@@ -1058,10 +1209,16 @@ int launch_paged_kernels(const PagedLaunchArgs& a) {
   return (int)cudaLaunchKernelEx(&cfg, fa2_paged_merge_kernel<D, BF16>, a.p);
 }
 
+template <int D, bool BF16>
+int launch_paged_rows(const PagedLaunchArgs& a) {
+  const bool wide = a.p.slot_rows > kPagedTileRows / 2;
+  if (a.band) return wide ? launch_paged_kernels<D, BF16, true, true>(a) : launch_paged_kernels<D, BF16, true, false>(a);
+  return wide ? launch_paged_kernels<D, BF16, false, true>(a) : launch_paged_kernels<D, BF16, false, false>(a);
+}
+
 template <int D>
 int launch_paged(const PagedLaunchArgs& a) {
-  if (a.band) return a.bf16 ? launch_paged_kernels<D, true, true>(a) : launch_paged_kernels<D, false, true>(a);
-  return a.bf16 ? launch_paged_kernels<D, true, false>(a) : launch_paged_kernels<D, false, false>(a);
+  return a.bf16 ? launch_paged_rows<D, true>(a) : launch_paged_rows<D, false>(a);
 }
 
 }  // namespace fa2

@@ -44,6 +44,7 @@ struct PagedParams {
   int tile_tokens;        // tokens of a query tile: 128 / group
   int total_q, max_q;
   int num_pages, page_size, max_pages;
+  unsigned page_magic, page_shift;   // k / page_size = (umulhi(k, magic) + k) >> shift for 0 <= k < 2^31
   int box_rows;           // key rows of a box: 8, 16, 32 or 64
   PagedSide k_side, v_side;
   int window_left, window_right, prefix;   // as KernelParams

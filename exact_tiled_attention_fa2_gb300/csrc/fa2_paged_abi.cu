@@ -23,7 +23,7 @@ constexpr int paged_ctas(int d) { return d == 256 ? 152 : 304; }
 // shortest piece worth a CTA: 256 keys, or (many rows) the keys whose K and V
 // are as many bytes as a partial's write and read four times over.
 constexpr int kPagedOverhead = 128;
-constexpr int kPagedMinShare = 256;
+constexpr int kPagedMinShare = 192;
 constexpr long long kPagedMaxKeys = (1ll << 31) - 4096;   // keys of a sequence, rounded up to tiles, stay below 2^31
 
 struct Range {
@@ -209,6 +209,10 @@ int paged_forward(const fa2_paged_params& a, void* workspace, size_t workspace_b
     rc = encode_map_nd(&la.tm_q, a.q, 4, dims, st, box, la.bf16);
     if (rc) return rc;
   }
+  // k / page_size for 0 <= k < 2^31 without a division: magic = 2^32 (2^shift - page_size) / page_size + 1, 2^shift >=
+  // page_size
+  while ((1ll << p.page_shift) < c.page_size) ++p.page_shift;
+  p.page_magic = (unsigned)(((1ull << 32) * ((1ull << p.page_shift) - (unsigned)c.page_size)) / (unsigned)c.page_size + 1);
   p.box_rows = c.page_size < kPagedKeyTile ? c.page_size : kPagedKeyTile;
   const bool merged_k = merged_side(kc, p.k_side), merged_v = merged_side(vc, p.v_side);
   if (!merged_k || !merged_v) p.box_rows = 8;
@@ -241,7 +245,7 @@ int paged_forward(const fa2_paged_params& a, void* workspace, size_t workspace_b
   p.scale_log2_mag = std::fmax(std::fabs(scale_log2), FLT_MIN);
   p.qk_negate = scale_log2 < 0.f ? 1u << 13 : 0u;   // the negate-A bit of the S product's descriptor
   p.slot_rows = s.group * s.box_tokens;
-  p.overhead = kPagedOverhead;
+  p.overhead = kPagedOverhead + 2 * p.slot_rows;
   p.ctas = s.ctas;
   p.pair_ctas = s.pair_ctas;
   p.min_share = kPagedMinShare > 8 * p.slot_rows ? kPagedMinShare : 8 * p.slot_rows;
