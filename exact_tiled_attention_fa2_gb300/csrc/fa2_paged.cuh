@@ -63,7 +63,9 @@ enum : int {
   PG_KEMPTY = 17,  // + stage
   PG_VFULL = 21,   // + stage
   PG_VEMPTY = 25,  // + stage
-  PG_BARS = 29,
+  PG_PLAN = 29,    // + f & 3: the fragment's description is there (planner -> TMA warp)
+  PG_FREE = 33,    // + f & 3: its slot is free (softmax warps -> planner)
+  PG_BARS = 37,
 };
 
 // Everything the softmax warps and the MMA thread need of a fragment: written
@@ -94,9 +96,14 @@ struct PagedConfig {
   static constexpr int BC = kPagedKeyTile;
   static constexpr int KSTAGES = D == 64 ? 4 : 2;
   static constexpr int VSTAGES = D == 64 ? 4 : 2;
-  static constexpr int THREADS = 192;
+  // Few rows: a warp of its own walks the fragments (many short ones).  Many
+  // rows: the TMA warp does, between loads (a seventh warp would leave the
+  // softmax 128 registers).
+  static constexpr bool PLANNER = !WIDE;
+  static constexpr int THREADS = PLANNER ? 224 : 192;
   static constexpr int MMA_WARP = 4;
   static constexpr int TMA_WARP = 5;
+  static constexpr int PLAN_WARP = 6;
   static constexpr int BLOCKS = D / 64;                 // 64-column blocks of a row
   static constexpr uint32_t GROUP_BYTES = BLOCKS * 1024;   // 8 key rows
   static constexpr uint32_t Q_BYTES = BR * D * 2;
@@ -436,10 +443,9 @@ struct FragWalk {
 
 };
 
-// The next fragment, to shared memory; false when the piece is done.  Out of
-// line (as the waits' slow path below): once per fragment.
+// The next fragment, to shared memory; false when the piece is done.
 template <bool BAND>
-static __device__ __noinline__ bool next_fragment(FragWalk<BAND>& k, const PagedParams& p, PagedFrag* dst, int lane) {
+__device__ __forceinline__ bool next_fragment(FragWalk<BAND>& k, const PagedParams& p, PagedFrag* dst, int lane) {
   while (k.more) {
     const bool from_start = k.begin <= k.x, to_end = k.end - k.x >= k.w, whole = from_start && to_end;
     const int j0 = from_start ? 0 : span_tile(p, k.begin - k.x, k.tiles_n);
@@ -530,7 +536,28 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
-// The TMA warp: walks the piece's fragments, publishes them (with Q) and loads
+// The planner warp (few rows): walks the piece's fragments, up to four ahead of
+// the softmax.
+template <class C, bool BAND>
+__device__ __forceinline__ void pg_plan(const PagedCtx<C>& t, const PagedParams& p, const PagedPlace& place, int piece,
+                                        int lane) {
+  FragWalk<BAND> walk;
+  walk.start(p, place, piece);
+  bool have = true;
+#pragma unroll 1
+  for (int nf = 0; have; ++nf) {
+    if (nf >= 4 && !t.warp_wait(PG_FREE + (nf & 3), (nf >> 2) - 1, kSiteProducerEmpty, lane)) break;
+    PagedFrag* f = t.frags + (nf & 3);
+    have = next_fragment(walk, p, f, lane);
+    if (lane == 0) {
+      if (!have) f->n = -1;
+      mbar_arrive(t.bar(PG_PLAN + (nf & 3)));
+      if (nf == 0 && piece < p.ctas) p.merges[piece] = walk.merge;   // (one pair per CTA: piece may be larger)
+    }
+  }
+}
+
+// The TMA warp: publishes the piece's fragments (with Q; many rows: walks them too) and loads
 // their key tiles, K_0 K_1 V_0 K_2 V_1 .. (a K stage frees at S(j), just before
 // PV(j - 1) frees a V stage).  The boxes of four tiles are worked out at once,
 // lane 8 q + b holding box b (rows b * box_rows ..) of tile q, and their
@@ -543,8 +570,10 @@ __device__ __forceinline__ void pg_load(const PagedCtx<C>& t, const PagedParams&
                                         const CUtensorMap* tm_k, const CUtensorMap* tm_v, const PagedPlace& place,
                                         int piece, int lane) {
   FragWalk<BAND> walk;
-  walk.start(p, place, piece);
-  if (lane == 0 && piece < p.ctas) p.merges[piece] = walk.merge;   // (one pair per CTA: piece may be larger)
+  if constexpr (!C::PLANNER) {
+    walk.start(p, place, piece);
+    if (lane == 0 && piece < p.ctas) p.merges[piece] = walk.merge;   // (one pair per CTA: piece may be larger)
+  }
   // Q loads of at most 64 rows leave room for the next fragment's in the other
   // half of the rows (the products then read 64 rows of whatever follows, which
   // reach no live row).
@@ -574,7 +603,12 @@ __device__ __forceinline__ void pg_load(const PagedCtx<C>& t, const PagedParams&
   // publishing the one before waited for a later one).
   auto look_ahead = [&]() {
     PagedFrag* f = t.frags + (walked & 3);
-    if (!next_fragment(walk, p, f, lane)) return;
+    if constexpr (C::PLANNER) {
+      ok = t.warp_wait(PG_PLAN + (walked & 3), walked >> 2, kSiteProducerEmpty, lane);
+      if (!ok || f->n < 0) return;
+    } else {
+      if (!next_fragment(walk, p, f, lane)) return;
+    }
     first4 = fetch(f, 0);
     ++walked;
   };
@@ -587,7 +621,7 @@ __device__ __forceinline__ void pg_load(const PagedCtx<C>& t, const PagedParams&
     if (!ok) return;
     if (lane == 0) {
       PagedFrag* f = t.frags + (nf & 3);
-      if (nf == walked) f->n = -1;
+      if (!C::PLANNER && nf == walked) f->n = -1;
       const uint32_t bar = t.bar(PG_Q + (nf & 1));
       if (f->n > 0) {
         const uint32_t sQ = t.sQ + (two_q && (nf & 1) ? C::BR / 2 * 128u : 0u);
@@ -657,11 +691,11 @@ __device__ __forceinline__ void pg_load(const PagedCtx<C>& t, const PagedParams&
       do {
         ++nf;
         if (nf == walked) look_ahead();
+        if (!ok) break;
         n = nf < walked ? t.frags[nf & 3].n : -1;
         if (published == nf && n <= 0) publish();   // without keys, or the end
-        if (!ok) n = -1;
-      } while (n == 0);
-      if (n < 0) break;
+      } while (ok && n == 0);
+      if (!ok || n < 0) break;
       next4 = first4;
     }
     if ((j & 3) == 0) {
@@ -683,6 +717,7 @@ __device__ __forceinline__ void pg_load(const PagedCtx<C>& t, const PagedParams&
     lanes_last = lanes;
     v_left = 1 + (j & 3);
     if (j > 0 && j == min(n, 3) - 1 && walked == nf + 1) look_ahead();
+    if (!ok) break;
     // this fragment at its first tile; the next one, with room for its Q, once V_j with j = VSTAGES has waited
     // for PV(0), which followed the epilogue of the fragment before
     if (published == nf || (two_q && j == C::VSTAGES + 1 && published == nf + 1 && walked > published)) publish();
@@ -1011,7 +1046,10 @@ __device__ __forceinline__ void pg_softmax(const PagedCtx<C>& t, const PagedPara
     }
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive(t.bar(PG_ODONE + (nf & 1)));
+    if (lane == 0) {
+      mbar_arrive(t.bar(PG_ODONE + (nf & 1)));
+      if (C::PLANNER) mbar_arrive(t.bar(PG_FREE + (nf & 3)));
+    }
   }
 }
 
@@ -1032,13 +1070,12 @@ __global__ void __launch_bounds__(PagedConfig<D, WIDE>::THREADS, PagedConfig<D, 
   const int lane = (int)(threadIdx.x & 31);
   grid_launch_dependents();   // the merge may be scheduled once every CTA has started; it waits for the partials
 
-  // The whole CTA leaves together, before any barrier or TMEM set-up, when it
-  // has no piece.
-  const int piece = (int)blockIdx.x;
-  const PagedPlace place = find_place<C::THREADS>(p, piece, scan, blockIdx.x == 0);
-  if (place.seq < 0) {
-    if (threadIdx.x == 0 && piece < p.ctas) p.merges[piece].first = -1;
-    return;
+  // Tensor memory and barriers before the schedule: an SM's second CTA starts
+  // only when the first has let go of the allocation permit (measured: 3.6 us
+  // into the kernel with the allocation behind the schedule, half of the CTAs).
+  if (warp == C::MMA_WARP) {
+    tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
+    tmem_relinquish();
   }
   PagedCtx<C> t;
   t.bar0 = sbase + C::OFF_BAR;
@@ -1048,10 +1085,10 @@ __global__ void __launch_bounds__(PagedConfig<D, WIDE>::THREADS, PagedConfig<D, 
   t.abort_flag = abort_flag;
   t.status = p.status;
   t.frags = reinterpret_cast<PagedFrag*>(smem + C::OFF_FRAG);
-
   if (warp == C::TMA_WARP && lane == 0) {
+#pragma unroll 1
     for (int i = 0; i < PG_BARS; ++i)
-      mbar_init(t.bar(i), (i == PG_P || i == PG_P + 1 || i == PG_ODONE || i == PG_ODONE + 1) ? 4 : 1);
+      mbar_init(t.bar(i), (i >= PG_P && i < PG_O) || i >= PG_FREE ? 4 : 1);   // four softmax warps, or one arrival
     *abort_flag = 0;
     fence_mbar_init();
     fence_proxy_async_smem();
@@ -1059,20 +1096,21 @@ __global__ void __launch_bounds__(PagedConfig<D, WIDE>::THREADS, PagedConfig<D, 
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
   }
-  if (warp == C::MMA_WARP) {
-    tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
-    tmem_relinquish();
-  }
+  const int piece = (int)blockIdx.x;
   tc_fence_before();
-  __syncthreads();
+  const PagedPlace place = find_place<C::THREADS>(p, piece, scan, blockIdx.x == 0);   // with its barriers
   tc_fence_after();
   t.tmem = *tmem_slot;
 
-  if (warp == C::TMA_WARP) {
+  if (place.seq < 0) {   // no piece for this CTA
+    if (threadIdx.x == 0 && piece < p.ctas) p.merges[piece].first = -1;
+  } else if (warp == C::TMA_WARP) {
     pg_load<C, BAND>(t, p, &tm_q, &tm_k, &tm_v, place, piece, lane);
   } else if (warp == C::MMA_WARP) {
     if (lane == 0) pg_mma<C, BF16>(t, p);
     __syncwarp();
+  } else if (C::PLANNER && warp == C::PLAN_WARP) {
+    pg_plan<C, BAND>(t, p, place, piece, lane);
   } else {
     pg_softmax<C, BF16, BAND>(t, p, warp, lane);
   }
@@ -1190,7 +1228,10 @@ int launch_paged_kernels(const PagedLaunchArgs& a) {
   auto kern = fa2_paged_kernel<D, BF16, BAND, WIDE>;
   static std::atomic<unsigned long long> configured{0};
   const int e = once_per_device(configured, [&]() -> int {
-    return (int)cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM_BYTES);
+    const cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM_BYTES);
+    if (r != cudaSuccess) return (int)r;
+    cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+    return (int)cudaFuncSetAttribute(fa2_paged_merge_kernel<D, BF16>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
   });
   if (e != 0) return e;
   const int grid = a.p.pair_ctas > a.p.ctas ? a.p.pair_ctas : a.p.ctas;
