@@ -439,8 +439,11 @@ _torch = None   # torch, its 16-bit dtypes' codes, int32, raw-stream and device 
 def _torch_facts():
     global _torch
     import torch
+    # the caching allocator without a tensor around its block, where this torch has it
+    alloc = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_alloc", None)
+    free = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_delete", None)
     _torch = (torch, {torch.float16: FA2_FP16, torch.bfloat16: FA2_BF16}, torch.int32,
-              torch._C._cuda_getCurrentRawStream, torch.cuda.current_device)
+              torch._C._cuda_getCurrentRawStream, torch.cuda.current_device, alloc if free else None, free)
     return _torch
 
 
@@ -643,11 +646,23 @@ def fa2_paged_fwd(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, o=N
     params = pack(o.data_ptr(), lse.data_ptr(), o.stride(), lse.stride(0),
                   1.0 / float(d) ** 0.5 if scale is None else float(scale), window_left, window_right, prefix_len)
     lib = _lib or load_library()
-    if workspace is None:
-        workspace = q.new_empty(max(lib.fa2_paged_fwd_workspace_bytes(params), 256), dtype=torch.uint8)
-    elif workspace.get_device() != dev or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on q's device")
-    rc = lib.fa2_paged_fwd(params, workspace.data_ptr(), workspace.numel() * workspace.element_size(), facts[3](dev))
+    handle = facts[3](dev)
+    if workspace is not None:
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on q's device")
+        rc = lib.fa2_paged_fwd(params, workspace.data_ptr(), workspace.numel() * workspace.element_size(), handle)
+    else:
+        # a block of the current stream, given back once the kernels are queued: its next user there follows them
+        need = lib.fa2_paged_fwd_workspace_bytes(params)
+        if need == 0 or facts[5] is None:
+            block = q.new_empty(max(need, 256), dtype=torch.uint8)
+            rc = lib.fa2_paged_fwd(params, block.data_ptr(), block.numel(), handle)
+        else:
+            block = facts[5](need, handle)
+            try:
+                rc = lib.fa2_paged_fwd(params, block, need, handle)
+            finally:
+                facts[6](block)
     if rc:
         raise Fa2Error(rc, "fa2_paged_fwd")
     return o, lse

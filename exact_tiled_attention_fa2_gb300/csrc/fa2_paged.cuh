@@ -166,11 +166,26 @@ __device__ __forceinline__ KeyMask paged_mask(const PagedParams& p, int n_q, int
   return km;
 }
 
+// Positions on the line: keys, in 64 bits; with tiles of few rows (WIDE false,
+// and every sequence one query tile) key tiles, in 32 bits, which the host has
+// made sure of.
+template <bool WIDE>
+struct LineOf {
+  using T = long long;
+  static constexpr int KEYS = 1;   // of a unit
+};
+template <>
+struct LineOf<false> {
+  using T = int;
+  static constexpr int KEYS = kPagedKeyTile;
+};
+
 // a / b for 0 <= a, 0 < b: a 32-bit division where both fit.
 __device__ __forceinline__ long long line_div(long long a, long long b) {
   if (((unsigned long long)(a | b) >> 32) == 0) return (long long)((unsigned)a / (unsigned)b);
   return a / b;
 }
+__device__ __forceinline__ int line_div(int a, int b) { return (int)((unsigned)a / (unsigned)b); }
 
 // One sequence's part of the line: `tiles` query tiles x heads_kv pairs, in
 // order of the tiles, heads fastest.
@@ -179,114 +194,139 @@ struct PagedSeq {
   int tiles;
   int keys;      // a pair's span in keys, or -1: a causal chunk, whose spans
                  // grow by tile_tokens from tile to tile and end at N_k
+  template <bool WIDE>
   __device__ __forceinline__ int width(const PagedParams& p, int t) const {
-    return p.overhead + (keys >= 0 ? keys : n_k - n_q + min((t + 1) * p.tile_tokens, n_q));
+    if constexpr (WIDE)
+      return p.overhead + (keys >= 0 ? keys : n_k - n_q + min((t + 1) * p.tile_tokens, n_q));
+    else
+      return (p.overhead + keys) / kPagedKeyTile;
   }
   // spans of the tiles before t (one head's)
   __device__ __forceinline__ long long before(const PagedParams& p, int t) const {
     return keys >= 0 ? (long long)t * (p.overhead + keys)
                      : (long long)t * (p.overhead + n_k - n_q) + (long long)p.tile_tokens * t * (t + 1) / 2;
   }
-  __device__ __forceinline__ long long span(const PagedParams& p) const {
-    return tiles == 0 ? 0 : (before(p, tiles - 1) + width(p, tiles - 1)) * p.heads_kv;
+  template <bool WIDE>
+  __device__ __forceinline__ typename LineOf<WIDE>::T span(const PagedParams& p) const {
+    if (tiles == 0) return 0;
+    if constexpr (WIDE)
+      return (before(p, tiles - 1) + width<true>(p, tiles - 1)) * p.heads_kv;
+    else
+      return width<false>(p, 0) * p.heads_kv;
   }
 };
 
 // The sequence of query rows [a, b) and k keys; no tiles (and the bad-offsets
 // bit, if `report`) when these are out of range.
-static __device__ __noinline__ PagedSeq paged_seq(const PagedParams& p, int a, int b, int k, bool report) {
+template <bool WIDE>
+__device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int a, int b, int k, bool report) {
   PagedSeq s;
   s.row0 = a;
   s.n_q = b - a;
   s.n_k = k;
   s.tiles = 0;
   s.keys = 0;
-  if (!(0 <= a && a <= b && b <= p.total_q && b - a <= p.max_q && 0 <= k &&
-        (long long)k <= (long long)p.max_pages * p.page_size)) {
+  if (!(0 <= a && a <= b && b <= p.total_q && b - a <= p.max_q && 0 <= k && k <= p.max_keys)) {
     if (report) atomicOr(p.status, kStatusBadSeqlens);
     return s;
   }
   if (s.n_q == 0) return s;
-  s.tiles = (s.n_q + p.tile_tokens - 1) / p.tile_tokens;
   const KeyMask km = paged_mask(p, s.n_q, s.n_k);
+  s.tiles = 1;
   int nv;   // most key tiles one of the query tiles visits
-  if (s.tiles == 1) {
-    nv = tile_walk(km, 0, s.n_q - 1).n;
-  } else if (p.window_left < 0) {
-    if (p.window_right == 0 && km.off + p.tile_tokens >= max(km.pre_end, 1)) {
+  if constexpr (WIDE) {
+    s.tiles = (s.n_q + p.tile_tokens - 1) / p.tile_tokens;
+    if (s.tiles > 1 && p.window_left < 0 && p.window_right == 0 && km.off + p.tile_tokens >= max(km.pre_end, 1)) {
       s.keys = -1;
       return s;
     }
-    nv = tile_walk(km, (s.tiles - 1) * p.tile_tokens, s.n_q - 1).n;   // the last tile visits the most
+    if (s.tiles > 1 && p.window_left >= 0) {
+      const long long band = (long long)p.window_left + (p.window_right < 0 ? s.n_k : p.window_right) + p.tile_tokens;
+      const long long all = (s.n_k + kPagedKeyTile - 1) / kPagedKeyTile;
+      const long long n = (km.pre_end + kPagedKeyTile - 1) / kPagedKeyTile + band / kPagedKeyTile + 2;
+      nv = (int)(n < all ? n : all);
+    } else {   // without a left window the last tile visits the most
+      nv = tile_walk(km, (s.tiles - 1) * p.tile_tokens, s.n_q - 1).n;
+    }
   } else {
-    const long long band = (long long)p.window_left + (p.window_right < 0 ? s.n_k : p.window_right) + p.tile_tokens;
-    const long long all = (s.n_k + kPagedKeyTile - 1) / kPagedKeyTile;
-    const long long n = (km.pre_end + kPagedKeyTile - 1) / kPagedKeyTile + band / kPagedKeyTile + 2;
-    nv = (int)(n < all ? n : all);
+    nv = tile_walk(km, 0, s.n_q - 1).n;
   }
   s.keys = max(nv, 1) * kPagedKeyTile;
   return s;
 }
 
-__device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int i, bool report) {
-  return paged_seq(p, __ldg(p.cu_q + i), __ldg(p.cu_q + i + 1), __ldg(p.lens_k + i), report);
+template <bool WIDE>
+static __device__ __noinline__ PagedSeq read_seq(const PagedParams& p, int i, bool report) {
+  return paged_seq<WIDE>(p, __ldg(p.cu_q + i), __ldg(p.cu_q + i + 1), __ldg(p.lens_k + i), report);
 }
 
 // Where a CTA starts, and the pieces' size.
+template <bool WIDE>
 struct PagedPlace {
-  long long at;      // the sequence's start on the line
-  long long share;   // keys of a piece; 0: one pair per CTA
-  long long total;   // the line's length
+  typename LineOf<WIDE>::T at;      // the sequence's start on the line
+  typename LineOf<WIDE>::T share;   // a piece; 0: one pair per CTA
+  typename LineOf<WIDE>::T total;   // the line's length
   PagedSeq s;        // the sequence that holds the position
   int seq;           // its index, or -1: past the end
   int rank;          // one pair per CTA: the pair's index in its sequence
 };
 
+template <bool WIDE>
 struct PagedScan {
-  long long warp_sum[3][8];
-  PagedPlace place;
+  typename LineOf<WIDE>::T warp_sum[3][8];
+  PagedPlace<WIDE> place;
 };
 
 // Finds the sequence that holds piece `piece`'s start (or, where the batch
 // runs one pair per CTA, pair `piece`).  Every thread sums a run of sequences;
 // every thread returns the same.
-template <int THREADS>
-__device__ __forceinline__ PagedPlace find_place(const PagedParams& p, int piece, PagedScan* sh, bool report) {
+template <int THREADS, bool WIDE>
+__device__ __forceinline__ PagedPlace<WIDE> find_place(const PagedParams& p, int piece, PagedScan<WIDE>* sh,
+                                                       bool report) {
+  using Line = typename LineOf<WIDE>::T;
   constexpr int NW = THREADS / 32;
   const int tid = (int)threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int per = (p.batch + THREADS - 1) / THREADS;
   const int i0 = min(tid * per, p.batch), i1 = min(i0 + per, p.batch);
-  long long span = 0, pairs = 0, chunks = 0;   // chunks: the line's part in sequences of several query tiles
+  // chunks: the line's part in sequences of several query tiles
+  Line span = 0, pairs = 0, chunks = 0;
   PagedSeq s;
   s.tiles = s.keys = s.n_q = s.n_k = s.row0 = 0;
+#pragma unroll 1
   for (int i = i0; i < i1; ++i) {
-    s = paged_seq(p, i, report);
-    const long long x = s.span(p);
+    s = read_seq<WIDE>(p, i, report);
+    const Line x = s.span<WIDE>(p);
     span += x;
-    pairs += (long long)s.tiles * p.heads_kv;
-    if (s.tiles > 1) chunks += x;
+    if constexpr (WIDE) {
+      pairs += (Line)s.tiles * p.heads_kv;
+      if (s.tiles > 1) chunks += x;
+    }
   }
-  long long a = span, b = pairs, c = chunks;
+  Line a = span, b = pairs, c = chunks;
 #pragma unroll 1
   for (int o = 1; o < 32; o <<= 1) {
-    const long long va = __shfl_up_sync(0xffffffffu, a, o), vb = __shfl_up_sync(0xffffffffu, b, o),
-                    vc = __shfl_up_sync(0xffffffffu, c, o);
-    if (lane >= o) {
-      a += va;
-      b += vb;
-      c += vc;
+    const Line va = __shfl_up_sync(0xffffffffu, a, o);
+    if (lane >= o) a += va;
+    if constexpr (WIDE) {
+      const Line vb = __shfl_up_sync(0xffffffffu, b, o), vc = __shfl_up_sync(0xffffffffu, c, o);
+      if (lane >= o) {
+        b += vb;
+        c += vc;
+      }
     }
   }
   if (lane == 31) {
     sh->warp_sum[0][w] = a;
-    sh->warp_sum[1][w] = b;
-    sh->warp_sum[2][w] = c;
+    if constexpr (WIDE) {
+      sh->warp_sum[1][w] = b;
+      sh->warp_sum[2][w] = c;
+    }
   }
   if (tid == 0) sh->place.seq = -1;
   __syncthreads();
   a -= span;
   b -= pairs;
-  long long total = 0, all_pairs = 0, all_chunks = 0;
+  Line total = 0, all_pairs = 0, all_chunks = 0;
 #pragma unroll 1
   for (int j = 0; j < NW; ++j) {
     if (j == w) {
@@ -294,19 +334,22 @@ __device__ __forceinline__ PagedPlace find_place(const PagedParams& p, int piece
       b += all_pairs;
     }
     total += sh->warp_sum[0][j];
-    all_pairs += sh->warp_sum[1][j];
-    all_chunks += sh->warp_sum[2][j];
+    if constexpr (WIDE) {
+      all_pairs += sh->warp_sum[1][j];
+      all_chunks += sh->warp_sum[2][j];
+    }
   }
-  long long share = line_div(total + p.ctas - 1, p.ctas);
-  if (share < p.min_share) share = p.min_share;
-  const bool whole = p.pair_ctas > 0 && all_pairs >= 4ll * p.ctas && 2 * all_chunks > total;
-  const long long pos = whole ? piece : piece * share;
-  const long long mine = whole ? b : a, size = whole ? pairs : span;
+  Line share = line_div(total + p.ctas - 1, (Line)p.ctas);
+  if (share < p.min_share / LineOf<WIDE>::KEYS) share = p.min_share / LineOf<WIDE>::KEYS;
+  const bool whole = WIDE && p.pair_ctas > 0 && all_pairs >= 4ll * p.ctas && 2 * all_chunks > total;
+  const Line pos = whole ? piece : piece * share;
+  const Line mine = whole ? b : a, size = whole ? pairs : span;
   if (pos >= mine && pos < mine + size) {
-    long long x = a, n = b;
+    Line x = a, n = b;
+#pragma unroll 1
     for (int i = i0; i < i1; ++i) {
-      if (per > 1) s = paged_seq(p, i, false);
-      const long long sx = s.span(p), sn = (long long)s.tiles * p.heads_kv;
+      if (per > 1) s = read_seq<WIDE>(p, i, false);
+      const Line sx = s.span<WIDE>(p), sn = WIDE ? (Line)s.tiles * p.heads_kv : 0;
       if (whole ? pos < n + sn : pos < x + sx) {
         sh->place.at = x;
         sh->place.s = s;
@@ -319,7 +362,7 @@ __device__ __forceinline__ PagedPlace find_place(const PagedParams& p, int piece
     }
   }
   __syncthreads();
-  PagedPlace r = sh->place;
+  PagedPlace<WIDE> r = sh->place;
   r.share = whole ? 0 : share;
   r.total = total;
   return r;
@@ -327,20 +370,27 @@ __device__ __forceinline__ PagedPlace find_place(const PagedParams& p, int piece
 
 // The pair of sequence s that holds offset y of the sequence's span: query
 // tile, head, and the pair's start within the span.
-__device__ __forceinline__ long long pair_at(const PagedParams& p, const PagedSeq& s, long long y, int& tile, int& h) {
-  int lo = 0, hi = s.tiles;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (s.before(p, mid) * p.heads_kv <= y)
-      lo = mid;
-    else
-      hi = mid;
+template <bool WIDE>
+__device__ __forceinline__ typename LineOf<WIDE>::T pair_at(const PagedParams& p, const PagedSeq& s,
+                                                            typename LineOf<WIDE>::T y, int& tile, int& h) {
+  tile = 0;
+  typename LineOf<WIDE>::T base = 0;
+  if constexpr (WIDE) {
+    int lo = 0, hi = s.tiles;
+#pragma unroll 1
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (s.before(p, mid) * p.heads_kv <= y)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    tile = lo;
+    base = s.before(p, lo) * p.heads_kv;
   }
-  tile = lo;
-  const long long base = s.before(p, lo) * p.heads_kv;
-  const int w = s.width(p, lo);
-  h = (int)line_div(y - base, w);
-  return base + (long long)h * w;
+  const int w = s.width<WIDE>(p, tile);
+  h = (int)line_div(y - base, (typename LineOf<WIDE>::T)w);
+  return base + (typename LineOf<WIDE>::T)h * w;
 }
 
 // First visited key tile at or after offset y of a pair's span, of n.
@@ -349,11 +399,14 @@ __device__ __forceinline__ int span_tile(const PagedParams& p, long long y, int 
   const long long j = k <= 0 ? 0 : (k + kPagedKeyTile - 1) / kPagedKeyTile;
   return (int)(j < n ? j : n);
 }
+__device__ __forceinline__ int span_tile(const PagedParams& p, int y, int n) {
+  return max(0, min(y - p.overhead / kPagedKeyTile, n));
+}
 
 // A pair whose partials are to be merged: left by the CTA at whose start the
-// pair is cut for the first time.
+// pair is cut for the first time.  In keys, whatever the line's unit.
 struct PagedMerge {
-  long long x, share;   // the pair's start on the line; keys of a piece
+  long long x, share;   // the pair's start on the line; a piece
   int w, n;             // its span; its key tiles
   int first;            // the piece that holds its start (last: (x + w - 1) / share), or -1: nothing to merge
   int row, rows, h;     // first row of q / o / lse; live rows; K/V head
@@ -363,14 +416,15 @@ static_assert(sizeof(PagedMerge) == kPagedMergeBytes, "merge description");
 // Walks the fragments of one CTA's piece; every lane of the TMA warp in step.
 // What the pairs of one query tile share is worked out once, and the next
 // sequence's lengths are read a sequence ahead.
-template <bool BAND>
+template <bool BAND, bool WIDE>
 struct FragWalk {
+  using Line = typename LineOf<WIDE>::T;
   PagedSeq s;
   PagedFrag base;     // the current query tile's facts, for all of its key tiles
   int tiles_n;        // its key tiles
   int w;              // its pairs' span
   const int* table;   // the sequence's block-table row
-  long long x, begin, end;   // the pair's start on the line; the piece
+  Line x, begin, end;   // the pair's start on the line; the piece
   int cta, seq, tile, h;
   int next_a, next_b, next_k;   // sequence seq + 1
   bool more, one;     // one: a single pair, whole
@@ -389,15 +443,14 @@ struct FragWalk {
     base.km = paged_mask(p, s.n_q, s.n_k);
     const TileWalk walk = tile_walk(base.km, q0, last);
     tiles_n = walk.n;
-    w = s.width(p, tile);
+    w = s.template width<WIDE>(p, tile);
     base.row = s.row0 + q0;
     base.q0 = q0;
     base.rows = (last + 1 - q0) * p.group;
     // few keys, or a tile of few rows, where the second PV product hides behind
     // reading the keys and the masked tiles would otherwise run code that the
-    // others have not brought in (measured: 256 requests of 1..1000 keys, d = 128
-    // bf16, 172 us with the masked tiles alone split)
-    base.split = s.n_k <= 2 * kPagedKeyTile || p.slot_rows <= kPagedTileRows / 2;
+    // others have not brought in
+    base.split = !WIDE || s.n_k <= 2 * kPagedKeyTile;
     base.npre = walk.npre;
     base.skip = walk.skip;
     base.lo = walk.lo;
@@ -408,7 +461,7 @@ struct FragWalk {
     base.tm.hi -= walk.skip;
   }
 
-  __device__ __forceinline__ void start(const PagedParams& p, const PagedPlace& pl, int piece) {
+  __device__ __forceinline__ void start(const PagedParams& p, const PagedPlace<WIDE>& pl, int piece) {
     cta = piece;
     seq = pl.seq;
     s = pl.s;
@@ -416,36 +469,35 @@ struct FragWalk {
     one = pl.share == 0;
     merge.first = -1;
     table = p.table + (long long)seq * p.table_stride;
-    if (one) {   // the query tiles from the last (the most keys) to the first
-      h = pl.rank % p.heads_kv;
-      tile = s.tiles - 1 - pl.rank / p.heads_kv;
-      x = begin = 0;
-      start_tile(p);
-      end = w;
-      return;
-    }
     begin = piece * pl.share;
     end = min(begin + pl.share, pl.total);
-    x = pl.at + pair_at(p, s, begin - pl.at, tile, h);
+    if (WIDE && one) {   // the query tiles from the last (the most keys) to the first
+      h = pl.rank % p.heads_kv;
+      tile = s.tiles - 1 - pl.rank / p.heads_kv;
+      x = 0;
+    } else {
+      x = pl.at + pair_at<WIDE>(p, s, begin - pl.at, tile, h);
+      read_ahead(p);
+    }
     start_tile(p);
-    read_ahead(p);
+    if (WIDE && one) end = w;
     if (begin > x) {
+      constexpr long long KEYS = LineOf<WIDE>::KEYS;
       merge.first = x >= begin - pl.share ? piece - 1 : -1;
-      merge.x = x;
-      merge.share = pl.share;
-      merge.w = w;
+      merge.x = x * KEYS;
+      merge.share = pl.share * KEYS;
+      merge.w = w * (int)KEYS;
       merge.n = tiles_n;
       merge.row = base.row;
       merge.rows = base.rows;
       merge.h = h;
     }
   }
-
 };
 
 // The next fragment, to shared memory; false when the piece is done.
-template <bool BAND>
-__device__ __forceinline__ bool next_fragment(FragWalk<BAND>& k, const PagedParams& p, PagedFrag* dst, int lane) {
+template <bool BAND, bool WIDE>
+__device__ __forceinline__ bool next_fragment(FragWalk<BAND, WIDE>& k, const PagedParams& p, PagedFrag* dst, int lane) {
   while (k.more) {
     const bool from_start = k.begin <= k.x, to_end = k.end - k.x >= k.w, whole = from_start && to_end;
     const int j0 = from_start ? 0 : span_tile(p, k.begin - k.x, k.tiles_n);
@@ -466,7 +518,7 @@ __device__ __forceinline__ bool next_fragment(FragWalk<BAND>& k, const PagedPara
       k.more = false;
     } else if (++k.h == p.heads_kv) {
       k.h = 0;
-      if (++k.tile == k.s.tiles) {
+      if (!WIDE || ++k.tile == k.s.tiles) {
         k.tile = 0;
         do {
           if (++k.seq >= p.batch) {
@@ -474,7 +526,7 @@ __device__ __forceinline__ bool next_fragment(FragWalk<BAND>& k, const PagedPara
             break;
           }
           k.table += p.table_stride;
-          k.s = paged_seq(p, k.next_a, k.next_b, k.next_k, false);
+          k.s = paged_seq<WIDE>(p, k.next_a, k.next_b, k.next_k, false);
           k.read_ahead(p);
         } while (k.s.tiles == 0);
       }
@@ -539,9 +591,9 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map
 // The planner warp (few rows): walks the piece's fragments, up to four ahead of
 // the softmax.
 template <class C, bool BAND>
-__device__ __forceinline__ void pg_plan(const PagedCtx<C>& t, const PagedParams& p, const PagedPlace& place, int piece,
+__device__ __forceinline__ void pg_plan(const PagedCtx<C>& t, const PagedParams& p, const PagedPlace<C::WIDE>& place, int piece,
                                         int lane) {
-  FragWalk<BAND> walk;
+  FragWalk<BAND, C::WIDE> walk;
   walk.start(p, place, piece);
   bool have = true;
 #pragma unroll 1
@@ -567,9 +619,9 @@ __device__ __forceinline__ void pg_plan(const PagedCtx<C>& t, const PagedParams&
 // wait and the issue.
 template <class C, bool BAND>
 __device__ __forceinline__ void pg_load(const PagedCtx<C>& t, const PagedParams& p, const CUtensorMap* tm_q,
-                                        const CUtensorMap* tm_k, const CUtensorMap* tm_v, const PagedPlace& place,
+                                        const CUtensorMap* tm_k, const CUtensorMap* tm_v, const PagedPlace<C::WIDE>& place,
                                         int piece, int lane) {
-  FragWalk<BAND> walk;
+  FragWalk<BAND, C::WIDE> walk;
   if constexpr (!C::PLANNER) {
     walk.start(p, place, piece);
     if (lane == 0 && piece < p.ctas) p.merges[piece] = walk.merge;   // (one pair per CTA: piece may be larger)
@@ -1064,8 +1116,8 @@ __global__ void __launch_bounds__(PagedConfig<D, WIDE>::THREADS, PagedConfig<D, 
   const uint32_t sbase = smem_u32(smem);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
-  PagedScan* scan = reinterpret_cast<PagedScan*>(smem + C::OFF_SCAN);
-  static_assert(sizeof(PagedScan) <= 320 && C::OFF_SCAN % 8 == 0, "scan area");
+  PagedScan<WIDE>* scan = reinterpret_cast<PagedScan<WIDE>*>(smem + C::OFF_SCAN);
+  static_assert(sizeof(PagedScan<WIDE>) <= 320 && C::OFF_SCAN % 8 == 0, "scan area");
   const int warp = (int)(threadIdx.x >> 5);
   const int lane = (int)(threadIdx.x & 31);
   grid_launch_dependents();   // the merge may be scheduled once every CTA has started; it waits for the partials
@@ -1098,7 +1150,7 @@ __global__ void __launch_bounds__(PagedConfig<D, WIDE>::THREADS, PagedConfig<D, 
   }
   const int piece = (int)blockIdx.x;
   tc_fence_before();
-  const PagedPlace place = find_place<C::THREADS>(p, piece, scan, blockIdx.x == 0);   // with its barriers
+  const PagedPlace<WIDE> place = find_place<C::THREADS, WIDE>(p, piece, scan, blockIdx.x == 0);   // with its barriers
   tc_fence_after();
   t.tmem = *tmem_slot;
 
@@ -1252,9 +1304,8 @@ int launch_paged_kernels(const PagedLaunchArgs& a) {
 
 template <int D, bool BF16>
 int launch_paged_rows(const PagedLaunchArgs& a) {
-  const bool wide = a.p.slot_rows > kPagedTileRows / 2;
-  if (a.band) return wide ? launch_paged_kernels<D, BF16, true, true>(a) : launch_paged_kernels<D, BF16, true, false>(a);
-  return wide ? launch_paged_kernels<D, BF16, false, true>(a) : launch_paged_kernels<D, BF16, false, false>(a);
+  if (a.band) return a.wide ? launch_paged_kernels<D, BF16, true, true>(a) : launch_paged_kernels<D, BF16, true, false>(a);
+  return a.wide ? launch_paged_kernels<D, BF16, false, true>(a) : launch_paged_kernels<D, BF16, false, false>(a);
 }
 
 template <int D>

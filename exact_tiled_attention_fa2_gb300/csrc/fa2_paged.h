@@ -43,7 +43,8 @@ struct PagedParams {
   int batch, heads_kv, group;
   int tile_tokens;        // tokens of a query tile: 128 / group
   int total_q, max_q;
-  int num_pages, page_size, max_pages;
+  int num_pages, page_size;
+  int max_keys;           // a sequence's keys at most: max_pages * page_size
   unsigned page_magic, page_shift;   // k / page_size = (umulhi(k, magic) + k) >> shift for 0 <= k < 2^31
   int box_rows;           // key rows of a box: 8, 16, 32 or 64
   PagedSide k_side, v_side;
@@ -53,8 +54,8 @@ struct PagedParams {
   int ctas;               // pieces the line of work is cut into
   int pair_ctas;          // CTAs for one (query tile, K/V head) pair each where
                           // the batch may have that many, or 0
-  int overhead;           // a pair's fixed cost on the line, in keys
-  int min_share;          // keys of a piece at least
+  int overhead;           // a pair's fixed cost on the line, in keys (whole key tiles)
+  int min_share;          // keys of a piece at least (whole key tiles)
   int slot_rows;          // rows of a Q load and of a partial state: group x tokens
   float* ws_o;            // [2 * ctas][d / 4][slot_rows][4] partial O~
   float* ws_ml;           // [2 * ctas][slot_rows][2] partial (m, l), exp2 domain
@@ -67,6 +68,7 @@ struct PagedLaunchArgs {
   PagedParams p;
   bool bf16;
   bool band;              // window_left >= 0 or prefix > 0
+  bool wide;              // more than 64 rows in a query tile, or a line of 2^31 key tiles
   cudaStream_t stream;
 };
 

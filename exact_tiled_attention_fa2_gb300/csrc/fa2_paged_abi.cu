@@ -237,7 +237,7 @@ int paged_forward(const fa2_paged_params& a, void* workspace, size_t workspace_b
   p.max_q = s.max_q;
   p.num_pages = c.num_pages;
   p.page_size = c.page_size;
-  p.max_pages = a.max_pages;
+  p.max_keys = a.max_pages * c.page_size;
   p.window_left = a.window_left;
   p.window_right = a.window_right;
   p.prefix = a.prefix_len;
@@ -245,13 +245,16 @@ int paged_forward(const fa2_paged_params& a, void* workspace, size_t workspace_b
   p.scale_log2_mag = std::fmax(std::fabs(scale_log2), FLT_MIN);
   p.qk_negate = scale_log2 < 0.f ? 1u << 13 : 0u;   // the negate-A bit of the S product's descriptor
   p.slot_rows = s.group * s.box_tokens;
-  p.overhead = kPagedOverhead + 2 * p.slot_rows;
+  p.overhead = (kPagedOverhead + 2 * p.slot_rows + 63) / 64 * 64;
   p.ctas = s.ctas;
   p.pair_ctas = s.pair_ctas;
-  p.min_share = kPagedMinShare > 8 * p.slot_rows ? kPagedMinShare : 8 * p.slot_rows;
+  p.min_share = kPagedMinShare > 8 * p.slot_rows ? kPagedMinShare : (8 * p.slot_rows + 63) / 64 * 64;
   p.ws_o = static_cast<float*>(workspace);
   p.ws_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + s.ws_o_bytes);
   p.merges = reinterpret_cast<PagedMerge*>(static_cast<uint8_t*>(workspace) + s.ws_o_bytes + s.ws_ml_bytes);
+  // few rows (every sequence is then one query tile): the line in key tiles and 32 bits
+  la.wide = p.slot_rows > kPagedTileRows / 2 ||
+            (double)a.batch * c.heads * ((p.max_keys + p.overhead) / 64 + 2.0) + 1e6 > 2147483647.0;
   la.band = a.window_left >= 0 || a.prefix_len > 0;
   la.stream = stream;
   int e = 0;
