@@ -49,23 +49,23 @@
 namespace fa2 {
 
 // Barriers (8 bytes each).  Phases count key tiles g (K, V, S, P, O) or
-// fragments f of the CTA (the others).
+// fragments f of the CTA (the others).  One completion tells all who wait for
+// it: S(g) the softmax warps (scores there) and the TMA warp (K stage free),
+// PV(g) the TMA warp (V stage free) and the softmax warps (O~ may be rescaled
+// or read); none of them can fall a whole round of stages behind.
 enum : int {
   PG_Q = 0,        // + f & 1: the fragment's description and Q are in shared memory
   PG_QEMPTY = 2,   // + f & 1: the fragment's last S product is done with Q
-  PG_S = 4,        // + buffer
-  PG_P = 6,        // + buffer (four softmax warps)
-  PG_ODONE = 8,    // + f & 1: the softmax warps are done with O~ and the description
-  PG_O = 10,       // after every PV product
-  PG_OLAST = 11,   // after a fragment's last PV product
-  PG_EXIT = 12,
-  PG_KFULL = 13,   // + stage
-  PG_KEMPTY = 17,  // + stage
+  PG_P = 4,        // + buffer (four softmax warps)
+  PG_ODONE = 6,    // + f & 1: the softmax warps are done with O~ and the description
+  PG_EXIT = 8,
+  PG_S = 9,        // + K stage: S(g) complete
+  PG_O = 13,       // + V stage: PV(g) complete
+  PG_KFULL = 17,   // + stage
   PG_VFULL = 21,   // + stage
-  PG_VEMPTY = 25,  // + stage
-  PG_PLAN = 29,    // + f & 3: the fragment's description is there (planner -> TMA warp)
-  PG_FREE = 33,    // + f & 3: its slot is free (softmax warps -> planner)
-  PG_BARS = 37,
+  PG_PLAN = 25,    // + f & 3: the fragment's description is there (planner -> TMA warp)
+  PG_FREE = 29,    // + f & 3: its slot is free (softmax warps -> planner)
+  PG_BARS = 33,
 };
 
 // Everything the softmax warps and the MMA thread need of a fragment: written
@@ -79,7 +79,7 @@ struct PagedFrag {
   int rows;        // live rows: group x tokens
   int h;           // K/V head
   int slot;        // partial slot, or -1: write O and L
-  int split;       // every bf16 P is split, not the masked tiles' alone
+  int split;       // every bf16 P is split (many rows: else the masked tiles')
   TileMask tm;     // key tiles every row sees, by index from j0
   KeyMask km;
   int npre, skip;  // visited index j is key tile j + (j >= npre ? skip : 0)
@@ -447,10 +447,10 @@ struct FragWalk {
     base.row = s.row0 + q0;
     base.q0 = q0;
     base.rows = (last + 1 - q0) * p.group;
-    // few keys, or a tile of few rows, where the second PV product hides behind
-    // reading the keys and the masked tiles would otherwise run code that the
-    // others have not brought in
-    base.split = !WIDE || s.n_k <= 2 * kPagedKeyTile;
+    // Few keys.  With few rows this is all (their masked tile is one of many keys'
+    // tiles, not a causal diagonal, and where a pair has many the MMA thread's
+    // issue bounds the loop: d = 64, 12 products a tile against 8)
+    base.split = WIDE ? s.n_k <= 2 * kPagedKeyTile : tiles_n <= 3;
     base.npre = walk.npre;
     base.skip = walk.skip;
     base.lo = walk.lo;
@@ -538,6 +538,14 @@ __device__ __forceinline__ bool next_fragment(FragWalk<BAND, WIDE>& k, const Pag
     }
   }
   return false;
+}
+
+// The same out of line, for the TMA warp between its loads (inlined there, a
+// prompt chunk of 2048 over 16384 keys takes 449 us in place of 428).
+template <bool BAND, bool WIDE>
+static __device__ __noinline__ bool next_fragment_far(FragWalk<BAND, WIDE>& k, const PagedParams& p, PagedFrag* dst,
+                                                      int lane) {
+  return next_fragment(k, p, dst, lane);
 }
 
 // ---------------------------------------------------------------- the warps' roles
@@ -659,7 +667,7 @@ __device__ __forceinline__ void pg_load(const PagedCtx<C>& t, const PagedParams&
       ok = t.warp_wait(PG_PLAN + (walked & 3), walked >> 2, kSiteProducerEmpty, lane);
       if (!ok || f->n < 0) return;
     } else {
-      if (!next_fragment(walk, p, f, lane)) return;
+      if (!next_fragment_far(walk, p, f, lane)) return;
     }
     first4 = fetch(f, 0);
     ++walked;
@@ -725,7 +733,7 @@ __device__ __forceinline__ void pg_load(const PagedCtx<C>& t, const PagedParams&
   auto load_v = [&]() {
     if (v_left == 0) return;
     const int s = gv % C::VSTAGES;
-    if (gv >= C::VSTAGES) ok = t.warp_wait(PG_VEMPTY + s, gv / C::VSTAGES - 1, kSiteProducerEmpty, lane);
+    if (gv >= C::VSTAGES) ok = t.warp_wait(PG_O + s, gv / C::VSTAGES - 1, kSiteProducerEmpty, lane);
     if (!ok) return;
     issue(cv_last, lanes_last, v_left - 1, tm_v, t.sV + s * C::KV_BYTES, t.bar(PG_VFULL + s));
     v_left = 0;
@@ -759,7 +767,7 @@ __device__ __forceinline__ void pg_load(const PagedCtx<C>& t, const PagedParams&
       lanes = __ballot_sync(0xffffffffu, now.row >= 0);
     }
     const int s = g % C::KSTAGES;
-    if (g >= C::KSTAGES) ok = t.warp_wait(PG_KEMPTY + s, g / C::KSTAGES - 1, kSiteProducerEmpty, lane);
+    if (g >= C::KSTAGES) ok = t.warp_wait(PG_S + s, g / C::KSTAGES - 1, kSiteProducerEmpty, lane);
     if (!ok) break;
     issue(ck, lanes, j & 3, tm_k, t.sK + s * C::KV_BYTES, t.bar(PG_KFULL + s));
     ++g;
@@ -830,8 +838,7 @@ __device__ __forceinline__ void pg_mma(const PagedCtx<C>& t, const PagedParams& 
       for (int k = 0; k < C::D / 16; ++k)
         umma_ss(tS, a0 + (uint64_t)(((k >> 2) * (C::BR * 128) + (k & 3) * 32) >> 4),
                 b0 + (uint64_t)(((k >> 2) * 1024 + (k & 3) * 32) >> 4), idesc_qk, k > 0 ? 1u : 0u);
-      umma_commit(t.bar(PG_S + (g & 1)));
-      umma_commit(t.bar(PG_KEMPTY + sk));
+      umma_commit(t.bar(PG_S + sk));
       if (i + 1 == n) umma_commit(t.bar(PG_QEMPTY + (nf & 1)));
       return true;
     };
@@ -843,7 +850,7 @@ __device__ __forceinline__ void pg_mma(const PagedCtx<C>& t, const PagedParams& 
       const uint64_t b0 = dv0 + (uint64_t)((sv * C::KV_BYTES) >> 4);
       const uint32_t tS = t.tmem + C::TMEM_S + 64 * (g & 1);
       const uint32_t tO = t.tmem + C::TMEM_O;
-      const bool split = split_tile<BF16>(!tm.full(j), always);
+      const bool split = BF16 && (always || (C::WIDE && !tm.full(j)));
       auto product = [&](bool both) {
 #pragma unroll
         for (int k = 0; k < C::BC / 16; ++k) {
@@ -853,13 +860,11 @@ __device__ __forceinline__ void pg_mma(const PagedCtx<C>& t, const PagedParams& 
           if (both) umma_ts(tO, pk + 16, bk, idesc_pv, 1u);
         }
       };
-      if (C::WIDE && !split)
-        product(false);
+      if (split)
+        product(true);
       else
-        product(BF16);   // few rows: bf16 P is always split
-      umma_commit(t.bar(PG_O));
-      umma_commit(t.bar(PG_VEMPTY + sv));
-      if (j + 1 == n) umma_commit(t.bar(PG_OLAST));
+        product(false);
+      umma_commit(t.bar(PG_O + sv));
       return true;
     };
     if constexpr (C::WIDE) {
@@ -931,7 +936,7 @@ __device__ __forceinline__ void pg_softmax(const PagedCtx<C>& t, const PagedPara
     const bool ok = paged_wait<C::WIDE>(t.bar(bar), (uint32_t)phase & 1, t.abort_flag, t.status, site);
     return __all_sync(0xffffffffu, ok);
   };
-  int g = 0, products = 0;   // key tiles; fragments that had some
+  int g = 0;   // key tiles
   for (int nf = 0;; ++nf) {
     if (!wait(PG_Q + (nf & 1), nf >> 1, kSiteMmaQ)) return;
     const PagedFrag* f = t.frags + (nf & 3);
@@ -947,12 +952,12 @@ __device__ __forceinline__ void pg_softmax(const PagedCtx<C>& t, const PagedPara
     float l_run = 0.f;
     for (int j = 0; j < n; ++j, ++g) {
       const uint32_t tS = t.tmem + lane_off + C::TMEM_S + 64 * (g & 1);
-      if (!wait(PG_S + (g & 1), g >> 1, kSiteSoftmaxS)) return;
+      if (!wait(PG_S + g % C::KSTAGES, g / C::KSTAGES, kSiteSoftmaxS)) return;
       tc_fence_after();
       const bool masked = !tmask.full(j);
       if (warp_live) {
         const int k0 = f->tile(f->j0 + j) * C::BC, tok_row = f->q0 + tok;
-        const bool split = split_tile<BF16>(masked, always);
+        const bool split = BF16 && (always || (C::WIDE && masked));
         // The tile's 64 scores: in registers (a warp of live rows, where the
         // softmax is what bounds the loop), or read from tensor memory twice in
         // runs of 32, half the code (few rows: the loop waits for the keys, and
@@ -1000,7 +1005,7 @@ __device__ __forceinline__ void pg_softmax(const PagedCtx<C>& t, const PagedPara
         const float2 neg_m2 = make_float2(-m_use, -m_use);
         float2 sum0 = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
         if constexpr (C::WIDE) {
-          if (BF16 && split) {
+          if (split) {
             paged_p_run<BF16, true>(sr, tS, scale2, neg_m2, sum0, sum1);
             paged_p_run<BF16, true>(sr + 32, tS + 32, scale2, neg_m2, sum0, sum1);
           } else {
@@ -1011,14 +1016,17 @@ __device__ __forceinline__ void pg_softmax(const PagedCtx<C>& t, const PagedPara
 #pragma unroll 1
           for (int c = 0; c < C::BC; c += 32) {
             read(c);
-            paged_p_run<BF16, BF16>(sr, tS + c, scale2, neg_m2, sum0, sum1);
+            if (split)
+              paged_p_run<BF16, true>(sr, tS + c, scale2, neg_m2, sum0, sum1);
+            else
+              paged_p_run<BF16, false>(sr, tS + c, scale2, neg_m2, sum0, sum1);
           }
         }
         const float2 sum2 = __fadd2_rn(sum0, sum1);
         l_run = l_run * alpha + (sum2.x + sum2.y);
         if (j > 0 && __any_sync(0xffffffffu, raise)) {
           // S(g) was issued before PV(g-1): wait for that product before rescaling
-          if (!wait(PG_O, g - 1, kSiteSoftmaxO)) return;
+          if (!wait(PG_O + (g - 1) % C::VSTAGES, (g - 1) / C::VSTAGES, kSiteSoftmaxO)) return;
           tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < C::D; c += 32) {
@@ -1048,7 +1056,7 @@ __device__ __forceinline__ void pg_softmax(const PagedCtx<C>& t, const PagedPara
       if (lane == 0) mbar_arrive(t.bar(PG_P + (g & 1)));
     }
     if (n > 0) {
-      if (!wait(PG_OLAST, products++, kSiteEpilogueO)) return;
+      if (!wait(PG_O + (g - 1) % C::VSTAGES, (g - 1) / C::VSTAGES, kSiteEpilogueO)) return;
       tc_fence_after();
     }
     const int slot_at = f->slot;
@@ -1140,7 +1148,7 @@ __global__ void __launch_bounds__(PagedConfig<D, WIDE>::THREADS, PagedConfig<D, 
   if (warp == C::TMA_WARP && lane == 0) {
 #pragma unroll 1
     for (int i = 0; i < PG_BARS; ++i)
-      mbar_init(t.bar(i), (i >= PG_P && i < PG_O) || i >= PG_FREE ? 4 : 1);   // four softmax warps, or one arrival
+      mbar_init(t.bar(i), (i >= PG_P && i < PG_EXIT) || i >= PG_FREE ? 4 : 1);   // four softmax warps, or one arrival
     *abort_flag = 0;
     fence_mbar_init();
     fence_proxy_async_smem();
