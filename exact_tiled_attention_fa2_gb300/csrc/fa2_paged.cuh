@@ -274,6 +274,7 @@ struct PagedPlace {
 template <bool WIDE>
 struct PagedScan {
   typename LineOf<WIDE>::T warp_sum[3][8];
+  int warp_longest[8];
   PagedPlace<WIDE> place;
 };
 
@@ -284,12 +285,14 @@ template <int THREADS, bool WIDE>
 __device__ __forceinline__ PagedPlace<WIDE> find_place(const PagedParams& p, int piece, PagedScan<WIDE>* sh,
                                                        bool report) {
   using Line = typename LineOf<WIDE>::T;
+  constexpr int KEYS = LineOf<WIDE>::KEYS;
   constexpr int NW = THREADS / 32;
   const int tid = (int)threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int per = (p.batch + THREADS - 1) / THREADS;
   const int i0 = min(tid * per, p.batch), i1 = min(i0 + per, p.batch);
   // chunks: the line's part in sequences of several query tiles
   Line span = 0, pairs = 0, chunks = 0;
+  int longest = 0;   // pair
   PagedSeq s;
   s.tiles = s.keys = s.n_q = s.n_k = s.row0 = 0;
 #pragma unroll 1
@@ -297,30 +300,27 @@ __device__ __forceinline__ PagedPlace<WIDE> find_place(const PagedParams& p, int
     s = read_seq<WIDE>(p, i, report);
     const Line x = s.span<WIDE>(p);
     span += x;
-    if constexpr (WIDE) {
-      pairs += (Line)s.tiles * p.heads_kv;
-      if (s.tiles > 1) chunks += x;
-    }
+    pairs += (Line)s.tiles * p.heads_kv;
+    if (s.tiles > 0) longest = max(longest, s.width<WIDE>(p, s.tiles - 1));
+    if (WIDE && s.tiles > 1) chunks += x;
   }
+  longest = __reduce_max_sync(0xffffffffu, longest);
   Line a = span, b = pairs, c = chunks;
 #pragma unroll 1
   for (int o = 1; o < 32; o <<= 1) {
-    const Line va = __shfl_up_sync(0xffffffffu, a, o);
-    if (lane >= o) a += va;
-    if constexpr (WIDE) {
-      const Line vb = __shfl_up_sync(0xffffffffu, b, o), vc = __shfl_up_sync(0xffffffffu, c, o);
-      if (lane >= o) {
-        b += vb;
-        c += vc;
-      }
+    const Line va = __shfl_up_sync(0xffffffffu, a, o), vb = __shfl_up_sync(0xffffffffu, b, o);
+    const Line vc = WIDE ? __shfl_up_sync(0xffffffffu, c, o) : 0;
+    if (lane >= o) {
+      a += va;
+      b += vb;
+      c += vc;
     }
   }
   if (lane == 31) {
     sh->warp_sum[0][w] = a;
-    if constexpr (WIDE) {
-      sh->warp_sum[1][w] = b;
-      sh->warp_sum[2][w] = c;
-    }
+    sh->warp_sum[1][w] = b;
+    sh->warp_sum[2][w] = c;
+    sh->warp_longest[w] = longest;
   }
   if (tid == 0) sh->place.seq = -1;
   __syncthreads();
@@ -334,14 +334,16 @@ __device__ __forceinline__ PagedPlace<WIDE> find_place(const PagedParams& p, int
       b += all_pairs;
     }
     total += sh->warp_sum[0][j];
-    if constexpr (WIDE) {
-      all_pairs += sh->warp_sum[1][j];
-      all_chunks += sh->warp_sum[2][j];
-    }
+    all_pairs += sh->warp_sum[1][j];
+    all_chunks += sh->warp_sum[2][j];
+    longest = max(longest, sh->warp_longest[j]);
   }
   Line share = line_div(total + p.ctas - 1, (Line)p.ctas);
-  if (share < p.min_share / LineOf<WIDE>::KEYS) share = p.min_share / LineOf<WIDE>::KEYS;
-  const bool whole = WIDE && p.pair_ctas > 0 && all_pairs >= 4ll * p.ctas && 2 * all_chunks > total;
+  if (share < p.min_share / KEYS) share = p.min_share / KEYS;
+  // One pair per CTA: where cutting pairs gains less than it costs to merge
+  // them, and (in the hardware's order, the longest first) for many query tiles
+  const bool whole = (all_pairs <= p.ctas && longest <= share + p.merge_cost / KEYS) ||
+                     (WIDE && p.pair_ctas > 0 && all_pairs >= 4ll * p.ctas && 2 * all_chunks > total);
   const Line pos = whole ? piece : piece * share;
   const Line mine = whole ? b : a, size = whole ? pairs : span;
   if (pos >= mine && pos < mine + size) {
@@ -349,7 +351,7 @@ __device__ __forceinline__ PagedPlace<WIDE> find_place(const PagedParams& p, int
 #pragma unroll 1
     for (int i = i0; i < i1; ++i) {
       if (per > 1) s = read_seq<WIDE>(p, i, false);
-      const Line sx = s.span<WIDE>(p), sn = WIDE ? (Line)s.tiles * p.heads_kv : 0;
+      const Line sx = s.span<WIDE>(p), sn = (Line)s.tiles * p.heads_kv;
       if (whole ? pos < n + sn : pos < x + sx) {
         sh->place.at = x;
         sh->place.s = s;
@@ -471,9 +473,9 @@ struct FragWalk {
     one = pl.share == 0;
     merge.count = -1;
     table = p.table + (long long)seq * p.table_stride;
-    begin = piece * pl.share;
+    begin = piece * pl.share;   // one: 0
     end = min(begin + pl.share, pl.total);
-    if (WIDE && one) {   // the query tiles from the last (the most keys) to the first
+    if (one) {   // the query tiles from the last (the most keys) to the first
       h = pl.rank % p.heads_kv;
       tile = s.tiles - 1 - pl.rank / p.heads_kv;
       x = 0;
@@ -482,7 +484,7 @@ struct FragWalk {
       read_ahead(p);
     }
     start_tile(p);
-    if (WIDE && one) end = w;
+    if (one) end = w;
     if (begin > x && x >= begin - pl.share) {
       // pieces with key tiles of the pair: the first whose end lies past the
       // pair's overhead, the last that starts before its last tile's end

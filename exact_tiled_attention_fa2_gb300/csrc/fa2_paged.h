@@ -56,6 +56,7 @@ struct PagedParams {
                           // the batch may have that many, or 0
   int overhead;           // a pair's fixed cost on the line, in keys (whole key tiles)
   int min_share;          // keys of a piece at least (whole key tiles)
+  int merge_cost;         // what a merge costs, in keys of one CTA's work (whole key tiles)
   int slot_rows;          // rows of a Q load and of a partial state: group x tokens
   float* ws_o;            // [2 * ctas][d / 4][slot_rows][4] partial O~
   float* ws_ml;           // [2 * ctas][slot_rows][2] partial (m, l), exp2 domain

@@ -255,6 +255,7 @@ int paged_forward(const fa2_paged_params& a, void* workspace, size_t workspace_b
   // few rows (every sequence is then one query tile): the line in key tiles and 32 bits
   la.wide = p.slot_rows > kPagedTileRows / 2 ||
             (double)a.batch * c.heads * ((p.max_keys + p.overhead) / 64 + 2.0) + 1e6 > 2147483647.0;
+  p.merge_cost = la.wide ? 768 : 256;
   la.band = a.window_left >= 0 || a.prefix_len > 0;
   la.stream = stream;
   int e = 0;
