@@ -481,24 +481,16 @@ def _block_table(t, dev, rows):
     return t.data_ptr(), st[0], shape[1]
 
 
-def _paged_cache(k_cache, v_cache):
-    """(device, shape, dtype, Fa2PagedCache fields) of cache tensors [num_pages, H_kv, page_size, d]."""
-    facts = _torch or _torch_facts()
-    shape = k_cache.shape
-    if len(shape) != 4 or v_cache.shape != shape:
+def _check_cache(k_cache, v_cache):
+    """Raises what is wrong with cache tensors [num_pages, H_kv, page_size, d], if anything."""
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
         raise ValueError("k_cache and v_cache must share one [num_pages, H_kv, page_size, d] shape")
-    dev, dtype = k_cache.get_device(), k_cache.dtype
-    if dev < 0 or v_cache.get_device() != dev:
+    if k_cache.get_device() < 0 or v_cache.get_device() != k_cache.get_device():
         raise ValueError("k_cache and v_cache must be CUDA tensors on one device")
-    code = facts[1].get(dtype)
-    if code is None or v_cache.dtype != dtype:
+    if k_cache.dtype not in _torch[1] or v_cache.dtype != k_cache.dtype:
         raise TypeError("k_cache and v_cache must share one dtype, float16 or bfloat16")
-    ks, vs = k_cache.stride(), v_cache.stride()
-    pages, heads, page_size, d = shape
-    if (ks[3] != 1 or vs[3] != 1) and d > 1:
+    if k_cache.stride(3) != 1 or v_cache.stride(3) != 1:
         raise ValueError("k_cache and v_cache must have a contiguous last dimension")
-    return dev, shape, dtype, (k_cache.data_ptr(), v_cache.data_ptr(), ks[0], ks[1], ks[2], vs[0], vs[1], vs[2],
-                               pages, page_size, heads, d, code)
 
 
 def fa2_paged_plan(context_lens, query_lens, block_table, free_pages, free_count, num_pages, page_size, total_q,
@@ -517,11 +509,11 @@ def fa2_paged_plan(context_lens, query_lens, block_table, free_pages, free_count
     is refused whole: empty outputs, the table as it was, and
     FA2_ERR_DEVICE_PAGES from the next fa2_get_device_status.
     """
-    facts = _torch or _torch_facts()
+    _, _, _, raw_stream, current, _, _ = _torch or _torch_facts()
     dev = context_lens.get_device()
     if dev < 0 or context_lens.dim() != 1:
         raise ValueError("context_lens must be an int32 CUDA tensor [B]")
-    if stream is not None or dev != facts[4]():
+    if stream is not None or dev != current():
         with _on_device(dev, stream):
             return fa2_paged_plan(context_lens, query_lens, block_table, free_pages, free_count, num_pages,
                                   page_size, total_q, cu_seqlens_q, seqlens_k, slots, free_left)
@@ -546,7 +538,7 @@ def fa2_paged_plan(context_lens, query_lens, block_table, free_pages, free_count
     params = _PAGED_PLAN_PACK.pack(
         ctx, new, free, count, table, cu_seqlens_q.data_ptr(), seqlens_k.data_ptr(), slots.data_ptr(),
         free_left.data_ptr(), table_stride, B, max_pages, num_pages, page_size, total_q, num_free)
-    rc = (_lib or load_library()).fa2_paged_plan(params, facts[3](dev))
+    rc = (_lib or load_library()).fa2_paged_plan(params, raw_stream(dev))
     if rc:
         raise Fa2Error(rc, "fa2_paged_plan")
     return cu_seqlens_q, seqlens_k, slots, free_left
@@ -561,55 +553,63 @@ def fa2_paged_append(k, v, slots, k_cache, v_cache, stream=None):
     with a contiguous last dimension (a [num_pages, page_size, H_kv, d] cache
     as ``x.transpose(1, 2)``); slot s is row s % page_size of page s // page_size.
     """
-    dev, shape, dtype, cache = _paged_cache(k_cache, v_cache)
-    facts = _torch
-    if stream is not None or dev != facts[4]():
+    _, codes, _, raw_stream, current, _, _ = _torch or _torch_facts()
+    _check_cache(k_cache, v_cache)
+    dev, dtype, shape = k_cache.get_device(), k_cache.dtype, k_cache.shape
+    if stream is not None or dev != current():
         with _on_device(dev, stream):
             return fa2_paged_append(k, v, slots, k_cache, v_cache)
-    rows = k.shape
+    rows, ks, vs = k.shape, k.stride(), v.stride()
     if len(rows) != 3 or v.shape != rows or rows[1] != shape[1] or rows[2] != shape[3]:
         raise ValueError("k and v must be [total, H_kv, d] with the cache's heads and head dim")
-    ks, vs = k.stride(), v.stride()
     if k.get_device() != dev or v.get_device() != dev or ks[2] != 1 or vs[2] != 1:
         raise ValueError("k and v must be on the cache's device with a contiguous last dimension")
     if k.dtype != dtype or v.dtype != dtype:
         raise TypeError("k, v and the cache must share one dtype")
-    total = rows[0]
-    params = _PAGED_APPEND_PACK.pack(*cache, k.data_ptr(), v.data_ptr(), _int32_1d(slots, "slots", dev, total),
-                                     ks[0], ks[1], vs[0], vs[1], total)
-    rc = (_lib or load_library()).fa2_paged_append(params, facts[3](dev))
+    kst, vst = k_cache.stride(), v_cache.stride()
+    params = _PAGED_APPEND_PACK.pack(k_cache.data_ptr(), v_cache.data_ptr(), kst[0], kst[1], kst[2], vst[0], vst[1],
+                                     vst[2], shape[0], shape[2], shape[1], shape[3], codes[dtype], k.data_ptr(),
+                                     v.data_ptr(), _int32_1d(slots, "slots", dev, rows[0]), ks[0], ks[1], vs[0], vs[1],
+                                     rows[0])
+    rc = (_lib or load_library()).fa2_paged_append(params, raw_stream(dev))
     if rc:
         raise Fa2Error(rc, "fa2_paged_append")
 
 
-def _paged_inputs(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, max_seqlen_q):
-    """A paged forward's inputs, checked: (device, function packing the call's parameters)."""
-    dev, shape, dtype, cache = _paged_cache(k_cache, v_cache)
-    q_shape, qs = q.shape, q.stride()
+def _paged_fwd_pack(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, o, lse, scale, window_left,
+                    window_right, prefix_len, max_seqlen_q):
+    """A paged forward's parameters, inputs checked; o and lse (pointer, strides) may be zeros."""
+    facts = _torch
+    ks, vs, qs, ts = k_cache.stride(), v_cache.stride(), q.stride(), block_table.stride()
+    shape, q_shape, t_shape = k_cache.shape, q.shape, block_table.shape
+    dev, dtype, int32, B = k_cache.get_device(), k_cache.dtype, facts[2], seqlens_k.numel()
+    if not (len(shape) == 4 and v_cache.shape == shape and ks[3] == 1 and vs[3] == 1 and dev >= 0
+            and v_cache.get_device() == dev and dtype in facts[1] and v_cache.dtype == dtype):
+        _check_cache(k_cache, v_cache)
     if len(q_shape) != 3 or q_shape[2] != shape[3]:
         raise ValueError("q must be [total_q, H, d] with the cache's head dim")
     if q.get_device() != dev or qs[2] != 1:
         raise ValueError("q must be on the cache's device with a contiguous last dimension")
     if q.dtype != dtype:
         raise TypeError("q and the cache must share one dtype")
-    B = seqlens_k.numel()
-    lens = _int32_1d(seqlens_k, "seqlens_k", dev, B)
-    cu = _int32_1d(cu_seqlens_q, "cu_seqlens_q", dev, B + 1)
-    table, table_stride, max_pages = _block_table(block_table, dev, B)
+    if not (len(t_shape) == 2 and t_shape[0] == B and (ts[1] == 1 or t_shape[1] <= 1) and block_table.dtype == int32
+            and block_table.get_device() == dev):
+        _block_table(block_table, dev, B)
     total, heads, d = q_shape
-    longest = total if max_seqlen_q is None else int(max_seqlen_q)
-
-    def pack(o, lse, os, lse_stride, scale=0.0, window_left=-1, window_right=-1, prefix_len=0):
-        return _PAGED_PACK.pack(*cache, q.data_ptr(), o, lse, table, cu, lens, table_stride, qs[0], qs[1], os[0],
-                                os[1], lse_stride, B, heads, total, longest, max_pages, window_left, window_right,
-                                prefix_len, scale)
-    return dev, pack
+    return _PAGED_PACK.pack(k_cache.data_ptr(), v_cache.data_ptr(), ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], shape[0],
+                            shape[2], shape[1], d, facts[1][dtype], q.data_ptr(), o[0], lse[0], block_table.data_ptr(),
+                            _int32_1d(cu_seqlens_q, "cu_seqlens_q", dev, B + 1),
+                            _int32_1d(seqlens_k, "seqlens_k", dev, B), ts[0], qs[0], qs[1], o[1], o[2], lse[1], B, heads,
+                            total, total if max_seqlen_q is None else max_seqlen_q, t_shape[1], window_left,
+                            window_right, prefix_len, 1.0 / d ** 0.5 if scale is None else scale)
 
 
 def fa2_paged_fwd_workspace_bytes(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, max_seqlen_q=None) -> int:
     """Workspace fa2_paged_fwd needs for these tensors; it depends on their shapes only."""
-    _, pack = _paged_inputs(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, max_seqlen_q)
-    return int(load_library().fa2_paged_fwd_workspace_bytes(pack(0, 0, (0, 0), 0)))
+    _torch or _torch_facts()
+    return int(load_library().fa2_paged_fwd_workspace_bytes(
+        _paged_fwd_pack(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, (0, 0, 0), (0, 0), 0.0, -1, -1, 0,
+                        max_seqlen_q)))
 
 
 def fa2_paged_fwd(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, o=None, lse=None, workspace=None,
@@ -627,27 +627,31 @@ def fa2_paged_fwd(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, o=N
     grid and the workspace.  Returns (o [total_q, H, d], lse [H, total_q]);
     rows outside every sequence are not written.
     """
-    dev, pack = _paged_inputs(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, max_seqlen_q)
-    facts = _torch
-    if stream is not None or dev != facts[4]():
+    torch, _, _, raw_stream, current, alloc, free = _torch or _torch_facts()
+    dev = q.get_device()
+    if dev < 0:
+        raise ValueError("fa2_paged_fwd takes CUDA tensors")
+    if stream is not None or dev != current():
         with _on_device(dev, stream):
             return fa2_paged_fwd(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, o, lse, workspace, scale,
                                  window_left, window_right, prefix_len, max_seqlen_q)
-    torch = facts[0]
-    total, heads, d = q.shape
     if o is None:
-        o = q.new_empty((total, heads, d))
-    elif o.shape != q.shape or o.dtype != q.dtype or o.get_device() != dev or o.stride(2) != 1:
+        o = q.new_empty(q.shape)
+    elif o.shape != q.shape or o.dtype != q.dtype or o.get_device() != dev or o.stride(-1) != 1:
         raise ValueError("o must have q's shape, dtype and device with a contiguous last dimension")
+    if q.dim() != 3:
+        raise ValueError("q must be [total_q, H, d] with the cache's head dim")
+    total, heads, _ = q.shape
     if lse is None:
         lse = q.new_empty((heads, total), dtype=torch.float32)
     elif (lse.shape != (heads, total) or lse.dtype != torch.float32 or lse.get_device() != dev
           or (lse.stride(1) != 1 and total > 1)):
         raise ValueError("lse must be float32 [H, total_q] on q's device with a contiguous last dimension")
-    params = pack(o.data_ptr(), lse.data_ptr(), o.stride(), lse.stride(0),
-                  1.0 / float(d) ** 0.5 if scale is None else float(scale), window_left, window_right, prefix_len)
+    os = o.stride()
+    params = _paged_fwd_pack(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, (o.data_ptr(), os[0], os[1]),
+                             (lse.data_ptr(), lse.stride(0)), scale, window_left, window_right, prefix_len, max_seqlen_q)
     lib = _lib or load_library()
-    handle = facts[3](dev)
+    handle = raw_stream(dev)
     if workspace is not None:
         if workspace.get_device() != dev or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on q's device")
@@ -655,15 +659,15 @@ def fa2_paged_fwd(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, o=N
     else:
         # a block of the current stream, given back once the kernels are queued: its next user there follows them
         need = lib.fa2_paged_fwd_workspace_bytes(params)
-        if need == 0 or facts[5] is None:
+        if need == 0 or alloc is None:
             block = q.new_empty(max(need, 256), dtype=torch.uint8)
             rc = lib.fa2_paged_fwd(params, block.data_ptr(), block.numel(), handle)
         else:
-            block = facts[5](need, handle)
+            block = alloc(need, handle)
             try:
                 rc = lib.fa2_paged_fwd(params, block, need, handle)
             finally:
-                facts[6](block)
+                free(block)
     if rc:
         raise Fa2Error(rc, "fa2_paged_fwd")
     return o, lse
