@@ -3,15 +3,16 @@
 A thin ctypes binding over the C ABI in ``include/fa2.h`` (library
 ``libfa2_gb300.so``, built in-tree by ``exact_tiled_attention_fa2_gb300.build``).
 Every step of the forward pass runs in the CUDA kernels; this module only
-marshals torch tensors (device memory, streams) into pointers and sizes.
-There is no CPU fallback: if the library is missing, calls raise.
+marshals torch tensors (device memory, streams) into pointers and sizes (the
+paged-cache calls, made once per layer of a serving step, through an extension
+module, ``_paged_binding.so``).  There is no CPU fallback: if the library is
+missing, calls raise.
 """
 from __future__ import annotations
 
 import contextlib
 import ctypes
 import os
-import struct
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libfa2_gb300.so")
@@ -161,20 +162,16 @@ def load_library():
     lib.fa2_bwd_ex.restype = ci
     lib.fa2_bwd_ex_workspace_bytes.argtypes = [ctypes.POINTER(Fa2FwdParams)]
     lib.fa2_bwd_ex_workspace_bytes.restype = sz
-    lib.fa2_paged_plan.argtypes = [vp, vp]   # the parameter struct, by reference or packed
+    lib.fa2_paged_plan.argtypes = [ctypes.POINTER(Fa2PagedPlanParams), vp]
     lib.fa2_paged_plan.restype = ci
-    lib.fa2_paged_append.argtypes = [vp, vp]
+    lib.fa2_paged_append.argtypes = [ctypes.POINTER(Fa2PagedAppendParams), vp]
     lib.fa2_paged_append.restype = ci
-    lib.fa2_paged_fwd.argtypes = [vp, vp, sz, vp]
+    lib.fa2_paged_fwd.argtypes = [ctypes.POINTER(Fa2PagedParams), vp, sz, vp]
     lib.fa2_paged_fwd.restype = ci
-    lib.fa2_paged_fwd_workspace_bytes.argtypes = [vp]
+    lib.fa2_paged_fwd_workspace_bytes.argtypes = [ctypes.POINTER(Fa2PagedParams)]
     lib.fa2_paged_fwd_workspace_bytes.restype = sz
     lib.fa2_paged_params_size.argtypes = []
     lib.fa2_paged_params_size.restype = sz
-    for pack, mirror in ((_PAGED_PACK, Fa2PagedParams), (_PAGED_APPEND_PACK, Fa2PagedAppendParams),
-                         (_PAGED_PLAN_PACK, Fa2PagedPlanParams)):
-        if pack.size != ctypes.sizeof(mirror):
-            raise RuntimeError("%s layout mismatch: packed %d bytes" % (mirror.__name__, pack.size))
     if lib.fa2_paged_params_size() != ctypes.sizeof(Fa2PagedParams):
         raise RuntimeError("fa2_paged_params layout mismatch: library %d bytes, binding %d bytes"
                            % (lib.fa2_paged_params_size(), ctypes.sizeof(Fa2PagedParams)))
@@ -426,71 +423,31 @@ def fa2_bwd_ex(q, k, v, o, lse, dout, dq=None, dk=None, dv=None, workspace=None,
     return dq, dk, dv
 
 
-# The paged calls run once per layer of a serving step on small tensors, so the
-# binding's own time shows: parameters are packed in one go (the formats mirror
-# the Structures above field by field; load_library checks their sizes) and
-# results come from the tensors' own allocators.
-_PAGED_PACK = struct.Struct("@PP3q3q5i4x3P3Pq2q2qq8if4x")
-_PAGED_APPEND_PACK = struct.Struct("@PP3q3q5i4x3P2q2qi4x")
-_PAGED_PLAN_PACK = struct.Struct("@9Pq6i")
-_torch = None   # torch, its 16-bit dtypes' codes, int32, raw-stream and device getters (set on first use)
+_paged = None   # the extension module of the paged calls (csrc/paged_binding.cpp)
 
 
-def _torch_facts():
-    global _torch
-    import torch
-    # the caching allocator without a tensor around its block, where this torch has it
-    alloc = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_alloc", None)
-    free = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_delete", None)
-    _torch = (torch, {torch.float16: FA2_FP16, torch.bfloat16: FA2_BF16}, torch.int32,
-              torch._C._cuda_getCurrentRawStream, torch.cuda.current_device, alloc if free else None, free)
-    return _torch
+def _paged_calls():
+    global _paged
+    if _paged is None:
+        load_library()
+        if not os.path.exists(os.path.join(_HERE, "_paged_binding.so")):
+            raise RuntimeError("_paged_binding.so is not built (run `python -m exact_tiled_attention_fa2_gb300.build` "
+                               "or __graft_entry__.build()); there is no fallback path")
+        import torch  # noqa: F401  (its libraries, before the module that uses them)
+        from . import _paged_binding as module
+        _paged = module
+    return _paged
 
 
 @contextlib.contextmanager
-def _on_device(device, stream):
-    """``device`` current, and ``stream`` (if given) the current stream there:
-    tensors allocated inside are not handed out again before its kernels are
-    done with them."""
+def _on_stream(stream, tensor):
+    """``stream`` the current stream of ``tensor``'s device: tensors allocated
+    inside are not handed out again before its kernels are done with them."""
     import torch
-    with torch.cuda.device(device):
-        if stream is None:
-            yield
-        elif stream.device.index != device:
-            raise ValueError("stream must belong to the tensors' device (cuda:%d)" % device)
-        else:
-            with torch.cuda.stream(stream):
-                yield
-
-
-def _int32_1d(t, name, dev, n):
-    if t.dtype != _torch[2] or t.get_device() != dev or t.dim() != 1 or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous int32 tensor [n] on the call's CUDA device" % name)
-    if t.numel() != n:
-        raise ValueError("%s must have %d elements, has %d" % (name, n, t.numel()))
-    return t.data_ptr()
-
-
-def _block_table(t, dev, rows):
-    """(pointer, row stride, columns) of a block table."""
-    shape, st = t.shape, t.stride()
-    if t.dtype != _torch[2] or t.get_device() != dev or len(shape) != 2 or shape[0] != rows:
-        raise ValueError("block_table must be an int32 tensor [%d, max_pages] on the call's CUDA device" % rows)
-    if st[1] != 1 and shape[1] > 1:
-        raise ValueError("block_table must have a contiguous last dimension")
-    return t.data_ptr(), st[0], shape[1]
-
-
-def _check_cache(k_cache, v_cache):
-    """Raises what is wrong with cache tensors [num_pages, H_kv, page_size, d], if anything."""
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
-        raise ValueError("k_cache and v_cache must share one [num_pages, H_kv, page_size, d] shape")
-    if k_cache.get_device() < 0 or v_cache.get_device() != k_cache.get_device():
-        raise ValueError("k_cache and v_cache must be CUDA tensors on one device")
-    if k_cache.dtype not in _torch[1] or v_cache.dtype != k_cache.dtype:
-        raise TypeError("k_cache and v_cache must share one dtype, float16 or bfloat16")
-    if k_cache.stride(3) != 1 or v_cache.stride(3) != 1:
-        raise ValueError("k_cache and v_cache must have a contiguous last dimension")
+    if stream.device != tensor.device:
+        raise ValueError("stream must belong to the tensors' device %s" % tensor.device)
+    with torch.cuda.stream(stream):
+        yield
 
 
 def fa2_paged_plan(context_lens, query_lens, block_table, free_pages, free_count, num_pages, page_size, total_q,
@@ -509,39 +466,15 @@ def fa2_paged_plan(context_lens, query_lens, block_table, free_pages, free_count
     is refused whole: empty outputs, the table as it was, and
     FA2_ERR_DEVICE_PAGES from the next fa2_get_device_status.
     """
-    _, _, _, raw_stream, current, _, _ = _torch or _torch_facts()
-    dev = context_lens.get_device()
-    if dev < 0 or context_lens.dim() != 1:
-        raise ValueError("context_lens must be an int32 CUDA tensor [B]")
-    if stream is not None or dev != current():
-        with _on_device(dev, stream):
-            return fa2_paged_plan(context_lens, query_lens, block_table, free_pages, free_count, num_pages,
-                                  page_size, total_q, cu_seqlens_q, seqlens_k, slots, free_left)
-    B, total_q, num_free = context_lens.numel(), int(total_q), free_pages.numel()
-    ctx = _int32_1d(context_lens, "context_lens", dev, B)
-    new = _int32_1d(query_lens, "query_lens", dev, B)
-    table, table_stride, max_pages = _block_table(block_table, dev, B)
-    free = _int32_1d(free_pages, "free_pages", dev, num_free)
-    count = _int32_1d(free_count, "free_count", dev, 1)
-    if total_q < 1:
-        raise ValueError("total_q must be at least 1")
-    empty = context_lens.new_empty
-    out = []
-    for t, name, n in ((cu_seqlens_q, "cu_seqlens_q", B + 1), (seqlens_k, "seqlens_k", B), (slots, "slots", total_q),
-                       (free_left, "free_left", 1)):
-        if t is None:
-            t = empty(n)
-        else:
-            _int32_1d(t, name, dev, n)
-        out.append(t)
-    cu_seqlens_q, seqlens_k, slots, free_left = out
-    params = _PAGED_PLAN_PACK.pack(
-        ctx, new, free, count, table, cu_seqlens_q.data_ptr(), seqlens_k.data_ptr(), slots.data_ptr(),
-        free_left.data_ptr(), table_stride, B, max_pages, num_pages, page_size, total_q, num_free)
-    rc = (_lib or load_library()).fa2_paged_plan(params, raw_stream(dev))
-    if rc:
-        raise Fa2Error(rc, "fa2_paged_plan")
-    return cu_seqlens_q, seqlens_k, slots, free_left
+    if stream is not None:
+        with _on_stream(stream, context_lens):
+            return fa2_paged_plan(context_lens, query_lens, block_table, free_pages, free_count, num_pages, page_size,
+                                  total_q, cu_seqlens_q, seqlens_k, slots, free_left)
+    out = (_paged or _paged_calls()).plan(context_lens, query_lens, block_table, free_pages, free_count, num_pages,
+                                            page_size, total_q, cu_seqlens_q, seqlens_k, slots, free_left)
+    if type(out) is int:
+        raise Fa2Error(out, "fa2_paged_plan")
+    return out
 
 
 def fa2_paged_append(k, v, slots, k_cache, v_cache, stream=None):
@@ -553,63 +486,17 @@ def fa2_paged_append(k, v, slots, k_cache, v_cache, stream=None):
     with a contiguous last dimension (a [num_pages, page_size, H_kv, d] cache
     as ``x.transpose(1, 2)``); slot s is row s % page_size of page s // page_size.
     """
-    _, codes, _, raw_stream, current, _, _ = _torch or _torch_facts()
-    _check_cache(k_cache, v_cache)
-    dev, dtype, shape = k_cache.get_device(), k_cache.dtype, k_cache.shape
-    if stream is not None or dev != current():
-        with _on_device(dev, stream):
+    if stream is not None:
+        with _on_stream(stream, k_cache):
             return fa2_paged_append(k, v, slots, k_cache, v_cache)
-    rows, ks, vs = k.shape, k.stride(), v.stride()
-    if len(rows) != 3 or v.shape != rows or rows[1] != shape[1] or rows[2] != shape[3]:
-        raise ValueError("k and v must be [total, H_kv, d] with the cache's heads and head dim")
-    if k.get_device() != dev or v.get_device() != dev or ks[2] != 1 or vs[2] != 1:
-        raise ValueError("k and v must be on the cache's device with a contiguous last dimension")
-    if k.dtype != dtype or v.dtype != dtype:
-        raise TypeError("k, v and the cache must share one dtype")
-    kst, vst = k_cache.stride(), v_cache.stride()
-    params = _PAGED_APPEND_PACK.pack(k_cache.data_ptr(), v_cache.data_ptr(), kst[0], kst[1], kst[2], vst[0], vst[1],
-                                     vst[2], shape[0], shape[2], shape[1], shape[3], codes[dtype], k.data_ptr(),
-                                     v.data_ptr(), _int32_1d(slots, "slots", dev, rows[0]), ks[0], ks[1], vs[0], vs[1],
-                                     rows[0])
-    rc = (_lib or load_library()).fa2_paged_append(params, raw_stream(dev))
+    rc = (_paged or _paged_calls()).append(k, v, slots, k_cache, v_cache)
     if rc:
         raise Fa2Error(rc, "fa2_paged_append")
 
 
-def _paged_fwd_pack(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, o, lse, scale, window_left,
-                    window_right, prefix_len, max_seqlen_q):
-    """A paged forward's parameters, inputs checked; o and lse (pointer, strides) may be zeros."""
-    facts = _torch
-    ks, vs, qs, ts = k_cache.stride(), v_cache.stride(), q.stride(), block_table.stride()
-    shape, q_shape, t_shape = k_cache.shape, q.shape, block_table.shape
-    dev, dtype, int32, B = k_cache.get_device(), k_cache.dtype, facts[2], seqlens_k.numel()
-    if not (len(shape) == 4 and v_cache.shape == shape and ks[3] == 1 and vs[3] == 1 and dev >= 0
-            and v_cache.get_device() == dev and dtype in facts[1] and v_cache.dtype == dtype):
-        _check_cache(k_cache, v_cache)
-    if len(q_shape) != 3 or q_shape[2] != shape[3]:
-        raise ValueError("q must be [total_q, H, d] with the cache's head dim")
-    if q.get_device() != dev or qs[2] != 1:
-        raise ValueError("q must be on the cache's device with a contiguous last dimension")
-    if q.dtype != dtype:
-        raise TypeError("q and the cache must share one dtype")
-    if not (len(t_shape) == 2 and t_shape[0] == B and (ts[1] == 1 or t_shape[1] <= 1) and block_table.dtype == int32
-            and block_table.get_device() == dev):
-        _block_table(block_table, dev, B)
-    total, heads, d = q_shape
-    return _PAGED_PACK.pack(k_cache.data_ptr(), v_cache.data_ptr(), ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], shape[0],
-                            shape[2], shape[1], d, facts[1][dtype], q.data_ptr(), o[0], lse[0], block_table.data_ptr(),
-                            _int32_1d(cu_seqlens_q, "cu_seqlens_q", dev, B + 1),
-                            _int32_1d(seqlens_k, "seqlens_k", dev, B), ts[0], qs[0], qs[1], o[1], o[2], lse[1], B, heads,
-                            total, total if max_seqlen_q is None else max_seqlen_q, t_shape[1], window_left,
-                            window_right, prefix_len, 1.0 / d ** 0.5 if scale is None else scale)
-
-
 def fa2_paged_fwd_workspace_bytes(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, max_seqlen_q=None) -> int:
     """Workspace fa2_paged_fwd needs for these tensors; it depends on their shapes only."""
-    _torch or _torch_facts()
-    return int(load_library().fa2_paged_fwd_workspace_bytes(
-        _paged_fwd_pack(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, (0, 0, 0), (0, 0), 0.0, -1, -1, 0,
-                        max_seqlen_q)))
+    return _paged_calls().workspace_bytes(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, max_seqlen_q)
 
 
 def fa2_paged_fwd(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, o=None, lse=None, workspace=None,
@@ -627,50 +514,15 @@ def fa2_paged_fwd(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, o=N
     grid and the workspace.  Returns (o [total_q, H, d], lse [H, total_q]);
     rows outside every sequence are not written.
     """
-    torch, _, _, raw_stream, current, alloc, free = _torch or _torch_facts()
-    dev = q.get_device()
-    if dev < 0:
-        raise ValueError("fa2_paged_fwd takes CUDA tensors")
-    if stream is not None or dev != current():
-        with _on_device(dev, stream):
+    if stream is not None:
+        with _on_stream(stream, q):
             return fa2_paged_fwd(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, o, lse, workspace, scale,
                                  window_left, window_right, prefix_len, max_seqlen_q)
-    if o is None:
-        o = q.new_empty(q.shape)
-    elif o.shape != q.shape or o.dtype != q.dtype or o.get_device() != dev or o.stride(-1) != 1:
-        raise ValueError("o must have q's shape, dtype and device with a contiguous last dimension")
-    if q.dim() != 3:
-        raise ValueError("q must be [total_q, H, d] with the cache's head dim")
-    total, heads, _ = q.shape
-    if lse is None:
-        lse = q.new_empty((heads, total), dtype=torch.float32)
-    elif (lse.shape != (heads, total) or lse.dtype != torch.float32 or lse.get_device() != dev
-          or (lse.stride(1) != 1 and total > 1)):
-        raise ValueError("lse must be float32 [H, total_q] on q's device with a contiguous last dimension")
-    os = o.stride()
-    params = _paged_fwd_pack(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, (o.data_ptr(), os[0], os[1]),
-                             (lse.data_ptr(), lse.stride(0)), scale, window_left, window_right, prefix_len, max_seqlen_q)
-    lib = _lib or load_library()
-    handle = raw_stream(dev)
-    if workspace is not None:
-        if workspace.get_device() != dev or not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous tensor on q's device")
-        rc = lib.fa2_paged_fwd(params, workspace.data_ptr(), workspace.numel() * workspace.element_size(), handle)
-    else:
-        # a block of the current stream, given back once the kernels are queued: its next user there follows them
-        need = lib.fa2_paged_fwd_workspace_bytes(params)
-        if need == 0 or alloc is None:
-            block = q.new_empty(max(need, 256), dtype=torch.uint8)
-            rc = lib.fa2_paged_fwd(params, block.data_ptr(), block.numel(), handle)
-        else:
-            block = alloc(need, handle)
-            try:
-                rc = lib.fa2_paged_fwd(params, block, need, handle)
-            finally:
-                free(block)
-    if rc:
-        raise Fa2Error(rc, "fa2_paged_fwd")
-    return o, lse
+    out = (_paged or _paged_calls()).forward(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, o, lse,
+                                               workspace, scale, window_left, window_right, prefix_len, max_seqlen_q)
+    if type(out) is int:
+        raise Fa2Error(out, "fa2_paged_fwd")
+    return out
 
 
 def _check_host_tensors(q, k, v, o, lse, where):

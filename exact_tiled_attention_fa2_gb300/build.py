@@ -5,6 +5,10 @@ Each translation unit under ``csrc/`` is compiled in parallel with nvcc
 shared library with the CUDA runtime linked statically, so loading it needs no
 driver until the first CUDA call.  The driver API entry point for TMA tensor
 maps is fetched at run time.
+
+The binding of the paged-cache calls to torch (``_paged_binding.so``, a Python
+extension module) is compiled beside it with g++ against torch's headers and
+linked to the library.
 """
 from __future__ import annotations
 
@@ -18,6 +22,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_NAME = "libfa2_gb300.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
+BINDING_SOURCE = "paged_binding.cpp"
+BINDING_PATH = os.path.join(HERE, "_paged_binding.so")
 SOURCES = ["fa2_abi.cu", "fa2_fwd_d64.cu", "fa2_fwd_d128.cu", "fa2_fwd_d256.cu", "fa2_bwd_d64.cu", "fa2_bwd_d128.cu",
            "fa2_bwd_d256.cu", "fa2_decode_d64.cu", "fa2_decode_d128.cu", "fa2_decode_d256.cu",
            "fa2_paged_abi.cu", "fa2_paged_cache.cu", "fa2_paged_d64.cu", "fa2_paged_d128.cu", "fa2_paged_d256.cu"]
@@ -44,6 +50,24 @@ def _stale(target: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _binding_commands(obj: str, out: str):
+    """Compile and link commands of _paged_binding.so."""
+    import sysconfig
+    import torch
+
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    compile_cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-D_GLIBCXX_USE_CXX11_ABI=%d"
+                   % int(torch._C._GLIBCXX_USE_CXX11_ABI), "-I", os.path.join(base, "include"),
+                   "-I", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+                   "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"),
+                   "-c", os.path.join(CSRC, BINDING_SOURCE), "-o", obj]
+    link_cmd = ["g++", "-shared", "-o", out, obj, "-L", HERE, "-l:" + LIB_NAME, "-L", os.path.join(base, "lib"),
+                "-ltorch", "-ltorch_cpu", "-ltorch_python", "-lc10", "-lc10_cuda", "-L", os.path.join(cuda, "lib64"),
+                "-lcudart", "-Wl,-rpath,$ORIGIN"]
+    return compile_cmd, link_cmd
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
     """Compile (if stale) and return the path of the shared library."""
     os.makedirs(BUILD_DIR, exist_ok=True)
@@ -59,20 +83,32 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
             if verbose:
                 print(" ".join(cmd), flush=True)
             procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
+    b_obj, b_tmp = os.path.join(BUILD_DIR, "paged_binding.o"), BINDING_PATH + ".tmp%d" % os.getpid()
+    header = os.path.join(os.path.dirname(HERE), "include", "fa2.h")
+    b_procs = []
+    if force or _stale(b_obj, [os.path.join(CSRC, BINDING_SOURCE), header]):
+        b_compile = _binding_commands(b_obj, b_tmp)[0]
+        if verbose:
+            print(" ".join(b_compile), flush=True)
+        b_procs.append((BINDING_SOURCE,
+                        subprocess.Popen(b_compile, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
     failed = []
-    for src, p in procs:
+    for src, p in procs + b_procs:
         out, _ = p.communicate()
         if verbose or ptxas_verbose or p.returncode:
             sys.stdout.write(out)
         if p.returncode:
             failed.append(src)
     if failed:
-        raise RuntimeError("nvcc failed for " + ", ".join(failed))
+        raise RuntimeError("compilation failed for " + ", ".join(failed))
     if force or procs or _stale(LIB_PATH, objs):
         tmp = LIB_PATH + ".tmp%d" % os.getpid()
         cmd = [nvcc] + ARCH + ["-shared", "-o", tmp] + objs
         subprocess.run(cmd, check=True)
         os.replace(tmp, LIB_PATH)
+    if force or b_procs or _stale(BINDING_PATH, [b_obj]):
+        subprocess.run(_binding_commands(b_obj, b_tmp)[1], check=True)
+        os.replace(b_tmp, BINDING_PATH)
     return LIB_PATH
 
 
