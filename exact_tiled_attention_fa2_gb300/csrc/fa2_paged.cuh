@@ -1218,24 +1218,38 @@ __global__ void __launch_bounds__(kPagedMergeThreads) fa2_paged_merge_kernel(con
   float4 acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int k = r < here ? sub : mg.count; k < mg.count; k += subs) {
-    const size_t slot = (size_t)(2 * (mg.c0 + k) + (k == 0 ? mg.from_start : 0)) * (size_t)p.slot_rows;
-    const float2 s = ml[slot];
-    const float4* src = part + slot * (D / 4);
-    float4 v[E];
+  // two partials at a time: the reads of both are in flight together
+  constexpr int U = E <= 4 ? 2 : 1;
+#pragma unroll 1
+  for (int k0 = r < here ? sub : mg.count; k0 < mg.count; k0 += U * subs) {
+    float2 s[U];
+    float4 v[U][E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = src[(size_t)(e * NW) * p.slot_rows];
-    if (s.x == -INFINITY) continue;   // shows the row nothing
-    const float top = fmaxf(m, s.x);
-    const float f0 = ex2_approx(m - top), f = ex2_approx(s.x - top);   // f0: 0 before the first
-    m = top;
-    l = l * f0 + s.y * f;
+    for (int u = 0; u < U; ++u) {
+      const int k = k0 + u * subs;
+      s[u] = make_float2(-INFINITY, 0.f);
+      if (k < mg.count) {
+        const size_t slot = (size_t)(2 * (mg.c0 + k) + (k == 0 ? mg.from_start : 0)) * (size_t)p.slot_rows;
+        s[u] = ml[slot];
+        const float4* src = part + slot * (D / 4);
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      acc[e].x = fmaf(f, v[e].x, acc[e].x * f0);
-      acc[e].y = fmaf(f, v[e].y, acc[e].y * f0);
-      acc[e].z = fmaf(f, v[e].z, acc[e].z * f0);
-      acc[e].w = fmaf(f, v[e].w, acc[e].w * f0);
+        for (int e = 0; e < E; ++e) v[u][e] = src[(size_t)(e * NW) * p.slot_rows];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (s[u].x == -INFINITY) continue;   // shows the row nothing
+      const float top = fmaxf(m, s[u].x);
+      const float f0 = ex2_approx(m - top), f = ex2_approx(s[u].x - top);   // f0: 0 before the first
+      m = top;
+      l = l * f0 + s[u].y * f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        acc[e].x = fmaf(f, v[u][e].x, acc[e].x * f0);
+        acc[e].y = fmaf(f, v[u][e].y, acc[e].y * f0);
+        acc[e].z = fmaf(f, v[u][e].z, acc[e].z * f0);
+        acc[e].w = fmaf(f, v[u][e].w, acc[e].w * f0);
+      }
     }
   }
   float M = m;

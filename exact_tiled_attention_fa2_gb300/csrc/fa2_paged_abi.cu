@@ -20,10 +20,11 @@ constexpr long long kMaxStride = 1ll << 39;   // elements: 16-bit strides stay b
 // nor the result depends on the device.
 constexpr int paged_ctas(int d) { return d == 256 ? 152 : 304; }
 // A pair's fixed cost (Q, the first products, the epilogue) in keys, and the
-// shortest piece worth a CTA: 256 keys, or (many rows) the keys whose K and V
+// shortest piece worth a CTA: 128 keys, or (many rows) the keys whose K and V
 // are as many bytes as a partial's write and read four times over.
 constexpr int kPagedOverhead = 128;
-constexpr int kPagedMinShare = 192;
+constexpr int kPagedMinShare = 128;
+constexpr int kPagedMaxHeads = 65536;
 constexpr long long kPagedMaxKeys = (1ll << 31) - 4096;   // keys of a sequence, rounded up to tiles, stay below 2^31
 
 struct Range {
@@ -69,7 +70,7 @@ int check_cache(const fa2_paged_cache& c, CacheView& k, CacheView& v) {
   if (c.head_dim != 64 && c.head_dim != 128 && c.head_dim != 256) return FA2_ERR_UNSUPPORTED;
   const int ps = c.page_size;
   if (!(ps == 8 || ps == 16 || ps == 32 || ps % 64 == 0)) return FA2_ERR_UNSUPPORTED;
-  if ((long long)c.num_pages * ps > INT_MAX) return FA2_ERR_UNSUPPORTED;
+  if ((long long)c.num_pages * ps > INT_MAX || c.heads > kPagedMaxHeads) return FA2_ERR_UNSUPPORTED;
   if (!c.k || !c.v) return FA2_ERR_INVALID_ARG;
   if (misaligned(c.k, 16) || misaligned(c.v, 16)) return FA2_ERR_MISALIGNED;
   CacheView* view[2] = {&k, &v};

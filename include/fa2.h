@@ -361,7 +361,7 @@ typedef struct fa2_paged_cache {
   int64_t v_strides[3];
   int num_pages;          /* >= 1; num_pages * page_size < 2^31 (FA2_ERR_UNSUPPORTED) */
   int page_size;          /* 8, 16, 32 or a multiple of 64 (FA2_ERR_UNSUPPORTED otherwise) */
-  int heads;              /* K/V heads >= 1 */
+  int heads;              /* K/V heads, 1 .. 65536 (FA2_ERR_UNSUPPORTED above) */
   int head_dim;           /* d: 64, 128 or 256 */
   int dtype;              /* FA2_FP16 or FA2_BF16 */
 } fa2_paged_cache;

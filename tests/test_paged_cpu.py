@@ -124,7 +124,7 @@ def _append(**kw):
 @pytest.mark.parametrize("kw,code", [
     (dict(total=0), INVALID), (dict(k=0), INVALID), (dict(v=0), INVALID), (dict(slots=0), INVALID),
     (dict(cache_k=0), INVALID), (dict(heads=0), INVALID), (dict(dtype=7), INVALID), (dict(head_dim=32), UNSUPPORTED),
-    (dict(page_size=24), UNSUPPORTED), (dict(num_pages=1 << 27), UNSUPPORTED),
+    (dict(page_size=24), UNSUPPORTED), (dict(num_pages=1 << 27), UNSUPPORTED), (dict(heads=65537), UNSUPPORTED),
     (dict(k=A + 8), MISALIGNED), (dict(v=2 * A + 4), MISALIGNED), (dict(slots=3 * A + 2), MISALIGNED),
     (dict(cache_v=11 * A + 8), MISALIGNED), (dict(k_strides=[132, 64]), MISALIGNED), (dict(v_strides=[128, -64]), INVALID),
     (dict(cache_k_strides=[2048, 1024, 4]), MISALIGNED),

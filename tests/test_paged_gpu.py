@@ -200,6 +200,60 @@ def test_many_sequences():
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
+def test_many_decoding_sequences():
+    """One to three tokens a sequence, more sequences than threads, some idle, some empty, a few long."""
+    r = np.random.default_rng(4)
+    lens_q = r.integers(0, 4, 1500).tolist()
+    lens_k = [int(x) for x in r.integers(0, 200, 1500)]
+    lens_k[3], lens_k[700], lens_k[1499], lens_q[1499] = 5000, 3000, 9000, 3
+    p = Problem(lens_q, lens_k, 10, 2, 128, "bf16", 8, seed=14, fill=float("nan"))
+    for kw in (dict(window_right=0), dict(window_left=90, window_right=0, prefix_len=3)):
+        o, lse = p.run(**kw)
+        assert status() == fa2.FA2_OK
+        p.check(o, lse, **kw)
+
+
+@pytest.mark.parametrize("d,dtype", [(64, "bf16"), (128, "fp16"), (256, "bf16")])
+@pytest.mark.parametrize("mask", sorted(MASKS))
+def test_few_tokens_against_definition(mask, d, dtype):
+    """Drafted tokens: several rows of each head, some before the sequence's first key."""
+    p = Problem([7, 1, 8, 5, 3, 8], [1500, 3, 5, 64, 0, 4111], 10, 2, d, dtype, 32, seed=d + 1, fill=float("nan"))
+    wl, wr, pre = MASKS[mask]
+    kw = dict(window_left=wl, window_right=wr, prefix_len=pre)
+    o, lse = p.run(**kw)
+    assert status() == fa2.FA2_OK
+    p.check(o, lse, **kw)
+
+
+@pytest.mark.parametrize("batch,n_k,new", [(1, 300, 1), (3, 700, 2), (1, 100, 100), (30, 960, 1), (2, 5000, 64)])
+def test_pairs_whole_and_cut(batch, n_k, new):
+    """Around the rule that gives every (query tile, K/V head) pair a CTA of its own."""
+    for hkv in (1, 8):
+        p = Problem([new] * batch, [n_k] * batch, 4 * hkv, hkv, 128, "bf16", 64, seed=batch + n_k)
+        o, lse = p.run(window_right=0)
+        assert status() == fa2.FA2_OK
+        p.check(o, lse, window_right=0)
+
+
+def test_tables_wider_than_a_32_bit_line():
+    """Table rows that could hold 2^31 keys each: few rows, but positions of the batch's work past 32 bits."""
+    page, hkv, d, batch = 1 << 20, 2, 64, 64
+    p = Problem([2] * batch, [130 + 7 * b for b in range(batch)], 4, hkv, d, "fp16", 64, seed=15)
+    # the same keys in one page of 2^20 rows
+    k = torch.zeros((1, hkv, page, d), dtype=torch.float16, device="cuda")
+    v = torch.zeros_like(k)
+    k[0, :, :700] = p.k[:11].transpose(0, 1).reshape(hkv, -1, d)[:, :700]
+    v[0, :, :700] = p.v[:11].transpose(0, 1).reshape(hkv, -1, d)[:, :700]
+    table = torch.full((batch, 2047), -1, dtype=torch.int32, device="cuda")
+    table[:, 0] = 0
+    q = Problem.__new__(Problem)
+    q.lens_q, q.lens_k, q.page, q.d, q.hq, q.hkv = p.lens_q, p.lens_k, page, d, 4, hkv
+    q.q, q.k, q.v, q.table, q.cu, q.lens = p.q, k, v, table, p.cu, p.lens
+    o, lse = q.run(window_right=0)
+    assert status() == fa2.FA2_OK
+    q.check(o, lse, window_right=0)
+
+
 def test_many_query_tiles():
     """Prompts from their start: enough (query tile, K/V head) pairs for one CTA each, beside short sequences."""
     lens_q = [2500, 1, 1300, 7, 0, 900]
