@@ -19,22 +19,21 @@
 // piece is a run of fragments: the end of one pair, whole pairs, the start of
 // another.  Whole pairs write O and L; the others leave fp32 partials (m, l,
 // O~) in the CTA's two slots, which a second kernel, launched as a programmatic
-// dependent, merges.  Batches of many query tiles (a long prompt from its
-// start, where equal pieces of the line would lose the CTAs' walking of the
-// same keys) run one pair per CTA instead, in the hardware's order.
+// dependent, merges.  Where cutting gains less than it costs (whole_pairs), all
+// pairs, or a batch's full waves of them, run one per CTA instead.
 //
-// One CTA, 192 threads, as the double-buffered forward kernel
-// (fa2_fwd_dbuf.cuh: tensor-memory layout, two S buffers, 2-stage K and V
-// rings, one softmax thread per row), with the rings' and barriers' phases
-// counted across its fragments: while the softmax warps finish a fragment, the
-// TMA warp already loads the next one's K, V and Q and the MMA thread issues
-// its first S products.
+// One CTA, 192 threads (224 with query tiles of few rows), as the
+// double-buffered forward kernel (fa2_fwd_dbuf.cuh: tensor-memory layout, two S
+// buffers, rings of K and V stages, one softmax thread per row), with the
+// rings' and barriers' phases counted across its fragments: while the softmax
+// warps finish a fragment, the TMA warp already loads the next one's K, V and Q
+// and the MMA thread issues its first S products.
 //
 // A 64-key tile lands as [8-row group][64-column block][8 rows][128 bytes]
 // (128-byte swizzle), so that rows of any page size follow each other with one
 // stride: one 5-D box per page and tile (pages of 8 .. 32 rows: 8 .. 2 boxes, of
 // 64 k rows: one), issued by one lane of the TMA warp per page, which reads
-// its page from the block table three tiles ahead.  Pages none of the tile's
+// its page from the block table four tiles ahead.  Pages none of the tile's
 // rows see are not loaded, and key tiles between a prefix and the band are not
 // visited.  V rows no row of the tile sees (the last page's tail, keys before
 // a window) may hold anything: they are zeroed in shared memory before the
@@ -87,6 +86,15 @@ struct PagedFrag {
   __device__ __forceinline__ int tile(int j) const { return j + (j >= npre ? skip : 0); }
 };
 
+// Registers of a thread at most.  What fits two CTAs on an SM is 168 (wide) and
+// 144; fewer make the compiler lay the softmax loop out otherwise, which is
+// faster with bf16 at d >= 128 (120 against 168: 2048 tokens over 16384 keys 386
+// and 412 us, 2432 over 16432 436 and 478, 2048 over 10048 at d = 256 513 and
+// 519; a chunk of 1000 beside decoding steps, 120 and 114, loses) and slower
+// elsewhere (2048 over 10048 keys, d = 64 bf16, 217 and 203; d = 128 fp16, 242
+// and 236).  The kernels of few rows need 94.
+constexpr int paged_max_regs(int d, bool bf16, bool wide) { return !wide ? 104 : bf16 && d >= 128 ? 120 : 168; }
+
 // WIDE: query tiles of more than 64 rows (p.slot_rows).
 template <int D_, bool WIDE_>
 struct PagedConfig {
@@ -97,8 +105,7 @@ struct PagedConfig {
   static constexpr int KSTAGES = D == 64 ? 4 : 2;
   static constexpr int VSTAGES = D == 64 ? 4 : 2;
   // Few rows: a warp of its own walks the fragments (many short ones).  Many
-  // rows: the TMA warp does, between loads (a seventh warp would leave the
-  // softmax 128 registers).
+  // rows: the TMA warp does, between loads.
   static constexpr bool PLANNER = !WIDE;
   static constexpr int THREADS = PLANNER ? 224 : 192;
   static constexpr int MMA_WARP = 4;
@@ -120,6 +127,7 @@ struct PagedConfig {
   static constexpr uint32_t TMEM_O = 128;
   static constexpr uint32_t TMEM_COLS = D == 256 ? 512 : 256;
   static constexpr int CTAS_PER_SM = D == 256 ? 1 : 2;
+  static_assert(CTAS_PER_SM * THREADS * paged_max_regs(D, false, WIDE) <= 65536, "registers per SM");
   static_assert(4 * sizeof(PagedFrag) <= 512, "fragment descriptions");
   static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
   static_assert(CTAS_PER_SM * (SMEM_BYTES + 1024) <= 233472, "shared memory per SM");
@@ -206,11 +214,12 @@ struct PagedSeq {
     return keys >= 0 ? (long long)t * (p.overhead + keys)
                      : (long long)t * (p.overhead + n_k - n_q) + (long long)p.tile_tokens * t * (t + 1) / 2;
   }
+  // and of the first t tiles, all heads
   template <bool WIDE>
-  __device__ __forceinline__ typename LineOf<WIDE>::T span(const PagedParams& p) const {
-    if (tiles == 0) return 0;
+  __device__ __forceinline__ typename LineOf<WIDE>::T span(const PagedParams& p, int t) const {
+    if (t == 0) return 0;
     if constexpr (WIDE)
-      return (before(p, tiles - 1) + width<true>(p, tiles - 1)) * p.heads_kv;
+      return (before(p, t - 1) + width<true>(p, t - 1)) * p.heads_kv;
     else
       return width<false>(p, 0) * p.heads_kv;
   }
@@ -260,29 +269,70 @@ static __device__ __noinline__ PagedSeq read_seq(const PagedParams& p, int i, bo
   return paged_seq<WIDE>(p, __ldg(p.cu_q + i), __ldg(p.cu_q + i + 1), __ldg(p.lens_k + i), report);
 }
 
-// Where a CTA starts, and the pieces' size.
+// What a CTA works on.
 template <bool WIDE>
 struct PagedPlace {
   typename LineOf<WIDE>::T at;      // the sequence's start on the line
-  typename LineOf<WIDE>::T share;   // a piece; 0: one pair per CTA
+  typename LineOf<WIDE>::T share;   // a piece; 0: this CTA has one pair, whole
   typename LineOf<WIDE>::T total;   // the line's length
-  PagedSeq s;        // the sequence that holds the position
-  int seq;           // its index, or -1: past the end
-  int rank;          // one pair per CTA: the pair's index in its sequence
+  PagedSeq s;        // the sequence that holds the piece's start (the pair)
+  int seq;           // its index, or -1: nothing to do
+  int piece;         // of the line
+  int rank;          // one pair: its index in its sequence
+  bool line;         // the line is cut at this CTA's piece, or ends before it (one pair: false)
 };
 
 template <bool WIDE>
 struct PagedScan {
   typename LineOf<WIDE>::T warp_sum[3][8];
   int warp_longest[8];
+  // the first pairs run whole, `whole` of them; the line holds the rest: of
+  // sequence cut_seq the first cut_tiles query tiles, and the sequences after it
+  int whole, cut_seq, cut_tiles;
+  typename LineOf<WIDE>::T shift;   // positions of the sequences after it lie this much lower
   PagedPlace<WIDE> place;
 };
 
-// Finds the sequence that holds piece `piece`'s start (or, where the batch
-// runs one pair per CTA, pair `piece`).  Every thread sums a run of sequences;
-// every thread returns the same.
+// How many pairs, in order (sequences, their query tiles from the last, heads
+// fastest), run whole, one per CTA, before the rest goes on the line: all,
+// where cutting pairs gains less than it costs to merge them; none; or the
+// full waves of a batch of long pairs, whose CTAs then walk the same keys
+// together (on the line they would not, and K and V past the L2 cache would be
+// read again for each: chunk of 2048 over 62048 keys, 1878 us all on the line,
+// 1618 us so; of 2048 over 16048 keys, which stay in L2, 389 and 430 us).
+// `spans`: the line's length were all on it; `chunk_keys`: keys of the
+// sequences of several query tiles, all K/V heads.
+template <bool WIDE>
+__device__ __forceinline__ int whole_pairs(const PagedParams& p, typename LineOf<WIDE>::T spans,
+                                           typename LineOf<WIDE>::T chunk_keys, typename LineOf<WIDE>::T pairs,
+                                           int longest) {
+  using Line = typename LineOf<WIDE>::T;
+  const Line cost = p.merge_cost / LineOf<WIDE>::KEYS, mean_load = line_div(spans, (Line)p.ctas);
+  if (pairs == 0) return 0;
+  if (longest > max(mean_load, (Line)(p.min_share / LineOf<WIDE>::KEYS)) + cost) {
+    // one of the pairs alone outlasts an even share
+  } else if (pairs <= p.ctas) {
+    return (int)pairs;
+  } else if (WIDE && pairs <= p.pair_ctas) {
+    // The last wave's `rest` pairs, taking the spans to fall evenly from the
+    // longest to the shortest: they end `w` after the full waves, in place of
+    // their spans' even share
+    const float P = (float)pairs, S = (float)p.ctas, mean = (float)spans / P;
+    const float low = fmaxf(2.f * mean - (float)longest, 0.f);
+    const int full = (int)(pairs / p.ctas) * p.ctas;
+    const float w = (float)longest - ((float)longest - low) * ((float)full / P);
+    if (full == pairs || w - 0.5f * (w + low) * ((float)(pairs - full) / S) <= (float)cost) return (int)pairs;
+  }
+  if (WIDE && pairs >= p.ctas && pairs <= p.pair_ctas && 2 * (Line)longest * pairs <= 3 * spans &&
+      chunk_keys > p.cached_keys)
+    return (int)(pairs / p.ctas) * p.ctas;
+  return 0;
+}
+
+// Finds what CTA `block` works on.  Every thread sums a run of sequences; every
+// thread returns the same.
 template <int THREADS, bool WIDE>
-__device__ __forceinline__ PagedPlace<WIDE> find_place(const PagedParams& p, int piece, PagedScan<WIDE>* sh,
+__device__ __forceinline__ PagedPlace<WIDE> find_place(const PagedParams& p, int block, PagedScan<WIDE>* sh,
                                                        bool report) {
   using Line = typename LineOf<WIDE>::T;
   constexpr int KEYS = LineOf<WIDE>::KEYS;
@@ -290,7 +340,7 @@ __device__ __forceinline__ PagedPlace<WIDE> find_place(const PagedParams& p, int
   const int tid = (int)threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int per = (p.batch + THREADS - 1) / THREADS;
   const int i0 = min(tid * per, p.batch), i1 = min(i0 + per, p.batch);
-  // chunks: the line's part in sequences of several query tiles
+  // chunks: keys of the sequences of several query tiles, all K/V heads
   Line span = 0, pairs = 0, chunks = 0;
   int longest = 0;   // pair
   PagedSeq s;
@@ -298,11 +348,11 @@ __device__ __forceinline__ PagedPlace<WIDE> find_place(const PagedParams& p, int
 #pragma unroll 1
   for (int i = i0; i < i1; ++i) {
     s = read_seq<WIDE>(p, i, report);
-    const Line x = s.span<WIDE>(p);
+    const Line x = s.span<WIDE>(p, s.tiles);
     span += x;
     pairs += (Line)s.tiles * p.heads_kv;
     if (s.tiles > 0) longest = max(longest, s.width<WIDE>(p, s.tiles - 1));
-    if (WIDE && s.tiles > 1) chunks += x;
+    if (WIDE && s.tiles > 1) chunks += (Line)s.n_k * p.heads_kv;
   }
   longest = __reduce_max_sync(0xffffffffu, longest);
   Line a = span, b = pairs, c = chunks;
@@ -338,35 +388,70 @@ __device__ __forceinline__ PagedPlace<WIDE> find_place(const PagedParams& p, int
     all_chunks += sh->warp_sum[2][j];
     longest = max(longest, sh->warp_longest[j]);
   }
-  Line share = line_div(total + p.ctas - 1, (Line)p.ctas);
+  int whole = whole_pairs<WIDE>(p, total, all_chunks, all_pairs, longest);
+  int cut_seq = -1, cut_tiles = 0;
+  Line shift = 0;
+  if (WIDE && whole > 0 && whole < all_pairs) {   // part of the pairs: cut at a query tile's first head
+    if (whole >= b && whole < b + pairs) {
+      Line x = a, n = b;
+#pragma unroll 1
+      for (int i = i0; i < i1; ++i) {
+        if (per > 1) s = read_seq<WIDE>(p, i, false);
+        const Line sx = s.span<WIDE>(p, s.tiles), sn = (Line)s.tiles * p.heads_kv;
+        if (whole < n + sn) {
+          const int tiles = (int)(whole - n) / p.heads_kv;   // from the last
+          sh->whole = (int)n + tiles * p.heads_kv;
+          sh->cut_seq = i;
+          sh->cut_tiles = s.tiles - tiles;
+          sh->shift = x + sx - s.span<WIDE>(p, s.tiles - tiles);
+          break;
+        }
+        x += sx;
+        n += sn;
+      }
+    }
+    __syncthreads();
+    whole = sh->whole;
+    cut_seq = sh->cut_seq;
+    cut_tiles = sh->cut_tiles;
+    shift = sh->shift;
+  }
+  const Line rest = whole == all_pairs ? 0 : total - shift;   // the line's length
+  Line share = line_div(rest + p.ctas - 1, (Line)p.ctas);
   if (share < p.min_share / KEYS) share = p.min_share / KEYS;
-  // One pair per CTA: where cutting pairs gains less than it costs to merge
-  // them, and (in the hardware's order, the longest first) for many query tiles
-  const bool whole = (all_pairs <= p.ctas && longest <= share + p.merge_cost / KEYS) ||
-                     (WIDE && p.pair_ctas > 0 && all_pairs >= 4ll * p.ctas && 2 * all_chunks > total);
-  const Line pos = whole ? piece : piece * share;
-  const Line mine = whole ? b : a, size = whole ? pairs : span;
-  if (pos >= mine && pos < mine + size) {
-    Line x = a, n = b;
+  const bool one = block < whole;
+  const Line pos = one ? block : (block - whole) * share;
+  const Line mine = one ? b : a - shift, size = one ? pairs : span;
+  if ((one || pos < rest) && pos >= mine && pos < mine + size) {
+    Line x = mine;
 #pragma unroll 1
     for (int i = i0; i < i1; ++i) {
       if (per > 1) s = read_seq<WIDE>(p, i, false);
-      const Line sx = s.span<WIDE>(p), sn = (Line)s.tiles * p.heads_kv;
-      if (whole ? pos < n + sn : pos < x + sx) {
+      const Line step = one ? (Line)s.tiles * p.heads_kv : s.span<WIDE>(p, s.tiles);
+      if (pos < x + step) {
+        if (WIDE && !one && i == cut_seq) {   // ends where it did, and starts the line
+          x += step - s.span<WIDE>(p, cut_tiles);
+          s.tiles = cut_tiles;
+        }
         sh->place.at = x;
         sh->place.s = s;
         sh->place.seq = i;
-        sh->place.rank = whole ? (int)(pos - n) : 0;
+        sh->place.rank = one ? (int)(pos - x) : 0;
         break;
       }
-      x += sx;
-      n += sn;
+      x += step;
     }
   }
   __syncthreads();
   PagedPlace<WIDE> r = sh->place;
-  r.share = whole ? 0 : share;
-  r.total = total;
+  r.share = one ? 0 : share;
+  r.total = rest;
+  r.piece = block - whole;
+  r.line = !one;
+  if (whole == all_pairs) {   // no line: the first CTAs say so to the merge
+    r.piece = block;
+    r.line = true;
+  }
   return r;
 }
 
@@ -465,7 +550,8 @@ struct FragWalk {
     base.tm.hi -= walk.skip;
   }
 
-  __device__ __forceinline__ void start(const PagedParams& p, const PagedPlace<WIDE>& pl, int piece) {
+  __device__ __forceinline__ void start(const PagedParams& p, const PagedPlace<WIDE>& pl) {
+    const int piece = pl.piece;
     cta = piece;
     seq = pl.seq;
     s = pl.s;
@@ -606,10 +692,9 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map
 // The planner warp (few rows): walks the piece's fragments, up to four ahead of
 // the softmax.
 template <class C, bool BAND>
-__device__ __forceinline__ void pg_plan(const PagedCtx<C>& t, const PagedParams& p, const PagedPlace<C::WIDE>& place, int piece,
-                                        int lane) {
+__device__ __forceinline__ void pg_plan(const PagedCtx<C>& t, const PagedParams& p, const PagedPlace<C::WIDE>& place, int lane) {
   FragWalk<BAND, C::WIDE> walk;
-  walk.start(p, place, piece);
+  walk.start(p, place);
   bool have = true;
 #pragma unroll 1
   for (int nf = 0; have; ++nf) {
@@ -619,7 +704,7 @@ __device__ __forceinline__ void pg_plan(const PagedCtx<C>& t, const PagedParams&
     if (lane == 0) {
       if (!have) f->n = -1;
       mbar_arrive(t.bar(PG_PLAN + (nf & 3)));
-      if (nf == 0 && piece < p.ctas) p.merges[piece] = walk.merge;   // (one pair per CTA: piece may be larger)
+      if (nf == 0 && place.line && place.piece < p.ctas) p.merges[place.piece] = walk.merge;
     }
   }
 }
@@ -635,11 +720,11 @@ __device__ __forceinline__ void pg_plan(const PagedCtx<C>& t, const PagedParams&
 template <class C, bool BAND>
 __device__ __forceinline__ void pg_load(const PagedCtx<C>& t, const PagedParams& p, const CUtensorMap* tm_q,
                                         const CUtensorMap* tm_k, const CUtensorMap* tm_v, const PagedPlace<C::WIDE>& place,
-                                        int piece, int lane) {
+                                        int lane) {
   FragWalk<BAND, C::WIDE> walk;
   if constexpr (!C::PLANNER) {
-    walk.start(p, place, piece);
-    if (lane == 0 && piece < p.ctas) p.merges[piece] = walk.merge;   // (one pair per CTA: piece may be larger)
+    walk.start(p, place);
+    if (lane == 0 && place.line && place.piece < p.ctas) p.merges[place.piece] = walk.merge;
   }
   // Q loads of at most 64 rows leave room for the next fragment's in the other
   // half of the rows (the products then read 64 rows of whatever follows, which
@@ -875,7 +960,9 @@ __device__ __forceinline__ void pg_mma(const PagedCtx<C>& t, const PagedParams& 
       return true;
     };
     if constexpr (C::WIDE) {
-      ok = issue_s(0) && (n == 1 || issue_s(1));
+#pragma unroll 1
+      for (int i = 0; i < min(n, 2) && ok; ++i) ok = issue_s(i);
+#pragma unroll 1
       for (int j = 0; j < n && ok; ++j) ok = issue_pv(j) && (j + 2 >= n || issue_s(j + 2));
     } else {
 #pragma unroll 1
@@ -1121,7 +1208,7 @@ __device__ __forceinline__ void pg_softmax(const PagedCtx<C>& t, const PagedPara
 }
 
 template <int D, bool BF16, bool BAND, bool WIDE>
-__global__ void __launch_bounds__(PagedConfig<D, WIDE>::THREADS, PagedConfig<D, WIDE>::CTAS_PER_SM)
+__global__ void __launch_bounds__(PagedConfig<D, WIDE>::THREADS) __maxnreg__(paged_max_regs(D, BF16, WIDE))
     fa2_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PagedParams p) {
   using C = PagedConfig<D, WIDE>;
@@ -1163,21 +1250,20 @@ __global__ void __launch_bounds__(PagedConfig<D, WIDE>::THREADS, PagedConfig<D, 
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
   }
-  const int piece = (int)blockIdx.x;
   tc_fence_before();
-  const PagedPlace<WIDE> place = find_place<C::THREADS, WIDE>(p, piece, scan, blockIdx.x == 0);   // with its barriers
+  const PagedPlace<WIDE> place = find_place<C::THREADS, WIDE>(p, (int)blockIdx.x, scan, blockIdx.x == 0);   // with its barriers
   tc_fence_after();
   t.tmem = *tmem_slot;
 
-  if (place.seq < 0) {   // no piece for this CTA
-    if (threadIdx.x == 0 && piece < p.ctas) p.merges[piece].count = -1;
+  if (place.seq < 0) {   // nothing for this CTA
+    if (threadIdx.x == 0 && place.line && place.piece < p.ctas) p.merges[place.piece].count = -1;
   } else if (warp == C::TMA_WARP) {
-    pg_load<C, BAND>(t, p, &tm_q, &tm_k, &tm_v, place, piece, lane);
+    pg_load<C, BAND>(t, p, &tm_q, &tm_k, &tm_v, place, lane);
   } else if (warp == C::MMA_WARP) {
     if (lane == 0) pg_mma<C, BF16>(t, p);
     __syncwarp();
   } else if (C::PLANNER && warp == C::PLAN_WARP) {
-    pg_plan<C, BAND>(t, p, place, piece, lane);
+    pg_plan<C, BAND>(t, p, place, lane);
   } else {
     pg_softmax<C, BF16, BAND>(t, p, warp, lane);
   }
@@ -1304,7 +1390,9 @@ int launch_paged_kernels(const PagedLaunchArgs& a) {
     return (int)cudaFuncSetAttribute(fa2_paged_merge_kernel<D, BF16>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
   });
   if (e != 0) return e;
-  const int grid = a.p.pair_ctas > a.p.ctas ? a.p.pair_ctas : a.p.ctas;
+  // whole waves (few rows: all of the batch is on the line, or at most `ctas` pairs)
+  const int waves = WIDE ? (a.p.pair_ctas + a.p.ctas - 1) / a.p.ctas : 1;
+  const int grid = a.p.ctas * (waves > 1 ? waves : 1);
   kern<<<(unsigned)grid, C::THREADS, C::SMEM_BYTES, a.stream>>>(a.tm_q, a.tm_k, a.tm_v, a.p);
   const cudaError_t r = cudaGetLastError();
   if (r != cudaSuccess) return (int)r;

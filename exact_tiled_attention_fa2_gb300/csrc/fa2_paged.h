@@ -52,8 +52,9 @@ struct PagedParams {
   float scale_log2_mag;   // as KernelParams
   uint32_t qk_negate;     // as KernelParams
   int ctas;               // pieces the line of work is cut into
-  int pair_ctas;          // CTAs for one (query tile, K/V head) pair each where
-                          // the batch may have that many, or 0
+  int pair_ctas;          // most pairs that may run whole (the grid holds that many
+                          // CTAs, rounded up to whole waves), or 0: up to ctas
+  int cached_keys;        // keys (of one K/V head) whose K and V stay in the L2 cache
   int overhead;           // a pair's fixed cost on the line, in keys (whole key tiles)
   int min_share;          // keys of a piece at least (whole key tiles)
   int merge_cost;         // what a merge costs, in keys of one CTA's work (whole key tiles)

@@ -114,9 +114,9 @@ int paged_shape(const fa2_paged_params& a, PagedShape& s) {
   if (tiles > a.batch * each) tiles = a.batch * each;
   if (tiles > a.total_q) tiles = a.total_q;
   const long long pairs = tiles * c.heads;
-  if (pairs > INT_MAX) return FA2_ERR_UNSUPPORTED;
+  if (pairs > INT_MAX - 1024) return FA2_ERR_UNSUPPORTED;
   s.ctas = paged_ctas(c.head_dim);
-  s.pair_ctas = pairs >= 4 * s.ctas ? (int)pairs : 0;
+  s.pair_ctas = pairs >= s.ctas ? (int)pairs : 0;
   const size_t rows = 2 * (size_t)s.ctas * (size_t)(s.group * s.box_tokens);
   s.ws_o_bytes = align256(rows * (size_t)c.head_dim * 4);
   s.ws_ml_bytes = align256(rows * 2 * 4);
@@ -249,6 +249,7 @@ int paged_forward(const fa2_paged_params& a, void* workspace, size_t workspace_b
   p.overhead = (kPagedOverhead + 2 * p.slot_rows + 63) / 64 * 64;
   p.ctas = s.ctas;
   p.pair_ctas = s.pair_ctas;
+  p.cached_keys = (96 << 20) / (4 * c.head_dim);   // 96 of the 126 MB
   p.min_share = kPagedMinShare > 8 * p.slot_rows ? kPagedMinShare : (8 * p.slot_rows + 63) / 64 * 64;
   p.ws_o = static_cast<float*>(workspace);
   p.ws_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + s.ws_o_bytes);

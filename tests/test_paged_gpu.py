@@ -267,6 +267,20 @@ def test_many_query_tiles():
     p.check(o, lse, window_left=300, window_right=0, prefix_len=10)
 
 
+@pytest.mark.parametrize("lens_q,lens_k", [
+    ([1, 700, 0, 100], [900, 12800, 30, 13000]),   # the first wave ends inside a sequence,
+    ([600, 100, 3], [13000, 13100, 500]),          # between two,
+    ([90, 700, 128], [700, 13000, 128]),           # and over short ones
+])
+def test_full_waves_of_long_pairs(lens_q, lens_k):
+    """Chunks whose keys outgrow the L2 cache: full waves of (query tile, K/V head) pairs run whole, the rest is cut."""
+    p = Problem(lens_q, lens_k, 32, 8, 256, "fp16", 64, seed=14, fill=float("nan"))
+    for kw in (dict(window_right=0), dict(window_right=3, prefix_len=100)):
+        o, lse = p.run(**kw)
+        assert status() == fa2.FA2_OK
+        p.check(o, lse, **kw)
+
+
 def test_layouts_equal_contiguous():
     """[page, row, head] caches, K and V interleaved, q and o as parts of wider rows, a sliced table."""
     p = Problem([3, 1, 70], [400, 33, 200], 8, 2, 128, "bf16", 16, seed=21)
