@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(kPlanThreads) fa2_paged_plan_kernel(const Page
   const int count = *a.free_count;
   if (bad_any || all_tok > a.total_q || count < 0 || count > a.num_free || all_pag > count) {
     // refused: an empty step, the table and the free list as they were
-    for (int i = (int)blockIdx.x * kPlanThreads + tid; i < max(a.total_q, a.batch + 1);
+    for (long long i = (long long)blockIdx.x * kPlanThreads + tid; i < max(a.total_q, a.batch + 1);
          i += (int)gridDim.x * kPlanThreads) {
       if (i < a.total_q) a.slots[i] = -1;
       if (i <= a.batch) a.cu_q[i] = 0;

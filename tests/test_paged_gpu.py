@@ -498,6 +498,18 @@ def test_plan_refuses_a_step_whole(why):
     assert (cache == 0).all() and (v_cache == 0).all() and (o == 3).all()
 
 
+@pytest.mark.parametrize("count,code", [(1, fa2.FA2_OK), (0, fa2.FA2_ERR_DEVICE_PAGES)])
+def test_plan_of_almost_2_31_rows(count, code):
+    """Padding whose row numbers end just below 2^31, in a step that fits and in one that is refused."""
+    total = 2 ** 31 - 1000
+    table = torch.full((2, 4), -1, dtype=torch.int32, device="cuda")
+    cu, lens, slots, left = fa2.fa2_paged_plan(i32([0, 0]), i32([3, 0]), table, i32([7]), i32([count]), 9, 16, total)
+    assert status() == code
+    assert slots[:3].tolist() == ([112, 113, 114] if count else [-1] * 3)
+    assert slots[3:].max().item() == -1 and slots[3:].min().item() == -1
+    assert cu.tolist() == ([0, 3, 3] if count else [0, 0, 0]) and left.item() == 0
+
+
 def test_plan_reports_bad_pages():
     # the held partial page of request 0 and the first page taken are out of range: their tokens get no slot
     table = i32([[64, -1, -1], [3, -1, -1]])
