@@ -303,6 +303,66 @@ def test_layouts_equal_contiguous():
     assert (lse_wide[:, :20] == 7).all() and (lse_wide[:, 94:] == 7).all()
 
 
+@pytest.mark.parametrize("mask", sorted(MASKS))
+@pytest.mark.parametrize("lens_q,lens_k", [([5, 2, 9], [2, 0, 8]), ([200, 130, 1, 64], [50, 0, 0, 63]), ([300], [299])])
+def test_more_tokens_than_keys(lens_q, lens_k, mask):
+    """The first tokens come before every key: rows that see nothing, or only the prefix."""
+    wl, wr, pre = MASKS[mask]
+    p = Problem(lens_q, lens_k, 6, 2, 128, "bf16", 16, seed=23, fill=float("nan"))
+    kw = dict(window_left=wl, window_right=wr, prefix_len=pre)
+    o, lse = p.run(**kw)
+    assert status() == fa2.FA2_OK
+    p.check(o, lse, **kw)
+
+
+def test_strides_of_single_dimensions_do_not_count():
+    """One token, one head, one page, one sequence: whatever stride the dimension has."""
+    p = Problem([1], [11], 1, 1, 64, "fp16", 16, seed=24, pages=1)
+    o, lse = p.run(window_right=0)
+    p.check(o, lse, window_right=0)
+    odd = lambda x, st: torch.as_strided(x, x.shape, st, x.storage_offset())
+    args = (odd(p.q, (3, 5, 1)), odd(p.k, (1, 7, 64, 1)), odd(p.v, (0, 1, 64, 1)), odd(p.table, (0, 1)), p.cu, p.lens)
+    o2, lse2 = fa2.fa2_paged_fwd(*args, window_right=0)
+    assert status() == fa2.FA2_OK
+    assert torch.equal(o2, o) and torch.equal(lse2, lse)
+    k, v = torch.zeros_like(p.k), torch.zeros_like(p.v)
+    new = torch.ones((1, 1, 64), dtype=torch.float16, device="cuda")
+    fa2.fa2_paged_append(odd(new, (3, 5, 1)), new, i32([4]), odd(k, (1, 7, 64, 1)), v)
+    assert status() == fa2.FA2_OK
+    assert (k[0, 0, 4] == 1).all() and k.sum() == 64 and torch.equal(k, v)
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_sequences_sharing_one_table_row(new):
+    """A prompt's pages read by several sequences through one row (stride 0), each with its own length."""
+    p = Problem([new] * 5, [700, 64, 333, 80, 699], 8, 2, 128, "bf16", 16, seed=25)
+    shared = p.table[:1].expand(5, -1)
+    q = Problem.__new__(Problem)
+    q.__dict__.update(p.__dict__)
+    q.table = shared
+    o, lse = q.run(window_right=0)
+    assert status() == fa2.FA2_OK
+    q.check(o, lse, window_right=0)
+
+
+def test_two_forwards_at_once():
+    """Long and short calls overlapping on two streams, few and many rows, each with its own workspace."""
+    probs = [Problem([1] * 40, [2000 + 37 * i for i in range(40)], 16, 4, 128, "bf16", 16, seed=26),
+             Problem([300, 77], [5000, 900], 16, 4, 128, "bf16", 64, seed=27)]
+    want = [p.run(window_right=0) for p in probs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in probs]
+    outs = [[], []]
+    for _ in range(20):
+        for p, st, out in zip(probs, streams, outs):
+            out.append(p.run(window_right=0, stream=st))
+    assert status() == fa2.FA2_OK
+    for p, (wo, wl), out in zip(probs, want, outs):
+        p.check(wo, wl, window_right=0)
+        for o, lse in out:
+            assert torch.equal(o, wo) and torch.equal(lse, wl)
+
+
 def test_padded_pages():
     """Page strides that are no whole number of head strides (pages padded apart), in K, in V and in both."""
     p = Problem([3, 1, 70], [400, 33, 200], 6, 3, 64, "fp16", 32, seed=22)
