@@ -21,7 +21,10 @@ constexpr long long kMaxStride = 1ll << 39;   // elements: 16-bit strides stay b
 constexpr int paged_ctas(int d) { return d == 256 ? 152 : 304; }
 // A pair's fixed cost (Q, the first products, the epilogue) in keys, and the
 // shortest piece worth a CTA: 128 keys, or (many rows) the keys whose K and V
-// are as many bytes as a partial's write and read four times over.
+// are twice as many bytes as a partial's write and read (100 tokens over 9000
+// keys, d = 128: 28.4 us, with pieces twice as long 32.1, half as long 28.5;
+// 8 drafted tokens x 8 heads, 4 requests of 2000 keys: 18.8, 21.0, 19.6; 60 over
+// 32000 at d = 256, few pairs of many partials, 42.7, 40.2, 55.5).
 constexpr int kPagedOverhead = 128;
 constexpr int kPagedMinShare = 128;
 constexpr int kPagedMaxHeads = 65536;
@@ -250,7 +253,7 @@ int paged_forward(const fa2_paged_params& a, void* workspace, size_t workspace_b
   p.ctas = s.ctas;
   p.pair_ctas = s.pair_ctas;
   p.cached_keys = (96 << 20) / (4 * c.head_dim);   // 96 of the 126 MB
-  p.min_share = kPagedMinShare > 8 * p.slot_rows ? kPagedMinShare : (8 * p.slot_rows + 63) / 64 * 64;
+  p.min_share = kPagedMinShare > 4 * p.slot_rows ? kPagedMinShare : (4 * p.slot_rows + 63) / 64 * 64;
   p.ws_o = static_cast<float*>(workspace);
   p.ws_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + s.ws_o_bytes);
   p.merges = reinterpret_cast<PagedMerge*>(static_cast<uint8_t*>(workspace) + s.ws_o_bytes + s.ws_ml_bytes);
