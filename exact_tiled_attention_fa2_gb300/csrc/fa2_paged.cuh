@@ -1224,13 +1224,6 @@ __global__ void __launch_bounds__(PagedConfig<D, WIDE>::THREADS) __maxnreg__(pag
   const int lane = (int)(threadIdx.x & 31);
   grid_launch_dependents();   // the merge may be scheduled once every CTA has started; it waits for the partials
 
-  // Tensor memory and barriers before the schedule: an SM's second CTA starts
-  // only when the first has let go of the allocation permit (measured: 3.6 us
-  // into the kernel with the allocation behind the schedule, half of the CTAs).
-  if (warp == C::MMA_WARP) {
-    tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
-    tmem_relinquish();
-  }
   PagedCtx<C> t;
   t.bar0 = sbase + C::OFF_BAR;
   t.sQ = sbase + C::OFF_Q;
@@ -1249,6 +1242,17 @@ __global__ void __launch_bounds__(PagedConfig<D, WIDE>::THREADS) __maxnreg__(pag
     tma_prefetch_desc(&tm_q);
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
+  }
+  // What precedes this kernel is complete: from here on it touches memory, and
+  // takes tensor memory (held while waiting, it could be what a kernel before
+  // this one waits for).
+  grid_dependency_wait();
+  // Tensor memory before the schedule: an SM's second CTA starts only when the
+  // first has let go of the allocation permit (measured: 3.6 us into the kernel
+  // with the allocation behind the schedule, half of the CTAs).
+  if (warp == C::MMA_WARP) {
+    tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
+    tmem_relinquish();
   }
   tc_fence_before();
   const PagedPlace<WIDE> place = find_place<C::THREADS, WIDE>(p, (int)blockIdx.x, scan, blockIdx.x == 0);   // with its barriers
@@ -1293,6 +1297,7 @@ __global__ void __launch_bounds__(kPagedMergeThreads) fa2_paged_merge_kernel(con
   const int r0 = (int)blockIdx.y * kPagedMergeRows;
   const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31;
   grid_dependency_wait();   // the partials and descriptions are complete and visible
+  grid_launch_dependents();
   const PagedMerge mg = p.merges[blockIdx.x + 1];
   if (mg.count < 0 || r0 >= mg.rows) return;
   const int here = min(mg.rows - r0, kPagedMergeRows);
@@ -1393,19 +1398,11 @@ int launch_paged_kernels(const PagedLaunchArgs& a) {
   // whole waves (few rows: all of the batch is on the line, or at most `ctas` pairs)
   const int waves = WIDE ? (a.p.pair_ctas + a.p.ctas - 1) / a.p.ctas : 1;
   const int grid = a.p.ctas * (waves > 1 ? waves : 1);
-  kern<<<(unsigned)grid, C::THREADS, C::SMEM_BYTES, a.stream>>>(a.tm_q, a.tm_k, a.tm_v, a.p);
-  const cudaError_t r = cudaGetLastError();
-  if (r != cudaSuccess) return (int)r;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(a.p.ctas - 1), (unsigned)((a.p.slot_rows + kPagedMergeRows - 1) / kPagedMergeRows));
-  cfg.blockDim = dim3(kPagedMergeThreads);
-  cfg.stream = a.stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return (int)cudaLaunchKernelEx(&cfg, fa2_paged_merge_kernel<D, BF16>, a.p);
+  const int r = launch_dependent(kern, dim3((unsigned)grid), C::THREADS, C::SMEM_BYTES, a.stream, a.tm_q, a.tm_k, a.tm_v,
+                                 a.p);
+  if (r != 0) return r;
+  const dim3 blocks((unsigned)(a.p.ctas - 1), (unsigned)((a.p.slot_rows + kPagedMergeRows - 1) / kPagedMergeRows));
+  return launch_dependent(fa2_paged_merge_kernel<D, BF16>, blocks, kPagedMergeThreads, 0, a.stream, a.p);
 }
 
 template <int D, bool BF16>

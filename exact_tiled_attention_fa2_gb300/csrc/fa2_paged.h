@@ -114,6 +114,25 @@ struct PagedAppendArgs {
 
 int launch_paged_append(const PagedAppendArgs& a, cudaStream_t stream);
 
+// Launches a kernel as a programmatic dependent of what precedes it on the
+// stream: it may be scheduled before that is done, and calls
+// grid_dependency_wait before it touches memory.
+template <class... Params, class... Args>
+int launch_dependent(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                     const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return (int)cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Services of the C-ABI translation unit: the current device's status word
 // (checks the device), and a tensor map of a 16-bit tensor whose innermost
 // dimension is contiguous (strides of the others in elements; 128-byte

@@ -6,6 +6,7 @@
 #include <atomic>
 
 #include "fa2_internal.h"
+#include "sm103_ptx.cuh"
 
 namespace fa2 {
 namespace {
@@ -64,6 +65,8 @@ __device__ __forceinline__ int last_at_most(const int* x, int n, int v) {
 // in a new page comes from the free list itself, not from the table entry
 // another block may still be writing.
 __global__ void __launch_bounds__(kPlanThreads) fa2_paged_plan_kernel(const PagedPlanArgs a) {
+  grid_launch_dependents();
+  grid_dependency_wait();
   extern __shared__ int sums[];             // [batch + 1] first token, [batch + 1] first new page
   __shared__ long long scratch[2 * kPlanThreads / 32];
   __shared__ int bad_any;
@@ -158,6 +161,8 @@ __global__ void __launch_bounds__(kPlanThreads) fa2_paged_plan_kernel(const Page
 // rows read beside its slot.  Bound by HBM: 32768 tokens of 8 heads x 128, 268
 // MB in 40.8 us, 6591 GB/s (four tokens a thread: 41.9 us).
 __global__ void __launch_bounds__(256) fa2_paged_append_kernel(const PagedAppendArgs a) {
+  grid_launch_dependents();
+  grid_dependency_wait();
   const int items = a.heads << a.row_chunks_log2;
   const int mask = (1 << a.row_chunks_log2) - 1;
   const long long t = (long long)blockIdx.x * blockDim.y + threadIdx.y;
@@ -188,17 +193,16 @@ int launch_paged_plan(const PagedPlanArgs& a, cudaStream_t stream) {
   long long blocks = ((long long)a.total_q + kPlanThreads - 1) / kPlanThreads;
   if (blocks > 152) blocks = 152;
   const size_t smem = 2 * ((size_t)a.batch + 1) * sizeof(int);
-  fa2_paged_plan_kernel<<<(unsigned)blocks, kPlanThreads, smem, stream>>>(a);
-  return (int)cudaGetLastError();
+  return launch_dependent(fa2_paged_plan_kernel, dim3((unsigned)blocks), kPlanThreads, smem, stream, a);
 }
 
 int launch_paged_append(const PagedAppendArgs& a, cudaStream_t stream) {
   const int items = a.heads << a.row_chunks_log2;
   int x = 8;
   while (x < 256 && x < items) x *= 2;
-  const dim3 block(x, 256 / x);
-  fa2_paged_append_kernel<<<(unsigned)(((long long)a.total + block.y - 1) / block.y), block, 0, stream>>>(a);
-  return (int)cudaGetLastError();
+  const int tokens = 256 / x;   // of a block
+  return launch_dependent(fa2_paged_append_kernel, dim3((unsigned)(((long long)a.total + tokens - 1) / tokens)),
+                          dim3(x, tokens), 0, stream, a);
 }
 
 }  // namespace fa2
