@@ -86,15 +86,6 @@ struct PagedFrag {
   __device__ __forceinline__ int tile(int j) const { return j + (j >= npre ? skip : 0); }
 };
 
-// Registers of a thread at most.  What fits two CTAs on an SM is 168 (wide) and
-// 144; fewer make the compiler lay the softmax loop out otherwise, which is
-// faster with bf16 at d >= 128 (120 against 168: 2048 tokens over 16384 keys 386
-// and 412 us, 2432 over 16432 436 and 478, 2048 over 10048 at d = 256 513 and
-// 519; a chunk of 1000 beside decoding steps, 120 and 114, loses) and slower
-// elsewhere (2048 over 10048 keys, d = 64 bf16, 217 and 203; d = 128 fp16, 242
-// and 236).  The kernels of few rows need 94.
-constexpr int paged_max_regs(int d, bool bf16, bool wide) { return !wide ? 104 : bf16 && d >= 128 ? 120 : 168; }
-
 // WIDE: query tiles of more than 64 rows (p.slot_rows).
 template <int D_, bool WIDE_>
 struct PagedConfig {
@@ -127,7 +118,6 @@ struct PagedConfig {
   static constexpr uint32_t TMEM_O = 128;
   static constexpr uint32_t TMEM_COLS = D == 256 ? 512 : 256;
   static constexpr int CTAS_PER_SM = D == 256 ? 1 : 2;
-  static_assert(CTAS_PER_SM * THREADS * paged_max_regs(D, false, WIDE) <= 65536, "registers per SM");
   static_assert(4 * sizeof(PagedFrag) <= 512, "fragment descriptions");
   static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
   static_assert(CTAS_PER_SM * (SMEM_BYTES + 1024) <= 233472, "shared memory per SM");
@@ -643,12 +633,12 @@ static __device__ __noinline__ bool next_fragment_far(FragWalk<BAND, WIDE>& k, c
 
 // ---------------------------------------------------------------- the warps' roles
 
-// Waits as wait_or_abort.  With few rows (C::WIDE false) all but the first look
-// is out of line: such a kernel runs little of its code often, and what each of
-// the many waits carries along is fetched from L2 again and again (256 requests
-// of 1..1000 keys, d = 128: 28 % of the instruction cache's requests missed).
-// With many rows the call itself costs more (prompt chunk of 2048 over 16384
-// keys: 469 against 426 us).
+// Waits as wait_or_abort.  A kernel of few rows runs little of its code often,
+// and what each of the many waits carries along is fetched from L2 again and
+// again (256 requests of 1..1000 keys, d = 128: 28 % of the instruction cache's
+// requests missed with them inline), so all but a wait's first look is out of
+// line.  With many rows the MMA thread's waits are inline (a call costs more:
+// prompt chunk of 2048 over 16384 keys 469 against 426 us).
 static __device__ __noinline__ bool paged_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                                     uint32_t* status, uint32_t site) {
   return wait_or_abort(bar, parity, abort_flag, status, site);
@@ -661,6 +651,29 @@ __device__ __forceinline__ bool paged_wait(uint32_t bar, uint32_t parity, volati
   else
     return mbar_try_wait(bar, parity) || paged_wait_slow(bar, parity, abort_flag, status, site);
 }
+// A whole warp whose lanes look together: a barrier already passed costs one
+// look and one vote.
+static __device__ __noinline__ bool paged_warp_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                                         uint32_t* status, uint32_t site) {
+  const uint64_t t0 = global_timer_ns();
+  for (uint32_t it = 1;; ++it) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if ((it & 31u) == 0) {
+      bool stop = *abort_flag != 0;
+      if (!stop && global_timer_ns() - t0 > kWaitLimitNs) {
+        *abort_flag = 1;
+        atomicOr(status, kStatusTimeout | (1u << (8 + site)));
+        stop = true;
+      }
+      if (__any_sync(0xffffffffu, stop)) return false;
+    }
+  }
+}
+__device__ __forceinline__ bool paged_warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                                uint32_t* status, uint32_t site) {
+  return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) ||
+         paged_warp_wait_slow(bar, parity, abort_flag, status, site);
+}
 static __device__ __noinline__ void paged_drain(uint32_t bar, uint32_t parity, uint32_t* status) {
   wait_drain(bar, parity, status);
 }
@@ -672,10 +685,13 @@ struct PagedCtx {
   uint32_t* status;
   PagedFrag* frags;   // four
   __device__ __forceinline__ uint32_t bar(int i) const { return bar0 + 8u * (uint32_t)i; }
-  // One warp waits through lane 0 (the others only need its answer).
+  // The TMA or planner warp: its lanes look together, then lane 0 waits for all.
+  // The TMA warp's time per tile is part of the tile loop's period (2048 tokens
+  // over 10048 keys in pages of 16, d = 128: 247 us, 274 with lane 0 alone).
   __device__ __forceinline__ bool warp_wait(int i, int phase, uint32_t site, int lane) const {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar(i), (uint32_t)phase & 1))) return true;
     bool ok = true;
-    if (lane == 0) ok = paged_wait<C::WIDE>(bar(i), (uint32_t)phase & 1, abort_flag, status, site);
+    if (lane == 0) ok = paged_wait_slow(bar(i), (uint32_t)phase & 1, abort_flag, status, site);
     return __all_sync(0xffffffffu, ok);
   }
 };
@@ -809,13 +825,17 @@ __device__ __forceinline__ void pg_load(const PagedCtx<C>& t, const PagedParams&
     return c;
   };
   const uint32_t box_bytes = (uint32_t)p.box_rows * (uint32_t)(C::D * 2);
-  // Tile q of the four whose lanes with a box are `lanes`.
+  // Tile q of the four whose lanes with a box are `lanes`.  (The boxes may land
+  // before lane 0 has announced their bytes: its arrival is what lets the
+  // barrier complete.  Keeping the lanes in step is faster with many rows, 240
+  // against 250 us for 2048 tokens over 10048 keys, and slower with few, 120
+  // against 102 for 256 requests of 1..1000 keys.)
   auto issue = [&](const At& c, unsigned lanes, int q, const CUtensorMap* tm, uint32_t s_tile, uint32_t bar) {
     const unsigned mine = lanes & (255u << (8 * q));
     if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)__popc(mine) * box_bytes);
-    __syncwarp();
+    if constexpr (C::WIDE) __syncwarp();
     if ((mine >> lane) & 1u) tma_load_5d(s_tile + (uint32_t)my_box * box_bytes, tm, 0, c.c1, 0, c.c3, c.c4, bar);
-    __syncwarp();
+    if constexpr (C::WIDE) __syncwarp();
   };
   int g = 0, gv = 0;            // key tiles loaded
   int nf = -1, j = 0, n = 0;    // the fragment, the tile to load next, its tiles
@@ -1027,8 +1047,12 @@ __device__ __forceinline__ void pg_softmax(const PagedCtx<C>& t, const PagedPara
   const uint32_t tO = t.tmem + lane_off + C::TMEM_O;
   const float sl2 = p.scale_log2_mag;
   auto wait = [&](int bar, int phase, uint32_t site) -> bool {
-    const bool ok = paged_wait<C::WIDE>(t.bar(bar), (uint32_t)phase & 1, t.abort_flag, t.status, site);
-    return __all_sync(0xffffffffu, ok);
+    // (2048 tokens over 10048 keys: d = 64 198 us with the looks together, 201
+    // apart, d = 256 497 and 515; but d = 128, many rows, 253 and 241)
+    if constexpr (C::WIDE && C::D == 128)
+      return __all_sync(0xffffffffu, wait_or_abort(t.bar(bar), (uint32_t)phase & 1, t.abort_flag, t.status, site));
+    else
+      return paged_warp_wait(t.bar(bar), (uint32_t)phase & 1, t.abort_flag, t.status, site);
   };
   int g = 0;   // key tiles
   for (int nf = 0;; ++nf) {
@@ -1208,7 +1232,7 @@ __device__ __forceinline__ void pg_softmax(const PagedCtx<C>& t, const PagedPara
 }
 
 template <int D, bool BF16, bool BAND, bool WIDE>
-__global__ void __launch_bounds__(PagedConfig<D, WIDE>::THREADS) __maxnreg__(paged_max_regs(D, BF16, WIDE))
+__global__ void __launch_bounds__(PagedConfig<D, WIDE>::THREADS, PagedConfig<D, WIDE>::CTAS_PER_SM)
     fa2_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PagedParams p) {
   using C = PagedConfig<D, WIDE>;
