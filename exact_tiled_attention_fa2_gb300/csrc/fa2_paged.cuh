@@ -888,6 +888,7 @@ __device__ __forceinline__ void pg_load(const PagedCtx<C>& t, const PagedParams&
     cv_last = cv;
     lanes_last = lanes;
     v_left = 1 + (j & 3);
+    if (j > C::VSTAGES + 1) continue;   // what follows is due by then
     if (j > 0 && j == min(n, 3) - 1 && walked == nf + 1) look_ahead();
     if (!ok) break;
     // this fragment at its first tile; the next one, with room for its Q, once V_j with j = VSTAGES has waited
