@@ -11,38 +11,40 @@
 namespace fa2 {
 namespace {
 
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 1024;   // of a block, at most
+
+// Inclusive prefix sums of (a, b) over a warp's lanes.
+__device__ __forceinline__ void warp_scan2(long long& a, long long& b, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long va = __shfl_up_sync(0xffffffffu, a, o), vb = __shfl_up_sync(0xffffffffu, b, o);
+    if (lane >= o) {
+      a += va;
+      b += vb;
+    }
+  }
+}
 
 // Exclusive prefix sums of (a, b) over the block's threads and their totals.
 __device__ __forceinline__ void block_scan2(long long& a, long long& b, long long& total_a, long long& total_b,
                                             long long* scratch) {
-  const int lane = (int)threadIdx.x & 31, w = (int)threadIdx.x >> 5;
+  const int lane = (int)threadIdx.x & 31, w = (int)threadIdx.x >> 5, warps = (int)blockDim.x >> 5;
   long long ia = a, ib = b;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long va = __shfl_up_sync(0xffffffffu, ia, o), vb = __shfl_up_sync(0xffffffffu, ib, o);
-    if (lane >= o) {
-      ia += va;
-      ib += vb;
-    }
-  }
+  warp_scan2(ia, ib, lane);
   if (lane == 31) {
     scratch[2 * w] = ia;
     scratch[2 * w + 1] = ib;
   }
   __syncthreads();
-  long long before_a = 0, before_b = 0;
-  total_a = total_b = 0;
-  for (int j = 0; j < (int)(blockDim.x >> 5); ++j) {
-    if (j == w) {
-      before_a = total_a;
-      before_b = total_b;
-    }
-    total_a += scratch[2 * j];
-    total_b += scratch[2 * j + 1];
-  }
-  a = before_a + ia - a;
-  b = before_b + ib - b;
+  // the warps' sums, scanned by every warp
+  long long wa = lane < warps ? scratch[2 * lane] : 0, wb = lane < warps ? scratch[2 * lane + 1] : 0;
+  warp_scan2(wa, wb, lane);
+  total_a = __shfl_sync(0xffffffffu, wa, 31);
+  total_b = __shfl_sync(0xffffffffu, wb, 31);
+  const long long before_a = __shfl_sync(0xffffffffu, wa, max(w - 1, 0));
+  const long long before_b = __shfl_sync(0xffffffffu, wb, max(w - 1, 0));
+  a = (w > 0 ? before_a : 0) + ia - a;
+  b = (w > 0 ? before_b : 0) + ib - b;
 }
 
 // Last index i in [0, n) with x[i] <= v (x non-decreasing, x[0] <= v).
@@ -72,9 +74,9 @@ __global__ void __launch_bounds__(kPlanThreads) fa2_paged_plan_kernel(const Page
   __shared__ int bad_any;
   int* tok = sums;
   int* pag = sums + a.batch + 1;
-  const int tid = (int)threadIdx.x;
+  const int tid = (int)threadIdx.x, threads = (int)blockDim.x;
   const unsigned ps = (unsigned)a.page_size;
-  const int per = (a.batch + kPlanThreads - 1) / kPlanThreads;
+  const int per = (a.batch + threads - 1) / threads;
   const int i0 = min(tid * per, a.batch), i1 = min(i0 + per, a.batch);
   if (tid == 0) bad_any = 0;
   __syncthreads();
@@ -95,8 +97,8 @@ __global__ void __launch_bounds__(kPlanThreads) fa2_paged_plan_kernel(const Page
   const int count = *a.free_count;
   if (bad_any || all_tok > a.total_q || count < 0 || count > a.num_free || all_pag > count) {
     // refused: an empty step, the table and the free list as they were
-    for (long long i = (long long)blockIdx.x * kPlanThreads + tid; i < max(a.total_q, a.batch + 1);
-         i += (int)gridDim.x * kPlanThreads) {
+    for (long long i = (long long)blockIdx.x * threads + tid; i < max(a.total_q, a.batch + 1);
+         i += (int)gridDim.x * threads) {
       if (i < a.total_q) a.slots[i] = -1;
       if (i <= a.batch) a.cu_q[i] = 0;
       if (i < a.batch) a.lens_k[i] = 0;
@@ -128,8 +130,8 @@ __global__ void __launch_bounds__(kPlanThreads) fa2_paged_plan_kernel(const Page
   }
   __syncthreads();
   bool bad_page = false;
-  const int stride = (int)gridDim.x * kPlanThreads;
-  for (long long tl = (long long)blockIdx.x * kPlanThreads + tid; tl < a.total_q; tl += stride) {
+  const int stride = (int)gridDim.x * threads;
+  for (long long tl = (long long)blockIdx.x * threads + tid; tl < a.total_q; tl += stride) {
     const int t = (int)tl;
     int slot = -1;
     if (t < (int)all_tok) {
@@ -145,7 +147,7 @@ __global__ void __launch_bounds__(kPlanThreads) fa2_paged_plan_kernel(const Page
     }
     a.slots[t] = slot;
   }
-  for (long long nl = (long long)blockIdx.x * kPlanThreads + tid; nl < all_pag; nl += stride) {
+  for (long long nl = (long long)blockIdx.x * threads + tid; nl < all_pag; nl += stride) {
     const int n = (int)nl;
     const int b = last_at_most(pag, a.batch, n);
     const unsigned held = ((unsigned)a.context_lens[b] + ps - 1) / ps;
@@ -190,10 +192,12 @@ int launch_paged_plan(const PagedPlanArgs& a, cudaStream_t stream) {
                                      2 * (kPagedPlanMaxBatch + 1) * (int)sizeof(int));
   });
   if (e != 0) return e;
-  long long blocks = ((long long)a.total_q + kPlanThreads - 1) / kPlanThreads;
-  if (blocks > 152) blocks = 152;
+  // few requests: small blocks, whose scan is short
+  const int threads = a.batch <= 256 ? 256 : kPlanThreads;
+  long long blocks = ((long long)a.total_q + threads - 1) / threads;
+  if (blocks > 152 * kPlanThreads / threads) blocks = 152 * kPlanThreads / threads;
   const size_t smem = 2 * ((size_t)a.batch + 1) * sizeof(int);
-  return launch_dependent(fa2_paged_plan_kernel, dim3((unsigned)blocks), kPlanThreads, smem, stream, a);
+  return launch_dependent(fa2_paged_plan_kernel, dim3((unsigned)blocks), threads, smem, stream, a);
 }
 
 int launch_paged_append(const PagedAppendArgs& a, cudaStream_t stream) {
