@@ -63,7 +63,7 @@ def _binding_commands(obj: str, out: str):
                    "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"),
                    "-c", os.path.join(CSRC, BINDING_SOURCE), "-o", obj]
     link_cmd = ["g++", "-shared", "-o", out, obj, "-L", HERE, "-l:" + LIB_NAME, "-L", os.path.join(base, "lib"),
-                "-ltorch", "-ltorch_cpu", "-ltorch_python", "-lc10", "-lc10_cuda", "-L", os.path.join(cuda, "lib64"),
+                "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-lc10", "-lc10_cuda", "-L", os.path.join(cuda, "lib64"),
                 "-lcudart", "-Wl,-rpath,$ORIGIN"]
     return compile_cmd, link_cmd
 

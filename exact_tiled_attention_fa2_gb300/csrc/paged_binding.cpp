@@ -7,7 +7,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -88,6 +88,12 @@ fa2_paged_cache cache(const at::Tensor& k, const at::Tensor& v) {
   c.page_size = size(k.size(2), "k_cache");
   c.head_dim = size(k.size(3), "k_cache");
   return c;
+}
+
+// An uninitialised contiguous tensor, past the dispatcher (host time of a plan,
+// four outputs, 7.7 -> 6.5 us; of a forward, two and a workspace, 9.6 -> 8.3).
+at::Tensor empty(at::IntArrayRef sizes, at::ScalarType dtype, const at::Device& dev) {
+  return at::Tensor(at::detail::empty_cuda(sizes, dtype, dev, std::nullopt));
 }
 
 void* current_stream(const at::Device& dev) { return c10::cuda::getCurrentCUDAStream(dev.index()).stream(); }
@@ -173,8 +179,8 @@ PyObject* forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
       raise(PyExc_ValueError, "%s must be float32 [H, total_q] on q's device with a contiguous last dimension", "lse");
     if (ws_in && (ws_in->device() != dev || !ws_in->is_contiguous()))
       raise(PyExc_ValueError, "%s must be a contiguous tensor on q's device", "workspace");
-    const at::Tensor o = o_in ? *o_in : at::empty(q.sizes(), q.options().memory_format(at::MemoryFormat::Contiguous));
-    const at::Tensor lse = lse_in ? *lse_in : at::empty({q.size(1), q.size(0)}, q.options().dtype(at::kFloat));
+    const at::Tensor o = o_in ? *o_in : empty(q.sizes(), q.scalar_type(), dev);
+    const at::Tensor lse = lse_in ? *lse_in : empty({q.size(1), q.size(0)}, at::kFloat, dev);
     // a workspace made here is a block of the current stream, given back once the kernels are queued: its next
     // user on that stream follows them
     at::Tensor ws;
@@ -182,7 +188,7 @@ PyObject* forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
       ws = *ws_in;
     } else {
       const size_t need = fa2_paged_fwd_workspace_bytes(&p);
-      ws = at::empty({(int64_t)(need ? need : 256)}, q.options().dtype(at::kByte));
+      ws = empty({(int64_t)(need ? need : 256)}, at::kByte, dev);
     }
     p.o = o.data_ptr();
     p.o_strides[0] = o.stride(0);
@@ -271,7 +277,7 @@ PyObject* plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
     int* at_out[4];
     for (int i = 0; i < 4; ++i) {
       const at::Tensor* given = tensor(a[8 + i], names[i], true);
-      out[i] = given ? *given : at::empty({sizes[i]}, ctx.options());
+      out[i] = given ? *given : empty({sizes[i]}, at::kInt, dev);
       at_out[i] = int32_1d(out[i], names[i], dev, sizes[i]);
     }
     p.cu_seqlens_q = at_out[0];
