@@ -319,7 +319,67 @@ __device__ __forceinline__ int whole_pairs(const PagedParams& p, typename LineOf
   return 0;
 }
 
-// Finds what CTA `block` works on.  Every thread sums a run of sequences; every
+// What follows for CTA `block` from the pairs that run whole and the line's rest.
+template <bool WIDE>
+__device__ __forceinline__ void place_piece(PagedPlace<WIDE>& r, int block, int whole, typename LineOf<WIDE>::T all_pairs,
+                                            typename LineOf<WIDE>::T share, typename LineOf<WIDE>::T rest) {
+  r.share = block < whole ? 0 : share;
+  r.total = rest;
+  r.piece = block - whole;
+  r.line = block >= whole;
+  if (whole == all_pairs) {   // no line: the first CTAs say so to the merge
+    r.piece = block;
+    r.line = true;
+  }
+}
+
+// Finds what CTA `block` works on, query tiles of few rows and at most 32
+// sequences: one a lane of the calling warp.
+__device__ __forceinline__ PagedPlace<false> find_place_small(const PagedParams& p, int block, bool report) {
+  constexpr int KEYS = LineOf<false>::KEYS;
+  const int lane = (int)threadIdx.x & 31;
+  int span = 0, pairs = 0, longest = 0;
+  PagedSeq s;
+  s.tiles = s.keys = s.n_q = s.n_k = s.row0 = 0;
+  if (lane < p.batch) {
+    s = paged_seq<false>(p, __ldg(p.cu_q + lane), __ldg(p.cu_q + lane + 1), __ldg(p.lens_k + lane), report);
+    span = s.span<false>(p, s.tiles);
+    pairs = s.tiles * p.heads_kv;
+    if (s.tiles > 0) longest = s.width<false>(p, 0);
+  }
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  int a = span, b = pairs;
+#pragma unroll 1
+  for (int o = 1; o < 32; o <<= 1) {
+    const int va = __shfl_up_sync(0xffffffffu, a, o), vb = __shfl_up_sync(0xffffffffu, b, o);
+    if (lane >= o) {
+      a += va;
+      b += vb;
+    }
+  }
+  const int total = __shfl_sync(0xffffffffu, a, 31), all_pairs = __shfl_sync(0xffffffffu, b, 31);
+  const int whole = whole_pairs<false>(p, total, 0, all_pairs, longest);   // all or none
+  const int rest = whole == all_pairs ? 0 : total;
+  const int share = max(line_div(rest + p.ctas - 1, p.ctas), p.min_share / KEYS);
+  const bool one = block < whole;
+  const int pos = one ? block : (block - whole) * share;
+  const int size = one ? pairs : span, mine = (one ? b : a) - size;
+  const unsigned holds = __ballot_sync(0xffffffffu, (one || pos < rest) && pos >= mine && pos < mine + size);
+  PagedPlace<false> r;
+  r.seq = __ffs(holds) - 1;   // -1: none
+  const int src = max(r.seq, 0);
+  r.at = __shfl_sync(0xffffffffu, mine, src);
+  r.s.row0 = __shfl_sync(0xffffffffu, s.row0, src);
+  r.s.n_q = __shfl_sync(0xffffffffu, s.n_q, src);
+  r.s.n_k = __shfl_sync(0xffffffffu, s.n_k, src);
+  r.s.tiles = __shfl_sync(0xffffffffu, s.tiles, src);
+  r.s.keys = __shfl_sync(0xffffffffu, s.keys, src);
+  r.rank = one ? pos - r.at : 0;
+  place_piece<false>(r, block, whole, all_pairs, share, rest);
+  return r;
+}
+
+// The same of any number of sequences: every thread sums a run of them; every
 // thread returns the same.
 template <int THREADS, bool WIDE>
 __device__ __forceinline__ PagedPlace<WIDE> find_place(const PagedParams& p, int block, PagedScan<WIDE>* sh,
@@ -434,14 +494,7 @@ __device__ __forceinline__ PagedPlace<WIDE> find_place(const PagedParams& p, int
   }
   __syncthreads();
   PagedPlace<WIDE> r = sh->place;
-  r.share = one ? 0 : share;
-  r.total = rest;
-  r.piece = block - whole;
-  r.line = !one;
-  if (whole == all_pairs) {   // no line: the first CTAs say so to the merge
-    r.piece = block;
-    r.line = true;
-  }
+  place_piece<WIDE>(r, block, whole, all_pairs, share, rest);
   return r;
 }
 
@@ -1232,7 +1285,11 @@ __device__ __forceinline__ void pg_softmax(const PagedCtx<C>& t, const PagedPara
   }
 }
 
-template <int D, bool BF16, bool BAND, bool WIDE>
+// SMALL: few rows and at most 32 sequences (find_place_small: 1 request of 600
+// keys 11.1 us, 11.8 with the general search; 8 x 5 drafted tokens 16.8, 17.8.
+// Its own kernel, since the code of both in one costs batches of hundreds: 500
+// requests of 1..300 keys 105 us, 115).
+template <int D, bool BF16, bool BAND, bool WIDE, bool SMALL>
 __global__ void __launch_bounds__(PagedConfig<D, WIDE>::THREADS, PagedConfig<D, WIDE>::CTAS_PER_SM)
     fa2_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PagedParams p) {
@@ -1280,7 +1337,17 @@ __global__ void __launch_bounds__(PagedConfig<D, WIDE>::THREADS, PagedConfig<D, 
     tmem_relinquish();
   }
   tc_fence_before();
-  const PagedPlace<WIDE> place = find_place<C::THREADS, WIDE>(p, (int)blockIdx.x, scan, blockIdx.x == 0);   // with its barriers
+  PagedPlace<WIDE> place;
+  if constexpr (SMALL) {
+    if (warp == C::PLAN_WARP) {
+      place = find_place_small(p, (int)blockIdx.x, blockIdx.x == 0);
+      if (lane == 0) scan->place = place;
+    }
+    __syncthreads();
+    place = scan->place;
+  } else {
+    place = find_place<C::THREADS, WIDE>(p, (int)blockIdx.x, scan, blockIdx.x == 0);   // with its barriers
+  }
   tc_fence_after();
   t.tmem = *tmem_slot;
 
@@ -1408,10 +1475,10 @@ __global__ void __launch_bounds__(kPagedMergeThreads) fa2_paged_merge_kernel(con
   }
 }
 
-template <int D, bool BF16, bool BAND, bool WIDE>
+template <int D, bool BF16, bool BAND, bool WIDE, bool SMALL>
 int launch_paged_kernels(const PagedLaunchArgs& a) {
   using C = PagedConfig<D, WIDE>;
-  auto kern = fa2_paged_kernel<D, BF16, BAND, WIDE>;
+  auto kern = fa2_paged_kernel<D, BF16, BAND, WIDE, SMALL>;
   static std::atomic<unsigned long long> configured{0};
   const int e = once_per_device(configured, [&]() -> int {
     const cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM_BYTES);
@@ -1430,15 +1497,17 @@ int launch_paged_kernels(const PagedLaunchArgs& a) {
   return launch_dependent(fa2_paged_merge_kernel<D, BF16>, blocks, kPagedMergeThreads, 0, a.stream, a.p);
 }
 
-template <int D, bool BF16>
+template <int D, bool BF16, bool BAND>
 int launch_paged_rows(const PagedLaunchArgs& a) {
-  if (a.band) return a.wide ? launch_paged_kernels<D, BF16, true, true>(a) : launch_paged_kernels<D, BF16, true, false>(a);
-  return a.wide ? launch_paged_kernels<D, BF16, false, true>(a) : launch_paged_kernels<D, BF16, false, false>(a);
+  if (a.wide) return launch_paged_kernels<D, BF16, BAND, true, false>(a);
+  return a.p.batch <= 32 ? launch_paged_kernels<D, BF16, BAND, false, true>(a)
+                         : launch_paged_kernels<D, BF16, BAND, false, false>(a);
 }
 
 template <int D>
 int launch_paged(const PagedLaunchArgs& a) {
-  return a.bf16 ? launch_paged_rows<D, true>(a) : launch_paged_rows<D, false>(a);
+  if (a.bf16) return a.band ? launch_paged_rows<D, true, true>(a) : launch_paged_rows<D, true, false>(a);
+  return a.band ? launch_paged_rows<D, false, true>(a) : launch_paged_rows<D, false, false>(a);
 }
 
 }  // namespace fa2

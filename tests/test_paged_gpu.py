@@ -303,6 +303,28 @@ def test_layouts_equal_contiguous():
     assert (lse_wide[:, :20] == 7).all() and (lse_wide[:, 94:] == 7).all()
 
 
+@pytest.mark.parametrize("mask", ["causal", "sinks"])
+@pytest.mark.parametrize("batch", [2, 31, 32, 33, 64])
+def test_batches_around_one_sequence_a_lane(batch, mask):
+    """Idle, empty, short and long sequences among up to 32 (a lane each) and more; then one of them out of range."""
+    r = np.random.default_rng(batch)
+    lens_q = r.integers(0, 4, batch).tolist()
+    lens_k = [int(n) * int(r.integers(0, 9)) // 8 for n in r.integers(0, 3000, batch)]
+    lens_q[-1], lens_k[-1] = 1, 1500
+    wl, wr, pre = MASKS[mask]
+    kw = dict(window_left=wl, window_right=wr, prefix_len=pre)
+    p = Problem(lens_q, lens_k, 8, 2, 128, "bf16", 16, seed=batch, fill=float("nan"))
+    o, lse = p.run(**kw)
+    assert status() == fa2.FA2_OK
+    p.check(o, lse, **kw)
+    p.lens[batch - 1] = -1
+    kept = torch.full_like(o, 3.0)
+    o2, lse2 = p.run(o=kept, **kw)
+    assert status() == fa2.FA2_ERR_DEVICE_SEQLENS
+    p.check(o2, lse2, skip=[batch - 1], **kw)
+    assert (o2[-1] == 3).all()
+
+
 @pytest.mark.parametrize("mask", sorted(MASKS))
 @pytest.mark.parametrize("lens_q,lens_k", [([5, 2, 9], [2, 0, 8]), ([200, 130, 1, 64], [50, 0, 0, 63]), ([300], [299])])
 def test_more_tokens_than_keys(lens_q, lens_k, mask):
