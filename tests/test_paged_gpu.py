@@ -710,6 +710,43 @@ def test_captured_step_replays_with_new_lengths():
         s.check(o, lse, new)
 
 
+@pytest.mark.parametrize("captured", [False, True])
+def test_step_forked_over_streams(captured):
+    """A step whose rows are appended in halves on two streams between the plan and the forward."""
+    s = Server(4, 6, 2, 128, "bf16", 16, pages=50, width=30, total=280, seed=2)
+    sides = [torch.cuda.Stream() for _ in range(2)]
+
+    def step():
+        cu, lens, slots, left = fa2.fa2_paged_plan(s.ctx, s.new, s.table, s.free, s.count, s.pages, s.page, s.total)
+        here = torch.cuda.current_stream()
+        for i, side in enumerate(sides):
+            part = slice(i * 140, i * 140 + 140)
+            side.wait_stream(here)
+            fa2.fa2_paged_append(s.nk[part], s.nv[part], slots[part], s.k, s.v, stream=side)
+        for side in sides:
+            here.wait_stream(side)
+        out = fa2.fa2_paged_fwd(s.q, s.k, s.v, s.table, cu, lens, window_right=0, max_seqlen_q=200)
+        s.ctx.copy_(lens)
+        s.count.copy_(left)
+        return out
+
+    step()   # an idle step
+    torch.cuda.synchronize()
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            o, lse = step()
+    for new in STEPS:
+        s.inputs(new)
+        if captured:
+            graph.replay()
+        else:
+            torch.cuda.synchronize()
+            o, lse = step()
+        assert status() == fa2.FA2_OK
+        s.check(o, lse, new)
+
+
 def test_side_streams():
     """Calls on streams of their own, results and workspaces allocated there."""
     probs = [Problem([1] * 8, [3000 + 100 * i] * 8, 8, 2, 128, "bf16", 16, seed=i) for i in range(3)]
