@@ -624,6 +624,27 @@ def test_append_against_indexing(hkv, page, total, d, dtype):
     assert torch.equal(kc, wk) and torch.equal(vc, wv)
 
 
+@pytest.mark.parametrize("total", [8191, 8192, 20000])
+def test_append_of_many_rows(total):
+    """Around 32 MB of rows, from which on they pass the L2 by."""
+    g = gen(total)
+    hkv, d, page = 8, 128, 64
+    pages = total // page + 2
+    slots = torch.randperm(pages * page, generator=g, device="cuda")[:total].to(torch.int32)
+    slots[::5] = -1
+    rows = torch.randint(-2 ** 15, 2 ** 15, (total, 2, hkv, d), generator=g, device="cuda", dtype=torch.int16)
+    rows = rows.view(torch.bfloat16)   # any bits
+    kc, vc = (torch.zeros((pages, hkv, page, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    fa2.fa2_paged_append(rows[:, 0], rows[:, 1], slots, kc, vc)
+    assert status() == fa2.FA2_OK
+    keep = slots >= 0
+    s = slots[keep].long()
+    for i, cache in enumerate((kc, vc)):
+        want = torch.zeros_like(cache)
+        want[s // page, :, s % page] = rows[keep, i]
+        assert torch.equal(cache.view(torch.int16), want.view(torch.int16))
+
+
 # ---------------------------------------------------------------- serving steps
 
 
