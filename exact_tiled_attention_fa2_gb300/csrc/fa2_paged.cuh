@@ -499,7 +499,8 @@ __device__ __forceinline__ PagedPlace<WIDE> find_place(const PagedParams& p, int
 }
 
 // The pair of sequence s that holds offset y of the sequence's span: query
-// tile, head, and the pair's start within the span.
+// tile, head, and the pair's start within the span.  (Many rows: by a whole
+// warp, the tile searched 32 ways at a time.)
 template <bool WIDE>
 __device__ __forceinline__ typename LineOf<WIDE>::T pair_at(const PagedParams& p, const PagedSeq& s,
                                                             typename LineOf<WIDE>::T y, int& tile, int& h) {
@@ -509,11 +510,10 @@ __device__ __forceinline__ typename LineOf<WIDE>::T pair_at(const PagedParams& p
     int lo = 0, hi = s.tiles;
 #pragma unroll 1
     while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (s.before(p, mid) * p.heads_kv <= y)
-        lo = mid;
-      else
-        hi = mid;
+      const int step = (hi - lo + 31) >> 5, mid = lo + ((int)threadIdx.x & 31) * step;
+      const unsigned below = __ballot_sync(0xffffffffu, mid < hi && s.before(p, mid) * p.heads_kv <= y);
+      lo += (31 - __clz(below)) * step;
+      hi = min(hi, lo + step);
     }
     tile = lo;
     base = s.before(p, lo) * p.heads_kv;
@@ -921,6 +921,10 @@ __device__ __forceinline__ void pg_load(const PagedCtx<C>& t, const PagedParams&
         if (published == nf && n <= 0) publish();   // without keys, or the end
       } while (ok && n == 0);
       if (!ok || n < 0) break;
+      if (C::WIDE && g == 0 && published == nf) {   // the first Q, the longest load, before the first K
+        publish();
+        if (!ok) break;
+      }
       next4 = first4;
     }
     if ((j & 3) == 0) {
