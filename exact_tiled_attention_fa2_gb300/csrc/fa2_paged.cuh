@@ -256,7 +256,7 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int a, int b
 
 template <bool WIDE>
 static __device__ __noinline__ PagedSeq read_seq(const PagedParams& p, int i, bool report) {
-  return paged_seq<WIDE>(p, __ldg(p.cu_q + i), __ldg(p.cu_q + i + 1), __ldg(p.lens_k + i), report);
+  return paged_seq<WIDE>(p, p.cu_q[i], p.cu_q[i + 1], p.lens_k[i], report);
 }
 
 // What a CTA works on.
@@ -342,7 +342,7 @@ __device__ __forceinline__ PagedPlace<false> find_place_small(const PagedParams&
   PagedSeq s;
   s.tiles = s.keys = s.n_q = s.n_k = s.row0 = 0;
   if (lane < p.batch) {
-    s = paged_seq<false>(p, __ldg(p.cu_q + lane), __ldg(p.cu_q + lane + 1), __ldg(p.lens_k + lane), report);
+    s = paged_seq<false>(p, p.cu_q[lane], p.cu_q[lane + 1], p.lens_k[lane], report);
     span = s.span<false>(p, s.tiles);
     pairs = s.tiles * p.heads_kv;
     if (s.tiles > 0) longest = s.width<false>(p, 0);
@@ -564,9 +564,9 @@ struct FragWalk {
 
   __device__ __forceinline__ void read_ahead(const PagedParams& p) {
     if (seq + 1 < p.batch) {
-      next_a = __ldg(p.cu_q + seq + 1);
-      next_b = __ldg(p.cu_q + seq + 2);
-      next_k = __ldg(p.lens_k + seq + 1);
+      next_a = p.cu_q[seq + 1];
+      next_b = p.cu_q[seq + 2];
+      next_k = p.lens_k[seq + 1];
     }
   }
 
@@ -814,7 +814,7 @@ __device__ __forceinline__ void pg_load(const PagedCtx<C>& t, const PagedParams&
     const int at = (int)((__umulhi((unsigned)k0, p.page_magic) + (unsigned)k0) >> p.page_shift);   // k0 / page_size
     const bool need = j4 + my_tile < f->n && has_box &&
                       (k0 < f->km.pre_end || (k0 < f->end && k0 + p.box_rows > f->lo));
-    x.page = need ? __ldg(f->table + at) : 0;
+    x.page = need ? f->table[at] : 0;
     x.row = need ? k0 - at * p.page_size : -1;
     return x;
   };

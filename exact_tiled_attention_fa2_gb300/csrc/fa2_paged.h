@@ -116,7 +116,10 @@ int launch_paged_append(const PagedAppendArgs& a, cudaStream_t stream);
 
 // Launches a kernel as a programmatic dependent of what precedes it on the
 // stream: it may be scheduled before that is done, and calls
-// grid_dependency_wait before it touches memory.
+// grid_dependency_wait before it touches memory.  What the kernel before may
+// still be writing when this one starts is not constant for this one's
+// lifetime, so it is read with ordinary loads, which stay behind the wait:
+// a read-only load (__ldg, ld.global.nc) may be moved across it.
 template <class... Params, class... Args>
 int launch_dependent(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
                      const Args&... args) {

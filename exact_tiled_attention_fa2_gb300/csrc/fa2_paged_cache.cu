@@ -175,12 +175,12 @@ __global__ void __launch_bounds__(256) fa2_paged_append_kernel(const PagedAppend
   const int mask = (1 << a.row_chunks_log2) - 1;
   const long long t = (long long)blockIdx.x * blockDim.y + threadIdx.y;
   if (t >= a.total) return;
-  const int slot = __ldg(a.slots + t);
+  const int slot = a.slots[t];
   for (int i = (int)threadIdx.x; i < items; i += (int)blockDim.x) {
     const long long h = i >> a.row_chunks_log2;
     const int c = i & mask;
     const uint4 *ks = a.k.src + t * a.k.src_rs + h * a.k.src_hs + c, *vs = a.v.src + t * a.v.src_rs + h * a.v.src_hs + c;
-    const uint4 x = STREAM ? __ldcs(ks) : __ldg(ks), y = STREAM ? __ldcs(vs) : __ldg(vs);
+    const uint4 x = STREAM ? __ldcs(ks) : *ks, y = STREAM ? __ldcs(vs) : *vs;
     if (slot < 0 || slot >= a.num_slots) continue;
     const long long page = slot / a.page_size, at = slot % a.page_size;
     uint4* kd = a.k.dst + page * a.k.dst_ps + at * a.k.dst_rs + h * a.k.dst_hs + c;
