@@ -85,7 +85,7 @@ class Fa2PagedParams(ctypes.Structure):
         ("lse_stride", ctypes.c_int64),
         ("batch", ctypes.c_int), ("heads", ctypes.c_int), ("total_q", ctypes.c_int), ("max_seqlen_q", ctypes.c_int),
         ("max_pages", ctypes.c_int), ("window_left", ctypes.c_int), ("window_right", ctypes.c_int),
-        ("prefix_len", ctypes.c_int), ("scale", ctypes.c_float),
+        ("prefix_len", ctypes.c_int), ("scale", ctypes.c_float), ("sink_len", ctypes.c_int),
     ]
 
 
@@ -500,7 +500,8 @@ def fa2_paged_fwd_workspace_bytes(q, k_cache, v_cache, block_table, cu_seqlens_q
 
 
 def fa2_paged_fwd(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, o=None, lse=None, workspace=None,
-                  scale=None, window_left=-1, window_right=-1, prefix_len=0, max_seqlen_q=None, stream=None):
+                  scale=None, window_left=-1, window_right=-1, prefix_len=0, max_seqlen_q=None, stream=None,
+                  sink_len=0):
     """Attention of each sequence's query tokens over its keys in a paged cache (fa2_paged_fwd).
 
     q [total_q, H, d] (packed: sequence b's tokens are rows cu_seqlens_q[b] ..
@@ -509,7 +510,9 @@ def fa2_paged_fwd(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, o=N
     i // (H // H_kv)), ``block_table`` int32 CUDA [B, max_pages],
     ``cu_seqlens_q`` [B + 1] and ``seqlens_k`` [B] int32 CUDA: keys of each
     sequence, its new tokens' own (already appended) among them.  Masks as
-    fa2_fwd_ex: causal is window (-1, 0).  ``max_seqlen_q`` (default: total_q)
+    fa2_fwd_ex: causal is window (-1, 0); ``sink_len`` keeps the first keys
+    visible beside a sliding window, up to each query's own right edge (a
+    prefix is visible to every query).  ``max_seqlen_q`` (default: total_q)
     bounds every sequence's query count; give it while decoding, it sizes the
     grid and the workspace.  Returns (o [total_q, H, d], lse [H, total_q]);
     rows outside every sequence are not written.
@@ -517,9 +520,9 @@ def fa2_paged_fwd(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, o=N
     if stream is not None:
         with _on_stream(stream, q):
             return fa2_paged_fwd(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, o, lse, workspace, scale,
-                                 window_left, window_right, prefix_len, max_seqlen_q)
+                                 window_left, window_right, prefix_len, max_seqlen_q, sink_len=sink_len)
     out = (_paged or _paged_calls()).forward(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, o, lse,
-                                               workspace, scale, window_left, window_right, prefix_len, max_seqlen_q)
+                                               workspace, scale, window_left, window_right, prefix_len, max_seqlen_q, sink_len)
     if type(out) is int:
         raise Fa2Error(out, "fa2_paged_fwd")
     return out

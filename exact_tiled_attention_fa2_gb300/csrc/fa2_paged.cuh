@@ -80,7 +80,7 @@ struct PagedFrag {
   int slot;        // partial slot, or -1: write O and L
   int split;       // every bf16 P is split (many rows: else the masked tiles')
   TileMask tm;     // key tiles every row sees, by index from j0
-  KeyMask km;
+  KeyMask km;      // with the last row's pre_end
   int npre, skip;  // visited index j is key tile j + (j >= npre ? skip : 0)
   int lo, end;     // the band's keys (the prefix's: km.pre_end)
   __device__ __forceinline__ int tile(int j) const { return j + (j >= npre ? skip : 0); }
@@ -154,13 +154,23 @@ __device__ __forceinline__ TileWalk tile_walk(const KeyMask& km, int first, int 
   return w;
 }
 
-__device__ __forceinline__ KeyMask paged_mask(const PagedParams& p, int n_q, int n_k) {
+// The end of the keys [0, end) that row `row` sees beside its band: the prefix
+// and, as far as the band's right edge, the sinks.  It does not fall from row to
+// row, so what some row of a tile sees ends with its last row's, what all see
+// with its first row's.
+__device__ __forceinline__ int prefix_end(const PagedParams& p, const KeyMask& km, int row) {
+  const int prefix = min(p.prefix, km.n_k);
+  return p.sinks > 0 ? max(prefix, min(p.sinks, km.row_hi(row) + 1)) : prefix;
+}
+
+// The mask whose pre_end is that of row `row`.
+__device__ __forceinline__ KeyMask paged_mask(const PagedParams& p, int n_q, int n_k, int row) {
   KeyMask km;
   km.n_k = n_k;
   km.off = n_k - n_q;
   km.wl = p.window_left;
   km.wr = p.window_right;
-  km.pre_end = min(p.prefix, n_k);
+  km.pre_end = prefix_end(p, km, row);
   return km;
 }
 
@@ -230,7 +240,7 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int a, int b
     return s;
   }
   if (s.n_q == 0) return s;
-  const KeyMask km = paged_mask(p, s.n_q, s.n_k);
+  const KeyMask km = paged_mask(p, s.n_q, s.n_k, s.n_q - 1);
   s.tiles = 1;
   int nv;   // most key tiles one of the query tiles visits
   if constexpr (WIDE) {
@@ -572,7 +582,7 @@ struct FragWalk {
 
   __device__ void start_tile(const PagedParams& p) {
     const int q0 = tile * p.tile_tokens, last = min(q0 + p.tile_tokens, s.n_q) - 1;
-    base.km = paged_mask(p, s.n_q, s.n_k);
+    base.km = paged_mask(p, s.n_q, s.n_k, last);
     const TileWalk walk = tile_walk(base.km, q0, last);
     tiles_n = walk.n;
     w = s.template width<WIDE>(p, tile);
@@ -587,7 +597,9 @@ struct FragWalk {
     base.skip = walk.skip;
     base.lo = walk.lo;
     base.end = walk.end;
-    base.tm = tile_mask<BAND>(base.km, q0, last, kPagedKeyTile);
+    KeyMask all = base.km;   // what all rows see
+    if constexpr (BAND) all.pre_end = prefix_end(p, all, q0);
+    base.tm = tile_mask<BAND>(all, q0, last, kPagedKeyTile);
     if (walk.npre == 0) base.tm.pre -= walk.skip;
     base.tm.lo -= walk.skip;
     base.tm.hi -= walk.skip;
@@ -1139,10 +1151,15 @@ __device__ __forceinline__ void pg_softmax(const PagedCtx<C>& t, const PagedPara
         // runs of 32, half the code (few rows: the loop waits for the keys, and
         // code costs more than the second read)
         uint32_t sr[C::WIDE ? C::BC : 32];
+        auto row_mask = [&]() {
+          KeyMask km = f->km;
+          if constexpr (BAND) km.pre_end = prefix_end(p, km, tok_row);
+          return km;
+        };
         auto read = [&](int c) {
           tmem_ld_32x32b_x32(tS + c, sr + (C::WIDE ? c : 0));
           tmem_ld_wait_x32(sr + (C::WIDE ? c : 0));
-          if (masked) mask_scores<32, BAND>(sr + (C::WIDE ? c : 0), f->km, tok_row, k0 + c);
+          if (masked) mask_scores<32, BAND>(sr + (C::WIDE ? c : 0), row_mask(), tok_row, k0 + c);
         };
         float m_tile = -INFINITY;
         auto top = [&](int c) {
@@ -1162,7 +1179,7 @@ __device__ __forceinline__ void pg_softmax(const PagedCtx<C>& t, const PagedPara
           tmem_ld_32x32b_x32(tS + 32, sr + 32);
           tmem_ld_wait_x32(sr);
           tmem_ld_wait_x32(sr + 32);
-          if (masked) mask_scores<C::BC, BAND>(sr, f->km, tok_row, k0);
+          if (masked) mask_scores<C::BC, BAND>(sr, row_mask(), tok_row, k0);
           top(0);
           top(32);
         } else {

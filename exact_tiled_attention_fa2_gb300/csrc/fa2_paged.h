@@ -62,6 +62,7 @@ struct PagedParams {
   float* ws_o;            // [2 * ctas][d / 4][slot_rows][4] partial O~
   float* ws_ml;           // [2 * ctas][slot_rows][2] partial (m, l), exp2 domain
   struct PagedMerge* merges;   // [ctas] pairs to merge, kPagedMergeBytes each
+  int sinks;              // first keys a row sees as far as its band's right edge (0 without a left window)
 };
 
 struct PagedLaunchArgs {

@@ -169,7 +169,7 @@ int paged_forward(const fa2_paged_params& a, void* workspace, size_t workspace_b
   rc = paged_shape(a, s);
   if (rc) return rc;
   if (!std::isfinite(a.scale)) return FA2_ERR_INVALID_ARG;
-  if (a.window_left < -1 || a.window_right < -1 || a.prefix_len < 0) return FA2_ERR_INVALID_ARG;
+  if (a.window_left < -1 || a.window_right < -1 || a.prefix_len < 0 || a.sink_len < 0) return FA2_ERR_INVALID_ARG;
   if (!a.q || !a.o || !a.lse || !a.block_table || !a.cu_seqlens_q || !a.seqlens_k || !workspace)
     return FA2_ERR_INVALID_ARG;
   if (misaligned(a.q, 16) || misaligned(a.o, 16) || misaligned(a.lse, 4) || misaligned(a.block_table, 4) ||
@@ -245,6 +245,7 @@ int paged_forward(const fa2_paged_params& a, void* workspace, size_t workspace_b
   p.window_left = a.window_left;
   p.window_right = a.window_right;
   p.prefix = a.prefix_len;
+  p.sinks = a.window_left >= 0 ? a.sink_len : 0;
   const float scale_log2 = a.scale * 1.4426950408889634f;
   p.scale_log2_mag = std::fmax(std::fabs(scale_log2), FLT_MIN);
   p.qk_negate = scale_log2 < 0.f ? 1u << 13 : 0u;   // the negate-A bit of the S product's descriptor

@@ -148,9 +148,9 @@ bool arguments(Py_ssize_t n, Py_ssize_t want, const char* name) {
 }
 
 // forward(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, o, lse, workspace, scale, window_left,
-//         window_right, prefix_len, max_seqlen_q): (o, lse), or a nonzero fa2_status
+//         window_right, prefix_len, max_seqlen_q, sink_len): (o, lse), or a nonzero fa2_status
 PyObject* forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (!arguments(n, 14, "forward")) return nullptr;
+  if (!arguments(n, 15, "forward")) return nullptr;
   return guarded([&]() -> PyObject* {
     const at::Tensor &q = *tensor(a[0], "q"), &k = *tensor(a[1], "k_cache"), &v = *tensor(a[2], "v_cache");
     const at::Tensor &table = *tensor(a[3], "block_table"), &cu = *tensor(a[4], "cu_seqlens_q"),
@@ -169,6 +169,7 @@ PyObject* forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     p.window_left = integer(a[10], "window_left");
     p.window_right = integer(a[11], "window_right");
     p.prefix_len = integer(a[12], "prefix_len");
+    p.sink_len = integer(a[14], "sink_len");
     const c10::cuda::CUDAGuard guard(dev);
     if (o_in && (o_in->sizes() != q.sizes() || o_in->scalar_type() != q.scalar_type() || o_in->device() != dev ||
                  o_in->stride(2) != 1))

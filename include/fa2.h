@@ -450,8 +450,15 @@ int fa2_paged_append(const fa2_paged_append_params* params, void* stream);
  * of pages block_table[b][j / page_size].  Query head i reads K/V head i /
  * (heads / cache.heads); heads is a multiple of cache.heads, at most 128 times
  * it (FA2_ERR_UNSUPPORTED).  Masks, scale, rows that see no key (O = 0, LSE =
- * -inf) and rounding as fa2_fwd_ex: causal attention is window (-1, 0), a
- * sliding window with sink keys (w, 0) with prefix_len.
+ * -inf) and rounding as fa2_fwd_ex: causal attention is window (-1, 0).
+ * Beside the prefix, which every query sees whole, also ahead of itself, there
+ * are sink keys: query i also sees key j iff
+ *
+ *     j < sink_len  and  j <= i + off + window_right
+ *
+ * (window_right = -1: any j < sink_len), so a sliding window that keeps the
+ * first s keys in sight is (w, 0) with sink_len = s.  Without a left window
+ * the sinks are in the band already.
  *
  * Rows of q / o / lse outside every sequence are left as they were.  Keys no
  * query row of a sequence sees (rows past its length, keys before a window)
@@ -495,6 +502,7 @@ typedef struct fa2_paged_params {
   int window_right;        /* >= 0, or -1 = unbounded */
   int prefix_len;          /* >= 0 */
   float scale;             /* any finite value */
+  int sink_len;            /* >= 0 */
 } fa2_paged_params;
 
 /* sizeof(fa2_paged_params) as compiled into the library (binding check). */
