@@ -1276,7 +1276,7 @@ __device__ __forceinline__ void pg_softmax(const PagedCtx<C>& t, const PagedPara
         *reinterpret_cast<float2*>(p.ws_ml + ((size_t)slot_at * (size_t)p.slot_rows + r) * 2) =
             make_float2(m_run, l_run);
     } else if (warp_live) {
-      const bool empty = !(l_run > 0.f);
+      const bool empty = l_run == 0.f;   // sees no key; a NaN sum is no such row's
       const float inv_l = empty ? 0.f : 1.f / l_run;
       uint8_t* o_row = paged_o_row(p, row, head);
 #pragma unroll 1
@@ -1442,7 +1442,7 @@ __global__ void __launch_bounds__(kPagedMergeThreads) fa2_paged_merge_kernel(con
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (s[u].x == -INFINITY) continue;   // shows the row nothing
+      if (s[u].y == 0.f) continue;   // shows the row nothing (a NaN sum stays)
       const float top = fmaxf(m, s[u].x);
       const float f0 = ex2_approx(m - top), f = ex2_approx(s[u].x - top);   // f0: 0 before the first
       m = top;
@@ -1474,7 +1474,7 @@ __global__ void __launch_bounds__(kPagedMergeThreads) fa2_paged_merge_kernel(con
       acc[e].w += __shfl_xor_sync(0xffffffffu, acc[e].w, o);
     }
   }
-  const bool empty = !(L > 0.f);
+  const bool empty = L == 0.f;
   const float inv_l = empty ? 0.f : 1.f / L;
   if (sub == 0 && r < here) {
 #pragma unroll

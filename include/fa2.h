@@ -462,8 +462,10 @@ int fa2_paged_append(const fa2_paged_append_params* params, void* stream);
  *
  * Rows of q / o / lse outside every sequence are left as they were.  Keys no
  * query row of a sequence sees (rows past its length, keys before a window)
- * may hold anything, NaN included, and their table entries are not read;
- * visible keys and values are finite.
+ * may hold anything, NaN included, and their table entries are not read.  A NaN
+ * in a query row or in a key that it sees makes the row's O and LSE NaN, a NaN
+ * in a value that it sees that column of O (and it may that column in other rows
+ * of the sequence); queries and visible keys and values are not infinite.
  *
  * Lengths, offsets and tables live on the device and are checked by the
  * kernel: a sequence with cu_seqlens_q[b] > cu_seqlens_q[b+1], an offset
