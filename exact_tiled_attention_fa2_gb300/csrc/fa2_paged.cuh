@@ -78,7 +78,7 @@ struct PagedFrag {
   int rows;        // live rows: group x tokens
   int h;           // K/V head
   int slot;        // partial slot, or -1: write O and L
-  int split;       // every bf16 P is split (many rows: else the masked tiles')
+  int split;       // every bf16 P is split (else the masked tiles')
   TileMask tm;     // key tiles every row sees, by index from j0
   KeyMask km;      // with the last row's pre_end
   int npre, skip;  // visited index j is key tile j + (j >= npre ? skip : 0)
@@ -589,10 +589,7 @@ struct FragWalk {
     base.row = s.row0 + q0;
     base.q0 = q0;
     base.rows = (last + 1 - q0) * p.group;
-    // Few keys.  With few rows this is all (their masked tile is one of many keys'
-    // tiles, not a causal diagonal, and where a pair has many the MMA thread's
-    // issue bounds the loop: d = 64, 12 products a tile against 8)
-    base.split = WIDE ? s.n_k <= 2 * kPagedKeyTile : tiles_n <= 3;
+    base.split = tiles_n <= 3;   // few keys: rounding shows most
     base.npre = walk.npre;
     base.skip = walk.skip;
     base.lo = walk.lo;
@@ -1032,7 +1029,7 @@ __device__ __forceinline__ void pg_mma(const PagedCtx<C>& t, const PagedParams& 
       const uint64_t b0 = dv0 + (uint64_t)((sv * C::KV_BYTES) >> 4);
       const uint32_t tS = t.tmem + C::TMEM_S + 64 * (g & 1);
       const uint32_t tO = t.tmem + C::TMEM_O;
-      const bool split = BF16 && (always || (C::WIDE && !tm.full(j)));
+      const bool split = BF16 && (always || !tm.full(j));
       auto product = [&](bool both) {
 #pragma unroll
         for (int k = 0; k < C::BC / 16; ++k) {
@@ -1145,7 +1142,7 @@ __device__ __forceinline__ void pg_softmax(const PagedCtx<C>& t, const PagedPara
       const bool masked = !tmask.full(j);
       if (warp_live) {
         const int k0 = f->tile(f->j0 + j) * C::BC, tok_row = f->q0 + tok;
-        const bool split = BF16 && (always || (C::WIDE && masked));
+        const bool split = BF16 && (always || masked);
         // The tile's 64 scores: in registers (a warp of live rows, where the
         // softmax is what bounds the loop), or read from tensor memory twice in
         // runs of 32, half the code (few rows: the loop waits for the keys, and

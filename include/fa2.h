@@ -449,8 +449,8 @@ int fa2_paged_append(const fa2_paged_append_params* params, void* stream);
  * the new tokens' own among them, already appended -- are rows j % page_size
  * of pages block_table[b][j / page_size].  Query head i reads K/V head i /
  * (heads / cache.heads); heads is a multiple of cache.heads, at most 128 times
- * it (FA2_ERR_UNSUPPORTED).  Masks, scale, rows that see no key (O = 0, LSE =
- * -inf) and rounding as fa2_fwd_ex: causal attention is window (-1, 0).
+ * it (FA2_ERR_UNSUPPORTED).  Masks, scale and rows that see no key (O = 0, LSE =
+ * -inf) as fa2_fwd_ex: causal attention is window (-1, 0).
  * Beside the prefix, which every query sees whole, also ahead of itself, there
  * are sink keys: query i also sees key j iff
  *
@@ -458,7 +458,12 @@ int fa2_paged_append(const fa2_paged_append_params* params, void* stream);
  *
  * (window_right = -1: any j < sink_len), so a sliding window that keeps the
  * first s keys in sight is (w, 0) with sink_len = s.  Without a left window
- * the sinks are in the band already.
+ * the sinks are in the band already.  P is rounded to 16 bits for the product
+ * with the values; in bf16 its low part is added on tiles of 64 keys that the
+ * mask cuts, and on all tiles of a query tile (128 / group tokens) that visits
+ * at most three.  Sums are fp32; a batch decides where a sequence's keys are
+ * cut into partial sums, so the same sequence may differ in its last bits in
+ * another batch or under another max_seqlen_q.
  *
  * Rows of q / o / lse outside every sequence are left as they were.  Keys no
  * query row of a sequence sees (rows past its length, keys before a window)
