@@ -5,13 +5,14 @@ A thin ctypes binding over the C ABI in ``include/fa2.h`` (library
 Every step of the forward pass runs in the CUDA kernels; this module only
 marshals torch tensors (device memory, streams) into pointers and sizes (the
 paged-cache calls, made once per layer of a serving step, through an extension
-module, ``_paged_binding.so``).  There is no CPU fallback: if the library is
+module, ``_paged_binding``).  There is no CPU fallback: if the library is
 missing, calls raise.
 """
 from __future__ import annotations
 
 import contextlib
 import ctypes
+import importlib
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -430,12 +431,12 @@ def _paged_calls():
     global _paged
     if _paged is None:
         load_library()
-        if not os.path.exists(os.path.join(_HERE, "_paged_binding.so")):
-            raise RuntimeError("_paged_binding.so is not built (run `python -m exact_tiled_attention_fa2_gb300.build` "
-                               "or __graft_entry__.build()); there is no fallback path")
         import torch  # noqa: F401  (its libraries, before the module that uses them)
-        from . import _paged_binding as module
-        _paged = module
+        try:
+            _paged = importlib.import_module(__name__ + "._paged_binding")
+        except ModuleNotFoundError as e:
+            raise RuntimeError("_paged_binding is not built (run `python -m exact_tiled_attention_fa2_gb300.build` "
+                               "or __graft_entry__.build()); there is no fallback path") from e
     return _paged
 
 
