@@ -16,6 +16,7 @@
 #include <climits>
 #include <cmath>
 #include <cstring>
+#include <exception>
 
 #include "../../include/fa2.h"
 
@@ -126,17 +127,16 @@ fa2_paged_params forward_params(const at::Tensor& q, const at::Tensor& k, const 
   return p;
 }
 
-// Runs `f` with C++ exceptions turned into Python's.
+// Runs `f` with C++ exceptions turned into Python's, torch's into their own
+// types (an allocation that fails: torch.OutOfMemoryError).
 template <class F>
 PyObject* guarded(F&& f) {
   try {
     return f();
   } catch (const Raised&) {
     return nullptr;
-  } catch (const python_error&) {
-    return nullptr;
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
+  } catch (...) {
+    torch::translate_exception_to_python(std::current_exception());
     return nullptr;
   }
 }
