@@ -97,6 +97,12 @@ at::Tensor empty(at::IntArrayRef sizes, at::ScalarType dtype, const at::Device& 
   return at::Tensor(at::detail::empty_cuda(sizes, dtype, dev, std::nullopt));
 }
 
+// Torch is told that a caller's tensor was written in place, so that a backward
+// pass that kept it says so.  (Inference tensors keep no such count.)
+void written(const at::Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 void* current_stream(const at::Device& dev) { return c10::cuda::getCurrentCUDAStream(dev.index()).stream(); }
 
 // Fills the inputs of a paged forward's parameters.
@@ -198,6 +204,9 @@ PyObject* forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     p.lse_stride = lse.stride(0);
     const int rc = fa2_paged_fwd(&p, ws.data_ptr(), ws.nbytes(), current_stream(dev));
     if (rc) return PyLong_FromLong(rc);
+    if (o_in) written(o);
+    if (lse_in) written(lse);
+    if (ws_in) written(ws);
     PyObject* out_o = o_in ? Py_NewRef(a[6]) : THPVariable_Wrap(o);
     PyObject* out_l = lse_in ? Py_NewRef(a[7]) : THPVariable_Wrap(lse);
     return Py_BuildValue("(NN)", out_o, out_l);
@@ -240,7 +249,12 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
       p.v_strides[i] = v.stride(i);
     }
     const c10::cuda::CUDAGuard guard(dev);
-    return PyLong_FromLong(fa2_paged_append(&p, current_stream(dev)));
+    const int rc = fa2_paged_append(&p, current_stream(dev));
+    if (rc == FA2_OK) {
+      written(kc);
+      written(vc);
+    }
+    return PyLong_FromLong(rc);
   });
 }
 
@@ -287,6 +301,9 @@ PyObject* plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
     p.free_left = at_out[3];
     const int rc = fa2_paged_plan(&p, current_stream(dev));
     if (rc) return PyLong_FromLong(rc);
+    written(table);
+    for (int i = 0; i < 4; ++i)
+      if (a[8 + i] != Py_None) written(out[i]);
     PyObject* tuple = PyTuple_New(4);
     if (!tuple) return nullptr;
     for (int i = 0; i < 4; ++i)
