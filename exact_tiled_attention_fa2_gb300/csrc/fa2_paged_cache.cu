@@ -12,7 +12,6 @@ namespace fa2 {
 namespace {
 
 constexpr int kPlanThreads = 1024;   // of a block, at most
-constexpr long long kStreamBytes = 32 << 20;   // a quarter of the L2
 
 // Inclusive prefix sums of (a, b) over a warp's lanes.
 __device__ __forceinline__ void warp_scan2(long long& a, long long& b, int lane) {
@@ -163,11 +162,9 @@ __global__ void __launch_bounds__(kPlanThreads) fa2_paged_plan_kernel(const Page
 // Threads x walk the 16-byte chunks of a token's heads (a head's row is
 // contiguous on both sides), threads y and the blocks the tokens: one each, its
 // rows read beside its slot.  Bound by HBM: 32768 tokens of 8 heads x 128, 268
-// MB in 42.2 us (6.36 TB/s; the same machine copies them in 43.7).  STREAM:
-// rows that would fill a good part of the L2 pass it by (that call 44.5 us
-// otherwise, 8192 tokens 13.0 and 12.4); fewer rows stay there for the forward
-// that reads them (64 tokens 1.9 us, 2.1 with STREAM).
-template <bool STREAM>
+// MB in 41.1 us (6.53 TB/s).  The rows stay in the L2 as far as it holds them, for
+// the forward that reads them (with loads and stores that pass it by, that call
+// alone 42.5 us, and with the forward of prompts of 128 tokens 419 us, 416 so).
 __global__ void __launch_bounds__(256) fa2_paged_append_kernel(const PagedAppendArgs a) {
   grid_launch_dependents();
   grid_dependency_wait();
@@ -180,18 +177,13 @@ __global__ void __launch_bounds__(256) fa2_paged_append_kernel(const PagedAppend
     const long long h = i >> a.row_chunks_log2;
     const int c = i & mask;
     const uint4 *ks = a.k.src + t * a.k.src_rs + h * a.k.src_hs + c, *vs = a.v.src + t * a.v.src_rs + h * a.v.src_hs + c;
-    const uint4 x = STREAM ? __ldcs(ks) : *ks, y = STREAM ? __ldcs(vs) : *vs;
+    const uint4 x = *ks, y = *vs;
     if (slot < 0 || slot >= a.num_slots) continue;
     const long long page = slot / a.page_size, at = slot % a.page_size;
     uint4* kd = a.k.dst + page * a.k.dst_ps + at * a.k.dst_rs + h * a.k.dst_hs + c;
     uint4* vd = a.v.dst + page * a.v.dst_ps + at * a.v.dst_rs + h * a.v.dst_hs + c;
-    if constexpr (STREAM) {
-      __stcs(kd, x);
-      __stcs(vd, y);
-    } else {
-      *kd = x;
-      *vd = y;
-    }
+    *kd = x;
+    *vd = y;
   }
   if (slot >= a.num_slots && threadIdx.x == 0) atomicOr(a.status, kStatusBadPages);
 }
@@ -218,9 +210,8 @@ int launch_paged_append(const PagedAppendArgs& a, cudaStream_t stream) {
   int x = 8;
   while (x < 256 && x < items) x *= 2;
   const int tokens = 256 / x;   // of a block
-  const bool stream_rows = 32ll * a.total * items >= kStreamBytes;   // K and V, 16 bytes an item
-  return launch_dependent(stream_rows ? fa2_paged_append_kernel<true> : fa2_paged_append_kernel<false>, dim3((unsigned)(((long long)a.total + tokens - 1) / tokens)),
-                          dim3(x, tokens), 0, stream, a);
+  const unsigned blocks = (unsigned)(((long long)a.total + tokens - 1) / tokens);
+  return launch_dependent(fa2_paged_append_kernel, dim3(blocks), dim3(x, tokens), 0, stream, a);
 }
 
 }  // namespace fa2
