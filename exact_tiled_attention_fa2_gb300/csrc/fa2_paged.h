@@ -134,7 +134,9 @@ int launch_dependent(void (*kernel)(Params...), dim3 grid, dim3 block, size_t sm
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return (int)cudaLaunchKernelEx(&cfg, kernel, args...);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  if (e != cudaSuccess) cudaGetLastError();   // returned here, not left for the next call that asks
+  return (int)e;
 }
 
 // Services of the C-ABI translation unit: the current device's status word
