@@ -108,3 +108,13 @@ def test_long_prompt_in_chunks_equals_one_call(gpu, monkeypatch):
         check(monkeypatch, p, o, lse, sinks, **kw)
         at += m
     assert at == n
+
+
+@pytest.mark.gpu
+def test_on_a_stream_of_its_own(gpu, monkeypatch):
+    p = paged.Problem([40, 1], [60, 300], 8, 2, 128, "bf16", 16, seed=9, fill=float("nan"))
+    kw = dict(window_left=20, window_right=0)
+    torch.cuda.synchronize()
+    o, lse = p.run(sink_len=6, stream=torch.cuda.Stream(), **kw)
+    assert paged.status() == fa2.FA2_OK
+    check(monkeypatch, p, o, lse, 6, **kw)
