@@ -21,6 +21,8 @@ import torch
 own = False
 
 _DTYPES = {"fp16": torch.float16, "bf16": torch.bfloat16}
+# a row's exponents, by the type that it is written from
+_EXPONENTS = {torch.float16: (-15, 8), torch.bfloat16: (-60, 60)}
 
 
 # ---------------------------------------------------------------- cases
@@ -209,13 +211,12 @@ def _rows(g, shape, dtype):
 
 def _quantise(x, dtype):
     """(codes, exponent bytes) of the rows along x's last dimension."""
-    x = x.float()
-    if dtype == torch.float16:
-        x = x.clamp(-61440.0, 61440.0)   # 2^16, the next code, is no fp16 value
+    low, high = _EXPONENTS[dtype]
+    x = x.float().clamp(-240.0 * 2.0 ** high, 240.0 * 2.0 ** high)   # the next code times 2^8 is no fp16 value
     top = x.abs().amax(dim=-1)
     fraction, e = torch.frexp(top)       # top = fraction * 2^e, fraction in [0.5, 1); 448 = 0.875 * 2^9
     e = e - 9 + (fraction > 0.875)
-    e = e.clamp(*((-15, 8) if dtype == torch.float16 else (-117, 120)))
+    e = e.clamp(low, high)
     e = torch.where(top == 0, torch.zeros_like(e), e)
     codes = torch.ldexp(x, -e[..., None]).to(torch.float8_e4m3fn)
     return codes, (e + 127).to(torch.uint8)
@@ -475,15 +476,13 @@ def _exact_row_values(state, x):
     2^-9 on, in units of the row's scale; halves to the even multiple."""
     rows = state[x].double()
     tokens = state["case"]["tokens"]
-    fp16 = state[x].dtype == torch.float16
-    if fp16:
-        rows = rows.clamp(-61440, 61440)
+    lowest, highest = (2.0 ** e for e in _EXPONENTS[state[x].dtype])
+    rows = rows.clamp(-240 * highest, 240 * highest)
     out = torch.zeros_like(rows)
     rows = rows[:tokens]
     top = rows.abs().amax(-1, keepdim=True)
     scale = torch.ones_like(top)
-    lowest, highest = (2.0 ** -15, 2.0 ** 8) if fp16 else (2.0 ** -117, 2.0 ** 120)
-    for _ in range(300):   # the smallest power of two with top <= 448 * scale
+    for _ in range(150):   # the smallest power of two with top <= 448 * scale
         scale = torch.where((top > 448 * scale) & (scale < highest), scale * 2, scale)
         scale = torch.where((top <= 224 * scale) & (scale > lowest) & (top > 0), scale / 2, scale)
     y = rows / scale
