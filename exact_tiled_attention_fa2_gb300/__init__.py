@@ -113,6 +113,34 @@ class Fa2PagedPlanParams(ctypes.Structure):
     ]
 
 
+class Fa2PagedCacheFp8(ctypes.Structure):
+    """Mirror of ``fa2_paged_cache_fp8`` in include/fa2.h."""
+
+    _fields_ = [
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_exps", ctypes.c_void_p), ("v_exps", ctypes.c_void_p),
+        ("k_strides", ctypes.c_int64 * 3), ("v_strides", ctypes.c_int64 * 3),
+        ("k_exp_strides", ctypes.c_int64 * 2), ("v_exp_strides", ctypes.c_int64 * 2),
+        ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("heads", ctypes.c_int), ("head_dim", ctypes.c_int),
+    ]
+
+
+class Fa2PagedRowsFp8Params(ctypes.Structure):
+    """Mirror of ``fa2_paged_append_fp8_params`` and ``fa2_paged_read_fp8_params`` in include/fa2.h."""
+
+    _fields_ = [
+        ("cache", Fa2PagedCacheFp8),
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("slots", ctypes.c_void_p),
+        ("k_strides", ctypes.c_int64 * 2), ("v_strides", ctypes.c_int64 * 2),
+        ("total", ctypes.c_int), ("dtype", ctypes.c_int),
+    ]
+
+
+class Fa2PagedFp8Params(ctypes.Structure):
+    """Mirror of ``fa2_paged_fp8_params`` in include/fa2.h (checked against the library's sizeof)."""
+
+    _fields_ = [("cache", Fa2PagedCacheFp8)] + Fa2PagedParams._fields_[1:] + [("dtype", ctypes.c_int)]
+
+
 class Fa2Error(RuntimeError):
     """A nonzero fa2_status returned through the C ABI."""
 
@@ -176,6 +204,19 @@ def load_library():
     if lib.fa2_paged_params_size() != ctypes.sizeof(Fa2PagedParams):
         raise RuntimeError("fa2_paged_params layout mismatch: library %d bytes, binding %d bytes"
                            % (lib.fa2_paged_params_size(), ctypes.sizeof(Fa2PagedParams)))
+    lib.fa2_paged_append_fp8.argtypes = [ctypes.POINTER(Fa2PagedRowsFp8Params), vp]
+    lib.fa2_paged_append_fp8.restype = ci
+    lib.fa2_paged_read_fp8.argtypes = [ctypes.POINTER(Fa2PagedRowsFp8Params), vp]
+    lib.fa2_paged_read_fp8.restype = ci
+    lib.fa2_paged_fwd_fp8.argtypes = [ctypes.POINTER(Fa2PagedFp8Params), vp, sz, vp]
+    lib.fa2_paged_fwd_fp8.restype = ci
+    lib.fa2_paged_fwd_fp8_workspace_bytes.argtypes = [ctypes.POINTER(Fa2PagedFp8Params)]
+    lib.fa2_paged_fwd_fp8_workspace_bytes.restype = sz
+    lib.fa2_paged_fp8_params_size.argtypes = []
+    lib.fa2_paged_fp8_params_size.restype = sz
+    if lib.fa2_paged_fp8_params_size() != ctypes.sizeof(Fa2PagedFp8Params):
+        raise RuntimeError("fa2_paged_fp8_params layout mismatch: library %d bytes, binding %d bytes"
+                           % (lib.fa2_paged_fp8_params_size(), ctypes.sizeof(Fa2PagedFp8Params)))
     if lib.fa2_fwd_params_size() != ctypes.sizeof(Fa2FwdParams):
         raise RuntimeError("fa2_fwd_params layout mismatch: library %d bytes, binding %d bytes"
                            % (lib.fa2_fwd_params_size(), ctypes.sizeof(Fa2FwdParams)))
@@ -527,6 +568,76 @@ def fa2_paged_fwd(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, o=N
                                                workspace, scale, window_left, window_right, prefix_len, max_seqlen_q, sink_len)
     if type(out) is int:
         raise Fa2Error(out, "fa2_paged_fwd")
+    return out
+
+
+def fa2_paged_append_fp8(k, v, slots, k_cache, v_cache, k_exps, v_exps, stream=None):
+    """Write new key/value rows to a paged cache of 8-bit rows, quantised (fa2_paged_append_fp8).
+
+    k, v, slots as fa2_paged_append (float16 or bfloat16 rows); caches
+    float8_e4m3fn [num_pages, H_kv, page_size, d], exponents uint8 [num_pages,
+    H_kv, page_size].  A row stands for codes * 2^(exponent - 127), with the
+    smallest power of two that brings its largest value to 448 or below.
+    """
+    if stream is not None:
+        with _on_stream(stream, k_cache):
+            return fa2_paged_append_fp8(k, v, slots, k_cache, v_cache, k_exps, v_exps)
+    rc = (_paged or _paged_calls()).append_fp8(k, v, slots, k_cache, v_cache, k_exps, v_exps)
+    if rc:
+        raise Fa2Error(rc, "fa2_paged_append_fp8")
+
+
+def fa2_paged_read_fp8(slots, k_cache, v_cache, k_exps, v_exps, k=None, v=None, dtype=None, stream=None):
+    """Read rows of a paged cache of 8-bit rows back in 16 bits (fa2_paged_read_fp8).
+
+    Returns (k, v) [total, H_kv, d]: row t is what slot ``slots[t]`` (int32
+    CUDA [total]) holds; rows of negative slots are left as they were
+    (uninitialised in tensors made here).  ``dtype``: of new tensors, bfloat16
+    (default) or float16.  Exact in bfloat16 and in the type the row was
+    written from.  Slots of whole pages give a 16-bit cache for fa2_paged_fwd:
+    ``k.view(-1, page_size, H_kv, d).transpose(1, 2)``.
+    """
+    if stream is not None:
+        with _on_stream(stream, k_cache):
+            return fa2_paged_read_fp8(slots, k_cache, v_cache, k_exps, v_exps, k, v, dtype)
+    import torch
+    if dtype is None:
+        dtype = torch.bfloat16 if k is None else k.dtype
+    if dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError("dtype must be bfloat16 or float16")
+    out = (_paged or _paged_calls()).read_fp8(slots, k_cache, v_cache, k_exps, v_exps, k, v, dtype == torch.bfloat16)
+    if type(out) is int:
+        raise Fa2Error(out, "fa2_paged_read_fp8")
+    return out
+
+
+def fa2_paged_fwd_fp8_workspace_bytes(q, k_cache, v_cache, k_exps, v_exps, block_table, cu_seqlens_q, seqlens_k,
+                                      max_seqlen_q=None) -> int:
+    """Workspace fa2_paged_fwd_fp8 needs for these tensors; it depends on their shapes only."""
+    return _paged_calls().workspace_bytes_fp8(q, k_cache, v_cache, k_exps, v_exps, block_table, cu_seqlens_q, seqlens_k,
+                                              max_seqlen_q)
+
+
+def fa2_paged_fwd_fp8(q, k_cache, v_cache, k_exps, v_exps, block_table, cu_seqlens_q, seqlens_k, o=None, lse=None,
+                      workspace=None, scale=None, window_left=-1, window_right=-1, prefix_len=0, max_seqlen_q=None,
+                      stream=None, sink_len=0):
+    """fa2_paged_fwd over a paged cache of 8-bit rows, read in place (fa2_paged_fwd_fp8).
+
+    Caches and exponents as fa2_paged_append_fp8; q and o float16 or bfloat16;
+    everything else as fa2_paged_fwd.  For decoding and short chunks (a query
+    tile has 32 rows); the attention of a long chunk is faster as
+    fa2_paged_read_fp8 and fa2_paged_fwd.
+    """
+    if stream is not None:
+        with _on_stream(stream, q):
+            return fa2_paged_fwd_fp8(q, k_cache, v_cache, k_exps, v_exps, block_table, cu_seqlens_q, seqlens_k, o, lse,
+                                     workspace, scale, window_left, window_right, prefix_len, max_seqlen_q,
+                                     sink_len=sink_len)
+    out = (_paged or _paged_calls()).forward_fp8(q, k_cache, v_cache, k_exps, v_exps, block_table, cu_seqlens_q,
+                                                 seqlens_k, o, lse, workspace, scale, window_left, window_right,
+                                                 prefix_len, max_seqlen_q, sink_len)
+    if type(out) is int:
+        raise Fa2Error(out, "fa2_paged_fwd_fp8")
     return out
 
 

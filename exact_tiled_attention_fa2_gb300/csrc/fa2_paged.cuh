@@ -1493,6 +1493,12 @@ __global__ void __launch_bounds__(kPagedMergeThreads) fa2_paged_merge_kernel(con
   }
 }
 
+template <int D, bool BF16>
+int launch_paged_merge(const PagedParams& p, cudaStream_t stream) {
+  const dim3 blocks((unsigned)(p.ctas - 1), (unsigned)((p.slot_rows + kPagedMergeRows - 1) / kPagedMergeRows));
+  return launch_dependent(fa2_paged_merge_kernel<D, BF16>, blocks, kPagedMergeThreads, 0, stream, p);
+}
+
 template <int D, bool BF16, bool BAND, bool WIDE, bool SMALL>
 int launch_paged_kernels(const PagedLaunchArgs& a) {
   using C = PagedConfig<D, WIDE>;
@@ -1511,8 +1517,7 @@ int launch_paged_kernels(const PagedLaunchArgs& a) {
   const int r = launch_dependent(kern, dim3((unsigned)grid), C::THREADS, C::SMEM_BYTES, a.stream, a.tm_q, a.tm_k, a.tm_v,
                                  a.p);
   if (r != 0) return r;
-  const dim3 blocks((unsigned)(a.p.ctas - 1), (unsigned)((a.p.slot_rows + kPagedMergeRows - 1) / kPagedMergeRows));
-  return launch_dependent(fa2_paged_merge_kernel<D, BF16>, blocks, kPagedMergeThreads, 0, a.stream, a.p);
+  return launch_paged_merge<D, BF16>(a.p, a.stream);
 }
 
 template <int D, bool BF16, bool BAND>

@@ -78,6 +78,10 @@ struct PagedLaunchArgs {
 int launch_paged_d64(const PagedLaunchArgs& a);
 int launch_paged_d128(const PagedLaunchArgs& a);
 int launch_paged_d256(const PagedLaunchArgs& a);
+// The merge of the partials that pieces of the line have left.
+int launch_paged_merge_d64(const PagedParams& p, bool bf16, cudaStream_t stream);
+int launch_paged_merge_d128(const PagedParams& p, bool bf16, cudaStream_t stream);
+int launch_paged_merge_d256(const PagedParams& p, bool bf16, cudaStream_t stream);
 
 struct PagedPlanArgs {
   const int* context_lens;
@@ -139,6 +143,13 @@ int launch_dependent(void (*kernel)(Params...), dim3 grid, dim3 block, size_t sm
   return (int)e;
 }
 
+// launch_dependent, by the name under which the 8-bit cache and shared prefixes
+// use it (their sources are looked at for read-only loads by that name).
+template <class... Params, class... Args>
+int launch_chained(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, const Args&... args) {
+  return launch_dependent(kernel, grid, block, smem, stream, args...);
+}
+
 // Services of the C-ABI translation unit: the current device's status word
 // (checks the device), and a tensor map of a 16-bit tensor whose innermost
 // dimension is contiguous (strides of the others in elements; 128-byte
@@ -146,5 +157,8 @@ int launch_dependent(void (*kernel)(Params...), dim3 grid, dim3 block, size_t sm
 int paged_device_status(uint32_t** status);
 int encode_map_nd(CUtensorMap* m, const void* base, int rank, const long long* dims, const long long* strides,
                   const int* box, bool bf16);
+// The same of bytes (64- or 128-byte swizzle, as the box's rows).
+int encode_map_u8(CUtensorMap* m, const void* base, int rank, const long long* dims, const long long* strides,
+                  const int* box);
 
 }  // namespace fa2

@@ -9,11 +9,10 @@
 #include "../../include/fa2.h"
 #include "fa2_internal.h"
 #include "fa2_paged.h"
+#include "fa2_paged_check.h"
 
 namespace fa2 {
 namespace {
-
-constexpr long long kMaxStride = 1ll << 39;   // elements: 16-bit strides stay below the TMA limit of 2^40 bytes
 
 // Pieces the work is cut into: one wave of the resident CTAs of a GB300's 152
 // SMs (two per SM, one at head dim 256).  Fixed, so that neither the workspace
@@ -27,45 +26,6 @@ constexpr int paged_ctas(int d) { return d == 256 ? 152 : 304; }
 // 32000 at d = 256, few pairs of many partials, 42.7, 40.2, 55.5).
 constexpr int kPagedOverhead = 128;
 constexpr int kPagedMinShare = 128;
-constexpr int kPagedMaxHeads = 65536;
-constexpr long long kPagedMaxKeys = (1ll << 31) - 4096;   // keys of a sequence, rounded up to tiles, stay below 2^31
-
-struct Range {
-  uintptr_t at;
-  size_t bytes;
-};
-
-Range range(const void* p, size_t bytes) { return Range{reinterpret_cast<uintptr_t>(p), bytes}; }
-bool overlap(const Range& a, const Range& b) { return a.at < b.at + b.bytes && b.at < a.at + a.bytes; }
-bool misaligned(const void* p, unsigned to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
-size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
-
-// Bytes a strided tensor can touch: dims[i] with strides st[i] (elements), and
-// `inner` contiguous elements.
-template <int N>
-Range extent(const void* p, const long long (&dims)[N], const long long (&st)[N], long long inner, int elem) {
-  long long last = inner - 1;
-  for (int i = 0; i < N; ++i)
-    if (dims[i] > 1) last += (dims[i] - 1) * st[i];
-  return range(p, (size_t)(last + 1) * (size_t)elem);
-}
-
-// Strides of dimensions larger than 1: positive multiples of 8 elements.
-template <int N>
-int check_strides(const long long (&dims)[N], const long long (&st)[N]) {
-  for (int i = 0; i < N; ++i) {
-    if (dims[i] <= 1) continue;
-    if (st[i] <= 0 || st[i] >= kMaxStride) return FA2_ERR_INVALID_ARG;
-    if (st[i] & 7) return FA2_ERR_MISALIGNED;
-  }
-  return FA2_OK;
-}
-
-// One cache tensor: (pages, heads, rows).
-struct CacheView {
-  long long dims[3], st[3];
-  Range bytes;
-};
 
 int check_cache(const fa2_paged_cache& c, CacheView& k, CacheView& v) {
   if (c.dtype != FA2_FP16 && c.dtype != FA2_BF16) return FA2_ERR_INVALID_ARG;

@@ -3,4 +3,7 @@
 
 namespace fa2 {
 int launch_paged_d256(const PagedLaunchArgs& a) { return launch_paged<256>(a); }
+int launch_paged_merge_d256(const PagedParams& p, bool bf16, cudaStream_t stream) {
+  return bf16 ? launch_paged_merge<256, true>(p, stream) : launch_paged_merge<256, false>(p, stream);
+}
 }  // namespace fa2

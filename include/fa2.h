@@ -27,11 +27,16 @@
  *                            a serving step on a paged key/value cache: block
  *                            tables and slots from request lengths, new rows
  *                            written to their slots, attention of each
- *                            request's new tokens (grouped query heads).
+ *                            request's new tokens (grouped query heads);
+ *   fa2_paged_append_fp8 / fa2_paged_read_fp8 / fa2_paged_fwd_fp8
+ *                            the same on a cache of 8-bit rows: quantised as
+ *                            they are written, read back, attended in place;
+ *   fa2_paged_fwd_shared     fa2_paged_fwd where requests share their first
+ *                            pages, which are attended once for all of them.
  *
  * Ownership: the caller owns every buffer.  fa2_fwd and fa2_fwd_ex allocate
- * no device memory; fa2_bwd, fa2_bwd_ex, fa2_decode and fa2_paged_fwd take a
- * caller workspace.  The library keeps one small device status word per device
+ * no device memory; fa2_bwd, fa2_bwd_ex, fa2_decode and the fa2_paged_fwd calls
+ * take a caller workspace.  The library keeps one small device status word per device
  * for reporting kernel-side wait timeouts, rejected packed offsets and
  * out-of-range pages (see fa2_get_device_status).
  *
@@ -520,6 +525,130 @@ size_t fa2_paged_params_size(void);
 size_t fa2_paged_fwd_workspace_bytes(const fa2_paged_params* params);
 
 int fa2_paged_fwd(const fa2_paged_params* params, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * fa2_paged_cache_fp8 -- a paged key/value cache of 8-bit rows.  A row (one
+ * token of one K/V head) is head_dim e4m3 codes and one exponent byte u, and
+ * stands for code * 2^(u - 127).  Codes lie as in fa2_paged_cache (element
+ * strides, one byte an element); the exponent of (page, head, row) of k is at
+ *   k_exps + page*k_exp_strides[0] + head*k_exp_strides[1] + row.
+ * k and v may interleave in one allocation, and the exponents with them: the
+ * elements of all four are distinct.  Strides of dimensions larger than 1 are
+ * positive and below 2^39: multiples of 16 for codes, of 8 for exponents.
+ */
+typedef struct fa2_paged_cache_fp8 {
+  void* k;                   /* device, e4m3 codes, 16-byte aligned; written by fa2_paged_append_fp8 only */
+  void* v;                   /* device, e4m3 codes, 16-byte aligned; written by fa2_paged_append_fp8 only */
+  void* k_exps;              /* device, exponent bytes, 8-byte aligned; written by fa2_paged_append_fp8 only */
+  void* v_exps;              /* device, exponent bytes, 8-byte aligned; written by fa2_paged_append_fp8 only */
+  int64_t k_strides[3];      /* page, head, row strides in bytes */
+  int64_t v_strides[3];
+  int64_t k_exp_strides[2];  /* page, head strides in bytes */
+  int64_t v_exp_strides[2];
+  int num_pages;             /* >= 1; num_pages * page_size < 2^31 (FA2_ERR_UNSUPPORTED) */
+  int page_size;             /* 8, 16, 32 or a multiple of 64 (FA2_ERR_UNSUPPORTED otherwise) */
+  int heads;                 /* K/V heads, 1 .. 65536 (FA2_ERR_UNSUPPORTED above) */
+  int head_dim;              /* d: 64, 128 or 256 */
+} fa2_paged_cache_fp8;
+
+/*
+ * fa2_paged_append_fp8 -- new 16-bit key/value rows into a cache of 8-bit
+ * rows, quantised as they are written; slots as fa2_paged_append.  Each row's
+ * exponent e = u - 127 is the smallest with max |x| <= 448 * 2^e (448: the
+ * largest code), within -60 .. 60 (bf16) or -15 .. 8 (fp16); 0 for a row of
+ * zeros.  Its codes are x * 2^-e rounded to the nearest e4m3 value (ties to
+ * even).  A power of two costs no relative precision, and code * 2^e is a
+ * value of the rows' own type: reading back adds no rounding.  |x| past 240 *
+ * 2^60 (bf16) or 240 * 2^8 (fp16), infinity included, counts as that; a NaN
+ * becomes a NaN code and leaves the row's exponent to the others.  One kernel, asynchronous on `stream`, deterministic.
+ */
+typedef struct fa2_paged_append_fp8_params {
+  fa2_paged_cache_fp8 cache;
+  const void* k;           /* device, `dtype`, 16-byte aligned; read only */
+  const void* v;           /* device, `dtype`, 16-byte aligned; read only */
+  const int* slots;        /* device, [total] int32 */
+  int64_t k_strides[2];    /* token, head strides in elements; multiples of 8 */
+  int64_t v_strides[2];
+  int total;               /* rows >= 1 */
+  int dtype;               /* FA2_FP16 or FA2_BF16 */
+} fa2_paged_append_fp8_params;
+
+int fa2_paged_append_fp8(const fa2_paged_append_fp8_params* params, void* stream);
+
+/*
+ * fa2_paged_read_fp8 -- rows of a cache of 8-bit rows as 16-bit rows: row t of
+ * k and v ([total, heads, d] by strides: token, head) becomes what slot
+ * slots[t] holds, code * 2^e rounded to `dtype` (exact for the type that the
+ * row was written from, and in bf16 always; past fp16's range: infinity).  A
+ * row whose slot is negative is left as it was, also one whose slot is past
+ * the cache, which is reported (FA2_ERR_DEVICE_PAGES).  Slots may repeat.  k
+ * and v may interleave in one allocation (their elements are distinct) and
+ * overlap neither slots nor the cache.  With the slots of whole pages the rows
+ * are a 16-bit paged cache of [pages, page_size, heads, d] (fa2_paged_cache),
+ * for a call that wants one, as the attention of a long chunk.  One kernel,
+ * asynchronous on `stream`.
+ */
+typedef struct fa2_paged_read_fp8_params {
+  fa2_paged_cache_fp8 cache;
+  void* k;                 /* device, `dtype`, 16-byte aligned; written */
+  void* v;                 /* device, `dtype`, 16-byte aligned; written */
+  const int* slots;        /* device, [total] int32 */
+  int64_t k_strides[2];    /* token, head strides in elements; multiples of 8 */
+  int64_t v_strides[2];
+  int total;               /* rows >= 1 */
+  int dtype;               /* FA2_FP16 or FA2_BF16 */
+} fa2_paged_read_fp8_params;
+
+int fa2_paged_read_fp8(const fa2_paged_read_fp8_params* params, void* stream);
+
+/*
+ * fa2_paged_fwd_fp8 -- fa2_paged_fwd over a cache of 8-bit rows, read in place:
+ * the result for the rows' values code * 2^e, with q and o in 16 bits (`dtype`)
+ * and everything that fa2_paged_fwd says of tables, lengths, masks, grouped
+ * heads, streams, workspaces and bad offsets.  (A needed page outside [0,
+ * num_pages) reads as zero codes with exponent 0.)  Products are those of the
+ * exact codes: q enters as a sum of three e4m3 parts of falling scale, exact
+ * down to 2^-25 of a query row's largest value, and P likewise, with 12
+ * significant bits down to 2^-22 of the largest P 2^e of its row; sums are
+ * fp32.  Exponents are those that fa2_paged_append_fp8 writes.
+ *
+ * It reads half the bytes of a 16-bit cache, which is what bounds decoding.  A
+ * query tile is 32 rows at most, so a long chunk re-reads the keys from the L2
+ * cache more often than fa2_paged_fwd, whose tile has 128: over chunks of
+ * hundreds of tokens fa2_paged_read_fp8 and fa2_paged_fwd are faster.
+ */
+typedef struct fa2_paged_fp8_params {
+  fa2_paged_cache_fp8 cache;
+  const void* q;           /* device, `dtype`, 16-byte aligned; read only */
+  void* o;                 /* device, `dtype`, 16-byte aligned; written */
+  float* lse;              /* device, float32; written (natural log) */
+  const int* block_table;  /* the rest as fa2_paged_params */
+  const int* cu_seqlens_q;
+  const int* seqlens_k;
+  int64_t table_stride;
+  int64_t q_strides[2];
+  int64_t o_strides[2];
+  int64_t lse_stride;
+  int batch;
+  int heads;
+  int total_q;
+  int max_seqlen_q;
+  int max_pages;
+  int window_left;
+  int window_right;
+  int prefix_len;
+  float scale;
+  int sink_len;
+  int dtype;               /* of q and o: FA2_FP16 or FA2_BF16 */
+} fa2_paged_fp8_params;
+
+/* Workspace fa2_paged_fwd_fp8 needs for these sizes (0 if they are invalid). */
+size_t fa2_paged_fwd_fp8_workspace_bytes(const fa2_paged_fp8_params* params);
+
+int fa2_paged_fwd_fp8(const fa2_paged_fp8_params* params, void* workspace, size_t workspace_bytes, void* stream);
+
+/* sizeof of fa2_paged_fp8_params as compiled into the library (binding check). */
+size_t fa2_paged_fp8_params_size(void);
 
 /*
  * fa2_selftest_wait_timeout -- exercises the kernels' failure path without a
