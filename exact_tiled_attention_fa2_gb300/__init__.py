@@ -113,6 +113,13 @@ class Fa2PagedPlanParams(ctypes.Structure):
     ]
 
 
+class Fa2PagedSharedParams(ctypes.Structure):
+    """Mirror of ``fa2_paged_shared_params`` in include/fa2.h (checked against the library's sizeof)."""
+
+    _fields_ = [("fwd", Fa2PagedParams), ("cu_groups", ctypes.c_void_p), ("shared_lens", ctypes.c_void_p),
+                ("num_groups", ctypes.c_int)]
+
+
 class Fa2PagedCacheFp8(ctypes.Structure):
     """Mirror of ``fa2_paged_cache_fp8`` in include/fa2.h."""
 
@@ -212,6 +219,15 @@ def load_library():
     lib.fa2_paged_fwd_fp8.restype = ci
     lib.fa2_paged_fwd_fp8_workspace_bytes.argtypes = [ctypes.POINTER(Fa2PagedFp8Params)]
     lib.fa2_paged_fwd_fp8_workspace_bytes.restype = sz
+    lib.fa2_paged_fwd_shared.argtypes = [ctypes.POINTER(Fa2PagedSharedParams), vp, sz, vp]
+    lib.fa2_paged_fwd_shared.restype = ci
+    lib.fa2_paged_fwd_shared_workspace_bytes.argtypes = [ctypes.POINTER(Fa2PagedSharedParams)]
+    lib.fa2_paged_fwd_shared_workspace_bytes.restype = sz
+    lib.fa2_paged_shared_params_size.argtypes = []
+    lib.fa2_paged_shared_params_size.restype = sz
+    if lib.fa2_paged_shared_params_size() != ctypes.sizeof(Fa2PagedSharedParams):
+        raise RuntimeError("fa2_paged_shared_params layout mismatch: library %d bytes, binding %d bytes"
+                           % (lib.fa2_paged_shared_params_size(), ctypes.sizeof(Fa2PagedSharedParams)))
     lib.fa2_paged_fp8_params_size.argtypes = []
     lib.fa2_paged_fp8_params_size.restype = sz
     if lib.fa2_paged_fp8_params_size() != ctypes.sizeof(Fa2PagedFp8Params):
@@ -568,6 +584,36 @@ def fa2_paged_fwd(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, o=N
                                                workspace, scale, window_left, window_right, prefix_len, max_seqlen_q, sink_len)
     if type(out) is int:
         raise Fa2Error(out, "fa2_paged_fwd")
+    return out
+
+
+def fa2_paged_fwd_shared_workspace_bytes(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, cu_groups,
+                                         shared_lens, max_seqlen_q=None) -> int:
+    """Workspace fa2_paged_fwd_shared needs for these tensors; it depends on their shapes only."""
+    return _paged_calls().workspace_bytes_shared(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, cu_groups,
+                                                 shared_lens, max_seqlen_q)
+
+
+def fa2_paged_fwd_shared(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, cu_groups, shared_lens, o=None,
+                         lse=None, workspace=None, scale=None, window_right=-1, max_seqlen_q=None, stream=None):
+    """fa2_paged_fwd for sequences that share the first pages of their prompts (fa2_paged_fwd_shared).
+
+    Tensors as fa2_paged_fwd (causal: ``window_right=0``; full: -1).
+    ``cu_groups`` [G + 1] and ``shared_lens`` [G], int32 CUDA: sequences
+    cu_groups[g] .. cu_groups[g+1] - 1 have their first shared_lens[g] keys on
+    the same pages, those that the table row of the group's first sequence
+    names, before any of their new tokens.  These keys are read and attended
+    once for the whole group.  The result is fa2_paged_fwd's, up to the order
+    of its sums.
+    """
+    if stream is not None:
+        with _on_stream(stream, q):
+            return fa2_paged_fwd_shared(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, cu_groups, shared_lens,
+                                        o, lse, workspace, scale, window_right, max_seqlen_q)
+    out = (_paged or _paged_calls()).forward_shared(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, cu_groups,
+                                                    shared_lens, o, lse, workspace, scale, window_right, max_seqlen_q)
+    if type(out) is int:
+        raise Fa2Error(out, "fa2_paged_fwd_shared")
     return out
 
 

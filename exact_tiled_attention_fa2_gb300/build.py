@@ -32,10 +32,10 @@ SOURCES = ["fa2_abi.cu", "fa2_fwd_d64.cu", "fa2_fwd_d128.cu", "fa2_fwd_d256.cu",
            "fa2_bwd_d256.cu", "fa2_decode_d64.cu", "fa2_decode_d128.cu", "fa2_decode_d256.cu",
            "fa2_paged_abi.cu", "fa2_paged_cache.cu", "fa2_paged_d64.cu", "fa2_paged_d128.cu", "fa2_paged_d256.cu",
            "fa2_paged_fp8_abi.cu", "fa2_paged_fp8_cache.cu", "fa2_paged_fp8_d64.cu", "fa2_paged_fp8_d128.cu",
-           "fa2_paged_fp8_d256.cu"]
+           "fa2_paged_fp8_d256.cu", "fa2_paged_shared_d64.cu", "fa2_paged_shared_d128.cu", "fa2_paged_shared_d256.cu"]
 HEADERS = ["fa2_common.cuh", "fa2_tile.cuh", "fa2_fwd_dbuf.cuh", "fa2_bwd.cuh", "fa2_bwd64.cuh", "fa2_bwd256.cuh",
            "fa2_decode.cuh", "fa2_decode_tc.cuh", "fa2_paged.cuh", "fa2_paged.h", "fa2_paged_check.h",
-           "fa2_paged_fp8.cuh", "fa2_paged_fp8.h",
+           "fa2_paged_fp8.cuh", "fa2_paged_fp8.h", "fa2_paged_shared.cuh",
            "fa2_internal.h",
            "sm103_ptx.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -264,9 +264,82 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int a, int b
   return s;
 }
 
-template <bool WIDE>
+// Keys that the sequences of group g share, as far as they are attended once for
+// all: whole units of the shared length, 0 for a single sequence, -1: out of range.
+__device__ __forceinline__ int group_keys(const PagedParams& p, int first, int end, int shared) {
+  if (shared < 0 || shared > p.max_keys) return -1;
+  return end - first < 2 ? 0 : shared / p.share_unit * p.share_unit;
+}
+
+// The group that holds sequence i (-1: none), its first sequence and the one
+// after its last.
+__device__ __forceinline__ int group_of(const PagedParams& p, int i, int& first, int& end) {
+  int lo = 0, hi = p.groups;   // the last group that starts at i or before
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (p.cu_groups[mid] <= i)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  first = p.cu_groups[lo];
+  end = p.cu_groups[lo + 1];
+  return first >= 0 && first <= i && i < end && end <= p.seqs ? lo : -1;
+}
+
+// What the schedule needs of sequence i: query rows [a, b), keys, block-table row.
+struct SeqRead {
+  int a, b, k;        // k < 0: out of range
+  const int* table;
+};
+
+template <bool SHARED>
+__device__ __forceinline__ SeqRead seq_read(const PagedParams& p, int i) {
+  SeqRead x;
+  if constexpr (!SHARED) {
+    x.a = p.cu_q[i];
+    x.b = p.cu_q[i + 1];
+    x.k = p.lens_k[i];
+    x.table = p.table + (long long)i * p.table_stride;
+  } else if (p.own) {
+    // the keys behind the group's shared ones: an ordinary sequence whose table row starts later
+    x.a = p.cu_q[i];
+    x.b = p.cu_q[i + 1];
+    x.k = p.lens_k[i];
+    x.table = p.table + (long long)i * p.table_stride;
+    int first, end;
+    const int g = group_of(p, i, first, end);
+    if (g >= 0 && x.b > x.a) {
+      const int keys = group_keys(p, first, end, p.shared_lens[g]);
+      if (keys != 0) {
+        const bool fits = keys > 0 && x.k <= p.max_keys && (long long)x.k - keys >= (long long)x.b - x.a &&
+                          0 <= p.cu_q[first] && p.cu_q[first] <= x.a && x.b <= p.cu_q[end] && p.cu_q[end] <= p.total_q;
+        x.k = fits ? x.k - keys : -1;
+        if (fits) x.table += keys / p.page_size;
+      }
+    }
+  } else {
+    // group i as one sequence: the query rows of all its sequences, the shared keys
+    const int first = p.cu_groups[i], end = p.cu_groups[i + 1];
+    x.a = x.b = x.k = 0;
+    x.table = p.table;
+    if (0 <= first && first < end && end <= p.seqs) {
+      const int keys = group_keys(p, first, end, p.shared_lens[i]);
+      if (keys > 0) {   // (out of range: each of the sequences is reported)
+        x.a = p.cu_q[first];
+        x.b = p.cu_q[end];
+        x.k = keys;
+        x.table = p.table + (long long)first * p.table_stride;
+      }
+    }
+  }
+  return x;
+}
+
+template <bool WIDE, bool SHARED>
 static __device__ __noinline__ PagedSeq read_seq(const PagedParams& p, int i, bool report) {
-  return paged_seq<WIDE>(p, p.cu_q[i], p.cu_q[i + 1], p.lens_k[i], report);
+  const SeqRead x = seq_read<SHARED>(p, i);
+  return paged_seq<WIDE>(p, x.a, x.b, x.k, report);
 }
 
 // What a CTA works on.
@@ -345,6 +418,7 @@ __device__ __forceinline__ void place_piece(PagedPlace<WIDE>& r, int block, int 
 
 // Finds what CTA `block` works on, query tiles of few rows and at most 32
 // sequences: one a lane of the calling warp.
+template <bool SHARED = false>
 __device__ __forceinline__ PagedPlace<false> find_place_small(const PagedParams& p, int block, bool report) {
   constexpr int KEYS = LineOf<false>::KEYS;
   const int lane = (int)threadIdx.x & 31;
@@ -352,7 +426,8 @@ __device__ __forceinline__ PagedPlace<false> find_place_small(const PagedParams&
   PagedSeq s;
   s.tiles = s.keys = s.n_q = s.n_k = s.row0 = 0;
   if (lane < p.batch) {
-    s = paged_seq<false>(p, p.cu_q[lane], p.cu_q[lane + 1], p.lens_k[lane], report);
+    const SeqRead x = seq_read<SHARED>(p, lane);
+    s = paged_seq<false>(p, x.a, x.b, x.k, report);
     span = s.span<false>(p, s.tiles);
     pairs = s.tiles * p.heads_kv;
     if (s.tiles > 0) longest = s.width<false>(p, 0);
@@ -391,7 +466,7 @@ __device__ __forceinline__ PagedPlace<false> find_place_small(const PagedParams&
 
 // The same of any number of sequences: every thread sums a run of them; every
 // thread returns the same.
-template <int THREADS, bool WIDE>
+template <int THREADS, bool WIDE, bool SHARED = false>
 __device__ __forceinline__ PagedPlace<WIDE> find_place(const PagedParams& p, int block, PagedScan<WIDE>* sh,
                                                        bool report) {
   using Line = typename LineOf<WIDE>::T;
@@ -407,7 +482,7 @@ __device__ __forceinline__ PagedPlace<WIDE> find_place(const PagedParams& p, int
   s.tiles = s.keys = s.n_q = s.n_k = s.row0 = 0;
 #pragma unroll 1
   for (int i = i0; i < i1; ++i) {
-    s = read_seq<WIDE>(p, i, report);
+    s = read_seq<WIDE, SHARED>(p, i, report);
     const Line x = s.span<WIDE>(p, s.tiles);
     span += x;
     pairs += (Line)s.tiles * p.heads_kv;
@@ -456,7 +531,7 @@ __device__ __forceinline__ PagedPlace<WIDE> find_place(const PagedParams& p, int
       Line x = a, n = b;
 #pragma unroll 1
       for (int i = i0; i < i1; ++i) {
-        if (per > 1) s = read_seq<WIDE>(p, i, false);
+        if (per > 1) s = read_seq<WIDE, SHARED>(p, i, false);
         const Line sx = s.span<WIDE>(p, s.tiles), sn = (Line)s.tiles * p.heads_kv;
         if (whole < n + sn) {
           const int tiles = (int)(whole - n) / p.heads_kv;   // from the last
@@ -486,7 +561,7 @@ __device__ __forceinline__ PagedPlace<WIDE> find_place(const PagedParams& p, int
     Line x = mine;
 #pragma unroll 1
     for (int i = i0; i < i1; ++i) {
-      if (per > 1) s = read_seq<WIDE>(p, i, false);
+      if (per > 1) s = read_seq<WIDE, SHARED>(p, i, false);
       const Line step = one ? (Line)s.tiles * p.heads_kv : s.span<WIDE>(p, s.tiles);
       if (pos < x + step) {
         if (WIDE && !one && i == cut_seq) {   // ends where it did, and starts the line
@@ -558,7 +633,7 @@ static_assert(sizeof(PagedMerge) == kPagedMergeBytes, "merge description");
 // Walks the fragments of one CTA's piece; every lane of the TMA warp in step.
 // What the pairs of one query tile share is worked out once, and the next
 // sequence's lengths are read a sequence ahead.
-template <bool BAND, bool WIDE>
+template <bool BAND, bool WIDE, bool SHARED = false>
 struct FragWalk {
   using Line = typename LineOf<WIDE>::T;
   PagedSeq s;
@@ -569,15 +644,25 @@ struct FragWalk {
   Line x, begin, end;   // the pair's start on the line; the piece
   int cta, seq, tile, h;
   int next_a, next_b, next_k;   // sequence seq + 1
+  const int* next_table;        // (SHARED)
+  int merge_id;                 // (SHARED) the pair of `merge`
   bool more, one;     // one: a single pair, whole
   PagedMerge merge;   // the pair cut by the piece's start
 
   __device__ __forceinline__ void read_ahead(const PagedParams& p) {
     if (seq + 1 < p.batch) {
-      next_a = p.cu_q[seq + 1];
-      next_b = p.cu_q[seq + 2];
-      next_k = p.lens_k[seq + 1];
+      const SeqRead x = seq_read<SHARED>(p, seq + 1);
+      next_a = x.a;
+      next_b = x.b;
+      next_k = x.k;
+      if constexpr (SHARED) next_table = x.table;
     }
+  }
+
+  // (SHARED) The current pair's place among the pairs: query tiles counted by
+  // their first rows, one more for each sequence before, so that none coincide.
+  __device__ __forceinline__ int pair_id(const PagedParams& p) const {
+    return (s.row0 / p.tile_tokens + seq + tile) * p.heads_kv + h;
   }
 
   __device__ void start_tile(const PagedParams& p) {
@@ -610,7 +695,7 @@ struct FragWalk {
     more = true;
     one = pl.share == 0;
     merge.count = -1;
-    table = p.table + (long long)seq * p.table_stride;
+    table = SHARED ? seq_read<SHARED>(p, seq).table : p.table + (long long)seq * p.table_stride;
     begin = piece * pl.share;   // one: 0
     end = min(begin + pl.share, pl.total);
     if (one) {   // the query tiles from the last (the most keys) to the first
@@ -636,13 +721,23 @@ struct FragWalk {
       merge.row = base.row;
       merge.rows = base.rows;
       merge.h = h;
+      if constexpr (SHARED) merge_id = pair_id(p);
+    }
+  }
+
+  // Leaves word of the pair cut by the piece's start for the merge.
+  __device__ __forceinline__ void tell_merge(const PagedParams& p, const PagedPlace<WIDE>& pl) const {
+    if constexpr (SHARED) {
+      if (merge.count >= 0) p.pairs[merge_id] = PagedPair{merge.count, merge.c0, merge.from_start, 0};
+    } else if (pl.line && pl.piece < p.ctas) {
+      p.merges[pl.piece] = merge;
     }
   }
 };
 
 // The next fragment, to shared memory; false when the piece is done.
-template <bool BAND, bool WIDE>
-__device__ __forceinline__ bool next_fragment(FragWalk<BAND, WIDE>& k, const PagedParams& p, PagedFrag* dst, int lane) {
+template <bool BAND, bool WIDE, bool SHARED>
+__device__ __forceinline__ bool next_fragment(FragWalk<BAND, WIDE, SHARED>& k, const PagedParams& p, PagedFrag* dst, int lane) {
   while (k.more) {
     const bool from_start = k.begin <= k.x, to_end = k.end - k.x >= k.w, whole = from_start && to_end;
     const int j0 = from_start ? 0 : span_tile(p, k.begin - k.x, k.tiles_n);
@@ -655,6 +750,11 @@ __device__ __forceinline__ bool next_fragment(FragWalk<BAND, WIDE>& k, const Pag
       dst->j0 = j0;
       dst->n = n;
       dst->slot = whole ? -1 : 2 * k.cta + (from_start ? 1 : 0);
+      if (SHARED && whole) {   // a partial all the same: the merge joins it with the other pass's
+        const int id = k.pair_id(p);
+        dst->slot = 2 * p.ctas + id;
+        p.pairs[id] = PagedPair{-1, 0, 0, 0};
+      }
       dst->tm = k.base.tm.from(j0);
     }
     // on to the next pair
@@ -670,7 +770,10 @@ __device__ __forceinline__ bool next_fragment(FragWalk<BAND, WIDE>& k, const Pag
             k.more = false;
             break;
           }
-          k.table += p.table_stride;
+          if constexpr (SHARED)
+            k.table = k.next_table;
+          else
+            k.table += p.table_stride;
           k.s = paged_seq<WIDE>(p, k.next_a, k.next_b, k.next_k, false);
           k.read_ahead(p);
         } while (k.s.tiles == 0);
@@ -687,8 +790,8 @@ __device__ __forceinline__ bool next_fragment(FragWalk<BAND, WIDE>& k, const Pag
 
 // The same out of line, for the TMA warp between its loads (inlined there, a
 // prompt chunk of 2048 over 16384 keys takes 449 us in place of 428).
-template <bool BAND, bool WIDE>
-static __device__ __noinline__ bool next_fragment_far(FragWalk<BAND, WIDE>& k, const PagedParams& p, PagedFrag* dst,
+template <bool BAND, bool WIDE, bool SHARED>
+static __device__ __noinline__ bool next_fragment_far(FragWalk<BAND, WIDE, SHARED>& k, const PagedParams& p, PagedFrag* dst,
                                                       int lane) {
   return next_fragment(k, p, dst, lane);
 }
@@ -769,9 +872,9 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map
 
 // The planner warp (few rows): walks the piece's fragments, up to four ahead of
 // the softmax.
-template <class C, bool BAND>
+template <class C, bool BAND, bool SHARED>
 __device__ __forceinline__ void pg_plan(const PagedCtx<C>& t, const PagedParams& p, const PagedPlace<C::WIDE>& place, int lane) {
-  FragWalk<BAND, C::WIDE> walk;
+  FragWalk<BAND, C::WIDE, SHARED> walk;
   walk.start(p, place);
   bool have = true;
 #pragma unroll 1
@@ -782,7 +885,7 @@ __device__ __forceinline__ void pg_plan(const PagedCtx<C>& t, const PagedParams&
     if (lane == 0) {
       if (!have) f->n = -1;
       mbar_arrive(t.bar(PG_PLAN + (nf & 3)));
-      if (nf == 0 && place.line && place.piece < p.ctas) p.merges[place.piece] = walk.merge;
+      if (nf == 0) walk.tell_merge(p, place);
     }
   }
 }
@@ -795,14 +898,14 @@ __device__ __forceinline__ void pg_plan(const PagedCtx<C>& t, const PagedParams&
 // while this one is loaded): with two stages, the time from a free stage to its
 // next load is part of the tile loop's period, and between the two stand only a
 // wait and the issue.
-template <class C, bool BAND>
+template <class C, bool BAND, bool SHARED>
 __device__ __forceinline__ void pg_load(const PagedCtx<C>& t, const PagedParams& p, const CUtensorMap* tm_q,
                                         const CUtensorMap* tm_k, const CUtensorMap* tm_v, const PagedPlace<C::WIDE>& place,
                                         int lane) {
-  FragWalk<BAND, C::WIDE> walk;
+  FragWalk<BAND, C::WIDE, SHARED> walk;
   if constexpr (!C::PLANNER) {
     walk.start(p, place);
-    if (lane == 0 && place.line && place.piece < p.ctas) p.merges[place.piece] = walk.merge;
+    if (lane == 0) walk.tell_merge(p, place);
   }
   // Q loads of at most 64 rows leave room for the next fragment's in the other
   // half of the rows (the products then read 64 rows of whatever follows, which
@@ -1307,7 +1410,7 @@ __device__ __forceinline__ void pg_softmax(const PagedCtx<C>& t, const PagedPara
 // keys 11.1 us, 11.8 with the general search; 8 x 5 drafted tokens 16.8, 17.8.
 // Its own kernel, since the code of both in one costs batches of hundreds: 500
 // requests of 1..300 keys 105 us, 115).
-template <int D, bool BF16, bool BAND, bool WIDE, bool SMALL>
+template <int D, bool BF16, bool BAND, bool WIDE, bool SMALL, bool SHARED>
 __global__ void __launch_bounds__(PagedConfig<D, WIDE>::THREADS, PagedConfig<D, WIDE>::CTAS_PER_SM)
     fa2_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PagedParams p) {
@@ -1322,7 +1425,9 @@ __global__ void __launch_bounds__(PagedConfig<D, WIDE>::THREADS, PagedConfig<D, 
   static_assert(sizeof(PagedScan<WIDE>) <= 320 && C::OFF_SCAN % 8 == 0, "scan area");
   const int warp = (int)(threadIdx.x >> 5);
   const int lane = (int)(threadIdx.x & 31);
-  grid_launch_dependents();   // the merge may be scheduled once every CTA has started; it waits for the partials
+  // The merge may be scheduled once every CTA has started; it waits for the
+  // partials.  (The pass over shared keys lets the other pass in further down.)
+  if (!SHARED || p.own) grid_launch_dependents();
 
   PagedCtx<C> t;
   t.bar0 = sbase + C::OFF_BAR;
@@ -1345,8 +1450,12 @@ __global__ void __launch_bounds__(PagedConfig<D, WIDE>::THREADS, PagedConfig<D, 
   }
   // What precedes this kernel is complete: from here on it touches memory, and
   // takes tensor memory (held while waiting, it could be what a kernel before
-  // this one waits for).
-  grid_dependency_wait();
+  // this one waits for).  The pass over the sequences' own keys needs nothing of
+  // the one over shared keys, only what preceded that: it is let in behind that
+  // pass's wait, and waits for its end at its own, so that the merge, which waits
+  // for this kernel, has both.
+  if (!SHARED || !p.own) grid_dependency_wait();
+  if (SHARED && !p.own) grid_launch_dependents();
   // Tensor memory before the schedule: an SM's second CTA starts only when the
   // first has let go of the allocation permit (measured: 3.6 us into the kernel
   // with the allocation behind the schedule, half of the CTAs).
@@ -1358,26 +1467,26 @@ __global__ void __launch_bounds__(PagedConfig<D, WIDE>::THREADS, PagedConfig<D, 
   PagedPlace<WIDE> place;
   if constexpr (SMALL) {
     if (warp == C::PLAN_WARP) {
-      place = find_place_small(p, (int)blockIdx.x, blockIdx.x == 0);
+      place = find_place_small<SHARED>(p, (int)blockIdx.x, blockIdx.x == 0);
       if (lane == 0) scan->place = place;
     }
     __syncthreads();
     place = scan->place;
   } else {
-    place = find_place<C::THREADS, WIDE>(p, (int)blockIdx.x, scan, blockIdx.x == 0);   // with its barriers
+    place = find_place<C::THREADS, WIDE, SHARED>(p, (int)blockIdx.x, scan, blockIdx.x == 0);   // with its barriers
   }
   tc_fence_after();
   t.tmem = *tmem_slot;
 
   if (place.seq < 0) {   // nothing for this CTA
-    if (threadIdx.x == 0 && place.line && place.piece < p.ctas) p.merges[place.piece].count = -1;
+    if (!SHARED && threadIdx.x == 0 && place.line && place.piece < p.ctas) p.merges[place.piece].count = -1;
   } else if (warp == C::TMA_WARP) {
-    pg_load<C, BAND>(t, p, &tm_q, &tm_k, &tm_v, place, lane);
+    pg_load<C, BAND, SHARED>(t, p, &tm_q, &tm_k, &tm_v, place, lane);
   } else if (warp == C::MMA_WARP) {
     if (lane == 0) pg_mma<C, BF16>(t, p);
     __syncwarp();
   } else if (C::PLANNER && warp == C::PLAN_WARP) {
-    pg_plan<C, BAND>(t, p, place, lane);
+    pg_plan<C, BAND, SHARED>(t, p, place, lane);
   } else {
     pg_softmax<C, BF16, BAND>(t, p, warp, lane);
   }
@@ -1387,6 +1496,7 @@ __global__ void __launch_bounds__(PagedConfig<D, WIDE>::THREADS, PagedConfig<D, 
     tc_fence_after();
     tmem_dealloc(t.tmem, C::TMEM_COLS);
   }
+  if (SHARED && p.own) grid_dependency_wait();
 }
 
 // ---------------------------------------------------------------- the merge
@@ -1499,23 +1609,32 @@ int launch_paged_merge(const PagedParams& p, cudaStream_t stream) {
   return launch_dependent(fa2_paged_merge_kernel<D, BF16>, blocks, kPagedMergeThreads, 0, stream, p);
 }
 
-template <int D, bool BF16, bool BAND, bool WIDE, bool SMALL>
-int launch_paged_kernels(const PagedLaunchArgs& a) {
+// The attention kernel by itself.
+template <int D, bool BF16, bool BAND, bool WIDE, bool SMALL, bool SHARED>
+int launch_paged_kernel(const PagedLaunchArgs& a) {
   using C = PagedConfig<D, WIDE>;
-  auto kern = fa2_paged_kernel<D, BF16, BAND, WIDE, SMALL>;
+  auto kern = fa2_paged_kernel<D, BF16, BAND, WIDE, SMALL, SHARED>;
   static std::atomic<unsigned long long> configured{0};
   const int e = once_per_device(configured, [&]() -> int {
     const cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM_BYTES);
     if (r != cudaSuccess) return (int)r;
-    cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
-    return (int)cudaFuncSetAttribute(fa2_paged_merge_kernel<D, BF16>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+    return (int)cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
   });
   if (e != 0) return e;
   // whole waves (few rows: all of the batch is on the line, or at most `ctas` pairs)
   const int waves = WIDE ? (a.p.pair_ctas + a.p.ctas - 1) / a.p.ctas : 1;
   const int grid = a.p.ctas * (waves > 1 ? waves : 1);
-  const int r = launch_dependent(kern, dim3((unsigned)grid), C::THREADS, C::SMEM_BYTES, a.stream, a.tm_q, a.tm_k, a.tm_v,
-                                 a.p);
+  return launch_dependent(kern, dim3((unsigned)grid), C::THREADS, C::SMEM_BYTES, a.stream, a.tm_q, a.tm_k, a.tm_v, a.p);
+}
+
+template <int D, bool BF16, bool BAND, bool WIDE, bool SMALL>
+int launch_paged_kernels(const PagedLaunchArgs& a) {
+  static std::atomic<unsigned long long> configured{0};
+  const int e = once_per_device(configured, [&]() -> int {
+    return (int)cudaFuncSetAttribute(fa2_paged_merge_kernel<D, BF16>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+  });
+  if (e != 0) return e;
+  const int r = launch_paged_kernel<D, BF16, BAND, WIDE, SMALL, false>(a);
   if (r != 0) return r;
   return launch_paged_merge<D, BF16>(a.p, a.stream);
 }

@@ -63,6 +63,21 @@ struct PagedParams {
   float* ws_ml;           // [2 * ctas][slot_rows][2] partial (m, l), exp2 domain
   struct PagedMerge* merges;   // [ctas] pairs to merge, kPagedMergeBytes each
   int sinks;              // first keys a row sees as far as its band's right edge (0 without a left window)
+  // Shared prefixes (fa2_paged_fwd_shared), else unused.  Two passes: over the
+  // groups, each one sequence of all its query rows and the shared keys (`batch`
+  // is then `groups`), and over the sequences' own keys.
+  const int* cu_groups;     // [groups + 1] first sequence of each group
+  const int* shared_lens;   // [groups]
+  int groups, seqs;         // seqs: sequences
+  int share_unit;           // shared keys count in whole units of pages and key tiles
+  int own;                  // the pass over the sequences' own keys
+  struct PagedPair* pairs;  // [whole_slots] where each (query tile, K/V head) pair's partials are
+};
+
+// A pair's partials: the slots of pieces c0 .. c0 + count - 1 (as PagedMerge), or
+// (count -1) the pair's own slot.
+struct PagedPair {
+  int count, c0, from_start, pad;
 };
 
 struct PagedLaunchArgs {
@@ -78,6 +93,10 @@ struct PagedLaunchArgs {
 int launch_paged_d64(const PagedLaunchArgs& a);
 int launch_paged_d128(const PagedLaunchArgs& a);
 int launch_paged_d256(const PagedLaunchArgs& a);
+// The pass over the shared keys, the one over the sequences' own, and the merge.
+int launch_paged_shared_d64(const PagedLaunchArgs& shared, const PagedLaunchArgs& own);
+int launch_paged_shared_d128(const PagedLaunchArgs& shared, const PagedLaunchArgs& own);
+int launch_paged_shared_d256(const PagedLaunchArgs& shared, const PagedLaunchArgs& own);
 // The merge of the partials that pieces of the line have left.
 int launch_paged_merge_d64(const PagedParams& p, bool bf16, cudaStream_t stream);
 int launch_paged_merge_d128(const PagedParams& p, bool bf16, cudaStream_t stream);

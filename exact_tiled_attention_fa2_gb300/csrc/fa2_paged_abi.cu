@@ -58,6 +58,31 @@ struct PagedShape {
   size_t ws_o_bytes, ws_ml_bytes, ws_bytes;   // ws_bytes: all, with the pairs to merge
 };
 
+// Sizes of a pass over `seqs` sequences of at most max_q rows, total_q in all
+// (s.group and s.tile_tokens are set): most pairs that may run whole, and the
+// workspace; whole: every pair's place among the partials and its word for the
+// merge, in place of the pairs to merge.
+int pass_shape(const fa2_paged_cache& c, int total_q, long long seqs, int max_q, bool whole, PagedShape& s) {
+  const long long T = s.tile_tokens;
+  s.max_q = max_q < total_q ? max_q : total_q;
+  s.box_tokens = (int)(T < s.max_q ? T : s.max_q);
+  // whole and partial query tiles of sequences whose rows do not overlap
+  long long tiles = ((long long)total_q + (T - 1) * seqs) / T;
+  const long long each = (s.max_q + T - 1) / T;
+  if (tiles > seqs * each) tiles = seqs * each;
+  if (tiles > total_q) tiles = total_q;
+  const long long pairs = tiles * c.heads, places = whole ? ((long long)total_q / T + seqs) * c.heads : 0;
+  if (pairs > INT_MAX - 1024 || places > INT_MAX - 1024) return FA2_ERR_UNSUPPORTED;
+  s.ctas = paged_ctas(c.head_dim);
+  s.pair_ctas = pairs >= s.ctas ? (int)pairs : 0;
+  const size_t rows = (2 * (size_t)s.ctas + (size_t)places) * (size_t)(s.group * s.box_tokens);
+  s.ws_o_bytes = align256(rows * (size_t)c.head_dim * 4);
+  s.ws_ml_bytes = align256(rows * 2 * 4);
+  s.ws_bytes = s.ws_o_bytes + s.ws_ml_bytes +
+               align256(whole ? (size_t)places * sizeof(PagedPair) : (size_t)s.ctas * kPagedMergeBytes);
+  return FA2_OK;
+}
+
 // Sizes of a paged forward call that follow from what the host knows.
 int paged_shape(const fa2_paged_params& a, PagedShape& s) {
   const fa2_paged_cache& c = a.cache;
@@ -68,23 +93,20 @@ int paged_shape(const fa2_paged_params& a, PagedShape& s) {
   s.group = a.heads / c.heads;
   if (s.group > kPagedTileRows) return FA2_ERR_UNSUPPORTED;
   if ((long long)a.max_pages * c.page_size > kPagedMaxKeys) return FA2_ERR_UNSUPPORTED;
-  s.max_q = a.max_seqlen_q < a.total_q ? a.max_seqlen_q : a.total_q;
-  const long long T = s.tile_tokens = kPagedTileRows / s.group;
-  s.box_tokens = (int)(T < s.max_q ? T : s.max_q);
-  // whole and partial query tiles of sequences whose rows do not overlap
-  long long tiles = ((long long)a.total_q + (T - 1) * a.batch) / T;
-  const long long each = (s.max_q + T - 1) / T;
-  if (tiles > a.batch * each) tiles = a.batch * each;
-  if (tiles > a.total_q) tiles = a.total_q;
-  const long long pairs = tiles * c.heads;
-  if (pairs > INT_MAX - 1024) return FA2_ERR_UNSUPPORTED;
-  s.ctas = paged_ctas(c.head_dim);
-  s.pair_ctas = pairs >= s.ctas ? (int)pairs : 0;
-  const size_t rows = 2 * (size_t)s.ctas * (size_t)(s.group * s.box_tokens);
-  s.ws_o_bytes = align256(rows * (size_t)c.head_dim * 4);
-  s.ws_ml_bytes = align256(rows * 2 * 4);
-  s.ws_bytes = s.ws_o_bytes + s.ws_ml_bytes + align256((size_t)s.ctas * kPagedMergeBytes);
-  return FA2_OK;
+  s.tile_tokens = kPagedTileRows / s.group;
+  return pass_shape(c, a.total_q, a.batch, a.max_seqlen_q, false, s);
+}
+
+// The two passes of a shared forward: `own` over the sequences, `shared` over the groups.
+int shared_shape(const fa2_paged_shared_params& a, PagedShape& own, PagedShape& shared) {
+  const fa2_paged_params& f = a.fwd;
+  int rc = paged_shape(f, own);
+  if (rc) return rc;
+  if (a.num_groups < 1 || a.num_groups > f.batch) return FA2_ERR_INVALID_ARG;
+  shared = own;
+  rc = pass_shape(f.cache, f.total_q, f.batch, f.max_seqlen_q, true, own);
+  if (rc) return rc;
+  return pass_shape(f.cache, f.total_q, a.num_groups, f.total_q, true, shared);
 }
 
 // Map of one cache tensor: a page's 8-row groups, with pages and heads as one
@@ -120,14 +142,48 @@ int cache_map(CUtensorMap* m, const void* at, const CacheView& x, const PagedSid
   return encode_map_nd(m, at, 5, dims, st, box, bf16);
 }
 
-int paged_forward(const fa2_paged_params& a, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+// What a pass needs of its shape: p's sizes and workspace, its map of q, the choice of kernel.
+int fill_pass(const fa2_paged_params& a, const PagedShape& s, uint8_t* workspace, bool whole, PagedLaunchArgs& la) {
+  const fa2_paged_cache& c = a.cache;
+  PagedParams& p = la.p;
+  // q as (d, group, heads_kv, total_q): a box is `group` heads of box_tokens tokens
+  const long long qs[2] = {(long long)a.q_strides[0], (long long)a.q_strides[1]};
+  const long long dims[4] = {c.head_dim, s.group, c.heads, a.total_q};
+  const long long st[3] = {qs[1], qs[1] * s.group, qs[0]};
+  const int box[4] = {64, s.group, 1, s.box_tokens};
+  const int rc = encode_map_nd(&la.tm_q, a.q, 4, dims, st, box, la.bf16);
+  if (rc) return rc;
+  p.max_q = s.max_q;
+  p.slot_rows = s.group * s.box_tokens;
+  p.overhead = (kPagedOverhead + 2 * p.slot_rows + 63) / 64 * 64;
+  p.ctas = s.ctas;
+  p.pair_ctas = s.pair_ctas;
+  p.min_share = kPagedMinShare > 4 * p.slot_rows ? kPagedMinShare : (4 * p.slot_rows + 63) / 64 * 64;
+  p.ws_o = reinterpret_cast<float*>(workspace);
+  p.ws_ml = reinterpret_cast<float*>(workspace + s.ws_o_bytes);
+  uint8_t* words = workspace + s.ws_o_bytes + s.ws_ml_bytes;
+  if (whole)
+    p.pairs = reinterpret_cast<PagedPair*>(words);
+  else
+    p.merges = reinterpret_cast<PagedMerge*>(words);
+  // few rows (every sequence is then one query tile): the line in key tiles and 32 bits
+  la.wide = p.slot_rows > kPagedTileRows / 2 ||
+            (double)p.batch * c.heads * ((p.max_keys + p.overhead) / 64 + 2.0) + 1e6 > 2147483647.0;
+  p.merge_cost = la.wide ? 768 : 256;
+  return FA2_OK;
+}
+
+// fa2_paged_fwd, or (x given) fa2_paged_fwd_shared.
+int paged_forward(const fa2_paged_params& a, const fa2_paged_shared_params* x, void* workspace, size_t workspace_bytes,
+                  cudaStream_t stream) {
   const fa2_paged_cache& c = a.cache;
   CacheView kc, vc;
   int rc = check_cache(c, kc, vc);
   if (rc) return rc;
-  PagedShape s;
-  rc = paged_shape(a, s);
+  PagedShape s, shared;
+  rc = x ? shared_shape(*x, s, shared) : paged_shape(a, s);
   if (rc) return rc;
+  const size_t need = s.ws_bytes + (x ? shared.ws_bytes : 0);
   if (!std::isfinite(a.scale)) return FA2_ERR_INVALID_ARG;
   if (a.window_left < -1 || a.window_right < -1 || a.prefix_len < 0 || a.sink_len < 0) return FA2_ERR_INVALID_ARG;
   if (!a.q || !a.o || !a.lse || !a.block_table || !a.cu_seqlens_q || !a.seqlens_k || !workspace)
@@ -135,7 +191,12 @@ int paged_forward(const fa2_paged_params& a, void* workspace, size_t workspace_b
   if (misaligned(a.q, 16) || misaligned(a.o, 16) || misaligned(a.lse, 4) || misaligned(a.block_table, 4) ||
       misaligned(a.cu_seqlens_q, 4) || misaligned(a.seqlens_k, 4) || misaligned(workspace, 256))
     return FA2_ERR_MISALIGNED;
-  if (workspace_bytes < s.ws_bytes) return FA2_ERR_INVALID_ARG;
+  if (x) {
+    if (!x->cu_groups || !x->shared_lens) return FA2_ERR_INVALID_ARG;
+    if (misaligned(x->cu_groups, 4) || misaligned(x->shared_lens, 4)) return FA2_ERR_MISALIGNED;
+    if (a.window_left >= 0 || a.prefix_len > 0) return FA2_ERR_UNSUPPORTED;
+  }
+  if (workspace_bytes < need) return FA2_ERR_INVALID_ARG;
   const long long qd[2] = {a.total_q, a.heads};
   const long long qs[2] = {(long long)a.q_strides[0], (long long)a.q_strides[1]};
   const long long os[2] = {(long long)a.o_strides[0], (long long)a.o_strides[1]};
@@ -148,10 +209,12 @@ int paged_forward(const fa2_paged_params& a, void* workspace, size_t workspace_b
   const long long ld[1] = {a.heads}, ls[1] = {(long long)a.lse_stride};
   if (a.heads > 1 && (ls[0] < a.total_q || ls[0] >= kMaxStride)) return FA2_ERR_INVALID_ARG;
   const Range out[3] = {extent(a.o, qd, os, c.head_dim, 2), extent(a.lse, ld, ls, a.total_q, 4),
-                        range(workspace, s.ws_bytes)};
-  const Range in[6] = {extent(a.q, qd, qs, c.head_dim, 2), kc.bytes, vc.bytes,
+                        range(workspace, need)};
+  const Range in[8] = {extent(a.q, qd, qs, c.head_dim, 2), kc.bytes, vc.bytes,
                        extent(a.block_table, td, ts, a.max_pages, 4),
-                       range(a.cu_seqlens_q, ((size_t)a.batch + 1) * 4), range(a.seqlens_k, (size_t)a.batch * 4)};
+                       range(a.cu_seqlens_q, ((size_t)a.batch + 1) * 4), range(a.seqlens_k, (size_t)a.batch * 4),
+                       range(x ? x->cu_groups : a.seqlens_k, x ? ((size_t)x->num_groups + 1) * 4 : 4),
+                       range(x ? x->shared_lens : a.seqlens_k, x ? (size_t)x->num_groups * 4 : 4)};
   for (int i = 0; i < 3; ++i) {
     for (int j = 0; j < i; ++j)
       if (overlap(out[i], out[j])) return FA2_ERR_INVALID_ARG;
@@ -165,14 +228,6 @@ int paged_forward(const fa2_paged_params& a, void* workspace, size_t workspace_b
   rc = paged_device_status(&p.status);
   if (rc) return rc;
   la.bf16 = c.dtype == FA2_BF16;
-  // q as (d, group, heads_kv, total_q): a box is `group` heads of box_tokens tokens
-  {
-    const long long dims[4] = {c.head_dim, s.group, c.heads, a.total_q};
-    const long long st[3] = {qs[1], qs[1] * s.group, qs[0]};
-    const int box[4] = {64, s.group, 1, s.box_tokens};
-    rc = encode_map_nd(&la.tm_q, a.q, 4, dims, st, box, la.bf16);
-    if (rc) return rc;
-  }
   // k / page_size for 0 <= k < 2^31 without a division: magic = 2^32 (2^shift - page_size) / page_size + 1, 2^shift >=
   // page_size
   while ((1ll << p.page_shift) < c.page_size) ++p.page_shift;
@@ -198,7 +253,6 @@ int paged_forward(const fa2_paged_params& a, void* workspace, size_t workspace_b
   p.group = s.group;
   p.tile_tokens = s.tile_tokens;
   p.total_q = a.total_q;
-  p.max_q = s.max_q;
   p.num_pages = c.num_pages;
   p.page_size = c.page_size;
   p.max_keys = a.max_pages * c.page_size;
@@ -209,22 +263,33 @@ int paged_forward(const fa2_paged_params& a, void* workspace, size_t workspace_b
   const float scale_log2 = a.scale * 1.4426950408889634f;
   p.scale_log2_mag = std::fmax(std::fabs(scale_log2), FLT_MIN);
   p.qk_negate = scale_log2 < 0.f ? 1u << 13 : 0u;   // the negate-A bit of the S product's descriptor
-  p.slot_rows = s.group * s.box_tokens;
-  p.overhead = (kPagedOverhead + 2 * p.slot_rows + 63) / 64 * 64;
-  p.ctas = s.ctas;
-  p.pair_ctas = s.pair_ctas;
   p.cached_keys = (96 << 20) / (4 * c.head_dim);   // 96 of the 126 MB
-  p.min_share = kPagedMinShare > 4 * p.slot_rows ? kPagedMinShare : (4 * p.slot_rows + 63) / 64 * 64;
-  p.ws_o = static_cast<float*>(workspace);
-  p.ws_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + s.ws_o_bytes);
-  p.merges = reinterpret_cast<PagedMerge*>(static_cast<uint8_t*>(workspace) + s.ws_o_bytes + s.ws_ml_bytes);
-  // few rows (every sequence is then one query tile): the line in key tiles and 32 bits
-  la.wide = p.slot_rows > kPagedTileRows / 2 ||
-            (double)a.batch * c.heads * ((p.max_keys + p.overhead) / 64 + 2.0) + 1e6 > 2147483647.0;
-  p.merge_cost = la.wide ? 768 : 256;
+  rc = fill_pass(a, s, static_cast<uint8_t*>(workspace), x != nullptr, la);
+  if (rc) return rc;
   la.band = a.window_left >= 0 || a.prefix_len > 0;
   la.stream = stream;
   int e = 0;
+  if (x) {
+    const long long unit = c.page_size < kPagedKeyTile ? kPagedKeyTile : c.page_size;
+    p.cu_groups = x->cu_groups;
+    p.shared_lens = x->shared_lens;
+    p.groups = x->num_groups;
+    p.seqs = a.batch;
+    p.share_unit = (int)unit;
+    p.own = 1;
+    PagedLaunchArgs ls = la;   // over the groups: every query row sees every shared key
+    ls.p.own = 0;
+    ls.p.batch = x->num_groups;
+    ls.p.window_right = -1;
+    rc = fill_pass(a, shared, static_cast<uint8_t*>(workspace) + s.ws_bytes, true, ls);
+    if (rc) return rc;
+    switch (c.head_dim) {
+      case 64: e = launch_paged_shared_d64(ls, la); break;
+      case 128: e = launch_paged_shared_d128(ls, la); break;
+      default: e = launch_paged_shared_d256(ls, la); break;
+    }
+    return e == 0 ? FA2_OK : FA2_ERR_CUDA;
+  }
   switch (c.head_dim) {
     case 64: e = launch_paged_d64(la); break;
     case 128: e = launch_paged_d128(la); break;
@@ -337,7 +402,22 @@ extern "C" size_t fa2_paged_fwd_workspace_bytes(const fa2_paged_params* params) 
 
 extern "C" int fa2_paged_fwd(const fa2_paged_params* params, void* workspace, size_t workspace_bytes, void* stream) {
   if (!params) return FA2_ERR_INVALID_ARG;
-  return paged_forward(*params, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
+  return paged_forward(*params, nullptr, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" size_t fa2_paged_shared_params_size(void) { return sizeof(fa2_paged_shared_params); }
+
+extern "C" size_t fa2_paged_fwd_shared_workspace_bytes(const fa2_paged_shared_params* params) {
+  if (!params) return 0;
+  PagedShape own, shared;
+  if (shared_shape(*params, own, shared)) return 0;
+  return own.ws_bytes + shared.ws_bytes;
+}
+
+extern "C" int fa2_paged_fwd_shared(const fa2_paged_shared_params* params, void* workspace, size_t workspace_bytes,
+                                    void* stream) {
+  if (!params) return FA2_ERR_INVALID_ARG;
+  return paged_forward(params->fwd, params, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" int fa2_paged_append(const fa2_paged_append_params* params, void* stream) {

@@ -243,7 +243,7 @@ __device__ __forceinline__ void pg8_plan(const Paged8Ctx<C>& t, const PagedFp8Pa
     if (lane == 0) {
       if (!have) f->n = -1;
       mbar_arrive(t.bar(P8_PLAN + (nf & 3)));
-      if (nf == 0 && place.line && place.piece < p.ctas) p.merges[place.piece] = walk.merge;
+      if (nf == 0) walk.tell_merge(p, place);
     }
     __syncwarp();
     if (nf >= 2 && !t.warp_wait(P8_FREE + ((nf - 2) & 3), (nf - 2) >> 2, kSiteProducerEmpty)) return;

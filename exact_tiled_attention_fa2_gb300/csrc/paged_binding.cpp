@@ -270,6 +270,45 @@ PyObject* forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// The same with groups: a: q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, cu_groups, shared_lens.
+fa2_paged_shared_params forward_params_shared(PyObject* const* a, PyObject* max_q) {
+  const at::Tensor &q = *tensor(a[0], "q"), &k = *tensor(a[1], "k_cache");
+  const at::Tensor &groups = *tensor(a[6], "cu_groups"), &shared = *tensor(a[7], "shared_lens");
+  fa2_paged_shared_params p;
+  std::memset(&p, 0, sizeof(p));
+  p.fwd = forward_params(q, k, *tensor(a[2], "v_cache"), *tensor(a[3], "block_table"), *tensor(a[4], "cu_seqlens_q"),
+                         *tensor(a[5], "seqlens_k"), max_q);
+  p.num_groups = size(shared.numel(), "shared_lens");
+  p.shared_lens = int32_1d(shared, "shared_lens", k.device(), p.num_groups);
+  p.cu_groups = int32_1d(groups, "cu_groups", k.device(), (int64_t)p.num_groups + 1);
+  p.fwd.window_left = -1;
+  return p;
+}
+
+// forward_shared(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, cu_groups, shared_lens, o, lse, workspace,
+//                scale, window_right, max_seqlen_q): (o, lse), or a nonzero fa2_status
+PyObject* forward_shared(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!arguments(n, 14, "forward_shared")) return nullptr;
+  return guarded([&]() -> PyObject* {
+    fa2_paged_shared_params p = forward_params_shared(a, a[13]);
+    const at::Tensor& q = *tensor(a[0], "q");
+    p.fwd.scale = scale_of(a[11], p.fwd.cache.head_dim);
+    p.fwd.window_right = integer(a[12], "window_right");
+    const c10::cuda::CUDAGuard guard(q.device());
+    return outputs(p.fwd, q, a + 8, a[10] == Py_None ? fa2_paged_fwd_shared_workspace_bytes(&p) : 0,
+                   [&](void* ws, size_t bytes, void* stream) { return fa2_paged_fwd_shared(&p, ws, bytes, stream); });
+  });
+}
+
+// workspace_bytes_shared(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, cu_groups, shared_lens, max_seqlen_q)
+PyObject* workspace_bytes_shared(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!arguments(n, 9, "workspace_bytes_shared")) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const fa2_paged_shared_params p = forward_params_shared(a, a[8]);
+    return PyLong_FromSize_t(fa2_paged_fwd_shared_workspace_bytes(&p));
+  });
+}
+
 // forward_fp8(q, k_cache, v_cache, k_exps, v_exps, block_table, cu_seqlens_q, seqlens_k, o, lse, workspace, scale,
 //             window_left, window_right, prefix_len, max_seqlen_q, sink_len): (o, lse), or a nonzero fa2_status
 PyObject* forward_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -469,6 +508,8 @@ PyMethodDef methods[] = {
     {"forward", (PyCFunction)(void (*)(void))forward, METH_FASTCALL, nullptr},
     {"workspace_bytes", (PyCFunction)(void (*)(void))workspace_bytes, METH_FASTCALL, nullptr},
     {"append", (PyCFunction)(void (*)(void))append, METH_FASTCALL, nullptr},
+    {"forward_shared", (PyCFunction)(void (*)(void))forward_shared, METH_FASTCALL, nullptr},
+    {"workspace_bytes_shared", (PyCFunction)(void (*)(void))workspace_bytes_shared, METH_FASTCALL, nullptr},
     {"forward_fp8", (PyCFunction)(void (*)(void))forward_fp8, METH_FASTCALL, nullptr},
     {"workspace_bytes_fp8", (PyCFunction)(void (*)(void))workspace_bytes_fp8, METH_FASTCALL, nullptr},
     {"append_fp8", (PyCFunction)(void (*)(void))append_fp8, METH_FASTCALL, nullptr},

@@ -651,6 +651,46 @@ int fa2_paged_fwd_fp8(const fa2_paged_fp8_params* params, void* workspace, size_
 size_t fa2_paged_fp8_params_size(void);
 
 /*
+ * fa2_paged_fwd_shared -- fa2_paged_fwd (full or causal attention) for a batch
+ * whose sequences share the first pages of their prompts.  Group g is sequences
+ * cu_groups[g] <= b < cu_groups[g+1]; the first shared_lens[g] keys of all of
+ * them are the same, held by the same pages: their block-table rows begin
+ * with the same shared_lens[g] / page_size entries, which are read from the row
+ * of the group's first sequence (also if that one is idle).  These keys lie
+ * before every sequence's new tokens: shared_lens[g] <= seqlens_k[b] - (query
+ * tokens of b).  The shared keys are read and attended once, for all query rows
+ * of the group, the others sequence by sequence; every row's O and LSE are those
+ * of fa2_paged_fwd on the same tensors, up to the order of its sums.  Whole
+ * pages (and whole tiles of 64 keys) of a shared length count, the rest is
+ * attended by each sequence for itself.  Groups of one sequence, groups that do
+ * not lie within the batch and sequences in no group share nothing.
+ *
+ * `fwd` as for fa2_paged_fwd, with window_left = -1 and prefix_len = 0
+ * (FA2_ERR_UNSUPPORTED otherwise).  cu_groups and shared_lens live on the device
+ * and are checked by the kernels: a sequence of a group whose shared length is
+ * out of range or reaches into the sequence's new tokens, or whose query rows
+ * do not lie between those of the group's first and last, is left unwritten and
+ * reported as FA2_ERR_DEVICE_SEQLENS.  Three kernels, asynchronous on `stream`;
+ * the host reads no length.  Deterministic.  The workspace holds the fp32 state
+ * of every query row of both passes, about 16 bytes per element of q while
+ * decoding; overlaps, captures and errors as fa2_paged_fwd.
+ */
+typedef struct fa2_paged_shared_params {
+  fa2_paged_params fwd;
+  const int* cu_groups;    /* device, [num_groups + 1] int32 */
+  const int* shared_lens;  /* device, [num_groups] int32 */
+  int num_groups;          /* 1 .. fwd.batch */
+} fa2_paged_shared_params;
+
+/* sizeof of fa2_paged_shared_params as compiled into the library (binding check). */
+size_t fa2_paged_shared_params_size(void);
+
+/* Workspace fa2_paged_fwd_shared needs for these sizes (0 if they are invalid). */
+size_t fa2_paged_fwd_shared_workspace_bytes(const fa2_paged_shared_params* params);
+
+int fa2_paged_fwd_shared(const fa2_paged_shared_params* params, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * fa2_selftest_wait_timeout -- exercises the kernels' failure path without a
  * GPU fault: launches one CTA whose single wait, made through the same
  * bounded-wait routine every forward-kernel wait uses, is on an mbarrier that
