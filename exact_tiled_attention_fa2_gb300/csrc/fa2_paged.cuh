@@ -181,11 +181,13 @@ template <bool WIDE>
 struct LineOf {
   using T = long long;
   static constexpr int KEYS = 1;   // of a unit
+  static constexpr long long MOST = LLONG_MAX;
 };
 template <>
 struct LineOf<false> {
   using T = int;
   static constexpr int KEYS = kPagedKeyTile;
+  static constexpr int MOST = INT_MAX;
 };
 
 // a / b for 0 <= a, 0 < b: a 32-bit division where both fit.
@@ -271,9 +273,26 @@ __device__ __forceinline__ int group_keys(const PagedParams& p, int first, int e
   return end - first < 2 ? 0 : shared / p.share_unit * p.share_unit;
 }
 
-// The group that holds sequence i (-1: none), its first sequence and the one
-// after its last.
-__device__ __forceinline__ int group_of(const PagedParams& p, int i, int& first, int& end) {
+// What the schedule needs of sequence i: query rows [a, b), keys, block-table row.
+struct SeqRead {
+  int a, b, k;        // k < 0: out of range
+  const int* table;
+};
+
+// Sequence i of a batch with shared prefixes: its rows, the keys behind its
+// group's shared ones, and how many these are (0: it is in no group that shares
+// any); its group and the row of that group's first query.
+struct OwnRead {
+  SeqRead s;
+  int keys, group, group_row;
+};
+
+__device__ __forceinline__ OwnRead own_read(const PagedParams& p, int i) {
+  OwnRead x;
+  x.s.a = p.cu_q[i];
+  x.s.b = p.cu_q[i + 1];
+  x.s.k = p.lens_k[i];
+  x.s.table = p.table + (long long)i * p.table_stride;
   int lo = 0, hi = p.groups;   // the last group that starts at i or before
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -282,49 +301,41 @@ __device__ __forceinline__ int group_of(const PagedParams& p, int i, int& first,
     else
       hi = mid;
   }
-  first = p.cu_groups[lo];
-  end = p.cu_groups[lo + 1];
-  return first >= 0 && first <= i && i < end && end <= p.seqs ? lo : -1;
+  const int first = p.cu_groups[lo], end = p.cu_groups[lo + 1], shared = p.shared_lens[lo];
+  x.group = lo;
+  x.keys = x.group_row = 0;
+  if (first >= 0 && first <= i && i < end && end <= p.seqs && x.s.b > x.s.a) {
+    x.keys = group_keys(p, first, end, shared);
+    if (x.keys != 0) {
+      x.group_row = p.cu_q[first];
+      const bool fits = x.keys > 0 && x.s.k <= p.max_keys && (long long)x.s.k - x.keys >= (long long)x.s.b - x.s.a &&
+                        0 <= x.group_row && x.group_row <= x.s.a && x.s.b <= p.cu_q[end] && p.cu_q[end] <= p.total_q;
+      x.s.k = fits ? x.s.k - x.keys : -1;
+      if (fits) x.s.table += x.keys / p.page_size;
+    }
+  }
+  return x;
 }
 
-// What the schedule needs of sequence i: query rows [a, b), keys, block-table row.
-struct SeqRead {
-  int a, b, k;        // k < 0: out of range
-  const int* table;
-};
-
-template <bool SHARED>
+// PASS 0: a batch by itself; of a batch with shared prefixes (fa2_paged_shared.cuh)
+// 1: the groups, each one sequence of all its query rows and the shared keys, 2:
+// the sequences, each an ordinary one whose table row starts behind those keys.
+template <int PASS>
 __device__ __forceinline__ SeqRead seq_read(const PagedParams& p, int i) {
   SeqRead x;
-  if constexpr (!SHARED) {
+  if constexpr (PASS == 0) {
     x.a = p.cu_q[i];
     x.b = p.cu_q[i + 1];
     x.k = p.lens_k[i];
     x.table = p.table + (long long)i * p.table_stride;
-  } else if (p.own) {
-    // the keys behind the group's shared ones: an ordinary sequence whose table row starts later
-    x.a = p.cu_q[i];
-    x.b = p.cu_q[i + 1];
-    x.k = p.lens_k[i];
-    x.table = p.table + (long long)i * p.table_stride;
-    int first, end;
-    const int g = group_of(p, i, first, end);
-    if (g >= 0 && x.b > x.a) {
-      const int keys = group_keys(p, first, end, p.shared_lens[g]);
-      if (keys != 0) {
-        const bool fits = keys > 0 && x.k <= p.max_keys && (long long)x.k - keys >= (long long)x.b - x.a &&
-                          0 <= p.cu_q[first] && p.cu_q[first] <= x.a && x.b <= p.cu_q[end] && p.cu_q[end] <= p.total_q;
-        x.k = fits ? x.k - keys : -1;
-        if (fits) x.table += keys / p.page_size;
-      }
-    }
+  } else if constexpr (PASS == 2) {
+    x = own_read(p, i).s;
   } else {
-    // group i as one sequence: the query rows of all its sequences, the shared keys
-    const int first = p.cu_groups[i], end = p.cu_groups[i + 1];
+    const int first = p.cu_groups[i], end = p.cu_groups[i + 1], shared = p.shared_lens[i];
     x.a = x.b = x.k = 0;
     x.table = p.table;
     if (0 <= first && first < end && end <= p.seqs) {
-      const int keys = group_keys(p, first, end, p.shared_lens[i]);
+      const int keys = group_keys(p, first, end, shared);
       if (keys > 0) {   // (out of range: each of the sequences is reported)
         x.a = p.cu_q[first];
         x.b = p.cu_q[end];
@@ -336,9 +347,9 @@ __device__ __forceinline__ SeqRead seq_read(const PagedParams& p, int i) {
   return x;
 }
 
-template <bool WIDE, bool SHARED>
+template <bool WIDE, int PASS>
 static __device__ __noinline__ PagedSeq read_seq(const PagedParams& p, int i, bool report) {
-  const SeqRead x = seq_read<SHARED>(p, i);
+  const SeqRead x = seq_read<PASS>(p, i);
   return paged_seq<WIDE>(p, x.a, x.b, x.k, report);
 }
 
@@ -352,6 +363,7 @@ struct PagedPlace {
   int seq;           // its index, or -1: nothing to do
   int piece;         // of the line
   int rank;          // one pair: its index in its sequence
+  int tile;          // (PASS 1) the query tile that the piece is of, `at` where its stretch starts; -1: as it falls
   bool line;         // the line is cut at this CTA's piece, or ends before it (one pair: false)
 };
 
@@ -376,29 +388,29 @@ struct PagedScan {
 // `spans`: the line's length were all on it; `chunk_keys`: keys of the
 // sequences of several query tiles, all K/V heads.
 template <bool WIDE>
-__device__ __forceinline__ int whole_pairs(const PagedParams& p, typename LineOf<WIDE>::T spans,
+__device__ __forceinline__ int whole_pairs(const PagedParams& p, int ctas, typename LineOf<WIDE>::T spans,
                                            typename LineOf<WIDE>::T chunk_keys, typename LineOf<WIDE>::T pairs,
                                            int longest) {
   using Line = typename LineOf<WIDE>::T;
-  const Line cost = p.merge_cost / LineOf<WIDE>::KEYS, mean_load = line_div(spans, (Line)p.ctas);
+  const Line cost = p.merge_cost / LineOf<WIDE>::KEYS, mean_load = line_div(spans, (Line)ctas);
   if (pairs == 0) return 0;
   if (longest > max(mean_load, (Line)(p.min_share / LineOf<WIDE>::KEYS)) + cost) {
     // one of the pairs alone outlasts an even share
-  } else if (pairs <= p.ctas) {
+  } else if (pairs <= ctas) {
     return (int)pairs;
   } else if (WIDE && pairs <= p.pair_ctas) {
     // The last wave's `rest` pairs, taking the spans to fall evenly from the
     // longest to the shortest: they end `w` after the full waves, in place of
     // their spans' even share
-    const float P = (float)pairs, S = (float)p.ctas, mean = (float)spans / P;
+    const float P = (float)pairs, S = (float)ctas, mean = (float)spans / P;
     const float low = fmaxf(2.f * mean - (float)longest, 0.f);
-    const int full = (int)(pairs / p.ctas) * p.ctas;
+    const int full = (int)(pairs / ctas) * ctas;
     const float w = (float)longest - ((float)longest - low) * ((float)full / P);
     if (full == pairs || w - 0.5f * (w + low) * ((float)(pairs - full) / S) <= (float)cost) return (int)pairs;
   }
-  if (WIDE && pairs >= p.ctas && pairs <= p.pair_ctas && 2 * (Line)longest * pairs <= 3 * spans &&
+  if (WIDE && pairs >= ctas && pairs <= p.pair_ctas && 2 * (Line)longest * pairs <= 3 * spans &&
       chunk_keys > p.cached_keys)
-    return (int)(pairs / p.ctas) * p.ctas;
+    return (int)(pairs / ctas) * ctas;
   return 0;
 }
 
@@ -418,7 +430,6 @@ __device__ __forceinline__ void place_piece(PagedPlace<WIDE>& r, int block, int 
 
 // Finds what CTA `block` works on, query tiles of few rows and at most 32
 // sequences: one a lane of the calling warp.
-template <bool SHARED = false>
 __device__ __forceinline__ PagedPlace<false> find_place_small(const PagedParams& p, int block, bool report) {
   constexpr int KEYS = LineOf<false>::KEYS;
   const int lane = (int)threadIdx.x & 31;
@@ -426,7 +437,7 @@ __device__ __forceinline__ PagedPlace<false> find_place_small(const PagedParams&
   PagedSeq s;
   s.tiles = s.keys = s.n_q = s.n_k = s.row0 = 0;
   if (lane < p.batch) {
-    const SeqRead x = seq_read<SHARED>(p, lane);
+    const SeqRead x = seq_read<0>(p, lane);
     s = paged_seq<false>(p, x.a, x.b, x.k, report);
     span = s.span<false>(p, s.tiles);
     pairs = s.tiles * p.heads_kv;
@@ -443,7 +454,7 @@ __device__ __forceinline__ PagedPlace<false> find_place_small(const PagedParams&
     }
   }
   const int total = __shfl_sync(0xffffffffu, a, 31), all_pairs = __shfl_sync(0xffffffffu, b, 31);
-  const int whole = whole_pairs<false>(p, total, 0, all_pairs, longest);   // all or none
+  const int whole = whole_pairs<false>(p, p.ctas, total, 0, all_pairs, longest);   // all or none
   const int rest = whole == all_pairs ? 0 : total;
   const int share = max(line_div(rest + p.ctas - 1, p.ctas), p.min_share / KEYS);
   const bool one = block < whole;
@@ -464,48 +475,64 @@ __device__ __forceinline__ PagedPlace<false> find_place_small(const PagedParams&
   return r;
 }
 
-// The same of any number of sequences: every thread sums a run of them; every
-// thread returns the same.
-template <int THREADS, bool WIDE, bool SHARED = false>
-__device__ __forceinline__ PagedPlace<WIDE> find_place(const PagedParams& p, int block, PagedScan<WIDE>* sh,
-                                                       bool report) {
+// The same of any number of sequences, in two steps: every thread sums a run of
+// them, and the run that holds CTA `block`'s start, of the `ctas` that share the
+// line, finds it; every thread returns the same.  (tid: among the threads that do
+// this together; other threads of the CTA may do it for another block, and those
+// from THREADS on have no run: `beside` is theirs, before the barrier.)
+template <bool WIDE>
+struct LineScan {
+  typename LineOf<WIDE>::T a, b, span, pairs;   // this thread's run: starts, lengths
+  typename LineOf<WIDE>::T total, all_pairs, all_chunks;
+  int longest, i0, i1, per;
+  PagedSeq s;   // the run's last sequence
+};
+
+template <int THREADS, bool WIDE, int PASS, class Beside>
+__device__ __forceinline__ LineScan<WIDE> line_scan(const PagedParams& p, int tid, PagedScan<WIDE>* sh, bool report,
+                                                    Beside&& beside) {
   using Line = typename LineOf<WIDE>::T;
-  constexpr int KEYS = LineOf<WIDE>::KEYS;
   constexpr int NW = THREADS / 32;
-  const int tid = (int)threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int lane = tid & 31, w = tid >> 5;
   const int per = (p.batch + THREADS - 1) / THREADS;
   const int i0 = min(tid * per, p.batch), i1 = min(i0 + per, p.batch);
   // chunks: keys of the sequences of several query tiles, all K/V heads
-  Line span = 0, pairs = 0, chunks = 0;
+  Line span = 0, pairs = 0, chunks = 0, a = 0, b = 0;
   int longest = 0;   // pair
   PagedSeq s;
   s.tiles = s.keys = s.n_q = s.n_k = s.row0 = 0;
+  if (tid >= THREADS) {
+    beside();
+  } else {
 #pragma unroll 1
-  for (int i = i0; i < i1; ++i) {
-    s = read_seq<WIDE, SHARED>(p, i, report);
-    const Line x = s.span<WIDE>(p, s.tiles);
-    span += x;
-    pairs += (Line)s.tiles * p.heads_kv;
-    if (s.tiles > 0) longest = max(longest, s.width<WIDE>(p, s.tiles - 1));
-    if (WIDE && s.tiles > 1) chunks += (Line)s.n_k * p.heads_kv;
-  }
-  longest = __reduce_max_sync(0xffffffffu, longest);
-  Line a = span, b = pairs, c = chunks;
-#pragma unroll 1
-  for (int o = 1; o < 32; o <<= 1) {
-    const Line va = __shfl_up_sync(0xffffffffu, a, o), vb = __shfl_up_sync(0xffffffffu, b, o);
-    const Line vc = WIDE ? __shfl_up_sync(0xffffffffu, c, o) : 0;
-    if (lane >= o) {
-      a += va;
-      b += vb;
-      c += vc;
+    for (int i = i0; i < i1; ++i) {
+      s = read_seq<WIDE, PASS>(p, i, report);
+      const Line x = s.span<WIDE>(p, s.tiles);
+      span += x;
+      pairs += (Line)s.tiles * p.heads_kv;
+      if (s.tiles > 0) longest = max(longest, s.width<WIDE>(p, s.tiles - 1));
+      if (WIDE && s.tiles > 1) chunks += (Line)s.n_k * p.heads_kv;
     }
-  }
-  if (lane == 31) {
-    sh->warp_sum[0][w] = a;
-    sh->warp_sum[1][w] = b;
-    sh->warp_sum[2][w] = c;
-    sh->warp_longest[w] = longest;
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    a = span;
+    b = pairs;
+    Line c = chunks;
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {
+      const Line va = __shfl_up_sync(0xffffffffu, a, o), vb = __shfl_up_sync(0xffffffffu, b, o);
+      const Line vc = WIDE ? __shfl_up_sync(0xffffffffu, c, o) : 0;
+      if (lane >= o) {
+        a += va;
+        b += vb;
+        c += vc;
+      }
+    }
+    if (lane == 31) {
+      sh->warp_sum[0][w] = a;
+      sh->warp_sum[1][w] = b;
+      sh->warp_sum[2][w] = c;
+      sh->warp_longest[w] = longest;
+    }
   }
   if (tid == 0) sh->place.seq = -1;
   __syncthreads();
@@ -523,7 +550,18 @@ __device__ __forceinline__ PagedPlace<WIDE> find_place(const PagedParams& p, int
     all_chunks += sh->warp_sum[2][j];
     longest = max(longest, sh->warp_longest[j]);
   }
-  int whole = whole_pairs<WIDE>(p, total, all_chunks, all_pairs, longest);
+  return LineScan<WIDE>{a, b, span, pairs, total, all_pairs, all_chunks, longest, i0, i1, per, s};
+}
+
+template <bool WIDE, int PASS>
+__device__ __forceinline__ PagedPlace<WIDE> line_place(const PagedParams& p, const LineScan<WIDE>& scan, int block, int ctas,
+                                                       PagedScan<WIDE>* sh) {
+  using Line = typename LineOf<WIDE>::T;
+  constexpr int KEYS = LineOf<WIDE>::KEYS;
+  const Line a = scan.a, b = scan.b, span = scan.span, pairs = scan.pairs, total = scan.total, all_pairs = scan.all_pairs;
+  const int i0 = scan.i0, i1 = scan.i1, per = scan.per;
+  PagedSeq s = scan.s;
+  int whole = whole_pairs<WIDE>(p, ctas, total, scan.all_chunks, all_pairs, scan.longest);
   int cut_seq = -1, cut_tiles = 0;
   Line shift = 0;
   if (WIDE && whole > 0 && whole < all_pairs) {   // part of the pairs: cut at a query tile's first head
@@ -531,7 +569,7 @@ __device__ __forceinline__ PagedPlace<WIDE> find_place(const PagedParams& p, int
       Line x = a, n = b;
 #pragma unroll 1
       for (int i = i0; i < i1; ++i) {
-        if (per > 1) s = read_seq<WIDE, SHARED>(p, i, false);
+        if (per > 1) s = read_seq<WIDE, PASS>(p, i, false);
         const Line sx = s.span<WIDE>(p, s.tiles), sn = (Line)s.tiles * p.heads_kv;
         if (whole < n + sn) {
           const int tiles = (int)(whole - n) / p.heads_kv;   // from the last
@@ -552,7 +590,7 @@ __device__ __forceinline__ PagedPlace<WIDE> find_place(const PagedParams& p, int
     shift = sh->shift;
   }
   const Line rest = whole == all_pairs ? 0 : total - shift;   // the line's length
-  Line share = line_div(rest + p.ctas - 1, (Line)p.ctas);
+  Line share = line_div(rest + ctas - 1, (Line)ctas);
   if (share < p.min_share / KEYS) share = p.min_share / KEYS;
   const bool one = block < whole;
   const Line pos = one ? block : (block - whole) * share;
@@ -561,7 +599,7 @@ __device__ __forceinline__ PagedPlace<WIDE> find_place(const PagedParams& p, int
     Line x = mine;
 #pragma unroll 1
     for (int i = i0; i < i1; ++i) {
-      if (per > 1) s = read_seq<WIDE, SHARED>(p, i, false);
+      if (per > 1) s = read_seq<WIDE, PASS>(p, i, false);
       const Line step = one ? (Line)s.tiles * p.heads_kv : s.span<WIDE>(p, s.tiles);
       if (pos < x + step) {
         if (WIDE && !one && i == cut_seq) {   // ends where it did, and starts the line
@@ -581,6 +619,12 @@ __device__ __forceinline__ PagedPlace<WIDE> find_place(const PagedParams& p, int
   PagedPlace<WIDE> r = sh->place;
   place_piece<WIDE>(r, block, whole, all_pairs, share, rest);
   return r;
+}
+
+template <int THREADS, bool WIDE>
+__device__ __forceinline__ PagedPlace<WIDE> find_place(const PagedParams& p, int block, PagedScan<WIDE>* sh, bool report) {
+  const LineScan<WIDE> scan = line_scan<THREADS, WIDE, 0>(p, (int)threadIdx.x, sh, report, [] {});
+  return line_place<WIDE, 0>(p, scan, block, p.ctas, sh);
 }
 
 // The pair of sequence s that holds offset y of the sequence's span: query
@@ -633,7 +677,7 @@ static_assert(sizeof(PagedMerge) == kPagedMergeBytes, "merge description");
 // Walks the fragments of one CTA's piece; every lane of the TMA warp in step.
 // What the pairs of one query tile share is worked out once, and the next
 // sequence's lengths are read a sequence ahead.
-template <bool BAND, bool WIDE, bool SHARED = false>
+template <bool BAND, bool WIDE, int PASS = 0>
 struct FragWalk {
   using Line = typename LineOf<WIDE>::T;
   PagedSeq s;
@@ -644,22 +688,22 @@ struct FragWalk {
   Line x, begin, end;   // the pair's start on the line; the piece
   int cta, seq, tile, h;
   int next_a, next_b, next_k;   // sequence seq + 1
-  const int* next_table;        // (SHARED)
-  int merge_id;                 // (SHARED) the pair of `merge`
+  const int* next_table;        // (PASS > 0)
+  int merge_id;                 // (PASS > 0) the pair of `merge`
   bool more, one;     // one: a single pair, whole
   PagedMerge merge;   // the pair cut by the piece's start
 
   __device__ __forceinline__ void read_ahead(const PagedParams& p) {
     if (seq + 1 < p.batch) {
-      const SeqRead x = seq_read<SHARED>(p, seq + 1);
+      const SeqRead x = seq_read<PASS>(p, seq + 1);
       next_a = x.a;
       next_b = x.b;
       next_k = x.k;
-      if constexpr (SHARED) next_table = x.table;
+      if constexpr (PASS != 0) next_table = x.table;
     }
   }
 
-  // (SHARED) The current pair's place among the pairs: query tiles counted by
+  // (PASS > 0) The current pair's place among the pairs: query tiles counted by
   // their first rows, one more for each sequence before, so that none coincide.
   __device__ __forceinline__ int pair_id(const PagedParams& p) const {
     return (s.row0 / p.tile_tokens + seq + tile) * p.heads_kv + h;
@@ -695,13 +739,18 @@ struct FragWalk {
     more = true;
     one = pl.share == 0;
     merge.count = -1;
-    table = SHARED ? seq_read<SHARED>(p, seq).table : p.table + (long long)seq * p.table_stride;
+    table = PASS != 0 ? seq_read<PASS>(p, seq).table : p.table + (long long)seq * p.table_stride;
     begin = piece * pl.share;   // one: 0
     end = min(begin + pl.share, pl.total);
     if (one) {   // the query tiles from the last (the most keys) to the first
       h = pl.rank % p.heads_kv;
       tile = s.tiles - 1 - pl.rank / p.heads_kv;
       x = 0;
+    } else if (PASS == 1 && pl.tile >= 0) {   // a query tile's own stretch of the line
+      tile = pl.tile;
+      const int each = s.template width<WIDE>(p, tile);
+      h = (int)line_div(begin - pl.at, (Line)each);
+      x = pl.at + (Line)h * each;
     } else {
       x = pl.at + pair_at<WIDE>(p, s, begin - pl.at, tile, h);
       read_ahead(p);
@@ -721,13 +770,13 @@ struct FragWalk {
       merge.row = base.row;
       merge.rows = base.rows;
       merge.h = h;
-      if constexpr (SHARED) merge_id = pair_id(p);
+      if constexpr (PASS != 0) merge_id = pair_id(p);
     }
   }
 
   // Leaves word of the pair cut by the piece's start for the merge.
   __device__ __forceinline__ void tell_merge(const PagedParams& p, const PagedPlace<WIDE>& pl) const {
-    if constexpr (SHARED) {
+    if constexpr (PASS != 0) {
       if (merge.count >= 0) p.pairs[merge_id] = PagedPair{merge.count, merge.c0, merge.from_start, 0};
     } else if (pl.line && pl.piece < p.ctas) {
       p.merges[pl.piece] = merge;
@@ -736,8 +785,8 @@ struct FragWalk {
 };
 
 // The next fragment, to shared memory; false when the piece is done.
-template <bool BAND, bool WIDE, bool SHARED>
-__device__ __forceinline__ bool next_fragment(FragWalk<BAND, WIDE, SHARED>& k, const PagedParams& p, PagedFrag* dst, int lane) {
+template <bool BAND, bool WIDE, int PASS>
+__device__ __forceinline__ bool next_fragment(FragWalk<BAND, WIDE, PASS>& k, const PagedParams& p, PagedFrag* dst, int lane) {
   while (k.more) {
     const bool from_start = k.begin <= k.x, to_end = k.end - k.x >= k.w, whole = from_start && to_end;
     const int j0 = from_start ? 0 : span_tile(p, k.begin - k.x, k.tiles_n);
@@ -750,7 +799,7 @@ __device__ __forceinline__ bool next_fragment(FragWalk<BAND, WIDE, SHARED>& k, c
       dst->j0 = j0;
       dst->n = n;
       dst->slot = whole ? -1 : 2 * k.cta + (from_start ? 1 : 0);
-      if (SHARED && whole) {   // a partial all the same: the merge joins it with the other pass's
+      if (PASS != 0 && whole) {   // a partial all the same: the merge joins both passes'
         const int id = k.pair_id(p);
         dst->slot = 2 * p.ctas + id;
         p.pairs[id] = PagedPair{-1, 0, 0, 0};
@@ -770,7 +819,7 @@ __device__ __forceinline__ bool next_fragment(FragWalk<BAND, WIDE, SHARED>& k, c
             k.more = false;
             break;
           }
-          if constexpr (SHARED)
+          if constexpr (PASS != 0)
             k.table = k.next_table;
           else
             k.table += p.table_stride;
@@ -790,8 +839,8 @@ __device__ __forceinline__ bool next_fragment(FragWalk<BAND, WIDE, SHARED>& k, c
 
 // The same out of line, for the TMA warp between its loads (inlined there, a
 // prompt chunk of 2048 over 16384 keys takes 449 us in place of 428).
-template <bool BAND, bool WIDE, bool SHARED>
-static __device__ __noinline__ bool next_fragment_far(FragWalk<BAND, WIDE, SHARED>& k, const PagedParams& p, PagedFrag* dst,
+template <bool BAND, bool WIDE, int PASS>
+static __device__ __noinline__ bool next_fragment_far(FragWalk<BAND, WIDE, PASS>& k, const PagedParams& p, PagedFrag* dst,
                                                       int lane) {
   return next_fragment(k, p, dst, lane);
 }
@@ -872,9 +921,9 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map
 
 // The planner warp (few rows): walks the piece's fragments, up to four ahead of
 // the softmax.
-template <class C, bool BAND, bool SHARED>
+template <class C, bool BAND, int PASS>
 __device__ __forceinline__ void pg_plan(const PagedCtx<C>& t, const PagedParams& p, const PagedPlace<C::WIDE>& place, int lane) {
-  FragWalk<BAND, C::WIDE, SHARED> walk;
+  FragWalk<BAND, C::WIDE, PASS> walk;
   walk.start(p, place);
   bool have = true;
 #pragma unroll 1
@@ -898,11 +947,11 @@ __device__ __forceinline__ void pg_plan(const PagedCtx<C>& t, const PagedParams&
 // while this one is loaded): with two stages, the time from a free stage to its
 // next load is part of the tile loop's period, and between the two stand only a
 // wait and the issue.
-template <class C, bool BAND, bool SHARED>
+template <class C, bool BAND, int PASS>
 __device__ __forceinline__ void pg_load(const PagedCtx<C>& t, const PagedParams& p, const CUtensorMap* tm_q,
                                         const CUtensorMap* tm_k, const CUtensorMap* tm_v, const PagedPlace<C::WIDE>& place,
                                         int lane) {
-  FragWalk<BAND, C::WIDE, SHARED> walk;
+  FragWalk<BAND, C::WIDE, PASS> walk;
   if constexpr (!C::PLANNER) {
     walk.start(p, place);
     if (lane == 0) walk.tell_merge(p, place);
@@ -1410,7 +1459,7 @@ __device__ __forceinline__ void pg_softmax(const PagedCtx<C>& t, const PagedPara
 // keys 11.1 us, 11.8 with the general search; 8 x 5 drafted tokens 16.8, 17.8.
 // Its own kernel, since the code of both in one costs batches of hundreds: 500
 // requests of 1..300 keys 105 us, 115).
-template <int D, bool BF16, bool BAND, bool WIDE, bool SMALL, bool SHARED>
+template <int D, bool BF16, bool BAND, bool WIDE, bool SMALL>
 __global__ void __launch_bounds__(PagedConfig<D, WIDE>::THREADS, PagedConfig<D, WIDE>::CTAS_PER_SM)
     fa2_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PagedParams p) {
@@ -1425,9 +1474,7 @@ __global__ void __launch_bounds__(PagedConfig<D, WIDE>::THREADS, PagedConfig<D, 
   static_assert(sizeof(PagedScan<WIDE>) <= 320 && C::OFF_SCAN % 8 == 0, "scan area");
   const int warp = (int)(threadIdx.x >> 5);
   const int lane = (int)(threadIdx.x & 31);
-  // The merge may be scheduled once every CTA has started; it waits for the
-  // partials.  (The pass over shared keys lets the other pass in further down.)
-  if (!SHARED || p.own) grid_launch_dependents();
+  grid_launch_dependents();   // the merge may be scheduled once every CTA has started; it waits for the partials
 
   PagedCtx<C> t;
   t.bar0 = sbase + C::OFF_BAR;
@@ -1450,12 +1497,8 @@ __global__ void __launch_bounds__(PagedConfig<D, WIDE>::THREADS, PagedConfig<D, 
   }
   // What precedes this kernel is complete: from here on it touches memory, and
   // takes tensor memory (held while waiting, it could be what a kernel before
-  // this one waits for).  The pass over the sequences' own keys needs nothing of
-  // the one over shared keys, only what preceded that: it is let in behind that
-  // pass's wait, and waits for its end at its own, so that the merge, which waits
-  // for this kernel, has both.
-  if (!SHARED || !p.own) grid_dependency_wait();
-  if (SHARED && !p.own) grid_launch_dependents();
+  // this one waits for).
+  grid_dependency_wait();
   // Tensor memory before the schedule: an SM's second CTA starts only when the
   // first has let go of the allocation permit (measured: 3.6 us into the kernel
   // with the allocation behind the schedule, half of the CTAs).
@@ -1467,26 +1510,26 @@ __global__ void __launch_bounds__(PagedConfig<D, WIDE>::THREADS, PagedConfig<D, 
   PagedPlace<WIDE> place;
   if constexpr (SMALL) {
     if (warp == C::PLAN_WARP) {
-      place = find_place_small<SHARED>(p, (int)blockIdx.x, blockIdx.x == 0);
+      place = find_place_small(p, (int)blockIdx.x, blockIdx.x == 0);
       if (lane == 0) scan->place = place;
     }
     __syncthreads();
     place = scan->place;
   } else {
-    place = find_place<C::THREADS, WIDE, SHARED>(p, (int)blockIdx.x, scan, blockIdx.x == 0);   // with its barriers
+    place = find_place<C::THREADS, WIDE>(p, (int)blockIdx.x, scan, blockIdx.x == 0);   // with its barriers
   }
   tc_fence_after();
   t.tmem = *tmem_slot;
 
   if (place.seq < 0) {   // nothing for this CTA
-    if (!SHARED && threadIdx.x == 0 && place.line && place.piece < p.ctas) p.merges[place.piece].count = -1;
+    if (threadIdx.x == 0 && place.line && place.piece < p.ctas) p.merges[place.piece].count = -1;
   } else if (warp == C::TMA_WARP) {
-    pg_load<C, BAND, SHARED>(t, p, &tm_q, &tm_k, &tm_v, place, lane);
+    pg_load<C, BAND, 0>(t, p, &tm_q, &tm_k, &tm_v, place, lane);
   } else if (warp == C::MMA_WARP) {
     if (lane == 0) pg_mma<C, BF16>(t, p);
     __syncwarp();
   } else if (C::PLANNER && warp == C::PLAN_WARP) {
-    pg_plan<C, BAND, SHARED>(t, p, place, lane);
+    pg_plan<C, BAND, 0>(t, p, place, lane);
   } else {
     pg_softmax<C, BF16, BAND>(t, p, warp, lane);
   }
@@ -1496,7 +1539,6 @@ __global__ void __launch_bounds__(PagedConfig<D, WIDE>::THREADS, PagedConfig<D, 
     tc_fence_after();
     tmem_dealloc(t.tmem, C::TMEM_COLS);
   }
-  if (SHARED && p.own) grid_dependency_wait();
 }
 
 // ---------------------------------------------------------------- the merge
@@ -1609,32 +1651,23 @@ int launch_paged_merge(const PagedParams& p, cudaStream_t stream) {
   return launch_dependent(fa2_paged_merge_kernel<D, BF16>, blocks, kPagedMergeThreads, 0, stream, p);
 }
 
-// The attention kernel by itself.
-template <int D, bool BF16, bool BAND, bool WIDE, bool SMALL, bool SHARED>
-int launch_paged_kernel(const PagedLaunchArgs& a) {
+template <int D, bool BF16, bool BAND, bool WIDE, bool SMALL>
+int launch_paged_kernels(const PagedLaunchArgs& a) {
   using C = PagedConfig<D, WIDE>;
-  auto kern = fa2_paged_kernel<D, BF16, BAND, WIDE, SMALL, SHARED>;
+  auto kern = fa2_paged_kernel<D, BF16, BAND, WIDE, SMALL>;
   static std::atomic<unsigned long long> configured{0};
   const int e = once_per_device(configured, [&]() -> int {
     const cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM_BYTES);
     if (r != cudaSuccess) return (int)r;
-    return (int)cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+    cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+    return (int)cudaFuncSetAttribute(fa2_paged_merge_kernel<D, BF16>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
   });
   if (e != 0) return e;
   // whole waves (few rows: all of the batch is on the line, or at most `ctas` pairs)
   const int waves = WIDE ? (a.p.pair_ctas + a.p.ctas - 1) / a.p.ctas : 1;
   const int grid = a.p.ctas * (waves > 1 ? waves : 1);
-  return launch_dependent(kern, dim3((unsigned)grid), C::THREADS, C::SMEM_BYTES, a.stream, a.tm_q, a.tm_k, a.tm_v, a.p);
-}
-
-template <int D, bool BF16, bool BAND, bool WIDE, bool SMALL>
-int launch_paged_kernels(const PagedLaunchArgs& a) {
-  static std::atomic<unsigned long long> configured{0};
-  const int e = once_per_device(configured, [&]() -> int {
-    return (int)cudaFuncSetAttribute(fa2_paged_merge_kernel<D, BF16>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
-  });
-  if (e != 0) return e;
-  const int r = launch_paged_kernel<D, BF16, BAND, WIDE, SMALL, false>(a);
+  const int r = launch_dependent(kern, dim3((unsigned)grid), C::THREADS, C::SMEM_BYTES, a.stream, a.tm_q, a.tm_k, a.tm_v,
+                                 a.p);
   if (r != 0) return r;
   return launch_paged_merge<D, BF16>(a.p, a.stream);
 }

@@ -64,13 +64,12 @@ struct PagedParams {
   struct PagedMerge* merges;   // [ctas] pairs to merge, kPagedMergeBytes each
   int sinks;              // first keys a row sees as far as its band's right edge (0 without a left window)
   // Shared prefixes (fa2_paged_fwd_shared), else unused.  Two passes: over the
-  // groups, each one sequence of all its query rows and the shared keys (`batch`
-  // is then `groups`), and over the sequences' own keys.
+  // groups (`batch` is then `groups`), and over the sequences' own keys.
   const int* cu_groups;     // [groups + 1] first sequence of each group
   const int* shared_lens;   // [groups]
   int groups, seqs;         // seqs: sequences
   int share_unit;           // shared keys count in whole units of pages and key tiles
-  int own;                  // the pass over the sequences' own keys
+  float share_weight;       // a shared key's cost in the division of the CTAs, in keys of the other pass
   struct PagedPair* pairs;  // [whole_slots] where each (query tile, K/V head) pair's partials are
 };
 
@@ -93,7 +92,7 @@ struct PagedLaunchArgs {
 int launch_paged_d64(const PagedLaunchArgs& a);
 int launch_paged_d128(const PagedLaunchArgs& a);
 int launch_paged_d256(const PagedLaunchArgs& a);
-// The pass over the shared keys, the one over the sequences' own, and the merge.
+// Both passes in one launch, and the merge.
 int launch_paged_shared_d64(const PagedLaunchArgs& shared, const PagedLaunchArgs& own);
 int launch_paged_shared_d128(const PagedLaunchArgs& shared, const PagedLaunchArgs& own);
 int launch_paged_shared_d256(const PagedLaunchArgs& shared, const PagedLaunchArgs& own);

@@ -26,6 +26,12 @@ constexpr int paged_ctas(int d) { return d == 256 ? 152 : 304; }
 // 32000 at d = 256, few pairs of many partials, 42.7, 40.2, 55.5).
 constexpr int kPagedOverhead = 128;
 constexpr int kPagedMinShare = 128;
+// Shared prefixes: what a key of the shared pass costs, in keys of the sequences'
+// own, with few and with many rows there (64 requests behind 8200 shared keys 66
+// to 68 us at 0.85 .. 1.4, 74 at 0.7; 128 behind 32000: 119 at 0.85, 132 at 1, 158
+// at 1.4; chunks of up to 300 tokens, d = 256: 103 at 1, 91 from 1.2 on).
+constexpr float kSharedWeightFew = 0.85f;
+constexpr float kSharedWeightMany = 1.25f;
 
 int check_cache(const fa2_paged_cache& c, CacheView& k, CacheView& v) {
   if (c.dtype != FA2_FP16 && c.dtype != FA2_BF16) return FA2_ERR_INVALID_ARG;
@@ -276,13 +282,14 @@ int paged_forward(const fa2_paged_params& a, const fa2_paged_shared_params* x, v
     p.groups = x->num_groups;
     p.seqs = a.batch;
     p.share_unit = (int)unit;
-    p.own = 1;
+    p.pair_ctas = 0;   // one wave of CTAs, which the two passes divide
+    p.share_weight = la.wide ? kSharedWeightMany : kSharedWeightFew;
     PagedLaunchArgs ls = la;   // over the groups: every query row sees every shared key
-    ls.p.own = 0;
     ls.p.batch = x->num_groups;
     ls.p.window_right = -1;
     rc = fill_pass(a, shared, static_cast<uint8_t*>(workspace) + s.ws_bytes, true, ls);
     if (rc) return rc;
+    ls.p.pair_ctas = 0;
     switch (c.head_dim) {
       case 64: e = launch_paged_shared_d64(ls, la); break;
       case 128: e = launch_paged_shared_d128(ls, la); break;

@@ -670,8 +670,8 @@ size_t fa2_paged_fp8_params_size(void);
  * and are checked by the kernels: a sequence of a group whose shared length is
  * out of range or reaches into the sequence's new tokens, or whose query rows
  * do not lie between those of the group's first and last, is left unwritten and
- * reported as FA2_ERR_DEVICE_SEQLENS.  Three kernels, asynchronous on `stream`;
- * the host reads no length.  Deterministic.  The workspace holds the fp32 state
+ * reported as FA2_ERR_DEVICE_SEQLENS.  Two kernels, asynchronous on `stream`; the
+ * host reads no length.  Deterministic.  The workspace holds the fp32 state
  * of every query row of both passes, about 16 bytes per element of q while
  * decoding; overlaps, captures and errors as fa2_paged_fwd.
  */
