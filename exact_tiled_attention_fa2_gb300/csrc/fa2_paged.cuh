@@ -493,6 +493,7 @@ __device__ __forceinline__ LineScan<WIDE> line_scan(const PagedParams& p, int ti
                                                     Beside&& beside) {
   using Line = typename LineOf<WIDE>::T;
   constexpr int NW = THREADS / 32;
+  static_assert(NW <= 8, "PagedScan holds eight warps' sums");
   const int lane = tid & 31, w = tid >> 5;
   const int per = (p.batch + THREADS - 1) / THREADS;
   const int i0 = min(tid * per, p.batch), i1 = min(i0 + per, p.batch);

@@ -29,9 +29,12 @@
 // loses nothing: exponents differ by 120 at most.
 //
 // Schedule, fragments and merging of cut pairs are the 16-bit kernel's
-// (fa2_paged.cuh); a step here is two of its 64-key tiles.  One CTA, 7 warps:
-// four softmax, the MMA thread, the TMA warp (keys, values, exponents), and the
-// planner, which walks the fragments and prepares their q parts.
+// (fa2_paged.cuh); a step here is two of its 64-key tiles.  One CTA: four softmax
+// warps for every eight rows of a tile (a thread has one key and eight rows), the
+// MMA thread, the TMA warp (keys, values, exponents), and the planner, which
+// walks the fragments and prepares their q parts.  What runs seldom is rolled or
+// shared: a call's code comes to each SM once, and with one thread for 32 rows,
+// four times the code, a call began 50 us later.
 #pragma once
 
 #include <cuda_fp8.h>
@@ -44,15 +47,15 @@ namespace fa2 {
 // Barriers.  Phases count steps g (of 128 keys) or fragments of the CTA.
 enum : int {
   P8_Q = 0,        // + f & 1: the fragment's description and q parts are there
-  P8_P = 2,        // + g & 1: P(g) is in shared memory (four softmax warps)
-  P8_ODONE = 4,    // + f & 1: the softmax warps are done with O (four)
-  P8_FREE = 6,     // + f & 3: and with the description (four)
+  P8_P = 2,        // + g & 1: P(g) is in shared memory (all softmax warps)
+  P8_ODONE = 4,    // + f & 1: the softmax warps are done with O (all)
+  P8_FREE = 6,     // + f & 3: and with the description (all)
   P8_PLAN = 10,    // + f & 3: the fragment's description is there
-  P8_VOTE = 14,    // the softmax warps' votes of step g (four)
-  P8_X = 15,       // their maxima, or their sums (four)
-  P8_EXIT = 16,
-  P8_EXP = 17,     // + g & 7: the exponents of step g are there (16 lanes)
-  P8_RINGS = 25,   // S complete (K stages), PV complete (V stages), K landed, V landed
+  P8_VOTE = 14,    // + row group: its four warps' votes of step g
+  P8_X = 18,       // + row group: their maxima, or their sums
+  P8_EXIT = 22,
+  P8_EXP = 23,     // + g & 7: the exponents of step g are there (16 lanes)
+  P8_RINGS = 31,   // S complete (K stages), PV complete (V stages), K landed, V landed
 };
 
 template <int D_, int R_, bool MANY_>
@@ -61,10 +64,11 @@ struct Paged8Config {
   static constexpr int R = R_;           // query rows of a tile, padded
   static constexpr bool MANY = MANY_;
   static constexpr int BC = 128;         // keys of a step
-  static constexpr int THREADS = 224;
-  static constexpr int MMA_WARP = 4;
-  static constexpr int TMA_WARP = 5;
-  static constexpr int PLAN_WARP = 6;
+  static constexpr int SOFT_WARPS = R / 2;         // four for eight rows
+  static constexpr int MMA_WARP = SOFT_WARPS;
+  static constexpr int TMA_WARP = SOFT_WARPS + 1;
+  static constexpr int PLAN_WARP = SOFT_WARPS + 2;
+  static constexpr int THREADS = 32 * (SOFT_WARPS + 3);
   static constexpr int ROW = D < 128 ? D : 128;   // bytes of a swizzled row
   static constexpr uint32_t LAYOUT = ROW == 64 ? 4 : 2;
   static constexpr int BLOCKS = D / ROW;
@@ -86,10 +90,10 @@ struct Paged8Config {
   static constexpr uint32_t OFF_V = OFF_K + KSTAGES * KV_BYTES;
   static constexpr uint32_t OFF_EXP = OFF_V + VSTAGES * KV_BYTES;   // + 256 * (g & 7): K, V
   static constexpr uint32_t OFF_FACTOR = OFF_EXP + ESTAGES * 256;   // + 4 R * (f & 1): 2^q exponent * scale * log2 e
-  static constexpr uint32_t OFF_MAX = OFF_FACTOR + 2 * 4 * R;       // four warps x R
-  static constexpr uint32_t OFF_SUM = OFF_MAX + 4 * 4 * R;          // four warps x R
-  static constexpr uint32_t OFF_VOTE = OFF_SUM + 4 * 4 * R;         // two x four bytes
-  static constexpr uint32_t OFF_BAR = OFF_VOTE + 16;
+  static constexpr uint32_t OFF_MAX = OFF_FACTOR + 2 * 4 * R;       // each softmax warp's eight rows
+  static constexpr uint32_t OFF_SUM = OFF_MAX + 4 * 8 * SOFT_WARPS; // the same
+  static constexpr uint32_t OFF_VOTE = OFF_SUM + 4 * 8 * SOFT_WARPS;   // two x four bytes a row group
+  static constexpr uint32_t OFF_BAR = OFF_VOTE + 32;
   static constexpr uint32_t OFF_MISC = OFF_BAR + (BARS + 1) / 2 * 16;
   static constexpr uint32_t OFF_FRAG = OFF_MISC + 16;
   static constexpr uint32_t OFF_SCAN = OFF_FRAG + 512;
@@ -114,12 +118,21 @@ constexpr float kFp8TopLog2 = 4.f;
 // 2^e; 0 below fp32's normal range.
 __device__ __forceinline__ float pow2_int(int e) { return e < -126 ? 0.f : __uint_as_float((unsigned)(min(e, 127) + 127) << 23); }
 
-// Order-preserving map of floats (no NaN) to ints.
-__device__ __forceinline__ int ordered(float x) {
-  const int i = __float_as_int(x);
-  return i ^ ((i >> 31) & 0x7fffffff);
+// Row i's value over a warp's lanes for eight rows at once: every exchange halves
+// the rows a lane still has.  The lane returns row warp_row(lane)'s.
+__device__ __forceinline__ int warp_row(int lane) { return (lane >> 4 & 1) * 4 + (lane >> 3 & 1) * 2 + (lane >> 2 & 1); }
+template <class Op>
+__device__ __forceinline__ float warp_rows(const float (&v)[8], int lane, Op op) {
+  float a[4], b[2];
+  const bool h4 = lane & 16, h3 = lane & 8, h2 = lane & 4;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) a[i] = op(h4 ? v[i + 4] : v[i], __shfl_xor_sync(0xffffffffu, h4 ? v[i] : v[i + 4], 16));
+#pragma unroll
+  for (int i = 0; i < 2; ++i) b[i] = op(h3 ? a[i + 2] : a[i], __shfl_xor_sync(0xffffffffu, h3 ? a[i] : a[i + 2], 8));
+  float x = op(h2 ? b[1] : b[0], __shfl_xor_sync(0xffffffffu, h2 ? b[0] : b[1], 4));
+  x = op(x, __shfl_xor_sync(0xffffffffu, x, 2));
+  return op(x, __shfl_xor_sync(0xffffffffu, x, 1));
 }
-__device__ __forceinline__ float unordered(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7fffffff)); }
 
 // The e4m3 parts of a pair of values at most 448: bits 0-7 and 8-15 of c[i] are
 // x's and y's part i.
@@ -157,7 +170,7 @@ __device__ __forceinline__ void pg8_q_parts(const Paged8Ctx<C>& t, const PagedFp
                                             int lane) {
   constexpr int E = C::D / 32;   // a lane's elements of a row, next to each other
   constexpr int W = E / 2;       // in 32-bit words
-  constexpr int AT_ONCE = 8;     // rows whose loads are in flight together
+  constexpr int AT_ONCE = 4;     // rows whose loads are in flight together
   const uint32_t sQ = t.base + C::OFF_Q + (uint32_t)buf * C::Q_BYTES;
   float* factor = reinterpret_cast<float*>(t.smem + C::OFF_FACTOR) + buf * C::R;
   const int group = a.p.group, head0 = f->h * group, rows = f->rows;
@@ -462,16 +475,17 @@ __device__ __forceinline__ void pg8_mma(const Paged8Ctx<C>& t) {
 
 // ---------------------------------------------------------------- the softmax warps
 
+// Warps 4 n .. 4 n + 3: rows 8 n .. 8 n + 7, a key a thread.
 template <class C>
 __device__ __forceinline__ void pg8_softmax(const Paged8Ctx<C>& t, const PagedFp8Params& a, int warp, int lane) {
-  constexpr int R = C::R;
   const PagedParams& p = a.p;
-  const int tid = warp * 32 + lane;
-  const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
-  const uint32_t tO = t.tmem + lane_off + C::TMEM_O;
-  float* s_max = reinterpret_cast<float*>(t.smem + C::OFF_MAX);
-  float* s_sum = reinterpret_cast<float*>(t.smem + C::OFF_SUM);
-  volatile uint8_t* s_vote = t.smem + C::OFF_VOTE;
+  const int rg = warp >> 2, r0 = rg * 8, quad = warp & 3, tid = quad * 32 + lane;
+  const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+  const uint32_t tO = t.tmem + lane_off + C::TMEM_O + r0;
+  float* s_max = reinterpret_cast<float*>(t.smem + C::OFF_MAX) + rg * 32;   // four warps x eight rows
+  float* s_sum = reinterpret_cast<float*>(t.smem + C::OFF_SUM) + rg * 32;
+  volatile uint8_t* s_vote = t.smem + C::OFF_VOTE + rg * 8;
+  const int tok0 = r0 / p.group, head0 = r0 - tok0 * p.group;   // the first row's token and head of its group
   auto wait = [&](int bar, int phase, uint32_t site) -> bool { return t.warp_wait(bar, phase, site); };
   int g = 0, x_phase = 0;
   for (int nf = 0;; ++nf) {
@@ -481,135 +495,127 @@ __device__ __forceinline__ void pg8_softmax(const Paged8Ctx<C>& t, const PagedFp
     if (n < 0) return;
     const int steps = (n + 1) >> 1;
     const TileMask tmask = f->tm;
-    const float4* factor = reinterpret_cast<const float4*>(t.smem + C::OFF_FACTOR + (nf & 1) * 4 * R);
-    float m[R], l[R];
+    const float4* factor = reinterpret_cast<const float4*>(t.smem + C::OFF_FACTOR + ((nf & 1) * C::R + r0) * 4);
+    const float4 f0 = factor[0], f1 = factor[1];
+    const float fr[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
+    float m[8], l[8];
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      m[r] = -INFINITY;
-      l[r] = 0.f;
+    for (int i = 0; i < 8; ++i) {
+      m[i] = -INFINITY;
+      l[i] = 0.f;
     }
+#pragma unroll 1
     for (int j = 0; j < steps; ++j, ++g) {
       const int half = 2 * j + (tid >> 6);   // this thread's key tile
       const bool masked = !tmask.full(2 * j) || 2 * j + 1 >= n || !tmask.full(2 * j + 1);
-      const int key = f->tile(f->j0 + min(half, n - 1)) * kPagedKeyTile + (tid & 63);
-      // seen by some row of the query tile
-      const bool alive = !masked || (half < n && (key < f->km.pre_end || (key >= f->lo && key < f->end)));
+      bool alive = true;        // the key is seen by some row of the query tile
+      unsigned seen = 0xffu;    // and by which of these eight
+      if (masked) {
+        const int key = f->tile(f->j0 + min(half, n - 1)) * kPagedKeyTile + (tid & 63);
+        alive = half < n && (key < f->km.pre_end || (key >= f->lo && key < f->end));
+        seen = 0;
+        int tok = f->q0 + tok0, left = p.group - head0;
+#pragma unroll 1
+        for (int i = 0; i < 8; ++tok) {   // a token's rows at a time
+          const int rows = min(left, 8 - i);
+          if (alive && (key < prefix_end(p, f->km, tok) || (key >= f->km.row_lo(tok) && key <= f->km.row_hi(tok))))
+            seen |= ((1u << rows) - 1) << i;
+          i += rows;
+          left = p.group;
+        }
+      }
       if (!wait(P8_EXP + (g & 7), g >> 3, kSiteSoftmaxS)) return;
       const uint8_t* e = t.smem + C::OFF_EXP + (g & 7) * 256 + tid;
       const int ev = (int)e[128] - 127;
       const float key_scale = __uint_as_float((unsigned)e[0] << 23), value_exp = (float)ev, value_inv = pow2_int(-ev);
       if (!wait(C::B_S + g % C::KSTAGES, g / C::KSTAGES, kSiteSoftmaxS)) return;
       tc_fence_after();
-      float x[R];
-      const uint32_t tS = t.tmem + lane_off + C::TMEM_S + (uint32_t)(g & 1) * C::N;
-#pragma unroll
-      for (int r = 0; r < R; r += 8) {
+      float x[8];
+      bool raise = false;   // a row's m
+      {
+        const uint32_t tS = t.tmem + lane_off + C::TMEM_S + (uint32_t)(g & 1) * C::N + r0;
         uint32_t c[3][8];
 #pragma unroll
-        for (int i = 0; i < 3; ++i) tmem_ld_32x32b_x8(tS + i * R + r, c[i]);
+        for (int i = 0; i < 3; ++i) tmem_ld_32x32b_x8(tS + i * C::R, c[i]);
 #pragma unroll
         for (int i = 0; i < 3; ++i) tmem_ld_wait_x8(c[i]);
-        const float4 f0 = factor[r / 4], f1 = factor[r / 4 + 1];
-        const float fr[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          x[r + i] = fmaf(fmaf(fmaf(__uint_as_float(c[2][i]), 0.0625f, __uint_as_float(c[1][i])), 0.0625f,
-                               __uint_as_float(c[0][i])),
-                          fr[i] * key_scale, value_exp);
-      }
-      if (masked) {
-        int tok = f->q0, left = p.group;
-        bool seen = false;
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          if (r == 0 || left == p.group)
-            seen = alive && (key < prefix_end(p, f->km, tok) || (key >= f->km.row_lo(tok) && key <= f->km.row_hi(tok)));
-          if (!seen) x[r] = -INFINITY;
-          if (--left == 0) {
-            left = p.group;
-            ++tok;
-          }
+        for (int i = 0; i < 8; ++i) {
+          x[i] = fmaf(fmaf(fmaf(__uint_as_float(c[2][i]), 0.0625f, __uint_as_float(c[1][i])), 0.0625f,
+                           __uint_as_float(c[0][i])),
+                      fr[i] * key_scale, value_exp);
+          if (!(seen >> i & 1u)) x[i] = -INFINITY;
+          raise |= x[i] > m[i] + kFp8RaiseLog2;
         }
       }
-      bool raise = false;   // a row's m
-#pragma unroll
-      for (int r = 0; r < R; ++r) raise |= x[r] > m[r] + kFp8RaiseLog2;
       raise = __any_sync(0xffffffffu, raise);
       if (lane == 0) {
-        s_vote[4 * (g & 1) + warp] = raise;
-        mbar_arrive(t.bar(P8_VOTE));
+        s_vote[4 * (g & 1) + quad] = raise;
+        mbar_arrive(t.bar(P8_VOTE + rg));
       }
-      if (!wait(P8_VOTE, g, kSiteSoftmaxO)) return;
-      if (*reinterpret_cast<volatile uint32_t*>(t.smem + C::OFF_VOTE + 4 * (g & 1)) != 0) {
-        float mine = 0.f;
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const float top = unordered(__reduce_max_sync(0xffffffffu, ordered(x[r] == x[r] ? x[r] : -INFINITY)));
-          if (lane == r) mine = top;
-        }
-        if (lane < R) s_max[warp * R + lane] = mine;
+      if (!wait(P8_VOTE + rg, g, kSiteSoftmaxO)) return;
+      if (*reinterpret_cast<volatile uint32_t*>(t.smem + C::OFF_VOTE + rg * 8 + 4 * (g & 1)) != 0) {
+        const float mine = warp_rows(x, lane, [](float u, float v) { return fmaxf(u, v); });   // (a NaN is passed over)
+        if ((lane & 3) == 0) s_max[quad * 8 + warp_row(lane)] = mine;
         __syncwarp();
-        if (lane == 0) mbar_arrive(t.bar(P8_X));
-        if (!wait(P8_X, x_phase, kSiteSoftmaxO)) return;
+        if (lane == 0) mbar_arrive(t.bar(P8_X + rg));
+        if (!wait(P8_X + rg, x_phase, kSiteSoftmaxO)) return;
         ++x_phase;
-        if (j > 0 && !wait(C::B_O + (g - 1) % C::VSTAGES, (g - 1) / C::VSTAGES, kSiteSoftmaxO)) return;
-        tc_fence_after();
+        float alpha[8];
 #pragma unroll
-        for (int r = 0; r < R; r += 8) {
-          float alpha[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float top = fmaxf(fmaxf(s_max[r + i], s_max[R + r + i]), fmaxf(s_max[2 * R + r + i], s_max[3 * R + r + i]));
-            const bool up = top > m[r + i] + kFp8RaiseLog2;
-            const float m_new = up ? top - kFp8TopLog2 : m[r + i];
-            alpha[i] = up ? ex2_approx(m[r + i] - m_new) : 1.f;
-            m[r + i] = m_new;
-            l[r + i] *= alpha[i];
-          }
-          if (j > 0) {
-#pragma unroll 1
-            for (int b = 0; b < C::BLOCKS * 3; ++b) {
-              const uint32_t at = tO + (uint32_t)(b / 3) * C::N + (uint32_t)(b % 3) * R + r;
-              uint32_t o[8];
-              tmem_ld_32x32b_x8(at, o);
-              tmem_ld_wait_x8(o);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha[i]);
-              tmem_st_32x32b_x8(at, o);
-            }
-          }
+        for (int i = 0; i < 8; ++i) {
+          const float top = fmaxf(fmaxf(s_max[i], s_max[8 + i]), fmaxf(s_max[16 + i], s_max[24 + i]));
+          const bool up = top > m[i] + kFp8RaiseLog2;
+          const float m_new = up ? top - kFp8TopLog2 : m[i];
+          alpha[i] = up ? ex2_approx(m[i] - m_new) : 1.f;
+          m[i] = m_new;
+          l[i] *= alpha[i];
         }
-        tmem_st_wait();
+        if (j > 0) {
+          if (!wait(C::B_O + (g - 1) % C::VSTAGES, (g - 1) / C::VSTAGES, kSiteSoftmaxO)) return;
+          tc_fence_after();
+#pragma unroll 1
+          for (int b = 0; b < C::BLOCKS * 3; ++b) {
+            const uint32_t at = tO + (uint32_t)(b / 3) * C::N + (uint32_t)(b % 3) * C::R;
+            uint32_t o[8];
+            tmem_ld_32x32b_x8(at, o);
+            tmem_ld_wait_x8(o);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha[i]);
+            tmem_st_32x32b_x8(at, o);
+          }
+          tmem_st_wait();
+        }
       }
       // P(g - 2), whose place P(g) takes, has been used
       if (g >= 2 && !wait(C::B_O + (g - 2) % C::VSTAGES, (g - 2) / C::VSTAGES, kSiteSoftmaxO)) return;
-      const uint32_t sP = t.base + C::OFF_P + (uint32_t)(g & 1) * C::P_BYTES + (uint32_t)(tid & 15);
+      const uint32_t sP = t.base + C::OFF_P + (uint32_t)(g & 1) * C::P_BYTES + (uint32_t)(r0 * 128 + (tid & 15));
 #pragma unroll
-      for (int r = 0; r < R; r += 2) {
-        const float m0 = m[r] == -INFINITY ? 0.f : m[r], m1 = m[r + 1] == -INFINITY ? 0.f : m[r + 1];
-        const float2 y = make_float2(ex2_approx(x[r] - m0), ex2_approx(x[r + 1] - m1));
-        l[r] = fmaf(y.x, value_inv, l[r]);
-        l[r + 1] = fmaf(y.y, value_inv, l[r + 1]);
+      for (int i = 0; i < 8; i += 2) {
+        const float m0 = m[i] == -INFINITY ? 0.f : m[i], m1 = m[i + 1] == -INFINITY ? 0.f : m[i + 1];
+        const float2 y = make_float2(ex2_approx(x[i] - m0), ex2_approx(x[i + 1] - m1));
+        l[i] = fmaf(y.x, value_inv, l[i]);
+        l[i + 1] = fmaf(y.y, value_inv, l[i + 1]);
         uint32_t c[3];
         fp8_parts(y, c);
 #pragma unroll
-        for (int i = 0; i < 3; ++i) {
+        for (int part = 0; part < 3; ++part) {
 #pragma unroll
           for (int k = 0; k < 2; ++k)
-            asm volatile("st.shared.u8 [%0], %1;" ::"r"(sP + (uint32_t)((i * R + r + k) * 128) +
-                                                        ((uint32_t)((tid >> 4) ^ ((r + k) & 7)) << 4)),
-                         "r"(c[i] >> (8 * k))
+            asm volatile("st.shared.u8 [%0], %1;" ::"r"(sP + (uint32_t)((part * C::R + i + k) * 128) +
+                                                        ((uint32_t)((tid >> 4) ^ (i + k)) << 4)),
+                         "r"(c[part] >> (8 * k))
                          : "memory");
         }
       }
-      if (__any_sync(0xffffffffu, !alive)) {
+      if (rg == 0 && __any_sync(0xffffffffu, !alive)) {
         // a row of V that no query row sees may hold anything, and 0 x NaN would reach the sums
         const int s = g % C::VSTAGES;
         if (!wait(C::B_VFULL + s, g / C::VSTAGES, kSiteMmaV)) return;
         if (!alive) {
           const uint32_t at = t.base + C::OFF_V + s * C::KV_BYTES + (uint32_t)(tid >> 3) * C::GROUP_BYTES +
                               (uint32_t)(tid & 7) * C::ROW;
-#pragma unroll
+#pragma unroll 1
           for (int b = 0; b < C::BLOCKS; ++b)
 #pragma unroll
             for (int i = 0; i < C::ROW; i += 16)
@@ -621,68 +627,67 @@ __device__ __forceinline__ void pg8_softmax(const Paged8Ctx<C>& t, const PagedFp
       __syncwarp();
       if (lane == 0) mbar_arrive(t.bar(P8_P + (g & 1)));
     }
-    // the rows' sums over all keys: by shuffles, then over the four warps
+    // the rows' sums over all keys: over the lanes, then over the four warps
     if (n > 0) {
-      float mine = 0.f;
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
-        if (lane == r) mine = l[r];
-      }
-      if (lane < R) s_sum[warp * R + lane] = mine;
+      const float mine = warp_rows(l, lane, [](float u, float v) { return u + v; });
+      if ((lane & 3) == 0) s_sum[quad * 8 + warp_row(lane)] = mine;
       __syncwarp();
-      if (lane == 0) mbar_arrive(t.bar(P8_X));
-      if (!wait(P8_X, x_phase, kSiteEpilogueO)) return;
+      if (lane == 0) mbar_arrive(t.bar(P8_X + rg));
+      if (!wait(P8_X + rg, x_phase, kSiteEpilogueO)) return;
       ++x_phase;
 #pragma unroll
-      for (int r = 0; r < R; ++r) l[r] = (s_sum[r] + s_sum[R + r]) + (s_sum[2 * R + r] + s_sum[3 * R + r]);
+      for (int i = 0; i < 8; ++i) l[i] = (s_sum[i] + s_sum[8 + i]) + (s_sum[16 + i] + s_sum[24 + i]);
       if (!wait(C::B_O + (g - 1) % C::VSTAGES, (g - 1) / C::VSTAGES, kSiteEpilogueO)) return;
       tc_fence_after();
     }
-    const int rows = f->rows, slot = f->slot;
-    const bool has_d = C::ROW == 128 || lane < 16;   // (64 rows of O^T lie in 16 lanes of each warp)
+    const int rows = f->rows - r0, slot = f->slot;   // of these eight
+    if (rows > 0) {
+      const bool has_d = C::ROW == 128 || lane < 16;   // (64 rows of O^T lie in 16 lanes of each warp)
+      float inv[8];
 #pragma unroll
-    for (int r = 0; r < R; r += 8) {
-      if (r >= rows) break;
-#pragma unroll
+      for (int i = 0; i < 8; ++i) inv[i] = slot >= 0 ? 1.f : l[i] == 0.f ? 0.f : 1.f / l[i];   // 0: sees no key (a NaN sum is no such row's)
+      const long long wrap = p.o_rs - (long long)(p.group - 1) * p.o_hs;   // from a token's last head to the next token's first
+#pragma unroll 1
       for (int b = 0; b < C::BLOCKS; ++b) {
         uint32_t c[3][8];
 #pragma unroll
-        for (int i = 0; i < 3; ++i) tmem_ld_32x32b_x8(tO + b * C::N + i * R + r, c[i]);   // n = 0: not used
+        for (int i = 0; i < 3; ++i) tmem_ld_32x32b_x8(tO + b * C::N + i * C::R, c[i]);   // n = 0: not used
 #pragma unroll
         for (int i = 0; i < 3; ++i) tmem_ld_wait_x8(c[i]);
-        const int d = C::ROW == 128 ? b * 128 + tid : warp * 16 + lane;
-        int tok = r / p.group, in_group = r - tok * p.group;
+        const int d = C::ROW == 128 ? b * 128 + tid : quad * 16 + lane;
+        float* part = p.ws_o + (((size_t)slot * (C::D / 4) + d / 4) * (size_t)p.slot_rows + r0) * 4 + (d & 3);
+        uint16_t* dst = reinterpret_cast<uint16_t*>(paged_o_row(p, f->row + tok0, f->h * p.group + head0)) + d;
+        int head = head0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float o = fmaf(fmaf(__uint_as_float(c[2][i]), 0.0625f, __uint_as_float(c[1][i])), 0.0625f,
                                __uint_as_float(c[0][i]));
-          if (r + i < rows && has_d) {
-            if (slot >= 0) {
-              p.ws_o[(((size_t)slot * (C::D / 4) + d / 4) * (size_t)p.slot_rows + r + i) * 4 + (d & 3)] = n > 0 ? o : 0.f;
-            } else {
-              const float y = l[r + i] == 0.f ? 0.f : o * (1.f / l[r + i]);   // sees no key; a NaN sum is no such row's
-              uint16_t* dst = reinterpret_cast<uint16_t*>(paged_o_row(p, f->row + tok, f->h * p.group + in_group)) + d;
+          const float y = l[i] == 0.f ? 0.f : o * inv[i];
+          if (i < rows && has_d) {
+            if (slot >= 0)
+              part[4 * i] = y;
+            else
               *dst = (uint16_t)(a.bf16 ? pack2<true>(y, 0.f) : pack2<false>(y, 0.f));
-            }
           }
-          if (++in_group == p.group) {
-            in_group = 0;
-            ++tok;
-          }
+          const bool last = ++head == p.group;
+          dst += last ? wrap : p.o_hs;
+          head = last ? 0 : head;
         }
       }
-    }
+      float my_m = m[0], my_l = l[0];
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      if (tid == r && r < rows) {
+      for (int i = 1; i < 8; ++i) {
+        my_m = lane == i ? m[i] : my_m;
+        my_l = lane == i ? l[i] : my_l;
+      }
+      if (quad == 0 && lane < min(rows, 8)) {
+        const int r = r0 + lane;
         if (slot >= 0) {
-          *reinterpret_cast<float2*>(p.ws_ml + ((size_t)slot * (size_t)p.slot_rows + r) * 2) = make_float2(m[r], l[r]);
+          *reinterpret_cast<float2*>(p.ws_ml + ((size_t)slot * (size_t)p.slot_rows + r) * 2) = make_float2(my_m, my_l);
         } else {
           const int tok = r / p.group;
           p.lse[(long long)(f->h * p.group + r - tok * p.group) * p.lse_hs + f->row + tok] =
-              l[r] == 0.f ? -INFINITY : (m[r] + log2f(l[r])) * 0.6931471805599453f;
+              my_l == 0.f ? -INFINITY : (my_m + log2f(my_l)) * 0.6931471805599453f;
         }
       }
     }
@@ -721,8 +726,8 @@ __global__ void __launch_bounds__(Paged8Config<D, R, MANY>::THREADS, Paged8Confi
   if (warp == C::TMA_WARP && lane == 0) {
 #pragma unroll 1
     for (int i = 0; i < C::BARS; ++i) {
-      const bool four = i >= P8_P && i < P8_PLAN;   // softmax warps
-      mbar_init(t.bar(i), i >= P8_EXP && i < P8_RINGS ? 16 : four || i == P8_VOTE || i == P8_X ? 4 : 1);
+      mbar_init(t.bar(i), i >= P8_EXP && i < P8_RINGS ? 16 : i >= P8_P && i < P8_PLAN ? C::SOFT_WARPS
+                                                         : i >= P8_VOTE && i < P8_EXIT ? 4 : 1);
     }
     *t.abort_flag = 0;
     fence_mbar_init();
@@ -745,7 +750,9 @@ __global__ void __launch_bounds__(Paged8Config<D, R, MANY>::THREADS, Paged8Confi
     __syncthreads();
     place = scan->place;
   } else {
-    place = find_place<C::THREADS, MANY>(p, (int)blockIdx.x, scan, blockIdx.x == 0);   // with its barriers
+    // (seven warps of any number sum the sequences, with their barriers)
+    const LineScan<MANY> sums = line_scan<224, MANY, 0>(p, (int)threadIdx.x, scan, blockIdx.x == 0, [] {});
+    place = line_place<MANY, 0>(p, sums, (int)blockIdx.x, p.ctas, scan);
   }
   tc_fence_after();
   t.tmem = *tmem_slot;
