@@ -78,9 +78,9 @@ struct Paged8Config {
   static constexpr int N = (NB + 15) / 16 * 16;    // columns of a product (those past NB are not read)
   static constexpr uint32_t Q_BYTES = NB * D;
   static constexpr uint32_t P_BYTES = NB * BC;
-  static constexpr int CTAS_PER_SM = D == 256 || R == 32 ? 1 : 2;
-  static constexpr int KSTAGES = R == 32 ? (D == 256 ? 2 : D == 128 ? 5 : 6) : (D == 64 ? 5 : 3);
-  static constexpr int VSTAGES = R == 32 ? KSTAGES : D == 64 ? 5 : R == 8 ? 3 : 2;
+  static constexpr int CTAS_PER_SM = D == 256 || R >= 16 ? 1 : 2;
+  static constexpr int KSTAGES = R == 32 && D == 256 ? 2 : R >= 16 && D == 128 ? 5 : D == 64 ? 6 - (R == 8) : 3;
+  static constexpr int VSTAGES = R == 16 && D == 256 ? 2 : KSTAGES;
   static constexpr int ESTAGES = 8;
   static constexpr int B_S = P8_RINGS, B_O = B_S + KSTAGES, B_KFULL = B_O + VSTAGES, B_VFULL = B_KFULL + KSTAGES;
   static constexpr int BARS = B_VFULL + VSTAGES;

@@ -146,7 +146,7 @@ int fp8_shape(const fa2_paged_fp8_params& a, Fp8Shape& s) {
   s.many = s.max_q > T || (double)a.batch * c.heads * s.parts *
                                   (((double)a.max_pages * c.page_size + kFp8Overhead) / 64 + 2.0) + 1e6 > 2147483647.0;
   // one wave of the resident CTAs of a GB300's 152 SMs, fixed (see paged_ctas)
-  s.ctas = c.head_dim == 256 || s.many || s.slot_rows > 16 ? 152 : 304;
+  s.ctas = c.head_dim == 256 || s.many || s.slot_rows > 8 ? 152 : 304;
   s.pair_ctas = pairs >= s.ctas ? (int)pairs : 0;
   const size_t rows = 2 * (size_t)s.ctas * (size_t)s.slot_rows;
   s.ws_o_bytes = align256(rows * (size_t)c.head_dim * 4);
