@@ -7,10 +7,10 @@
 namespace fa2 {
 
 // One of K and V: 16-bit rows [total][heads][d] (strides in 16-byte units), codes
-// [page][head][row][d] (strides in 16-byte units), exponents [page][head][row].
+// [page][head][row][d] (strides in 8-byte units), exponents [page][head][row].
 struct PagedFp8Side {
   uint4* rows;
-  uint4* codes;
+  uint2* codes;
   uint8_t* exps;
   long long row_rs, row_hs;                // token, head
   long long code_ps, code_hs, code_rs;     // page, head, row of a page
@@ -22,7 +22,8 @@ struct PagedFp8RowsArgs {
   const int* slots;
   uint32_t* status;
   int total, heads, num_slots, page_size;
-  int chunks_log2;   // 16-code chunks of a head's row: d / 16 = 1 << chunks_log2
+  int head_dim;
+  unsigned page_magic, page_shift;   // as PagedParams
   bool bf16;
 };
 

@@ -62,6 +62,12 @@ int log2_of(int x) {
   return n;
 }
 
+// k / page_size for 0 <= k < 2^31 without a division (see the 16-bit forward).
+void page_division(int page_size, unsigned& magic, unsigned& shift) {
+  shift = (unsigned)log2_of(page_size);
+  magic = (unsigned)(((1ull << 32) * ((1ull << shift) - (unsigned)page_size)) / (unsigned)page_size + 1);
+}
+
 // The launch of fa2_paged_append_fp8 (write: the cache is written) or fa2_paged_read_fp8.
 int fp8_rows(const fa2_paged_cache_fp8& c, void* k, void* v, const int* slots, const int64_t* k_st, const int64_t* v_st,
              int total, int dtype, bool write, cudaStream_t stream) {
@@ -96,8 +102,8 @@ int fp8_rows(const fa2_paged_cache_fp8& c, void* k, void* v, const int* slots, c
   rc = paged_device_status(&a.status);
   if (rc) return rc;
   auto side = [&](int i, void* row, const long long* st, void* code, void* exps) {
-    return PagedFp8Side{static_cast<uint4*>(row), static_cast<uint4*>(code), static_cast<uint8_t*>(exps),
-                        st[0] / 8, st[1] / 8, x.code[i].st[0] / 16, x.code[i].st[1] / 16, x.code[i].st[2] / 16,
+    return PagedFp8Side{static_cast<uint4*>(row), static_cast<uint2*>(code), static_cast<uint8_t*>(exps),
+                        st[0] / 8, st[1] / 8, x.code[i].st[0] / 8, x.code[i].st[1] / 8, x.code[i].st[2] / 8,
                         x.exp_st[i][0], x.exp_st[i][1]};
   };
   a.k = side(0, k, ks, c.k, c.k_exps);
@@ -107,7 +113,8 @@ int fp8_rows(const fa2_paged_cache_fp8& c, void* k, void* v, const int* slots, c
   a.heads = c.heads;
   a.num_slots = c.num_pages * c.page_size;
   a.page_size = c.page_size;
-  a.chunks_log2 = log2_of(c.head_dim / 16);
+  a.head_dim = c.head_dim;
+  page_division(c.page_size, a.page_magic, a.page_shift);
   a.bf16 = dtype == FA2_BF16;
   return (write ? launch_paged_append_fp8(a, stream) : launch_paged_read_fp8(a, stream)) == 0 ? FA2_OK : FA2_ERR_CUDA;
 }
@@ -230,9 +237,7 @@ int fp8_forward(const fa2_paged_fp8_params& a, void* workspace, size_t workspace
   PagedParams& p = f.p;
   rc = paged_device_status(&p.status);
   if (rc) return rc;
-  // k / page_size without a division (see the 16-bit forward)
-  while ((1ll << p.page_shift) < c.page_size) ++p.page_shift;
-  p.page_magic = (unsigned)(((1ull << 32) * ((1ull << p.page_shift) - (unsigned)c.page_size)) / (unsigned)c.page_size + 1);
+  page_division(c.page_size, p.page_magic, p.page_shift);
   p.box_rows = c.page_size < kPagedKeyTile ? c.page_size : kPagedKeyTile;
   const bool merged_k = merged_side(x.code[0], p.k_side), merged_v = merged_side(x.code[1], p.v_side);
   if (!merged_k || !merged_v) p.box_rows = 8;

@@ -8,9 +8,14 @@
 // fp32, so each value is rounded once, to its code; code * 2^e has four
 // significant bits and is exact in bf16, and in fp16 within e's limits there.
 //
-// Both kernels move 16 codes a thread (32 bytes of 16-bit values), K and V
-// together; a head's row is d / 16 = 4, 8 or 16 neighbouring lanes, which find
-// its maximum by shuffles.  Bound by HBM.
+// Both kernels move 16 values of K and of V a thread and head, as pieces of 8 half
+// a row apart, so that every access of a warp is made of whole runs; a head's row
+// is d / 16 = 4, 8 or 16 neighbouring lanes, which find its maximum by shuffles.
+// Reading is bound by HBM: 32768 rows of 8 heads x 128, 202 MB in 29.2 us (6.9
+// TB/s; two heads a thread, so that enough loads are in flight; one, 32 us;
+// neighbouring pieces a thread, whose stores half-fill their sectors, 41).  Writing
+// is bound by HBM and its instructions together (10 a value; 37 us for the same
+// rows, 44 with indexes computed at run time and every value clamped).
 #include "fa2_paged_fp8.h"
 
 #include <cuda_fp8.h>
@@ -25,20 +30,6 @@ constexpr int kRowThreads = 256;
 // 2^e, -126 <= e <= 127.
 __device__ __forceinline__ float exp2_int(int e) { return __uint_as_float((unsigned)(e + 127) << 23); }
 
-template <bool BF16>
-__device__ __forceinline__ void widen16(const uint4 (&w)[2], float (&x)[16]) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 f = unpack2<BF16>(u[j]);
-      x[8 * i + 2 * j] = f.x;
-      x[8 * i + 2 * j + 1] = f.y;
-    }
-  }
-}
-
 // The row's exponent from its largest |value| (0: a row of zeros).
 template <bool BF16>
 __device__ __forceinline__ int row_exponent(float top) {
@@ -48,90 +39,136 @@ __device__ __forceinline__ int row_exponent(float top) {
   return top == 0.f ? 0 : e;
 }
 
-// 16 codes of the row that `lanes` lanes share; e: its exponent.
+// The largest |value| of a word's two and of `top`'s, packed (a NaN is passed over).
 template <bool BF16>
-__device__ __forceinline__ uint4 quantise16(const uint4 (&w)[2], int lanes, unsigned mask, int& e) {
-  float x[16];
-  widen16<BF16>(w, x);
-  float top = 0.f;
+__device__ __forceinline__ uint32_t max_abs2(uint32_t top, uint32_t w) {
+  const uint32_t m = w & 0x7fff7fffu;
+  if constexpr (BF16) {
+    const __nv_bfloat162 r = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&top), *reinterpret_cast<const __nv_bfloat162*>(&m));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  } else {
+    const __half2 r = __hmax2(*reinterpret_cast<const __half2*>(&top), *reinterpret_cast<const __half2*>(&m));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
+}
+
+// A word's two values within 240 times the last power of two (a NaN stays).
+template <bool BF16>
+__device__ __forceinline__ uint32_t clamp2(uint32_t w) {
+  if constexpr (BF16) {
+    const __nv_bfloat162 hi = __float2bfloat162_rn(240.f * 1152921504606846976.f);   // 240 * 2^60
+    const __nv_bfloat162 r = __hmax2_nan(__hmin2_nan(*reinterpret_cast<const __nv_bfloat162*>(&w), hi), __hneg2(hi));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  } else {
+    const __half2 hi = __float2half2_rn(61440.f);   // 240 * 2^8
+    const __half2 r = __hmax2_nan(__hmin2_nan(*reinterpret_cast<const __half2*>(&w), hi), __hneg2(hi));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
+}
+
+// A thread's 16 values of a row, 8 in each half.
+struct Row16 {
+  uint4 w[2];
+};
+struct Codes16 {
+  uint2 c[2];
+};
+
+// Their codes; the row is shared by LANES lanes.  e: its exponent.
+template <int LANES, bool BF16>
+__device__ __forceinline__ Codes16 quantise16(const Row16& x, unsigned mask, int& e) {
+  uint32_t w[8] = {x.w[0].x, x.w[0].y, x.w[0].z, x.w[0].w, x.w[1].x, x.w[1].y, x.w[1].z, x.w[1].w};
+  uint32_t top2 = 0;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(x[i]));   // a NaN is passed over
-  for (int o = 1; o < lanes; o <<= 1) top = fmaxf(top, __shfl_xor_sync(mask, top, o));
+  for (int i = 0; i < 8; ++i) top2 = max_abs2<BF16>(top2, w[i]);
+#pragma unroll
+  for (int o = 1; o < LANES; o <<= 1) top2 = max_abs2<BF16>(top2, __shfl_xor_sync(mask, top2, o));
+  const float2 tops = unpack2<BF16>(top2);
+  const float top = fmaxf(tops.x, tops.y);
   e = row_exponent<BF16>(top);
-  // at the last exponent codes end at 240: past it fp16 has no value for 2^8 * code
-  const float lim = e == (BF16 ? 60 : 8) ? 240.f : 448.f;
+  // x 2^-e is at most 448 unless e is at its end: there codes end at 240, past
+  // which fp16 has no value for 2^8 code
+  if (top > (BF16 ? 240.f * 1152921504606846976.f : 61440.f)) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = clamp2<BF16>(w[i]);
+  }
   const float f = exp2_int(-e);
   uint32_t c[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    uint32_t u = 0;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      float2 y = make_float2(x[4 * i + 2 * j] * f, x[4 * i + 2 * j + 1] * f);
-      // (a NaN fails both comparisons and stays)
-      y.x = y.x > lim ? lim : y.x < -lim ? -lim : y.x;
-      y.y = y.y > lim ? lim : y.y < -lim ? -lim : y.y;
-      u |= (uint32_t)__nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3) << (16 * j);
-    }
-    c[i] = u;
+    const float2 y = __fmul2_rn(unpack2<BF16>(w[2 * i]), make_float2(f, f));
+    const float2 z = __fmul2_rn(unpack2<BF16>(w[2 * i + 1]), make_float2(f, f));
+    c[i] = (uint32_t)__nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3) |
+           (uint32_t)__nv_cvt_float2_to_fp8x2(z, __NV_SATFINITE, __NV_E4M3) << 16;
   }
-  return make_uint4(c[0], c[1], c[2], c[3]);
+  return Codes16{{make_uint2(c[0], c[1]), make_uint2(c[2], c[3])}};
 }
 
 template <bool BF16>
-__device__ __forceinline__ void values16(const uint4& codes, float f, uint4 (&w)[2]) {
-  const uint32_t c[4] = {codes.x, codes.y, codes.z, codes.w};
-  uint32_t out[8];
+__device__ __forceinline__ uint4 values8(const uint2& codes, float f) {
+  const uint32_t c[2] = {codes.x, codes.y};
+  uint32_t out[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c[i] >> (16 * j)), __NV_E4M3);
-      const float2 y = __half22float2(__half2(h));
-      out[2 * i + j] = pack2<BF16>(y.x * f, y.y * f);
-    }
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c[i >> 1] >> (16 * (i & 1))), __NV_E4M3);
+    const float2 y = __fmul2_rn(__half22float2(__half2(h)), make_float2(f, f));
+    out[i] = pack2<BF16>(y.x, y.y);
   }
-  w[0] = make_uint4(out[0], out[1], out[2], out[3]);
-  w[1] = make_uint4(out[4], out[5], out[6], out[7]);
+  return make_uint4(out[0], out[1], out[2], out[3]);
 }
 
-// Threads x walk the 16-code chunks of a token's heads, threads y and the blocks
-// the tokens.
-template <bool BF16>
+// Page and row of a slot.
+struct SlotAt {
+  long long page, row;
+};
+__device__ __forceinline__ SlotAt slot_at(const PagedFp8RowsArgs& a, int slot) {
+  const int page = (int)((__umulhi((unsigned)slot, a.page_magic) + (unsigned)slot) >> a.page_shift);   // slot / page_size
+  return SlotAt{page, slot - page * a.page_size};
+}
+
+// Threads x walk the pieces of a token's heads, threads y and the blocks the
+// tokens.  (mask: the lanes that share the thread's row, whole rows at any item.)
+template <int LANES, bool BF16>
 __global__ void __launch_bounds__(kRowThreads) fa2_paged_append_fp8_kernel(const PagedFp8RowsArgs a) {
   grid_launch_dependents();
   grid_dependency_wait();
-  const int lanes = 1 << a.chunks_log2, items = a.heads << a.chunks_log2;
+  const int items = a.heads * LANES;
   const int lane = (int)((threadIdx.y * blockDim.x + threadIdx.x) & 31);
-  const unsigned mask = (unsigned)((1ull << lanes) - 1) << (lane & ~(lanes - 1));   // the row's lanes
+  const unsigned mask = (unsigned)((1ull << LANES) - 1) << (lane & ~(LANES - 1));
   const long long t = (long long)blockIdx.x * blockDim.y + threadIdx.y;
   if (t >= a.total) return;
   const int slot = a.slots[t];
+  const uint4 *kr = a.k.rows + t * a.k.row_rs, *vr = a.v.rows + t * a.v.row_rs;
+  const bool skip = slot < 0 || slot >= a.num_slots;
+  const SlotAt s = slot_at(a, skip ? 0 : slot);
+  uint2 *kc = a.k.codes + s.page * a.k.code_ps + s.row * a.k.code_rs, *vc = a.v.codes + s.page * a.v.code_ps + s.row * a.v.code_rs;
+  uint8_t *ke = a.k.exps + s.page * a.k.exp_ps + s.row, *ve = a.v.exps + s.page * a.v.exp_ps + s.row;
   for (int i = (int)threadIdx.x; i < items; i += (int)blockDim.x) {
-    const long long h = i >> a.chunks_log2;
-    const int c = i & (lanes - 1);
-    const uint4* ks = a.k.rows + t * a.k.row_rs + h * a.k.row_hs + 2 * c;
-    const uint4* vs = a.v.rows + t * a.v.row_rs + h * a.v.row_hs + 2 * c;
-    const uint4 x[2] = {ks[0], ks[1]}, y[2] = {vs[0], vs[1]};
-    if (slot < 0 || slot >= a.num_slots) continue;
-    int ke, ve;
-    const uint4 kc = quantise16<BF16>(x, lanes, mask, ke), vc = quantise16<BF16>(y, lanes, mask, ve);
-    const long long page = slot / a.page_size, at = slot % a.page_size;
-    a.k.codes[page * a.k.code_ps + h * a.k.code_hs + at * a.k.code_rs + c] = kc;
-    a.v.codes[page * a.v.code_ps + h * a.v.code_hs + at * a.v.code_rs + c] = vc;
+    const int h = i / LANES, c = i % LANES;
+    const uint4 *ks = kr + (h * a.k.row_hs + c), *vs = vr + (h * a.v.row_hs + c);
+    const Row16 x = {{ks[0], ks[LANES]}}, y = {{vs[0], vs[LANES]}};
+    if (skip) continue;
+    int kx, vx;
+    const Codes16 k = quantise16<LANES, BF16>(x, mask, kx), v = quantise16<LANES, BF16>(y, mask, vx);
+    uint2 *kd = kc + (h * a.k.code_hs + c), *vd = vc + (h * a.v.code_hs + c);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      kd[j * LANES] = k.c[j];
+      vd[j * LANES] = v.c[j];
+    }
     if (c == 0) {
-      a.k.exps[page * a.k.exp_ps + h * a.k.exp_hs + at] = (uint8_t)(ke + 127);
-      a.v.exps[page * a.v.exp_ps + h * a.v.exp_hs + at] = (uint8_t)(ve + 127);
+      ke[h * a.k.exp_hs] = (uint8_t)(kx + 127);
+      ve[h * a.v.exp_hs] = (uint8_t)(vx + 127);
     }
   }
   if (slot >= a.num_slots && threadIdx.x == 0) atomicOr(a.status, kStatusBadPages);
 }
 
-template <bool BF16>
-__global__ void __launch_bounds__(kRowThreads) fa2_paged_read_fp8_kernel(const PagedFp8RowsArgs a) {
+template <int LANES, bool BF16>
+__global__ void __launch_bounds__(kRowThreads, 4) fa2_paged_read_fp8_kernel(const PagedFp8RowsArgs a) {
   grid_launch_dependents();
   grid_dependency_wait();
-  const int lanes = 1 << a.chunks_log2, items = a.heads << a.chunks_log2;
+  const int items = a.heads * LANES, step = (int)blockDim.x;
   const long long t = (long long)blockIdx.x * blockDim.y + threadIdx.y;
   if (t >= a.total) return;
   const int slot = a.slots[t];
@@ -139,42 +176,70 @@ __global__ void __launch_bounds__(kRowThreads) fa2_paged_read_fp8_kernel(const P
     if (slot >= 0 && threadIdx.x == 0) atomicOr(a.status, kStatusBadPages);
     return;
   }
-  const long long page = slot / a.page_size, at = slot % a.page_size;
-  for (int i = (int)threadIdx.x; i < items; i += (int)blockDim.x) {
-    const long long h = i >> a.chunks_log2;
-    const int c = i & (lanes - 1);
-    const uint4 kc = a.k.codes[page * a.k.code_ps + h * a.k.code_hs + at * a.k.code_rs + c];
-    const uint4 vc = a.v.codes[page * a.v.code_ps + h * a.v.code_hs + at * a.v.code_rs + c];
-    const int ke = a.k.exps[page * a.k.exp_ps + h * a.k.exp_hs + at], ve = a.v.exps[page * a.v.exp_ps + h * a.v.exp_hs + at];
-    uint4 x[2], y[2];
-    values16<BF16>(kc, __uint_as_float((unsigned)ke << 23), x);
-    values16<BF16>(vc, __uint_as_float((unsigned)ve << 23), y);
-    uint4* kd = a.k.rows + t * a.k.row_rs + h * a.k.row_hs + 2 * c;
-    uint4* vd = a.v.rows + t * a.v.row_rs + h * a.v.row_hs + 2 * c;
-    kd[0] = x[0];
-    kd[1] = x[1];
-    vd[0] = y[0];
-    vd[1] = y[1];
+  const SlotAt s = slot_at(a, slot);
+  uint4 *kr = a.k.rows + t * a.k.row_rs, *vr = a.v.rows + t * a.v.row_rs;
+  const uint2 *kc = a.k.codes + s.page * a.k.code_ps + s.row * a.k.code_rs, *vc = a.v.codes + s.page * a.v.code_ps + s.row * a.v.code_rs;
+  const uint8_t *ke = a.k.exps + s.page * a.k.exp_ps + s.row, *ve = a.v.exps + s.page * a.v.exp_ps + s.row;
+  for (int i0 = (int)threadIdx.x; i0 < items; i0 += 2 * step) {
+    Codes16 x[2], y[2];
+    unsigned kx[2], vx[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int i = i0 + u * step;
+      if (i >= items) break;
+      const int h = i / LANES, c = i % LANES;
+      const uint2 *ks = kc + (h * a.k.code_hs + c), *vs = vc + (h * a.v.code_hs + c);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        x[u].c[j] = ks[j * LANES];
+        y[u].c[j] = vs[j * LANES];
+      }
+      kx[u] = ke[h * a.k.exp_hs];
+      vx[u] = ve[h * a.v.exp_hs];
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int i = i0 + u * step;
+      if (i >= items) break;
+      const int h = i / LANES, c = i % LANES;
+      uint4 *kd = kr + (h * a.k.row_hs + c), *vd = vr + (h * a.v.row_hs + c);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        kd[j * LANES] = values8<BF16>(x[u].c[j], __uint_as_float(kx[u] << 23));
+        vd[j * LANES] = values8<BF16>(y[u].c[j], __uint_as_float(vx[u] << 23));
+      }
+    }
   }
 }
 
-int launch_rows(void (*kernel)(PagedFp8RowsArgs), const PagedFp8RowsArgs& a, cudaStream_t stream) {
-  const int items = a.heads << a.chunks_log2;
+// each: items a thread.
+int launch_rows(void (*kernel)(PagedFp8RowsArgs), int lanes, int each, const PagedFp8RowsArgs& a, cudaStream_t stream) {
+  const int items = a.heads * lanes;
   int x = 16;   // a row's lanes lie in one warp
-  while (x < kRowThreads && x < items) x *= 2;
+  while (x < kRowThreads && each * x < items) x *= 2;
   const int tokens = kRowThreads / x;   // of a block
   const unsigned blocks = (unsigned)(((long long)a.total + tokens - 1) / tokens);
   return launch_chained(kernel, dim3(blocks), dim3(x, tokens), 0, stream, a);
 }
 
+template <int LANES>
+int launch_append(const PagedFp8RowsArgs& a, cudaStream_t stream) {
+  return launch_rows(a.bf16 ? fa2_paged_append_fp8_kernel<LANES, true> : fa2_paged_append_fp8_kernel<LANES, false>, LANES, 1, a,
+                     stream);
+}
+template <int LANES>
+int launch_read(const PagedFp8RowsArgs& a, cudaStream_t stream) {
+  return launch_rows(a.bf16 ? fa2_paged_read_fp8_kernel<LANES, true> : fa2_paged_read_fp8_kernel<LANES, false>, LANES, 2, a, stream);
+}
+
 }  // namespace
 
 int launch_paged_append_fp8(const PagedFp8RowsArgs& a, cudaStream_t stream) {
-  return launch_rows(a.bf16 ? fa2_paged_append_fp8_kernel<true> : fa2_paged_append_fp8_kernel<false>, a, stream);
+  return a.head_dim == 64 ? launch_append<4>(a, stream) : a.head_dim == 128 ? launch_append<8>(a, stream) : launch_append<16>(a, stream);
 }
 
 int launch_paged_read_fp8(const PagedFp8RowsArgs& a, cudaStream_t stream) {
-  return launch_rows(a.bf16 ? fa2_paged_read_fp8_kernel<true> : fa2_paged_read_fp8_kernel<false>, a, stream);
+  return a.head_dim == 64 ? launch_read<4>(a, stream) : a.head_dim == 128 ? launch_read<8>(a, stream) : launch_read<16>(a, stream);
 }
 
 }  // namespace fa2
