@@ -143,22 +143,31 @@ int launch_paged_append(const PagedAppendArgs& a, cudaStream_t stream);
 // still be writing when this one starts is not constant for this one's
 // lifetime, so it is read with ordinary loads, which stay behind the wait:
 // a read-only load (__ldg, ld.global.nc) may be moved across it.
+// cluster: CTAs of a thread-block cluster (1: none).
 template <class... Params, class... Args>
-int launch_dependent(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
-                     const Args&... args) {
+int launch_dependent_clusters(void (*kernel)(Params...), int cluster, dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                              const Args&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
   if (e != cudaSuccess) cudaGetLastError();   // returned here, not left for the next call that asks
   return (int)e;
+}
+template <class... Params, class... Args>
+int launch_dependent(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                     const Args&... args) {
+  return launch_dependent_clusters(kernel, 1, grid, block, smem, stream, args...);
 }
 
 // launch_dependent, by the name under which the 8-bit cache and shared prefixes

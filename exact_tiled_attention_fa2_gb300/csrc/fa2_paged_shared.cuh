@@ -128,12 +128,13 @@ __device__ __forceinline__ PagedPlace<WIDE> group_place(const PagedParams& p, co
   return r;
 }
 
-// CTAs of `ctas` that take the shared keys, `limit` at most: `group` and `own` are
-// the lines' lengths in keys.
-__device__ __forceinline__ int shared_ctas(const PagedParams& pa, long long group, long long own, int ctas, int limit) {
+// CTAs of `ctas` that take the shared keys, whole units and `limit` at most: `group`
+// and `own` are the lines' lengths in keys.
+__device__ __forceinline__ int shared_ctas(const PagedParams& pa, long long group, long long own, int ctas, int limit,
+                                           int unit) {
   if (group == 0) return 0;
   const float a = (float)group * pa.share_weight, b = (float)own;
-  const int n = (int)rintf((float)ctas * a / (a + b));
+  const int n = max((int)rintf((float)(ctas / unit) * a / (a + b)), 1) * unit;
   const long long most = (group + pa.min_share - 1) / pa.min_share;   // pieces there are
   return max(1, min(min(n, limit), (int)(most < limit ? most : limit)));
 }
@@ -158,14 +159,17 @@ __device__ __forceinline__ void shared_roles(const PagedCtx<C>& t, const PagedPa
 // WA, WB: many rows (PagedConfig) in the pass over the shared keys, over the
 // sequences' own.  Where two CTAs fit an SM they are the two halves of one block
 // here, each a CTA of fa2_paged_kernel with its own shared and tensor memory, and
-// always of the same pass: the code of both on one SM does not fit its
-// instruction caches (64 requests behind 8200 shared keys: CTAs of an SM with one
-// pass end at 48 and 51 us, with both at 71).
+// blocks come in clusters of two, the SMs of a TPC; all of these are of the same
+// pass: the code of both does not fit the instruction caches that they share (128
+// requests behind 32000 shared keys: the shared pass ends at 97 us on TPCs of that
+// pass alone, at 150 beside an SM of the other, at 164 on an SM with both).
 template <int D, bool WA, bool WB>
 struct SharedConfig {
   using A = PagedConfig<D, WA>;
   using B = PagedConfig<D, WB>;
   static constexpr int HALVES = B::CTAS_PER_SM;
+  static constexpr int CLUSTER = 2;
+  static constexpr int UNIT = HALVES * CLUSTER;   // CTAs of one pass together
   static constexpr int HALF_THREADS = A::THREADS > B::THREADS ? A::THREADS : B::THREADS;
   static constexpr int THREADS = HALVES * HALF_THREADS;
   static constexpr uint32_t HALF_BYTES = (B::SMEM_BYTES - 1024 + 1023) / 1024 * 1024;
@@ -217,7 +221,7 @@ __global__ void __launch_bounds__(SharedConfig<D, WA, WB>::THREADS, 1)
   // the line of shared keys: by query tile, or (more than 32 groups, or more query tiles than CTAs) as it falls
   const bool first = blockIdx.x == 0 && half == 0;
   constexpr int SCAN_THREADS = S::HALF_THREADS - 32;
-  const int ctas = (int)gridDim.x * S::HALVES, limit = ctas - S::HALVES;   // at least one block for the other pass
+  const int ctas = (int)gridDim.x * S::HALVES, limit = ctas - S::UNIT;   // the rest for the other pass
   // (each half's last warp looks at the groups while the others sum the sequences)
   PagedScan<WA>* scan_a = reinterpret_cast<PagedScan<WA>*>(smem + A::OFF_SCAN);
   PagedScan<WB>* scan_b = reinterpret_cast<PagedScan<WB>*>(smem + B::OFF_SCAN);
@@ -241,10 +245,10 @@ __global__ void __launch_bounds__(SharedConfig<D, WA, WB>::THREADS, 1)
   }
   tc_fence_after();
   const uint32_t tmem = *tmem_slot + (uint32_t)half * B::TMEM_COLS;
-  int group_ctas = shared_ctas(pa, groups.total, (long long)own_scan.total * LineOf<WB>::KEYS, ctas, limit), pieces = 0;
+  int group_ctas = shared_ctas(pa, groups.total, (long long)own_scan.total * LineOf<WB>::KEYS, ctas, limit, S::UNIT), pieces = 0;
   typename LineOf<WA>::T share = 0;
   if (by_tile) share = group_share<WA>(pa, groups, max(group_ctas, groups.tiles), pieces, group_ctas);
-  const int group_blocks = (group_ctas + S::HALVES - 1) / S::HALVES;
+  const int group_blocks = (group_ctas + S::UNIT - 1) / S::UNIT * S::CLUSTER;
   auto context = [&](auto& t, const PagedParams& p) {
     t.bar0 = sbase + B::OFF_BAR;
     t.sQ = sbase + B::OFF_Q;
@@ -433,8 +437,8 @@ int launch_paged_shared_kernels(const PagedLaunchArgs& shared, const PagedLaunch
   });
   if (e != 0) return e;
   const PagedParams& p = own.p;
-  const int r = launch_chained(kern, dim3((unsigned)(p.ctas / S::HALVES)), S::THREADS, S::SMEM_BYTES, own.stream,
-                               shared.tm_q, own.tm_q, own.tm_k, own.tm_v, shared.p, p);
+  const int r = launch_dependent_clusters(kern, S::CLUSTER, dim3((unsigned)(p.ctas / S::HALVES)), S::THREADS, S::SMEM_BYTES,
+                                          own.stream, shared.tm_q, own.tm_q, own.tm_k, own.tm_v, shared.p, p);
   if (r != 0) return r;
   const long long most = ((long long)p.max_q * p.group + kSharedMergeRows - 1) / kSharedMergeRows * p.heads_kv;
   const dim3 blocks((unsigned)p.batch, (unsigned)(most < 256 ? most : 256));
