@@ -27,10 +27,10 @@ constexpr int paged_ctas(int d) { return d == 256 ? 152 : 304; }
 constexpr int kPagedOverhead = 128;
 constexpr int kPagedMinShare = 128;
 // Shared prefixes: what a key of the shared pass costs, in keys of the sequences'
-// own, with few and with many rows there (64 requests behind 8200 shared keys 66
-// to 68 us at 0.85 .. 1.4, 74 at 0.7; 128 behind 32000: 119 at 0.85, 132 at 1, 158
-// at 1.4; chunks of up to 300 tokens, d = 256: 103 at 1, 91 from 1.2 on).
-constexpr float kSharedWeightFew = 0.85f;
+// own, with few and with many rows there (64 requests behind 8200 shared keys 61 us
+// at 0.7, 56 to 58 at 0.85 .. 1.3, 62 at 2; 128 behind 32000: 118, 110 at 0.9, 127
+// at 1.3; chunks of up to 300 tokens, d = 256: 91 to 1, 81 from 1.15 on).
+constexpr float kSharedWeightFew = 0.9f;
 constexpr float kSharedWeightMany = 1.25f;
 
 int check_cache(const fa2_paged_cache& c, CacheView& k, CacheView& v) {

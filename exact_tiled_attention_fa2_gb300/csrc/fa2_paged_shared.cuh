@@ -292,18 +292,20 @@ __global__ void __launch_bounds__(SharedConfig<D, WA, WB>::THREADS, 1)
   }
 }
 
-// Block (b, y): of sequence b, chunk y of 32 rows of a K/V head, and on by the grid.
-// The first warp finds where the rows' partials are, a row a lane (every warp for
+// Block (b, y): of sequence b's rows, those of one K/V head after those of another,
+// chunk y of `chunk`, and on by the grid.  The first warp finds where the rows' partials are, a row a lane (every warp for
 // itself: 820 instructions a warp, most of a merge's 15 us).  The lanes of a warp
 // are then rows x partials, its columns every eighth run of four, as in
 // fa2_paged_merge_kernel.
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kSharedMergeThreads, D == 256 ? 3 : 4)
-    fa2_paged_shared_merge_kernel(const __grid_constant__ PagedParams shared, const __grid_constant__ PagedParams own) {
+    fa2_paged_shared_merge_kernel(const __grid_constant__ PagedParams shared, const __grid_constant__ PagedParams own,
+                                  int chunk) {
   constexpr int NW = kSharedMergeThreads / 32;
   constexpr int E = D / 4 / NW;   // column runs of a warp
   __shared__ uint2 stage[kSharedMergeRows][D / 4];
   __shared__ SharedRow rows[2][kSharedMergeRows];   // of the sequence's own keys, of the shared ones
+  __shared__ long long o_at[kSharedMergeRows], lse_at[kSharedMergeRows];
   __shared__ OwnRead seq_of;
   const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31;
   const int seq = (int)blockIdx.x, group = own.group, T = own.tile_tokens;
@@ -316,15 +318,13 @@ __global__ void __launch_bounds__(kSharedMergeThreads, D == 256 ? 3 : 4)
     seq_of = q;
   }
   __syncthreads();
-  const int row0 = seq_of.s.a, rows_all = (seq_of.s.b - row0) * group;
+  const int row0 = seq_of.s.a, each = (seq_of.s.b - row0) * group, rows_all = each * own.heads_kv;   // each: of a K/V head
   grid_dependency_wait();   // both passes are complete and visible
   grid_launch_dependents();
-  const int chunks = (rows_all + kSharedMergeRows - 1) / kSharedMergeRows;
-  for (int i = (int)blockIdx.y; i < chunks * own.heads_kv; i += (int)gridDim.y) {
-    const int h = i % own.heads_kv, r0 = i / own.heads_kv * kSharedMergeRows;
-    const int here = min(rows_all - r0, kSharedMergeRows);
+  for (int r0 = (int)blockIdx.y * chunk; r0 < rows_all; r0 += (int)gridDim.y * chunk) {
+    const int here = min(rows_all - r0, chunk);
     if (warp == 0 && lane < here) {
-      const int at = r0 + lane, tok = at / group, in_group = at - tok * group, tile = tok / T;
+      const int h = (r0 + lane) / each, at = r0 + lane - h * each, tok = at / group, in_group = at - tok * group, tile = tok / T;
       rows[0][lane] = shared_row(own, (row0 / T + seq + tile) * own.heads_kv + h, (tok - tile * T) * group + in_group);
       SharedRow x;
       x.count = x.first = x.odd = x.row = 0;
@@ -334,6 +334,9 @@ __global__ void __launch_bounds__(kSharedMergeThreads, D == 256 ? 3 : 4)
                        (g_tok - g_tile * T) * group + in_group);
       }
       rows[1][lane] = x;
+      const long long head = h * group + in_group;
+      o_at[lane] = (long long)(row0 + tok) * own.o_rs + head * own.o_hs;
+      lse_at[lane] = head * own.lse_hs + row0 + tok;
     }
     __syncthreads();
     const int width_log2 = here <= 1 ? 0 : 32 - __clz(here - 1);   // lanes of rows
@@ -407,17 +410,12 @@ __global__ void __launch_bounds__(kSharedMergeThreads, D == 256 ? 3 : 4)
         stage[r][warp + e * NW] = empty ? make_uint2(0u, 0u)
                                         : make_uint2(pack2<BF16>(acc[e].x * inv_l, acc[e].y * inv_l),
                                                      pack2<BF16>(acc[e].z * inv_l, acc[e].w * inv_l));
-      if (warp == 0) {
-        const int at = r0 + r, tok = at / group;
-        own.lse[(long long)(h * group + at - tok * group) * own.lse_hs + row0 + tok] =
-            empty ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
-      }
+      if (warp == 0) own.lse[lse_at[r]] = empty ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
     }
     __syncthreads();
     for (int w = (int)threadIdx.x; w < here * (D / 8); w += kSharedMergeThreads) {
-      const int row = w / (D / 8), c = w % (D / 8), t = (r0 + row) / group;
-      reinterpret_cast<uint4*>(paged_o_row(own, row0 + t, h * group + r0 + row - t * group))[c] =
-          reinterpret_cast<const uint4*>(stage[row])[c];
+      const int row = w / (D / 8), c = w % (D / 8);
+      reinterpret_cast<uint4*>(static_cast<uint16_t*>(own.o) + o_at[row])[c] = reinterpret_cast<const uint4*>(stage[row])[c];
     }
     __syncthreads();
   }
@@ -440,9 +438,13 @@ int launch_paged_shared_kernels(const PagedLaunchArgs& shared, const PagedLaunch
   const int r = launch_dependent_clusters(kern, S::CLUSTER, dim3((unsigned)(p.ctas / S::HALVES)), S::THREADS, S::SMEM_BYTES,
                                           own.stream, shared.tm_q, own.tm_q, own.tm_k, own.tm_v, shared.p, p);
   if (r != 0) return r;
-  const long long most = ((long long)p.max_q * p.group + kSharedMergeRows - 1) / kSharedMergeRows * p.heads_kv;
+  // few rows a block while the blocks fit the GPU at once (four an SM): 2048 rows 58.0 us the call at 4, 59.4 at 8, 70.7 at
+  // 32; 4096 rows 110, 106, 119; 7000 rows of d = 256 96, 86, 81
+  const long long all = (long long)p.total_q * p.group * p.heads_kv;
+  const int chunk = all <= 600 * 4 ? 4 : all <= 600 * 8 ? 8 : kSharedMergeRows;
+  const long long most = ((long long)p.max_q * p.group * p.heads_kv + chunk - 1) / chunk;
   const dim3 blocks((unsigned)p.batch, (unsigned)(most < 256 ? most : 256));
-  return launch_chained(fa2_paged_shared_merge_kernel<D, BF16>, blocks, kSharedMergeThreads, 0, own.stream, shared.p, p);
+  return launch_chained(fa2_paged_shared_merge_kernel<D, BF16>, blocks, kSharedMergeThreads, 0, own.stream, shared.p, p, chunk);
 }
 
 template <int D, bool BF16>
