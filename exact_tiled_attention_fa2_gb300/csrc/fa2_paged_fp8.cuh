@@ -78,6 +78,13 @@ struct Paged8Config {
   static constexpr int N = (NB + 15) / 16 * 16;    // columns of a product (those past NB are not read)
   static constexpr uint32_t Q_BYTES = NB * D;
   static constexpr uint32_t P_BYTES = NB * BC;
+  // P^T with a key's bytes next to each other (no swizzle: 16 bytes of 8 keys are a
+  // block of 128 bytes, N / 16 blocks in a row): a thread writes its eight rows' parts
+  // as three 8-byte words in place of 24 bytes.  With eight rows N is padded to 32
+  // and two CTAs' shared memory has no room for that: there a row's 128 keys are
+  // next to each other, with the 128-byte swizzle.
+  static constexpr bool P_KEYS = R >= 16;
+  static constexpr uint32_t P_GROUP = N / 16 * 128;   // eight keys
   static constexpr int CTAS_PER_SM = D == 256 || R >= 16 ? 1 : 2;
   static constexpr int KSTAGES = R == 32 && D == 256 ? 2 : R >= 16 && D == 128 ? 5 : D == 64 ? 6 - (R == 8) : 3;
   static constexpr int VSTAGES = R == 16 && D == 256 ? 2 : KSTAGES;
@@ -114,6 +121,7 @@ struct Paged8Config {
 // (two exchanges between the softmax warps and a pass over O) is rare.
 constexpr float kFp8RaiseLog2 = 8.f;
 constexpr float kFp8TopLog2 = 4.f;
+constexpr float kFp8NoMax = -1e30f;   // m before a row's first key: finite, so that -inf - m is no NaN
 
 // 2^e; 0 below fp32's normal range.
 __device__ __forceinline__ float pow2_int(int e) { return e < -126 ? 0.f : __uint_as_float((unsigned)(min(e, 127) + 127) << 23); }
@@ -142,8 +150,7 @@ __device__ __forceinline__ void fp8_parts(float2 v, uint32_t (&c)[3]) {
     c[i] = (uint32_t)__nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
     if (i < 2) {
       const float2 back = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)c[i], __NV_E4M3)));
-      v.x = (v.x - back.x) * 16.f;
-      v.y = (v.y - back.y) * 16.f;
+      v = __ffma2_rn(back, make_float2(-16.f, -16.f), __fmul2_rn(v, make_float2(16.f, 16.f)));   // exact
     }
   }
 }
@@ -418,11 +425,11 @@ __device__ __forceinline__ void pg8_load(const Paged8Ctx<C>& t, const PagedFp8Pa
 template <class C>
 __device__ __forceinline__ void pg8_mma(const Paged8Ctx<C>& t) {
   constexpr uint32_t idesc_s = make_idesc_e4m3(C::BC, C::N, false, false);
-  constexpr uint32_t idesc_o = make_idesc_e4m3(C::ROW, C::N, true, false);
+  constexpr uint32_t idesc_o = make_idesc_e4m3(C::ROW, C::N, true, C::P_KEYS);
   const uint64_t dk = make_sdesc(t.base + C::OFF_K, 16, C::GROUP_BYTES, C::LAYOUT);
   const uint64_t dq = make_sdesc(t.base + C::OFF_Q, 16, 8 * C::ROW, C::LAYOUT);
   const uint64_t dv = make_sdesc(t.base + C::OFF_V, 1024, C::GROUP_BYTES, C::LAYOUT);
-  const uint64_t dp = make_sdesc(t.base + C::OFF_P, 16, 1024, 2);
+  const uint64_t dp = C::P_KEYS ? make_sdesc(t.base + C::OFF_P, C::P_GROUP, 128, 0) : make_sdesc(t.base + C::OFF_P, 16, 1024, 2);
   auto wait = [&](int bar, int phase, uint32_t site) -> bool {
     return paged_wait<false>(t.bar(bar), (uint32_t)phase & 1, t.abort_flag, t.status, site);
   };
@@ -463,7 +470,7 @@ __device__ __forceinline__ void pg8_mma(const Paged8Ctx<C>& t) {
 #pragma unroll
           for (int k = 0; k < C::BC / 32; ++k)
             umma_f8_ss(t.tmem + C::TMEM_O + b * C::N, a_v + (uint64_t)((k * 4 * C::GROUP_BYTES + b * 8 * C::ROW) >> 4),
-                       b_p + (uint64_t)((k * 32) >> 4), idesc_o, (j > 0 || k > 0) ? 1u : 0u);
+                       b_p + (uint64_t)((k * (C::P_KEYS ? 4 * C::P_GROUP : 32)) >> 4), idesc_o, (j > 0 || k > 0) ? 1u : 0u);
         umma_commit(t.bar(C::B_O + s));
       }
     }
@@ -501,7 +508,7 @@ __device__ __forceinline__ void pg8_softmax(const Paged8Ctx<C>& t, const PagedFp
     float m[8], l[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      m[i] = -INFINITY;
+      m[i] = kFp8NoMax;
       l[i] = 0.f;
     }
 #pragma unroll 1
@@ -544,9 +551,14 @@ __device__ __forceinline__ void pg8_softmax(const Paged8Ctx<C>& t, const PagedFp
           x[i] = fmaf(fmaf(fmaf(__uint_as_float(c[2][i]), 0.0625f, __uint_as_float(c[1][i])), 0.0625f,
                            __uint_as_float(c[0][i])),
                       fr[i] * key_scale, value_exp);
-          if (!(seen >> i & 1u)) x[i] = -INFINITY;
-          raise |= x[i] > m[i] + kFp8RaiseLog2;
         }
+        if (masked) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (!(seen >> i & 1u)) x[i] = -INFINITY;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) raise |= x[i] > m[i] + kFp8RaiseLog2;
       }
       raise = __any_sync(0xffffffffu, raise);
       if (lane == 0) {
@@ -589,22 +601,32 @@ __device__ __forceinline__ void pg8_softmax(const Paged8Ctx<C>& t, const PagedFp
       }
       // P(g - 2), whose place P(g) takes, has been used
       if (g >= 2 && !wait(C::B_O + (g - 2) % C::VSTAGES, (g - 2) / C::VSTAGES, kSiteSoftmaxO)) return;
-      const uint32_t sP = t.base + C::OFF_P + (uint32_t)(g & 1) * C::P_BYTES + (uint32_t)(r0 * 128 + (tid & 15));
+      uint32_t c[4][3];   // parts of two rows
 #pragma unroll
       for (int i = 0; i < 8; i += 2) {
-        const float m0 = m[i] == -INFINITY ? 0.f : m[i], m1 = m[i + 1] == -INFINITY ? 0.f : m[i + 1];
-        const float2 y = make_float2(ex2_approx(x[i] - m0), ex2_approx(x[i + 1] - m1));
+        const float2 y = make_float2(ex2_approx(x[i] - m[i]), ex2_approx(x[i + 1] - m[i + 1]));
         l[i] = fmaf(y.x, value_inv, l[i]);
         l[i + 1] = fmaf(y.y, value_inv, l[i + 1]);
-        uint32_t c[3];
-        fp8_parts(y, c);
+        fp8_parts(y, c[i / 2]);
+      }
+      if constexpr (C::P_KEYS) {
+        const uint32_t sP = t.base + C::OFF_P + (uint32_t)(g & 1) * C::P_BYTES + (uint32_t)(tid >> 3) * C::P_GROUP +
+                            (uint32_t)(tid & 7) * 16;
 #pragma unroll
         for (int part = 0; part < 3; ++part) {
+          const int at = part * C::R + r0;
+          asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(sP + (uint32_t)(at / 16 * 128 + at % 16)),
+                       "r"(c[0][part] | c[1][part] << 16), "r"(c[2][part] | c[3][part] << 16)
+                       : "memory");
+        }
+      } else {
+        const uint32_t sP = t.base + C::OFF_P + (uint32_t)(g & 1) * C::P_BYTES + (uint32_t)(r0 * 128 + (tid & 15));
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
-            asm volatile("st.shared.u8 [%0], %1;" ::"r"(sP + (uint32_t)((part * C::R + i + k) * 128) +
-                                                        ((uint32_t)((tid >> 4) ^ (i + k)) << 4)),
-                         "r"(c[part] >> (8 * k))
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t at = sP + ((uint32_t)((tid >> 4) ^ i) << 4);
+#pragma unroll
+          for (int part = 0; part < 3; ++part)
+            asm volatile("st.shared.u8 [%0], %1;" ::"r"(at + (uint32_t)((part * C::R + i) * 128)), "r"(c[i / 2][part] >> (8 * (i & 1)))
                          : "memory");
         }
       }
