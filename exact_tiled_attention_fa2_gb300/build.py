@@ -37,7 +37,7 @@ HEADERS = ["fa2_common.cuh", "fa2_tile.cuh", "fa2_fwd_dbuf.cuh", "fa2_bwd.cuh", 
            "fa2_decode.cuh", "fa2_decode_tc.cuh", "fa2_paged.cuh", "fa2_paged.h", "fa2_paged_check.h",
            "fa2_paged_fp8.cuh", "fa2_paged_fp8.h", "fa2_paged_shared.cuh",
            "fa2_internal.h",
-           "sm103_ptx.cuh"]
+           "sm103_ptx.cuh", "sm103_ptx_fp8.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
                      "--expt-relaxed-constexpr"]

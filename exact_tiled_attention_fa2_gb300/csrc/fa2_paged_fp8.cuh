@@ -41,6 +41,7 @@
 
 #include "fa2_paged.cuh"
 #include "fa2_paged_fp8.h"
+#include "sm103_ptx_fp8.cuh"
 
 namespace fa2 {
 
