@@ -1060,22 +1060,6 @@ int encode_map_nd(CUtensorMap* m, const void* base, int rank, const long long* d
   return r == CUDA_SUCCESS ? FA2_OK : FA2_ERR_CUDA;
 }
 
-int encode_map_u8(CUtensorMap* m, const void* base, int rank, const long long* dims, const long long* strides,
-                  const int* box) {
-  cuuint64_t d[5], st[4];
-  cuuint32_t b[5], estr[5] = {1, 1, 1, 1, 1};
-  for (int i = 0; i < rank; ++i) {
-    d[i] = (cuuint64_t)dims[i];
-    b[i] = (cuuint32_t)box[i];
-  }
-  for (int i = 0; i + 1 < rank; ++i) st[i] = (cuuint64_t)(dims[i + 1] > 1 ? strides[i] : dims[0]);
-  const CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, (cuuint32_t)rank, const_cast<void*>(base), d, st, b, estr,
-                              CU_TENSOR_MAP_INTERLEAVE_NONE,
-                              box[0] == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
-                              CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? FA2_OK : FA2_ERR_CUDA;
-}
-
 }  // namespace fa2
 
 extern "C" int fa2_get_device_status(void* stream, uint32_t* detail) {

@@ -184,8 +184,5 @@ int launch_chained(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem
 int paged_device_status(uint32_t** status);
 int encode_map_nd(CUtensorMap* m, const void* base, int rank, const long long* dims, const long long* strides,
                   const int* box, bool bf16);
-// The same of bytes (64- or 128-byte swizzle, as the box's rows).
-int encode_map_u8(CUtensorMap* m, const void* base, int rank, const long long* dims, const long long* strides,
-                  const int* box);
 
 }  // namespace fa2

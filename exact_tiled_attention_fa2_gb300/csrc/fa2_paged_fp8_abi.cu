@@ -1,6 +1,8 @@
 // fa2_paged_fp8_abi.cu -- the entry points of include/fa2.h on a paged cache of
 // 8-bit rows: argument checks, tensor maps and launches.
-#include <cfloat>
+#include <cudaTypedefs.h>
+
+#include <atomic>
 #include <climits>
 #include <cmath>
 #include <cstring>
@@ -177,18 +179,43 @@ bool merged_side(const CacheView& x, PagedSide& side) {
   return true;
 }
 
+// A 5-D map of bytes (64- or 128-byte swizzle, as the box's rows; as encode_map_nd).
+int encode_map_u8(CUtensorMap* m, const void* base, const long long* dims, const long long* strides, const int* box) {
+  static std::atomic<void*> found{nullptr};   // the driver's entry point
+  void* fn = found.load(std::memory_order_acquire);
+  if (!fn) {
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess || !fn)
+      return FA2_ERR_CUDA;
+    found.store(fn, std::memory_order_release);
+  }
+  cuuint64_t d[5], st[4];
+  cuuint32_t b[5], estr[5] = {1, 1, 1, 1, 1};
+  for (int i = 0; i < 5; ++i) {
+    d[i] = (cuuint64_t)dims[i];
+    b[i] = (cuuint32_t)box[i];
+  }
+  for (int i = 0; i < 4; ++i) st[i] = (cuuint64_t)(dims[i + 1] > 1 ? strides[i] : dims[0]);
+  const CUresult r = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn)(
+      m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<void*>(base), d, st, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+      box[0] == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? FA2_OK : FA2_ERR_CUDA;
+}
+
 int cache_map(CUtensorMap* m, const void* at, const CacheView& x, const PagedSide& side, int d, int box_rows) {
   const long long rows = x.dims[2], rs = x.st[2], row = d < 128 ? d : 128;
   if (side.ratio > 0) {
     const long long dims[5] = {row, 8, d / row, rows / 8, side.extent};
     const long long st[4] = {rs, row, 8 * rs, x.dims[1] > 1 ? x.st[1] : x.st[0]};
     const int box[5] = {(int)row, 8, (int)(d / row), box_rows / 8, 1};
-    return encode_map_u8(m, at, 5, dims, st, box);
+    return encode_map_u8(m, at, dims, st, box);
   }
   const long long dims[5] = {row, rows, d / row, x.dims[1], x.dims[0]};
   const long long st[4] = {rs, row, x.st[1], x.st[0]};
   const int box[5] = {(int)row, 8, (int)(d / row), 1, 1};
-  return encode_map_u8(m, at, 5, dims, st, box);
+  return encode_map_u8(m, at, dims, st, box);
 }
 
 int fp8_forward(const fa2_paged_fp8_params& a, void* workspace, size_t workspace_bytes, cudaStream_t stream) {

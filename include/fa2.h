@@ -553,7 +553,8 @@ typedef struct fa2_paged_cache_fp8 {
 
 /*
  * fa2_paged_append_fp8 -- new 16-bit key/value rows into a cache of 8-bit
- * rows, quantised as they are written; slots as fa2_paged_append.  Each row's
+ * rows, quantised as they are written; slots as fa2_paged_append (of two rows with
+ * one slot, which one's codes and exponent remain is not determined).  Each row's
  * exponent e = u - 127 is the smallest with max |x| <= 448 * 2^e (448: the
  * largest code), within -60 .. 60 (bf16) or -15 .. 8 (fp16); 0 for a row of
  * zeros.  Its codes are x * 2^-e rounded to the nearest e4m3 value (ties to
@@ -653,7 +654,7 @@ size_t fa2_paged_fp8_params_size(void);
 /*
  * fa2_paged_fwd_shared -- fa2_paged_fwd (full or causal attention) for a batch
  * whose sequences share the first pages of their prompts.  Group g is sequences
- * cu_groups[g] <= b < cu_groups[g+1]; the first shared_lens[g] keys of all of
+ * cu_groups[g] <= b < cu_groups[g+1] (cu_groups does not decrease); the first shared_lens[g] keys of all of
  * them are the same, held by the same pages: their block-table rows begin
  * with the same shared_lens[g] / page_size entries, which are read from the row
  * of the group's first sequence (also if that one is idle).  These keys lie
@@ -671,9 +672,10 @@ size_t fa2_paged_fp8_params_size(void);
  * out of range or reaches into the sequence's new tokens, or whose query rows
  * do not lie between those of the group's first and last, is left unwritten and
  * reported as FA2_ERR_DEVICE_SEQLENS.  Two kernels, asynchronous on `stream`; the
- * host reads no length.  Deterministic.  The workspace holds the fp32 state
- * of every query row of both passes, about 16 bytes per element of q while
- * decoding; overlaps, captures and errors as fa2_paged_fwd.
+ * host reads no length.  Deterministic.  The workspace holds fp32 partial states
+ * of every query row in both passes and of the rows where a CTA's share of the
+ * keys ends: 44 MB for 64 decoding requests of 32 heads of 128, 185 MB beside a
+ * chunk of 2048 tokens.  Overlaps, captures and errors as fa2_paged_fwd.
  */
 typedef struct fa2_paged_shared_params {
   fa2_paged_params fwd;

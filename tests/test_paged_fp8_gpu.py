@@ -320,10 +320,11 @@ class Problem:
         exps = self.cache[2 + i][page_of, :, at].double() - 127
         return torch.from_numpy(VALUES).cuda()[codes].transpose(0, 1), exps.T
 
-    def check(self, o, lse, scale=None, window_left=-1, window_right=-1, prefix_len=0, sink_len=0, skip=()):
+    def check(self, o, lse, scale=None, window_left=-1, window_right=-1, prefix_len=0, sink_len=0, skip=(), u=None,
+              e_max=None):
         d, group = self.d, self.hq // self.hkv
         scale = 1.0 / d ** 0.5 if scale is None else scale
-        u = torch.finfo(o.dtype).eps / 2
+        u = torch.finfo(o.dtype).eps / 2 if u is None else u
         row = 0
         for b, (n, n_k) in enumerate(zip(self.lens_q, self.lens_k)):
             if b in skip or n == 0:
@@ -350,7 +351,7 @@ class Problem:
                 lost = 2.0 ** -25 * q.abs().amax(-1) * (k.abs().sum(-1)[:, None].masked_fill(hidden, 0.0)).amax(-1)
                 ds = abs(scale) * (1.07 * d * 2.0 ** -23 * size + lost)
                 n_vis = (~hidden).sum(-1).double()[None, :]
-                small = 2.0 ** -18 + 2.0 ** -23 * ve.abs().max()
+                small = 2.0 ** -18 + 2.0 ** -23 * (ve.abs().max() if e_max is None else e_max)
                 floor = 2.0 ** -22 * (p * unit[:, None]).amax(-1)[..., None] * ((~hidden).double() @ vc.abs())
                 tol = u * ref_o.abs() + floor + 1e-7 + a * (
                     2.0 ** -12 + 2 * ds + 2 * n_vis * 2.0 ** -23 + small)[..., None]
@@ -432,6 +433,27 @@ def test_sink_of_large_weight_and_small_values(d):
     o, lse = p.run(window_right=0)
     assert status() == fa2.FA2_OK
     p.check(o, lse, window_right=0)
+
+
+@pytest.mark.parametrize("low,high", [(-58, -50), (40, 52), (-60, 52)])
+def test_exponents_far_from_zero(low, high):
+    """Values whose rows' exponents lie near the ends, or far apart: L counts every key, O what its values weigh."""
+    n, d = 700, 128
+    p = Problem([1, 2], [n, 300], 4, 2, d, "bf16", 16, seed=17)
+    g = gen(18)
+    for b, m in ((0, n), (1, 300)):
+        j = torch.arange(m, device="cuda")
+        size = torch.randint(low, high + 1, (m, 2, 1), generator=g, device="cuda").float()
+        k = torch.randn((m, 2, d), generator=g, device="cuda").bfloat16()
+        v = (torch.randn((m, 2, d), generator=g, device="cuda") * torch.exp2(size + 6)).bfloat16()
+        slots = (p.table[b, j // 16].long() * 16 + j % 16).to(torch.int32)
+        fa2.fa2_paged_append_fp8(k, v, slots, *p.cache)
+    o, lse = p.run(window_right=0)
+    assert status() == fa2.FA2_OK
+    # (relative to the output's size: the check's own floor of 1e-7 would hide values of 2^-50)
+    unit = 2.0 ** -high
+    p.cache[3] = (p.cache[3].int() - high).clamp(0, 254).to(torch.uint8)
+    p.check((o.double() * unit).float(), lse, window_right=0, u=torch.finfo(torch.bfloat16).eps / 2, e_max=60)
 
 
 @pytest.mark.parametrize("scale", [0.0, -0.3, 1.0, 1e-4])

@@ -118,6 +118,31 @@ def test_a_long_prefix_and_many_rows():
         p.check(o, lse, window_right=0)
 
 
+@pytest.mark.parametrize("hkv,tokens,batch", [(1, 62, 5), (2, 3, 70), (1, 302, 1)])
+def test_more_query_tiles_of_groups_than_ctas(hkv, tokens, batch):
+    """128 query heads a K/V head: every token is a query tile, and the groups have more of them than there are CTAs."""
+    groups, new = ([(batch, 200)] if batch > 1 else [(1, 200)]), [tokens] * batch
+    p = Shared(new, lens_of(groups, [2] * batch, new), groups, 128 * hkv, hkv, 64, "bf16", 16, seed=tokens)
+    o, lse = p.run()
+    assert status() == fa2.FA2_OK
+    p.check(o, lse, window_right=0)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_many_groups_of_several_lengths(d):
+    """Up to 32 groups are laid out by query tile, more as they fall on the line."""
+    r = np.random.RandomState(d)
+    for n in (5, 32, 33, 90):
+        groups = [(int(r.randint(1, 4)), int(r.randint(0, 900))) for _ in range(n)]
+        batch = sum(g for g, _ in groups)
+        new = [int(x) for x in r.randint(0, 4, batch)]
+        own = [int(x) for x in r.randint(0, 100, batch)]
+        p = Shared(new, lens_of(groups, own, new), groups, 6, 2, d, "bf16", 32, seed=n)
+        o, lse = p.run()
+        assert status() == fa2.FA2_OK
+        p.check(o, lse, window_right=0)
+
+
 def test_equals_the_forward_that_shares_nothing():
     groups, new = [(6, 2000)], [1] * 6
     p = Shared(new, lens_of(groups, [10 * i for i in range(6)], new), groups, 8, 2, 128, "bf16", 16, seed=3)
