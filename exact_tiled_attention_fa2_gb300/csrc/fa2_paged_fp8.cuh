@@ -29,12 +29,21 @@
 // loses nothing: exponents differ by 120 at most.
 //
 // Schedule, fragments and merging of cut pairs are the 16-bit kernel's
-// (fa2_paged.cuh); a step here is two of its 64-key tiles.  One CTA: four softmax
+// (fa2_paged.cuh); a step here is two of its 64-key tiles, and pairs always lie on
+// the line: with one CTA an SM nothing would overlap a pair's start and end (8
+// chunks of 512 tokens over 4096 keys, d = 128: 1104 us, a CTA a pair 1489).  One CTA: four softmax
 // warps for every eight rows of a tile (a thread has one key and eight rows), the
 // MMA thread, the TMA warp (keys, values, exponents), and the planner, which
 // walks the fragments and prepares their q parts.  What runs seldom is rolled or
 // shared: a call's code comes to each SM once, and with one thread for 32 rows,
 // four times the code, a call began 50 us later.
+//
+// Bounds.  Decoding: HBM (64 requests of 1000 .. 32000 keys, 8 K/V heads of 128:
+// 331 us, 6.6 TB/s); below some thousand keys a CTA the start (6 us) and the merge
+// (4 us).  With 32 rows a tile the softmax warps' instructions: 350 a step and
+// warp, 60 % of the issue slots (128 requests x heads of 8192 keys, d = 128: 91 us
+// at 32 rows, 76 at 16, 70 at 4; a chunk of 2048 tokens over 16384 keys 1750 us,
+// 334 TFLOP/s).
 #pragma once
 
 #include <cuda_fp8.h>
@@ -505,12 +514,12 @@ __device__ __forceinline__ void pg8_softmax(const Paged8Ctx<C>& t, const PagedFp
     const TileMask tmask = f->tm;
     const float4* factor = reinterpret_cast<const float4*>(t.smem + C::OFF_FACTOR + ((nf & 1) * C::R + r0) * 4);
     const float4 f0 = factor[0], f1 = factor[1];
-    const float fr[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
-    float m[8], l[8];
+    const float2 fr[4] = {make_float2(f0.x, f0.y), make_float2(f0.z, f0.w), make_float2(f1.x, f1.y), make_float2(f1.z, f1.w)};
+    float2 neg_m[4], l[4];   // -m and the sums, rows in pairs
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      m[i] = kFp8NoMax;
-      l[i] = 0.f;
+    for (int i = 0; i < 4; ++i) {
+      neg_m[i] = make_float2(-kFp8NoMax, -kFp8NoMax);
+      l[i] = make_float2(0.f, 0.f);
     }
 #pragma unroll 1
     for (int j = 0; j < steps; ++j, ++g) {
@@ -536,10 +545,10 @@ __device__ __forceinline__ void pg8_softmax(const Paged8Ctx<C>& t, const PagedFp
       const uint8_t* e = t.smem + C::OFF_EXP + (g & 7) * 256 + tid;
       const int ev = (int)e[128] - 127;
       const float key_scale = __uint_as_float((unsigned)e[0] << 23), value_exp = (float)ev, value_inv = pow2_int(-ev);
+      // S(g), which was asked for after PV(g - 2): P(g - 2), whose place P(g) takes, has been used
       if (!wait(C::B_S + g % C::KSTAGES, g / C::KSTAGES, kSiteSoftmaxS)) return;
       tc_fence_after();
-      float x[8];
-      bool raise = false;   // a row's m
+      float2 x[4];
       {
         const uint32_t tS = t.tmem + lane_off + C::TMEM_S + (uint32_t)(g & 1) * C::N + r0;
         uint32_t c[3][8];
@@ -547,42 +556,59 @@ __device__ __forceinline__ void pg8_softmax(const Paged8Ctx<C>& t, const PagedFp
         for (int i = 0; i < 3; ++i) tmem_ld_32x32b_x8(tS + i * C::R, c[i]);
 #pragma unroll
         for (int i = 0; i < 3; ++i) tmem_ld_wait_x8(c[i]);
+        const float2 down = make_float2(0.0625f, 0.0625f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          x[i] = fmaf(fmaf(fmaf(__uint_as_float(c[2][i]), 0.0625f, __uint_as_float(c[1][i])), 0.0625f,
-                           __uint_as_float(c[0][i])),
-                      fr[i] * key_scale, value_exp);
+        for (int i = 0; i < 4; ++i) {
+          auto two = [&](int part) { return make_float2(__uint_as_float(c[part][2 * i]), __uint_as_float(c[part][2 * i + 1])); };
+          x[i] = __ffma2_rn(__ffma2_rn(__ffma2_rn(two(2), down, two(1)), down, two(0)),
+                            __fmul2_rn(fr[i], make_float2(key_scale, key_scale)), make_float2(value_exp, value_exp));
         }
         if (masked) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (!(seen >> i & 1u)) x[i] = -INFINITY;
+          for (int i = 0; i < 4; ++i) {
+            if (!(seen >> (2 * i) & 1u)) x[i].x = -INFINITY;
+            if (!(seen >> (2 * i + 1) & 1u)) x[i].y = -INFINITY;
+          }
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) raise |= x[i] > m[i] + kFp8RaiseLog2;
       }
-      raise = __any_sync(0xffffffffu, raise);
+      auto over = [&]() {   // of the rows' scores over their m, the largest (a NaN is passed over)
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 y = __fadd2_rn(x[i], neg_m[i]);
+          top = fmaxf(top, fmaxf(y.x, y.y));
+        }
+        return top;
+      };
+      const bool raise = __any_sync(0xffffffffu, over() > kFp8RaiseLog2);
       if (lane == 0) {
         s_vote[4 * (g & 1) + quad] = raise;
         mbar_arrive(t.bar(P8_VOTE + rg));
       }
       if (!wait(P8_VOTE + rg, g, kSiteSoftmaxO)) return;
       if (*reinterpret_cast<volatile uint32_t*>(t.smem + C::OFF_VOTE + rg * 8 + 4 * (g & 1)) != 0) {
-        const float mine = warp_rows(x, lane, [](float u, float v) { return fmaxf(u, v); });   // (a NaN is passed over)
+        const float rows8[8] = {x[0].x, x[0].y, x[1].x, x[1].y, x[2].x, x[2].y, x[3].x, x[3].y};
+        const float mine = warp_rows(rows8, lane, [](float u, float v) { return fmaxf(u, v); });
         if ((lane & 3) == 0) s_max[quad * 8 + warp_row(lane)] = mine;
         __syncwarp();
         if (lane == 0) mbar_arrive(t.bar(P8_X + rg));
         if (!wait(P8_X + rg, x_phase, kSiteSoftmaxO)) return;
         ++x_phase;
         float alpha[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        auto up = [&](int i, float& neg) {
           const float top = fmaxf(fmaxf(s_max[i], s_max[8 + i]), fmaxf(s_max[16 + i], s_max[24 + i]));
-          const bool up = top > m[i] + kFp8RaiseLog2;
-          const float m_new = up ? top - kFp8TopLog2 : m[i];
-          alpha[i] = up ? ex2_approx(m[i] - m_new) : 1.f;
-          m[i] = m_new;
-          l[i] *= alpha[i];
+          alpha[i] = 1.f;
+          if (top + neg > kFp8RaiseLog2) {
+            const float neg_new = kFp8TopLog2 - top;
+            alpha[i] = ex2_approx(neg_new - neg);
+            neg = neg_new;
+          }
+        };
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          up(2 * i, neg_m[i].x);
+          up(2 * i + 1, neg_m[i].y);
+          l[i] = __fmul2_rn(l[i], make_float2(alpha[2 * i], alpha[2 * i + 1]));
         }
         if (j > 0) {
           if (!wait(C::B_O + (g - 1) % C::VSTAGES, (g - 1) / C::VSTAGES, kSiteSoftmaxO)) return;
@@ -600,15 +626,13 @@ __device__ __forceinline__ void pg8_softmax(const Paged8Ctx<C>& t, const PagedFp
           tmem_st_wait();
         }
       }
-      // P(g - 2), whose place P(g) takes, has been used
-      if (g >= 2 && !wait(C::B_O + (g - 2) % C::VSTAGES, (g - 2) / C::VSTAGES, kSiteSoftmaxO)) return;
       uint32_t c[4][3];   // parts of two rows
 #pragma unroll
-      for (int i = 0; i < 8; i += 2) {
-        const float2 y = make_float2(ex2_approx(x[i] - m[i]), ex2_approx(x[i + 1] - m[i + 1]));
-        l[i] = fmaf(y.x, value_inv, l[i]);
-        l[i + 1] = fmaf(y.y, value_inv, l[i + 1]);
-        fp8_parts(y, c[i / 2]);
+      for (int i = 0; i < 4; ++i) {
+        float2 y = __fadd2_rn(x[i], neg_m[i]);
+        y = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+        l[i] = __ffma2_rn(y, make_float2(value_inv, value_inv), l[i]);
+        fp8_parts(y, c[i]);
       }
       if constexpr (C::P_KEYS) {
         const uint32_t sP = t.base + C::OFF_P + (uint32_t)(g & 1) * C::P_BYTES + (uint32_t)(tid >> 3) * C::P_GROUP +
@@ -651,15 +675,17 @@ __device__ __forceinline__ void pg8_softmax(const Paged8Ctx<C>& t, const PagedFp
       if (lane == 0) mbar_arrive(t.bar(P8_P + (g & 1)));
     }
     // the rows' sums over all keys: over the lanes, then over the four warps
+    float sum[8] = {};
     if (n > 0) {
-      const float mine = warp_rows(l, lane, [](float u, float v) { return u + v; });
+      const float rows8[8] = {l[0].x, l[0].y, l[1].x, l[1].y, l[2].x, l[2].y, l[3].x, l[3].y};
+      const float mine = warp_rows(rows8, lane, [](float u, float v) { return u + v; });
       if ((lane & 3) == 0) s_sum[quad * 8 + warp_row(lane)] = mine;
       __syncwarp();
       if (lane == 0) mbar_arrive(t.bar(P8_X + rg));
       if (!wait(P8_X + rg, x_phase, kSiteEpilogueO)) return;
       ++x_phase;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) l[i] = (s_sum[i] + s_sum[8 + i]) + (s_sum[16 + i] + s_sum[24 + i]);
+      for (int i = 0; i < 8; ++i) sum[i] = (s_sum[i] + s_sum[8 + i]) + (s_sum[16 + i] + s_sum[24 + i]);
       if (!wait(C::B_O + (g - 1) % C::VSTAGES, (g - 1) / C::VSTAGES, kSiteEpilogueO)) return;
       tc_fence_after();
     }
@@ -668,7 +694,7 @@ __device__ __forceinline__ void pg8_softmax(const Paged8Ctx<C>& t, const PagedFp
       const bool has_d = C::ROW == 128 || lane < 16;   // (64 rows of O^T lie in 16 lanes of each warp)
       float inv[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) inv[i] = slot >= 0 ? 1.f : l[i] == 0.f ? 0.f : 1.f / l[i];   // 0: sees no key (a NaN sum is no such row's)
+      for (int i = 0; i < 8; ++i) inv[i] = slot >= 0 ? 1.f : sum[i] == 0.f ? 0.f : 1.f / sum[i];   // 0: sees no key (a NaN sum is no such row's)
       const long long wrap = p.o_rs - (long long)(p.group - 1) * p.o_hs;   // from a token's last head to the next token's first
 #pragma unroll 1
       for (int b = 0; b < C::BLOCKS; ++b) {
@@ -685,7 +711,7 @@ __device__ __forceinline__ void pg8_softmax(const Paged8Ctx<C>& t, const PagedFp
         for (int i = 0; i < 8; ++i) {
           const float o = fmaf(fmaf(__uint_as_float(c[2][i]), 0.0625f, __uint_as_float(c[1][i])), 0.0625f,
                                __uint_as_float(c[0][i]));
-          const float y = l[i] == 0.f ? 0.f : o * inv[i];
+          const float y = sum[i] == 0.f ? 0.f : o * inv[i];
           if (i < rows && has_d) {
             if (slot >= 0)
               part[4 * i] = y;
@@ -697,11 +723,11 @@ __device__ __forceinline__ void pg8_softmax(const Paged8Ctx<C>& t, const PagedFp
           head = last ? 0 : head;
         }
       }
-      float my_m = m[0], my_l = l[0];
+      float my_m = 0.f, my_l = 0.f;
 #pragma unroll
-      for (int i = 1; i < 8; ++i) {
-        my_m = lane == i ? m[i] : my_m;
-        my_l = lane == i ? l[i] : my_l;
+      for (int i = 0; i < 8; ++i) {
+        my_m = lane == i ? -(i & 1 ? neg_m[i / 2].y : neg_m[i / 2].x) : my_m;
+        my_l = lane == i ? sum[i] : my_l;
       }
       if (quad == 0 && lane < min(rows, 8)) {
         const int r = r0 + lane;
@@ -818,9 +844,7 @@ int launch_paged_fp8_kernels(const PagedFp8LaunchArgs& x) {
   });
   if (e != 0) return e;
   const PagedParams& p = x.a.p;
-  const int waves = MANY ? (p.pair_ctas + p.ctas - 1) / p.ctas : 1;
-  const int grid = p.ctas * (waves > 1 ? waves : 1);
-  const int r = launch_chained(kern, dim3((unsigned)grid), C::THREADS, C::SMEM_BYTES, x.stream, x.tm_k, x.tm_v, x.a);
+  const int r = launch_chained(kern, dim3((unsigned)p.ctas), C::THREADS, C::SMEM_BYTES, x.stream, x.tm_k, x.tm_v, x.a);
   if (r != 0) return r;
   return launch_paged_fp8_merge<D>(p, x.a.bf16 != 0, x.stream);
 }

@@ -15,7 +15,12 @@
 namespace fa2 {
 namespace {
 
-// A pair's fixed cost and the shortest piece worth a CTA, in keys.
+// In keys: a pair's fixed cost (32 requests of 1 .. 8192 keys, d = 128: 57 us at
+// 128, 54.3, 55.5 at 512; 8 requests of 5 tokens, d = 64: 21.2, 20.3, 19.0; windows
+// of 1023 at d = 256: 40.4, 40.5, 49.3), the shortest piece worth a CTA (128 and
+// 512 within 0.3 us of 256, but one request of 600 keys 10.7 and 13.4 against 11.2)
+// and what a merge may cost before pairs are left whole (the windows 51 us at 256,
+// 40.4 from 512 to 2048; the 8 requests 20.2, 20.3 and at 2048 22.0).
 constexpr int kFp8Overhead = 256;
 constexpr int kFp8MinShare = 256;
 constexpr int kFp8MergeCost = 512;
@@ -123,7 +128,7 @@ int fp8_rows(const fa2_paged_cache_fp8& c, void* k, void* v, const int* slots, c
 
 struct Fp8Shape {
   int group, parts, tile_tokens, box_tokens, max_q, slot_rows;
-  int ctas, pair_ctas;
+  int ctas;
   size_t ws_o_bytes, ws_ml_bytes, ws_bytes;
   bool many;
 };
@@ -154,9 +159,11 @@ int fp8_shape(const fa2_paged_fp8_params& a, Fp8Shape& s) {
   if (pairs > INT_MAX - 1024 || (long long)c.heads * s.parts > INT_MAX) return FA2_ERR_UNSUPPORTED;
   s.many = s.max_q > T || (double)a.batch * c.heads * s.parts *
                                   (((double)a.max_pages * c.page_size + kFp8Overhead) / 64 + 2.0) + 1e6 > 2147483647.0;
-  // one wave of the resident CTAs of a GB300's 152 SMs, fixed (see paged_ctas)
+  // One wave of the resident CTAs of a GB300's 152 SMs, fixed (see paged_ctas): two
+  // an SM with up to eight rows (32 requests of 1 .. 8192 keys: 70 us, with one CTA
+  // and deeper rings 88, from an empty L2 cache), one with more (16 requests of 8192
+  // keys, 16 rows: 80 us, with two CTAs 90)
   s.ctas = c.head_dim == 256 || s.many || s.slot_rows > 8 ? 152 : 304;
-  s.pair_ctas = pairs >= s.ctas ? (int)pairs : 0;
   const size_t rows = 2 * (size_t)s.ctas * (size_t)s.slot_rows;
   s.ws_o_bytes = align256(rows * (size_t)c.head_dim * 4);
   s.ws_ml_bytes = align256(rows * 2 * 4);
@@ -309,8 +316,7 @@ int fp8_forward(const fa2_paged_fp8_params& a, void* workspace, size_t workspace
   p.slot_rows = s.slot_rows;
   p.overhead = kFp8Overhead;
   p.ctas = s.ctas;
-  p.pair_ctas = s.pair_ctas;
-  p.cached_keys = (96 << 20) / (2 * c.head_dim);   // 96 of the 126 MB
+  p.pair_ctas = 0;   // (never a CTA a pair)
   p.min_share = kFp8MinShare;
   p.merge_cost = kFp8MergeCost;
   p.ws_o = static_cast<float*>(workspace);
