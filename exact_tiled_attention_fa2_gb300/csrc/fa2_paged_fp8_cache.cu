@@ -11,11 +11,13 @@
 // Both kernels move 16 values of K and of V a thread and head, as pieces of 8 half
 // a row apart, so that every access of a warp is made of whole runs; a head's row
 // is d / 16 = 4, 8 or 16 neighbouring lanes, which find its maximum by shuffles.
-// Reading is bound by HBM: 32768 rows of 8 heads x 128, 202 MB in 29.2 us (6.9
+// Reading is bound by HBM: 32768 rows of 8 heads x 128, 202 MB in 29 to 31 us (6.7
 // TB/s; two heads a thread, so that enough loads are in flight; one, 32 us;
 // neighbouring pieces a thread, whose stores half-fill their sectors, 41).  Writing
-// is bound by HBM and its instructions together (10 a value; 37 us for the same
-// rows, 44 with indexes computed at run time and every value clamped).
+// is bound by HBM and its instructions together: the same rows in 33 us (37 with
+// 80 registers and three blocks an SM, 44 with indexes computed at run time and
+// every value clamped; both ways 65.3 us with six blocks, 69.5 with three, 71.5 with
+// seven, whose registers spill).
 #include "fa2_paged_fp8.h"
 
 #include <cuda_fp8.h>
@@ -129,7 +131,7 @@ __device__ __forceinline__ SlotAt slot_at(const PagedFp8RowsArgs& a, int slot) {
 // Threads x walk the pieces of a token's heads, threads y and the blocks the
 // tokens.  (mask: the lanes that share the thread's row, whole rows at any item.)
 template <int LANES, bool BF16>
-__global__ void __launch_bounds__(kRowThreads) fa2_paged_append_fp8_kernel(const PagedFp8RowsArgs a) {
+__global__ void __launch_bounds__(kRowThreads, 6) fa2_paged_append_fp8_kernel(const PagedFp8RowsArgs a) {
   grid_launch_dependents();
   grid_dependency_wait();
   const int items = a.heads * LANES;
