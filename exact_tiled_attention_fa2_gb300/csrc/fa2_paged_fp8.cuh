@@ -40,8 +40,8 @@
 //
 // Bounds.  Decoding: HBM (64 requests of 1000 .. 32000 keys, 8 K/V heads of 128:
 // 331 us, 6.6 TB/s); below some thousand keys a CTA the start (6 us) and the merge
-// (4 us).  With 32 rows a tile the softmax warps' instructions: 350 a step and
-// warp, 60 % of the issue slots (128 requests x heads of 8192 keys, d = 128: 91 us
+// (4 us).  With 32 rows a tile the softmax warps' instructions: 340 a step and
+// warp, 57 % of the issue slots (128 requests x heads of 8192 keys, d = 128: 91 us
 // at 32 rows, 76 at 16, 70 at 4; a chunk of 2048 tokens over 16384 keys 1750 us,
 // 334 TFLOP/s).
 #pragma once
@@ -228,7 +228,8 @@ __device__ __forceinline__ void pg8_q_parts(const Paged8Ctx<C>& t, const PagedFp
       top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
       // largest value f 2^n, f in [1, 2): scaled by 2^(7 - n)
       const int field = min(261 - (int)(__float_as_uint(top) >> 23), 253);   // of 2^(7 - n)
-      const float up = __uint_as_float((unsigned)field << 23);
+      // (an infinity's products are NaN or infinite, and its row is NaN either way)
+      const float up = __uint_as_float(__float_as_uint(top) >= 0x7f800000u ? 0x7fffffffu : (unsigned)field << 23);
       if (lane == 0) factor[r] = a.scale_log2 * __uint_as_float((unsigned)(254 - field) << 23);
       uint32_t parts[3][W];
 #pragma unroll

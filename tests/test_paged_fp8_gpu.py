@@ -540,6 +540,27 @@ def test_a_nan_makes_its_row_nan():
     assert torch.isfinite(o[0]).all() and torch.isfinite(o[1, :3]).all() and torch.isfinite(o[2, 2:]).all()
 
 
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("value", [float("inf"), float("-inf")])
+def test_an_infinity_in_a_query_row_makes_it_nan(dtype, value):
+    p = Problem([3, 1], [300, 40], 4, 2, 64, dtype, 16, seed=9)
+    p.q[1, 2, 60] = value
+    o, lse = p.run(window_right=0)
+    assert status() == fa2.FA2_OK
+    assert torch.isnan(o[1, 2]).all() and torch.isnan(lse[2, 1])
+    o[1, 2], lse[2, 1] = 0, 0
+    assert torch.isfinite(o).all() and torch.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("d,mask", [(64, "causal"), (128, "window"), (256, "causal"), (128, "sinks")])
+def test_more_pairs_than_ctas(d, mask):
+    """Chunks whose pairs of query tile and head are several for each CTA, between decoding and idle requests."""
+    p = Problem([700, 1, 0, 333, 5], [900, 500, 9, 333, 1200], 8, 8, d, "bf16", 32, seed=11)
+    o, lse = p.run(**MASKS[mask])
+    assert status() == fa2.FA2_OK
+    p.check(o, lse, **MASKS[mask])
+
+
 def test_rows_outside_sequences_are_left_and_runs_repeat():
     p = Problem([2, 0, 3], [77, 10, 2000], 4, 1, 128, "fp16", 16, seed=10)
     q = torch.cat([p.q, p.q[:3]])
