@@ -41,9 +41,9 @@
 // Bounds.  Decoding: HBM (64 requests of 1000 .. 32000 keys, 8 K/V heads of 128:
 // 331 us, 6.6 TB/s); below some thousand keys a CTA the start (6 us) and the merge
 // (4 us).  With 32 rows a tile the softmax warps' instructions: 340 a step and
-// warp, 57 % of the issue slots (128 requests x heads of 8192 keys, d = 128: 91 us
-// at 32 rows, 76 at 16, 70 at 4; a chunk of 2048 tokens over 16384 keys 1750 us,
-// 334 TFLOP/s).
+// warp, 57 % of the issue slots (128 requests x heads of 8192 keys, d = 128: 82 us
+// at 32 rows, 75 at 16, 70 at 4; a chunk of 2048 tokens over 16384 keys 1712 us,
+// 341 TFLOP/s).
 #pragma once
 
 #include <cuda_fp8.h>
@@ -65,7 +65,8 @@ enum : int {
   P8_X = 18,       // + row group: their maxima, or their sums
   P8_EXIT = 22,
   P8_EXP = 23,     // + g & 7: the exponents of step g are there (16 lanes)
-  P8_RINGS = 31,   // S complete (K stages), PV complete (V stages), K landed, V landed
+  P8_HELP = 31,    // the first fragment's q parts are written (the warps that do)
+  P8_RINGS = 32,   // S complete (K stages), PV complete (V stages), K landed, V landed
 };
 
 template <int D_, int R_, bool MANY_>
@@ -75,6 +76,10 @@ struct Paged8Config {
   static constexpr bool MANY = MANY_;
   static constexpr int BC = 128;         // keys of a step
   static constexpr int SOFT_WARPS = R / 2;         // four for eight rows
+  // From nine rows on the softmax warps write the first fragment's q parts, for which
+  // everything waits (windows of 1023 keys at d = 256, 32 rows: 32.0 us, by the
+  // planner alone 40.7; with eight rows 32 requests 55.0, 54.2).
+  static constexpr bool HELP = R > 8;
   static constexpr int MMA_WARP = SOFT_WARPS;
   static constexpr int TMA_WARP = SOFT_WARPS + 1;
   static constexpr int PLAN_WARP = SOFT_WARPS + 2;
@@ -180,21 +185,21 @@ struct Paged8Ctx {
 
 // ---------------------------------------------------------------- the planner warp
 
-// q's parts of fragment f into buffer `buf`, and each row's factor: the power of
-// two that was taken out of it, times scale log2 e.  Rows past the fragment's are zero.
-template <class C>
+// q's parts of fragment f's rows [from, to) into buffer `buf`, and each row's factor:
+// the power of two that was taken out of it, times scale log2 e.  Rows past the
+// fragment's are zero.
+template <class C, int AT_ONCE>   // rows whose loads are in flight together
 __device__ __forceinline__ void pg8_q_parts(const Paged8Ctx<C>& t, const PagedFp8Params& a, const PagedFrag* f, int buf,
-                                            int lane) {
+                                            int lane, int from, int to) {
   constexpr int E = C::D / 32;   // a lane's elements of a row, next to each other
   constexpr int W = E / 2;       // in 32-bit words
-  constexpr int AT_ONCE = 4;     // rows whose loads are in flight together
   const uint32_t sQ = t.base + C::OFF_Q + (uint32_t)buf * C::Q_BYTES;
   float* factor = reinterpret_cast<float*>(t.smem + C::OFF_FACTOR) + buf * C::R;
   const int group = a.p.group, head0 = f->h * group, rows = f->rows;
   const int e0 = lane * E;
   const uint32_t block = (uint32_t)(e0 / C::ROW) * (C::NB * C::ROW), in_row = (uint32_t)(e0 % C::ROW);
 #pragma unroll 1
-  for (int r0 = 0; r0 < C::R; r0 += AT_ONCE) {
+  for (int r0 = from; r0 < to; r0 += AT_ONCE) {
     uint32_t w[AT_ONCE][W];
 #pragma unroll
     for (int i = 0; i < AT_ONCE; ++i) {
@@ -260,6 +265,7 @@ __device__ __forceinline__ void pg8_q_parts(const Paged8Ctx<C>& t, const PagedFp
 
 // Fragment nf's description goes to its slot when nf - 4 is done, its q parts to
 // their buffer when nf - 2 is (so none of its waiters can be two phases behind).
+// (C::HELP: the softmax warps write the first fragment's.)
 template <class C>
 __device__ __forceinline__ void pg8_plan(const Paged8Ctx<C>& t, const PagedFp8Params& a, const PagedPlace<C::MANY>& place,
                                          int lane) {
@@ -278,7 +284,11 @@ __device__ __forceinline__ void pg8_plan(const Paged8Ctx<C>& t, const PagedFp8Pa
     }
     __syncwarp();
     if (nf >= 2 && !t.warp_wait(P8_FREE + ((nf - 2) & 3), (nf - 2) >> 2, kSiteProducerEmpty)) return;
-    if (have && f->n > 0) pg8_q_parts(t, a, f, nf & 1, lane);
+    if (C::HELP && nf == 0) {
+      if (!t.warp_wait(P8_HELP, 0, kSiteMmaQ)) return;
+    } else if (have && f->n > 0) {
+      pg8_q_parts<C, 4>(t, a, f, nf & 1, lane, 0, C::R);
+    }
     __syncwarp();
     if (lane == 0) mbar_arrive(t.bar(P8_Q + (nf & 1)));
   }
@@ -505,6 +515,13 @@ __device__ __forceinline__ void pg8_softmax(const Paged8Ctx<C>& t, const PagedFp
   volatile uint8_t* s_vote = t.smem + C::OFF_VOTE + rg * 8;
   const int tok0 = r0 / p.group, head0 = r0 - tok0 * p.group;   // the first row's token and head of its group
   auto wait = [&](int bar, int phase, uint32_t site) -> bool { return t.warp_wait(bar, phase, site); };
+  if constexpr (C::HELP) {
+    constexpr int ROWS = C::R / C::SOFT_WARPS;
+    if (!wait(P8_PLAN, 0, kSiteMmaQ)) return;
+    if (t.frags[0].n > 0) pg8_q_parts<C, ROWS>(t, a, t.frags, 0, lane, warp * ROWS, (warp + 1) * ROWS);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(t.bar(P8_HELP));
+  }
   int g = 0, x_phase = 0;
   for (int nf = 0;; ++nf) {
     if (!wait(P8_Q + (nf & 1), nf >> 1, kSiteMmaQ)) return;
@@ -776,7 +793,7 @@ __global__ void __launch_bounds__(Paged8Config<D, R, MANY>::THREADS, Paged8Confi
   if (warp == C::TMA_WARP && lane == 0) {
 #pragma unroll 1
     for (int i = 0; i < C::BARS; ++i) {
-      mbar_init(t.bar(i), i >= P8_EXP && i < P8_RINGS ? 16 : i >= P8_P && i < P8_PLAN ? C::SOFT_WARPS
+      mbar_init(t.bar(i), i == P8_HELP ? C::SOFT_WARPS : i >= P8_EXP && i < P8_HELP ? 16 : i >= P8_P && i < P8_PLAN ? C::SOFT_WARPS
                                                          : i >= P8_VOTE && i < P8_EXIT ? 4 : 1);
     }
     *t.abort_flag = 0;
