@@ -14,10 +14,8 @@
 // Reading is bound by HBM: 32768 rows of 8 heads x 128, 202 MB in 29 to 31 us (6.7
 // TB/s; two heads a thread, so that enough loads are in flight; one, 32 us;
 // neighbouring pieces a thread, whose stores half-fill their sectors, 41).  Writing
-// is bound by HBM and its instructions together: the same rows in 33 us (37 with
-// 80 registers and three blocks an SM, 44 with indexes computed at run time and
-// every value clamped; both ways 65.3 us with six blocks, 69.5 with three, 71.5 with
-// seven, whose registers spill).
+// is bound by HBM and its instructions together: the same rows in 33 us (44 with
+// indexes computed at run time and every value clamped).
 #include "fa2_paged_fp8.h"
 
 #include <cuda_fp8.h>
@@ -130,8 +128,11 @@ __device__ __forceinline__ SlotAt slot_at(const PagedFp8RowsArgs& a, int slot) {
 
 // Threads x walk the pieces of a token's heads, threads y and the blocks the
 // tokens.  (mask: the lanes that share the thread's row, whole rows at any item.)
-template <int LANES, bool BF16>
-__global__ void __launch_bounds__(kRowThreads, 6) fa2_paged_append_fp8_kernel(const PagedFp8RowsArgs a) {
+// SM_BLOCKS: blocks an SM holds, which sets the registers: six with K's loads before
+// V's, or three with all in flight together (8 heads x 128, three and six: 2047 rows
+// 2.9 and 3.7 us, 4096 4.6 both, 6000 7.9 and 7.1, 32768 37.7 and 33.0).
+template <int LANES, bool BF16, int SM_BLOCKS>
+__global__ void __launch_bounds__(kRowThreads, SM_BLOCKS) fa2_paged_append_fp8_kernel(const PagedFp8RowsArgs a) {
   grid_launch_dependents();
   grid_dependency_wait();
   const int items = a.heads * LANES;
@@ -214,24 +215,34 @@ __global__ void __launch_bounds__(kRowThreads, 4) fa2_paged_read_fp8_kernel(cons
   }
 }
 
+struct RowsGrid {
+  dim3 blocks, threads;
+};
 // each: items a thread.
-int launch_rows(void (*kernel)(PagedFp8RowsArgs), int lanes, int each, const PagedFp8RowsArgs& a, cudaStream_t stream) {
+RowsGrid rows_grid(int lanes, int each, const PagedFp8RowsArgs& a) {
   const int items = a.heads * lanes;
   int x = 16;   // a row's lanes lie in one warp
   while (x < kRowThreads && each * x < items) x *= 2;
   const int tokens = kRowThreads / x;   // of a block
-  const unsigned blocks = (unsigned)(((long long)a.total + tokens - 1) / tokens);
-  return launch_chained(kernel, dim3(blocks), dim3(x, tokens), 0, stream, a);
+  return RowsGrid{dim3((unsigned)(((long long)a.total + tokens - 1) / tokens)), dim3((unsigned)x, (unsigned)tokens)};
 }
 
+template <int LANES, int SM_BLOCKS>
+int launch_append_rows(const RowsGrid& g, const PagedFp8RowsArgs& a, cudaStream_t stream) {
+  return launch_chained(a.bf16 ? fa2_paged_append_fp8_kernel<LANES, true, SM_BLOCKS> : fa2_paged_append_fp8_kernel<LANES, false, SM_BLOCKS>,
+                        g.blocks, g.threads, 0, stream, a);
+}
 template <int LANES>
 int launch_append(const PagedFp8RowsArgs& a, cudaStream_t stream) {
-  return launch_rows(a.bf16 ? fa2_paged_append_fp8_kernel<LANES, true> : fa2_paged_append_fp8_kernel<LANES, false>, LANES, 1, a,
-                     stream);
+  const RowsGrid g = rows_grid(LANES, 1, a);
+  // up to twice what the GPU holds of three blocks an SM
+  return g.blocks.x <= 2 * 3 * 152 ? launch_append_rows<LANES, 3>(g, a, stream) : launch_append_rows<LANES, 6>(g, a, stream);
 }
 template <int LANES>
 int launch_read(const PagedFp8RowsArgs& a, cudaStream_t stream) {
-  return launch_rows(a.bf16 ? fa2_paged_read_fp8_kernel<LANES, true> : fa2_paged_read_fp8_kernel<LANES, false>, LANES, 2, a, stream);
+  const RowsGrid g = rows_grid(LANES, 2, a);
+  return launch_chained(a.bf16 ? fa2_paged_read_fp8_kernel<LANES, true> : fa2_paged_read_fp8_kernel<LANES, false>, g.blocks, g.threads, 0,
+                        stream, a);
 }
 
 }  // namespace

@@ -616,7 +616,7 @@ int fa2_paged_read_fp8(const fa2_paged_read_fp8_params* params, void* stream);
  *
  * It reads half the bytes of a 16-bit cache, which is what bounds decoding.  A
  * query tile is 32 rows at most, where fa2_paged_fwd's has 128: from chunks of
- * some 32 tokens on, fa2_paged_read_fp8 and fa2_paged_fwd are faster where
+ * some 32 to 100 tokens on, fa2_paged_read_fp8 and fa2_paged_fwd are faster where
  * there is room for the rows in 16 bits (8 requests of 64 tokens over 4096 keys, 4
  * heads of 128 to a K/V head: 140 and 88 us; of 8 tokens 42 and 71).
  */

@@ -138,6 +138,27 @@ def test_rows_quantised_and_read_back(total, hkv, d, page, dtype):
         assert (back[i][total // 2] == 7).all()                              # a skipped row is left
 
 
+@pytest.mark.parametrize("d,hkv", [(64, 16), (128, 9), (256, 4)])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_many_rows_as_few_rows_at_a_time(d, hkv, dtype):
+    """One call for a long prompt's rows (special values, skipped and bad slots among them) leaves what calls of 500 leave."""
+    total, page = 4200, 16
+    g = gen(d)
+    k, v = rows_of(g, (total, hkv, d), DT[dtype]), rows_of(g, (total, hkv, d), DT[dtype])
+    k[7, 0, 3], k[4000, 1], v[4100, 0, 0], v[11, 1, 5] = float("nan"), 0.0, float("inf"), -6e4
+    pages = total // page + 1
+    slots = torch.randperm(pages * page, generator=g, device="cuda")[:total].to(torch.int32)
+    slots[3000], slots[4150] = -1, pages * page
+    one, many = (new_cache(pages, hkv, page, d, fill=0x35) for _ in range(2))
+    fa2.fa2_paged_append_fp8(k, v, slots, *one)
+    assert status() == fa2.FA2_ERR_DEVICE_PAGES
+    for i in range(0, total, 500):
+        fa2.fa2_paged_append_fp8(k[i:i + 500], v[i:i + 500], slots[i:i + 500], *many)
+    assert status() == fa2.FA2_ERR_DEVICE_PAGES
+    for x, y in zip(one, many):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])
 def test_every_16_bit_value_is_rounded_to_its_nearest_code(dtype):
     """All 65536 values of the type, in rows whose exponent a 448-sized head value fixes, then by themselves."""
