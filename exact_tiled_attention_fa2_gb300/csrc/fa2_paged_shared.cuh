@@ -293,10 +293,12 @@ __global__ void __launch_bounds__(SharedConfig<D, WA, WB>::THREADS, 1)
 }
 
 // Block (b, y): of sequence b's rows, those of one K/V head after those of another,
-// chunk y of `chunk`, and on by the grid.  The first warp finds where the rows' partials are, a row a lane (every warp for
-// itself: 820 instructions a warp, most of a merge's 15 us).  The lanes of a warp
-// are then rows x partials, its columns every eighth run of four, as in
-// fa2_paged_merge_kernel.
+// chunk y of `chunk`, and on by the grid.  The first warp finds where the rows'
+// partials are, a row a lane (every warp for itself: 820 instructions a warp, most
+// of a merge's 15 us).  The lanes of a warp are then rows x partials, its columns
+// every eighth run of four, as in fa2_paged_merge_kernel.  (With two partials of a
+// lane in flight 64 requests behind 8200 keys take 60.1 us in place of 57.1, chunks
+// at d = 256 103 in place of 82.)
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kSharedMergeThreads, D == 256 ? 3 : 4)
     fa2_paged_shared_merge_kernel(const __grid_constant__ PagedParams shared, const __grid_constant__ PagedParams own,
@@ -347,41 +349,29 @@ __global__ void __launch_bounds__(kSharedMergeThreads, D == 256 ? 3 : 4)
     float4 acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-    constexpr int U = 1;   // partials whose reads are in flight together
 #pragma unroll 1
-    for (int k0 = r < here ? sub : parts; k0 < parts; k0 += U * subs) {
-      float2 st[U];
-      float4 v[U][E];
+    for (int k = r < here ? sub : parts; k < parts; k += subs) {
+      const bool is_mine = k < mine.count;
+      const SharedRow& x = is_mine ? mine : theirs;
+      const PagedParams& p = is_mine ? own : shared;
+      const int n = is_mine ? k : k - mine.count;
+      const size_t slot = (size_t)(x.first + 2 * n + (n == 0 ? x.odd : 0)) * (size_t)p.slot_rows;
+      const float2 st = reinterpret_cast<const float2*>(p.ws_ml)[slot + x.row];
+      const float4* src = reinterpret_cast<const float4*>(p.ws_o) + slot * (D / 4) + (size_t)(warp * p.slot_rows + x.row);
+      float4 v[E];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int k = k0 + u * subs;
-        st[u] = make_float2(-INFINITY, 0.f);
-        if (k < parts) {
-          const bool is_mine = k < mine.count;
-          const SharedRow& x = is_mine ? mine : theirs;
-          const PagedParams& p = is_mine ? own : shared;
-          const int n = is_mine ? k : k - mine.count;
-          const size_t slot = (size_t)(x.first + 2 * n + (n == 0 ? x.odd : 0)) * (size_t)p.slot_rows;
-          st[u] = reinterpret_cast<const float2*>(p.ws_ml)[slot + x.row];
-          const float4* src = reinterpret_cast<const float4*>(p.ws_o) + slot * (D / 4) + (size_t)(warp * p.slot_rows + x.row);
+      for (int e = 0; e < E; ++e) v[e] = src[(size_t)(e * NW) * p.slot_rows];
+      if (st.y == 0.f) continue;   // shows the row nothing (a NaN sum stays)
+      const float top = fmaxf(m, st.x);
+      const float f0 = ex2_approx(m - top), f = ex2_approx(st.x - top);   // f0: 0 before the first
+      m = top;
+      l = l * f0 + st.y * f;
 #pragma unroll
-          for (int e = 0; e < E; ++e) v[u][e] = src[(size_t)(e * NW) * p.slot_rows];
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (st[u].y == 0.f) continue;   // shows the row nothing (a NaN sum stays)
-        const float top = fmaxf(m, st[u].x);
-        const float f0 = ex2_approx(m - top), f = ex2_approx(st[u].x - top);   // f0: 0 before the first
-        m = top;
-        l = l * f0 + st[u].y * f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          acc[e].x = fmaf(f, v[u][e].x, acc[e].x * f0);
-          acc[e].y = fmaf(f, v[u][e].y, acc[e].y * f0);
-          acc[e].z = fmaf(f, v[u][e].z, acc[e].z * f0);
-          acc[e].w = fmaf(f, v[u][e].w, acc[e].w * f0);
-        }
+      for (int e = 0; e < E; ++e) {
+        acc[e].x = fmaf(f, v[e].x, acc[e].x * f0);
+        acc[e].y = fmaf(f, v[e].y, acc[e].y * f0);
+        acc[e].z = fmaf(f, v[e].z, acc[e].z * f0);
+        acc[e].w = fmaf(f, v[e].w, acc[e].w * f0);
       }
     }
     float M = m;
@@ -438,8 +428,9 @@ int launch_paged_shared_kernels(const PagedLaunchArgs& shared, const PagedLaunch
   const int r = launch_dependent_clusters(kern, S::CLUSTER, dim3((unsigned)(p.ctas / S::HALVES)), S::THREADS, S::SMEM_BYTES,
                                           own.stream, shared.tm_q, own.tm_q, own.tm_k, own.tm_v, shared.p, p);
   if (r != 0) return r;
-  // few rows a block while the blocks fit the GPU at once (four an SM): 2048 rows 58.0 us the call at 4, 59.4 at 8, 70.7 at
-  // 32; 4096 rows 110, 106, 119; 7000 rows of d = 256 96, 86, 81
+  // few rows a block while the blocks fit the GPU at once (four an SM): 2048 rows
+  // 58.0 us the call at 4, 59.4 at 8, 70.7 at 32; 4096 rows 110, 106, 119; 7000 rows
+  // of d = 256 96, 86, 81
   const long long all = (long long)p.total_q * p.group * p.heads_kv;
   const int chunk = all <= 600 * 4 ? 4 : all <= 600 * 8 ? 8 : kSharedMergeRows;
   const long long most = ((long long)p.max_q * p.group * p.heads_kv + chunk - 1) / chunk;
