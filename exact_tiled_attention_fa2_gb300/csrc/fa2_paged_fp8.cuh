@@ -548,16 +548,15 @@ __device__ __forceinline__ void pg8_softmax(const Paged8Ctx<C>& t, const PagedFp
       if (masked) {
         const int key = f->tile(f->j0 + min(half, n - 1)) * kPagedKeyTile + (tid & 63);
         alive = half < n && (key < f->km.pre_end || (key >= f->lo && key < f->end));
-        seen = 0;
-        int tok = f->q0 + tok0, left = p.group - head0;
-#pragma unroll 1
-        for (int i = 0; i < 8; ++tok) {   // a token's rows at a time
-          const int rows = min(left, 8 - i);
-          if (alive && (key < prefix_end(p, f->km, tok) || (key >= f->km.row_lo(tok) && key <= f->km.row_hi(tok))))
-            seen |= ((1u << rows) - 1) << i;
-          i += rows;
-          left = p.group;
-        }
+        // tokens (from the first of the eight rows' on) that see it: from key - off - wr
+        // to key - off + wl, or as far as the mask has no such edge there
+        const KeyMask km = f->km;
+        const long long at = (long long)key - km.off - (f->q0 + tok0);
+        const bool all = key < p.prefix;
+        const int from = all || km.wr < 0 ? 0 : (int)max(0ll, min(8ll, at - km.wr));
+        const int to = all || km.wl < 0 || key < p.sinks ? 8 : (int)max(0ll, min(8ll, at + km.wl + 1));
+        const int r_from = max(0, min(8, from * p.group - head0)), r_to = max(0, min(8, to * p.group - head0));
+        seen = alive && r_from < r_to ? (1u << r_to) - (1u << r_from) : 0u;
       }
       if (!wait(P8_EXP + (g & 7), g >> 3, kSiteSoftmaxS)) return;
       const uint8_t* e = t.smem + C::OFF_EXP + (g & 7) * 256 + tid;

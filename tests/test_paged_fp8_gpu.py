@@ -485,6 +485,17 @@ def test_scales(scale):
     p.check(o, lse, window_right=0, scale=scale)
 
 
+@pytest.mark.parametrize("mask", [dict(window_left=2 ** 31 - 1, window_right=2 ** 31 - 1),
+                                  dict(window_left=2 ** 31 - 1, window_right=0, sink_len=2 ** 31 - 1),
+                                  dict(window_left=5, window_right=0, prefix_len=2 ** 31 - 1),
+                                  dict(window_left=0, window_right=2, sink_len=3)])
+def test_widest_and_narrowest_masks(mask):
+    p = Problem([9, 1, 40], [300, 77, 40], 6, 2, 64, "fp16", 16, seed=14)
+    o, lse = p.run(**mask)
+    assert status() == fa2.FA2_OK
+    p.check(o, lse, **mask)
+
+
 def test_rising_scores_raise_the_maximum_on_every_step():
     """Key j's score grows with j: by 12 powers of two a step of 128 keys, past the margin of 8, and by less."""
     for rise in (12.0, 7.9, 3.0):
