@@ -15,13 +15,15 @@
 namespace fa2 {
 namespace {
 
-// In keys: a pair's fixed cost (32 requests of 1 .. 8192 keys, d = 128: 57 us at
-// 128, 54.3, 55.5 at 512; 8 requests of 5 tokens, d = 64: 21.2, 20.3, 19.0; windows
-// of 1023 at d = 256: 40.4, 40.5, 49.3), the shortest piece worth a CTA (128 and
-// 512 within 0.3 us of 256, but one request of 600 keys 10.7 and 13.4 against 11.2)
-// and what a merge may cost before pairs are left whole (the windows 51 us at 256,
-// 40.4 from 512 to 2048; the 8 requests 20.2, 20.3 and at 2048 22.0).
+// In keys: a pair's fixed cost with up to eight rows (32 requests of 1 .. 8192 keys,
+// d = 128: 55.7 us at 128, 54.4, 54.7 at 384; one of 600: 13.2, 10.8, 11.5) and with
+// more (8 tokens over 16384 keys: 28.0 at 256, 22.6, 22.5 at 512; 16 requests of one
+// token, 16 rows, over 1000 .. 3000 keys: 28.5, 26.5, 27.6; windows of 1023 at d =
+// 256: 28.8, 28.8, 40.4), the shortest piece worth a CTA (128 and 384 within 0.2 us
+// of 256, but the 600 keys 13.4 at 384) and what a merge may cost before pairs are
+// left whole (the windows 41.8 us at 256, 28.8, 28.8 at 1024; the 600 keys 13.4 there).
 constexpr int kFp8Overhead = 256;
+constexpr int kFp8OverheadMore = 384;
 constexpr int kFp8MinShare = 256;
 constexpr int kFp8MergeCost = 512;
 
@@ -127,7 +129,7 @@ int fp8_rows(const fa2_paged_cache_fp8& c, void* k, void* v, const int* slots, c
 }
 
 struct Fp8Shape {
-  int group, parts, tile_tokens, box_tokens, max_q, slot_rows;
+  int group, parts, tile_tokens, box_tokens, max_q, slot_rows, overhead;
   int ctas;
   size_t ws_o_bytes, ws_ml_bytes, ws_bytes;
   bool many;
@@ -150,6 +152,7 @@ int fp8_shape(const fa2_paged_fp8_params& a, Fp8Shape& s) {
   const long long T = s.tile_tokens = kPagedFp8Rows / s.group;
   s.box_tokens = (int)(T < s.max_q ? T : s.max_q);
   s.slot_rows = s.group * s.box_tokens;
+  s.overhead = s.slot_rows > 8 ? kFp8OverheadMore : kFp8Overhead;
   // whole and partial query tiles of sequences whose rows do not overlap
   long long tiles = ((long long)a.total_q + (T - 1) * a.batch) / T;
   const long long each = (s.max_q + T - 1) / T;
@@ -158,7 +161,7 @@ int fp8_shape(const fa2_paged_fp8_params& a, Fp8Shape& s) {
   const long long pairs = tiles * c.heads * s.parts;
   if (pairs > INT_MAX - 1024 || (long long)c.heads * s.parts > INT_MAX) return FA2_ERR_UNSUPPORTED;
   s.many = s.max_q > T || (double)a.batch * c.heads * s.parts *
-                                  (((double)a.max_pages * c.page_size + kFp8Overhead) / 64 + 2.0) + 1e6 > 2147483647.0;
+                                  (((double)a.max_pages * c.page_size + s.overhead) / 64 + 2.0) + 1e6 > 2147483647.0;
   // One wave of the resident CTAs of a GB300's 152 SMs, fixed (see paged_ctas): two
   // an SM with up to eight rows (32 requests of 1 .. 8192 keys: 70 us, with one CTA
   // and deeper rings 88, from an empty L2 cache), one with more (16 requests of 8192
@@ -314,7 +317,7 @@ int fp8_forward(const fa2_paged_fp8_params& a, void* workspace, size_t workspace
   p.prefix = a.prefix_len;
   p.sinks = a.window_left >= 0 ? a.sink_len : 0;
   p.slot_rows = s.slot_rows;
-  p.overhead = kFp8Overhead;
+  p.overhead = s.overhead;
   p.ctas = s.ctas;
   p.pair_ctas = 0;   // (never a CTA a pair)
   p.min_share = kFp8MinShare;
