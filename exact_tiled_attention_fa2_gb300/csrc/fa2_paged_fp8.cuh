@@ -77,7 +77,7 @@ struct Paged8Config {
   static constexpr int BC = 128;         // keys of a step
   static constexpr int SOFT_WARPS = R / 2;         // four for eight rows
   // From nine rows on the softmax warps write the first fragment's q parts, for which
-  // everything waits (windows of 1023 keys at d = 256, 32 rows: 32.0 us, by the
+  // everything waits (windows of 1023 keys at d = 256, 32 rows: 32 us, by the
   // planner alone 40.7; with eight rows 32 requests 55.0, 54.2).
   static constexpr bool HELP = R > 8;
   static constexpr int MMA_WARP = SOFT_WARPS;
