@@ -364,6 +364,7 @@ struct PagedPlace {
   int piece;         // of the line
   int rank;          // one pair: its index in its sequence
   int tile;          // (PASS 1) the query tile that the piece is of, `at` where its stretch starts; -1: as it falls
+  int skip;          // (PASS 2) its table row's entries of shared keys; (PASS 1, tile >= 0) its first sequence
   bool line;         // the line is cut at this CTA's piece, or ends before it (one pair: false)
 };
 
@@ -486,7 +487,21 @@ struct LineScan {
   typename LineOf<WIDE>::T total, all_pairs, all_chunks;
   int longest, i0, i1, per;
   PagedSeq s;   // the run's last sequence
+  int skip;     // (PASS 2) its table row's entries of shared keys
 };
+
+// Sequence i; skip: PagedPlace::skip (PASS 2; found here so that the piece's walk need not look again, two
+// rounds of dependent reads).
+template <bool WIDE, int PASS>
+__device__ __forceinline__ PagedSeq scan_seq(const PagedParams& p, int i, bool report, int& skip) {
+  if constexpr (PASS == 2) {
+    const SeqRead x = seq_read<PASS>(p, i);
+    skip = (int)(x.table - (p.table + (long long)i * p.table_stride));
+    return paged_seq<WIDE>(p, x.a, x.b, x.k, report);
+  } else {
+    return read_seq<WIDE, PASS>(p, i, report);
+  }
+}
 
 template <int THREADS, bool WIDE, int PASS, class Beside>
 __device__ __forceinline__ LineScan<WIDE> line_scan(const PagedParams& p, int tid, PagedScan<WIDE>* sh, bool report,
@@ -502,12 +517,13 @@ __device__ __forceinline__ LineScan<WIDE> line_scan(const PagedParams& p, int ti
   int longest = 0;   // pair
   PagedSeq s;
   s.tiles = s.keys = s.n_q = s.n_k = s.row0 = 0;
+  int skip = 0;
   if (tid >= THREADS) {
     beside();
   } else {
 #pragma unroll 1
     for (int i = i0; i < i1; ++i) {
-      s = read_seq<WIDE, PASS>(p, i, report);
+      s = scan_seq<WIDE, PASS>(p, i, report, skip);
       const Line x = s.span<WIDE>(p, s.tiles);
       span += x;
       pairs += (Line)s.tiles * p.heads_kv;
@@ -551,7 +567,7 @@ __device__ __forceinline__ LineScan<WIDE> line_scan(const PagedParams& p, int ti
     all_chunks += sh->warp_sum[2][j];
     longest = max(longest, sh->warp_longest[j]);
   }
-  return LineScan<WIDE>{a, b, span, pairs, total, all_pairs, all_chunks, longest, i0, i1, per, s};
+  return LineScan<WIDE>{a, b, span, pairs, total, all_pairs, all_chunks, longest, i0, i1, per, s, skip};
 }
 
 template <bool WIDE, int PASS>
@@ -562,6 +578,7 @@ __device__ __forceinline__ PagedPlace<WIDE> line_place(const PagedParams& p, con
   const Line a = scan.a, b = scan.b, span = scan.span, pairs = scan.pairs, total = scan.total, all_pairs = scan.all_pairs;
   const int i0 = scan.i0, i1 = scan.i1, per = scan.per;
   PagedSeq s = scan.s;
+  int skip = scan.skip;
   int whole = whole_pairs<WIDE>(p, ctas, total, scan.all_chunks, all_pairs, scan.longest);
   int cut_seq = -1, cut_tiles = 0;
   Line shift = 0;
@@ -600,7 +617,7 @@ __device__ __forceinline__ PagedPlace<WIDE> line_place(const PagedParams& p, con
     Line x = mine;
 #pragma unroll 1
     for (int i = i0; i < i1; ++i) {
-      if (per > 1) s = read_seq<WIDE, PASS>(p, i, false);
+      if (per > 1) s = scan_seq<WIDE, PASS>(p, i, false, skip);
       const Line step = one ? (Line)s.tiles * p.heads_kv : s.span<WIDE>(p, s.tiles);
       if (pos < x + step) {
         if (WIDE && !one && i == cut_seq) {   // ends where it did, and starts the line
@@ -611,6 +628,7 @@ __device__ __forceinline__ PagedPlace<WIDE> line_place(const PagedParams& p, con
         sh->place.s = s;
         sh->place.seq = i;
         sh->place.rank = one ? (int)(pos - x) : 0;
+        if constexpr (PASS == 2) sh->place.skip = skip;
         break;
       }
       x += step;
@@ -681,6 +699,9 @@ static_assert(sizeof(PagedMerge) == kPagedMergeBytes, "merge description");
 template <bool BAND, bool WIDE, int PASS = 0>
 struct FragWalk {
   using Line = typename LineOf<WIDE>::T;
+  // The next sequence's lengths read only when it is come to: with shared prefixes they take two rounds of dependent
+  // reads, for which the first fragment would wait; the planner warp is up to four fragments ahead.
+  static constexpr bool LATE = PASS != 0 && !WIDE;
   PagedSeq s;
   PagedFrag base;     // the current query tile's facts, for all of its key tiles
   int tiles_n;        // its key tiles
@@ -740,7 +761,10 @@ struct FragWalk {
     more = true;
     one = pl.share == 0;
     merge.count = -1;
-    table = PASS != 0 ? seq_read<PASS>(p, seq).table : p.table + (long long)seq * p.table_stride;
+    if constexpr (PASS == 1)
+      table = pl.tile >= 0 ? p.table + (long long)pl.skip * p.table_stride : seq_read<PASS>(p, seq).table;
+    else
+      table = p.table + (long long)seq * p.table_stride + (PASS == 2 ? pl.skip : 0);
     begin = piece * pl.share;   // one: 0
     end = min(begin + pl.share, pl.total);
     if (one) {   // the query tiles from the last (the most keys) to the first
@@ -754,7 +778,7 @@ struct FragWalk {
       x = pl.at + (Line)h * each;
     } else {
       x = pl.at + pair_at<WIDE>(p, s, begin - pl.at, tile, h);
-      read_ahead(p);
+      if constexpr (!LATE) read_ahead(p);
     }
     start_tile(p);
     if (one) end = w;
@@ -820,12 +844,13 @@ __device__ __forceinline__ bool next_fragment(FragWalk<BAND, WIDE, PASS>& k, con
             k.more = false;
             break;
           }
+          if constexpr (FragWalk<BAND, WIDE, PASS>::LATE) --k.seq, k.read_ahead(p), ++k.seq;
           if constexpr (PASS != 0)
             k.table = k.next_table;
           else
             k.table += p.table_stride;
           k.s = paged_seq<WIDE>(p, k.next_a, k.next_b, k.next_k, false);
-          k.read_ahead(p);
+          if constexpr (!FragWalk<BAND, WIDE, PASS>::LATE) k.read_ahead(p);
         } while (k.s.tiles == 0);
       }
       if (k.more) k.start_tile(p);

@@ -27,10 +27,10 @@ constexpr int paged_ctas(int d) { return d == 256 ? 152 : 304; }
 constexpr int kPagedOverhead = 128;
 constexpr int kPagedMinShare = 128;
 // Shared prefixes: what a key of the shared pass costs, in keys of the sequences'
-// own, with few and with many rows there (64 requests behind 8200 shared keys 61 us
-// at 0.7, 56 to 58 at 0.85 .. 1.3, 62 at 2; 128 behind 32000: 118, 110 at 0.9, 127
-// at 1.3; chunks of up to 300 tokens, d = 256: 91 to 1, 81 from 1.15 on).
-constexpr float kSharedWeightFew = 0.9f;
+// own, with few and with many rows there (64 requests behind 8200 shared keys 57.1 us
+// at 0.9, 53.8, 54.2 at 1.1; 128 behind 32000: 108.3, 106.6, 106.7, and 115.8 at 1.2;
+// chunks of up to 300 tokens, d = 256: 91 up to 1, 81 from 1.15 to 1.5).
+constexpr float kSharedWeightFew = 1.0f;
 constexpr float kSharedWeightMany = 1.25f;
 
 int check_cache(const fa2_paged_cache& c, CacheView& k, CacheView& v) {

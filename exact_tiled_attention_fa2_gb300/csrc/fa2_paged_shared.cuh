@@ -52,6 +52,7 @@ template <bool WIDE>
 struct GroupLine {
   using Line = typename LineOf<WIDE>::T;
   PagedSeq s;          // the lane's group
+  int first;           // its first sequence
   Line stretch;        // of one of its query tiles, all K/V heads
   long long total;     // all stretches, in keys
   int tiles;           // of all groups
@@ -63,7 +64,9 @@ __device__ __forceinline__ GroupLine<WIDE> group_line(const PagedParams& p, bool
   GroupLine<WIDE> g;
   g.s.tiles = g.s.keys = g.s.n_q = g.s.n_k = g.s.row0 = 0;
   g.stretch = 0;
+  g.first = 0;
   if (lane < p.batch) {
+    g.first = p.cu_groups[lane];
     g.s = read_seq<WIDE, 1>(p, lane, report);
     if (g.s.tiles > 0) g.stretch = (typename LineOf<WIDE>::T)g.s.template width<WIDE>(p, 0) * p.heads_kv;
   }
@@ -124,17 +127,20 @@ __device__ __forceinline__ PagedPlace<WIDE> group_place(const PagedParams& p, co
   r.share = share;
   r.total = r.at + stretch;
   r.rank = 0;
+  r.skip = __shfl_sync(0xffffffffu, g.first, src);
   r.line = true;
   return r;
 }
 
 // CTAs of `ctas` that take the shared keys, whole units and `limit` at most: `group`
-// and `own` are the lines' lengths in keys.
+// and `own` are the lines' lengths in keys.  Rounded down, for a short line of the
+// sequences' own suffers more from a unit less (two requests behind 20000 shared
+// keys: 39.8 us, rounded to the nearest 51.4).
 __device__ __forceinline__ int shared_ctas(const PagedParams& pa, long long group, long long own, int ctas, int limit,
                                            int unit) {
   if (group == 0) return 0;
   const float a = (float)group * pa.share_weight, b = (float)own;
-  const int n = max((int)rintf((float)(ctas / unit) * a / (a + b)), 1) * unit;
+  const int n = max((int)((float)(ctas / unit) * a / (a + b)), 1) * unit;
   const long long most = (group + pa.min_share - 1) / pa.min_share;   // pieces there are
   return max(1, min(min(n, limit), (int)(most < limit ? most : limit)));
 }
