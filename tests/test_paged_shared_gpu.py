@@ -108,6 +108,19 @@ def test_batches(batch):
         p.check(o, lse, window_right=0)
 
 
+@pytest.mark.parametrize("batch,d,most", [(193, 64, 3), (500, 128, 2), (385, 256, 2), (260, 128, 20)])
+def test_hundreds_of_sequences(batch, d, most):
+    """Several sequences for each thread that sums them, in some and in many groups, with short and long own keys."""
+    r = np.random.RandomState(batch)
+    new = [int(x) for x in r.randint(0, most, batch)]
+    own = [int(x) for x in np.where(r.rand(batch) < 0.1, r.randint(0, 700, batch), r.randint(0, 30, batch))]
+    for groups in ([(batch - 3, 900)], [(5, int(s)) for s in r.randint(0, 300, batch // 5)]):
+        p = Shared(new, lens_of(groups, own, new), groups, 6, 2, d, "bf16", 16, seed=batch)
+        o, lse = p.run()
+        assert status() == fa2.FA2_OK
+        p.check(o, lse, window_right=0)
+
+
 def test_a_long_prefix_and_many_rows():
     """The shared pass in several query tiles (of 128 rows) of one group, cut and whole."""
     for tokens, shared in ((2, 20000), (60, 700)):
