@@ -25,7 +25,7 @@
 // with its value's scale, 2^(s + ev - m), under a running maximum m of s + ev
 // that keeps the largest at 2^4 .. 2^8: 12 bits, down to 2^-22 of the largest
 // contribution to O, also where a key of large weight has small values (the
-// first tokens of a prompt).  The sum l adds 2^(s + ev - m) 2^-ev in fp32, which
+// first tokens of a prompt) or zeros (kFp8ZeroLog2).  The sum l adds 2^(s + ev - m) 2^-ev in fp32, which
 // loses nothing: exponents differ by 120 at most.
 //
 // Schedule, fragments and merging of cut pairs are the 16-bit kernel's
@@ -136,6 +136,13 @@ struct Paged8Config {
 // (two exchanges between the softmax warps and a pass over O) is rare.
 constexpr float kFp8RaiseLog2 = 8.f;
 constexpr float kFp8TopLog2 = 4.f;
+// A value row of zeros adds nothing to O, whatever P is, but is stored with exponent
+// 0, above ordinary rows' (values of size 1: -8): where such a key would raise m, it
+// counts with this exponent instead, and the others' P keeps its bits while their
+// largest s + ev lies within 88 of its s.  (P at most 2^8 and so l 2^96 a key: below
+// 2^128 over 2^31 keys.)
+constexpr float kFp8ZeroLog2 = 88.f;
+constexpr float kFp8ZeroInv = 309485009821345068724781056.f;   // 2^88
 constexpr float kFp8NoMax = -1e30f;   // m before a row's first key: finite, so that -inf - m is no NaN
 
 // 2^e; 0 below fp32's normal range.
@@ -503,6 +510,27 @@ __device__ __forceinline__ void pg8_mma(const Paged8Ctx<C>& t) {
 
 // ---------------------------------------------------------------- the softmax warps
 
+// Row `key` of V stage s: rows of C::ROW bytes, 8 C::ROW apart, whose 16-byte chunks the swizzle permutes.
+template <class C>
+__device__ __forceinline__ uint32_t pg8_v_row(const Paged8Ctx<C>& t, int s, int key) {
+  return t.base + C::OFF_V + s * C::KV_BYTES + (uint32_t)(key >> 3) * C::GROUP_BYTES + (uint32_t)(key & 7) * C::ROW;
+}
+
+// Whether that row's codes are all zero, of either sign.
+template <class C>
+__device__ __forceinline__ bool pg8_zero_row(uint32_t at) {
+  uint32_t any = 0;
+#pragma unroll 1
+  for (int b = 0; b < C::BLOCKS; ++b)
+#pragma unroll 1
+    for (int i = 0; i < C::ROW; i += 16) {
+      uint32_t x, y, z, w;
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x), "=r"(y), "=r"(z), "=r"(w) : "r"(at + b * 8 * C::ROW + i) : "memory");
+      any |= x | y | z | w;
+    }
+  return (any & 0x7f7f7f7fu) == 0;
+}
+
 // Warps 4 n .. 4 n + 3: rows 8 n .. 8 n + 7, a key a thread.
 template <class C>
 __device__ __forceinline__ void pg8_softmax(const Paged8Ctx<C>& t, const PagedFp8Params& a, int warp, int lane) {
@@ -561,7 +589,8 @@ __device__ __forceinline__ void pg8_softmax(const Paged8Ctx<C>& t, const PagedFp
       if (!wait(P8_EXP + (g & 7), g >> 3, kSiteSoftmaxS)) return;
       const uint8_t* e = t.smem + C::OFF_EXP + (g & 7) * 256 + tid;
       const int ev = (int)e[128] - 127;
-      const float key_scale = __uint_as_float((unsigned)e[0] << 23), value_exp = (float)ev, value_inv = pow2_int(-ev);
+      const float key_scale = __uint_as_float((unsigned)e[0] << 23), value_exp = (float)ev;
+      float value_inv = pow2_int(-ev);
       // S(g), which was asked for after PV(g - 2): P(g - 2), whose place P(g) takes, has been used
       if (!wait(C::B_S + g % C::KSTAGES, g / C::KSTAGES, kSiteSoftmaxS)) return;
       tc_fence_after();
@@ -604,6 +633,17 @@ __device__ __forceinline__ void pg8_softmax(const Paged8Ctx<C>& t, const PagedFp
       }
       if (!wait(P8_VOTE + rg, g, kSiteSoftmaxO)) return;
       if (*reinterpret_cast<volatile uint32_t*>(t.smem + C::OFF_VOTE + rg * 8 + 4 * (g & 1)) != 0) {
+        // a value row of zeros (exponent 0) must not set the others' scale
+        const bool asks = value_inv == 1.f && over() > kFp8RaiseLog2;
+        if (__any_sync(0xffffffffu, asks)) {
+          const int s = g % C::VSTAGES;
+          if (!wait(C::B_VFULL + s, g / C::VSTAGES, kSiteMmaV)) return;
+          if (asks && pg8_zero_row<C>(pg8_v_row(t, s, tid))) {
+            value_inv = kFp8ZeroInv;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = __fadd2_rn(x[i], make_float2(-kFp8ZeroLog2, -kFp8ZeroLog2));
+          }
+        }
         const float rows8[8] = {x[0].x, x[0].y, x[1].x, x[1].y, x[2].x, x[2].y, x[3].x, x[3].y};
         const float mine = warp_rows(rows8, lane, [](float u, float v) { return fmaxf(u, v); });
         if ((lane & 3) == 0) s_max[quad * 8 + warp_row(lane)] = mine;
@@ -677,8 +717,7 @@ __device__ __forceinline__ void pg8_softmax(const Paged8Ctx<C>& t, const PagedFp
         const int s = g % C::VSTAGES;
         if (!wait(C::B_VFULL + s, g / C::VSTAGES, kSiteMmaV)) return;
         if (!alive) {
-          const uint32_t at = t.base + C::OFF_V + s * C::KV_BYTES + (uint32_t)(tid >> 3) * C::GROUP_BYTES +
-                              (uint32_t)(tid & 7) * C::ROW;
+          const uint32_t at = pg8_v_row(t, s, tid);
 #pragma unroll 1
           for (int b = 0; b < C::BLOCKS; ++b)
 #pragma unroll

@@ -610,8 +610,8 @@ int fa2_paged_read_fp8(const fa2_paged_read_fp8_params* params, void* stream);
  * num_pages) reads as zero codes with exponent 0.)  Products are those of the
  * exact codes: q enters as a sum of three e4m3 parts of falling scale, exact
  * down to 2^-25 of a query row's largest value, and P likewise, with 12
- * significant bits down to 2^-22 of the largest P 2^e of its row; sums are
- * fp32.  An infinite value makes its query row NaN.  Exponents are those that
+ * significant bits down to 2^-22 of the largest P 2^e of its row, value rows of
+ * zeros apart; sums are fp32.  An infinite value makes its query row NaN.  Exponents are those that
  * fa2_paged_append_fp8 writes.
  *
  * It reads half the bytes of a 16-bit cache, which is what bounds decoding.  A
