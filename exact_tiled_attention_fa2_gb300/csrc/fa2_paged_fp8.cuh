@@ -48,6 +48,8 @@
 
 #include <cuda_fp8.h>
 
+#include <cfloat>
+
 #include "fa2_paged.cuh"
 #include "fa2_paged_fp8.h"
 #include "sm103_ptx_fp8.cuh"
@@ -143,7 +145,7 @@ constexpr float kFp8TopLog2 = 4.f;
 // 2^128 over 2^31 keys.)
 constexpr float kFp8ZeroLog2 = 88.f;
 constexpr float kFp8ZeroInv = 309485009821345068724781056.f;   // 2^88
-constexpr float kFp8NoMax = -1e30f;   // m before a row's first key: finite, so that -inf - m is no NaN
+constexpr float kFp8NoMax = -FLT_MAX;   // m before a row's first key: the lowest finite score, so that -inf - m is no NaN
 
 // 2^e; 0 below fp32's normal range.
 __device__ __forceinline__ float pow2_int(int e) { return e < -126 ? 0.f : __uint_as_float((unsigned)(min(e, 127) + 127) << 23); }
