@@ -25,8 +25,8 @@
 // with its value's scale, 2^(s + ev - m), under a running maximum m of s + ev
 // that keeps the largest at 2^4 .. 2^8: 12 bits, down to 2^-22 of the largest
 // contribution to O, also where a key of large weight has small values (the
-// first tokens of a prompt) or zeros (kFp8ZeroLog2).  The sum l adds 2^(s + ev - m) 2^-ev in fp32, which
-// loses nothing: exponents differ by 120 at most.
+// first tokens of a prompt) or zeros (kFp8ZeroLog2).  The sum l adds 2^(s + ev -
+// m) 2^-ev in fp32, with low exponents apart (kFp8LowInv).
 //
 // Schedule, fragments and merging of cut pairs are the 16-bit kernel's
 // (fa2_paged.cuh); a step here is two of its 64-key tiles, and pairs always lie on
@@ -145,6 +145,11 @@ constexpr float kFp8TopLog2 = 4.f;
 // 2^128 over 2^31 keys.)
 constexpr float kFp8ZeroLog2 = 88.f;
 constexpr float kFp8ZeroInv = 309485009821345068724781056.f;   // 2^88
+// A key with an exponent below -20 adds its part of l by itself, 2^(s - m), not by
+// way of P.  m is at least 4 below the largest s + ev and exponents end at 60: any
+// other key that leaves l because its 2^(s + ev - m) is no fp32 number weighs less
+// than 2^-50 of one that stays, 2^-19 over 2^31 of them.
+constexpr float kFp8LowInv = 1048576.f;   // 2^20
 constexpr float kFp8NoMax = -FLT_MAX;   // m before a row's first key: the lowest finite score, so that -inf - m is no NaN
 
 // 2^e; 0 below fp32's normal range.
@@ -654,20 +659,21 @@ __device__ __forceinline__ void pg8_softmax(const Paged8Ctx<C>& t, const PagedFp
         if (!wait(P8_X + rg, x_phase, kSiteSoftmaxO)) return;
         ++x_phase;
         float alpha[8];
-        auto up = [&](int i, float& neg) {
+        auto up = [&](int i, float& neg, float& sum) {
           const float top = fmaxf(fmaxf(s_max[i], s_max[8 + i]), fmaxf(s_max[16 + i], s_max[24 + i]));
           alpha[i] = 1.f;
           if (top + neg > kFp8RaiseLog2) {
             const float neg_new = kFp8TopLog2 - top;
-            alpha[i] = ex2_approx(neg_new - neg);
+            const float half = ex2_approx(0.5f * (neg_new - neg));   // (l can be 2^88 and more where alpha is too small a number)
+            alpha[i] = half * half;
+            sum = sum * half * half;
             neg = neg_new;
           }
         };
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          up(2 * i, neg_m[i].x);
-          up(2 * i + 1, neg_m[i].y);
-          l[i] = __fmul2_rn(l[i], make_float2(alpha[2 * i], alpha[2 * i + 1]));
+          up(2 * i, neg_m[i].x, l[i].x);
+          up(2 * i + 1, neg_m[i].y, l[i].y);
         }
         if (j > 0) {
           if (!wait(C::B_O + (g - 1) % C::VSTAGES, (g - 1) / C::VSTAGES, kSiteSoftmaxO)) return;
@@ -684,6 +690,16 @@ __device__ __forceinline__ void pg8_softmax(const Paged8Ctx<C>& t, const PagedFp
           }
           tmem_st_wait();
         }
+      }
+      const bool low = value_inv > kFp8LowInv;
+      if (__any_sync(0xffffffffu, low)) {   // their part of l by itself
+        const float shift = low ? (float)((int)(__float_as_uint(value_inv) >> 23) - 127) : -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 y = __fadd2_rn(__fadd2_rn(x[i], neg_m[i]), make_float2(shift, shift));
+          l[i] = __fadd2_rn(l[i], make_float2(ex2_approx(y.x), ex2_approx(y.y)));
+        }
+        value_inv = low ? 0.f : value_inv;
       }
       uint32_t c[4][3];   // parts of two rows
 #pragma unroll
@@ -750,9 +766,21 @@ __device__ __forceinline__ void pg8_softmax(const Paged8Ctx<C>& t, const PagedFp
     const int rows = f->rows - r0, slot = f->slot;   // of these eight
     if (rows > 0) {
       const bool has_d = C::ROW == 128 || lane < 16;   // (64 rows of O^T lie in 16 lanes of each warp)
+      // A partial goes out with its sum in [1, 2) and m raised by the rest: m + log2 l is
+      // the row's weight among the partials, whatever its keys' exponents.
       float inv[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) inv[i] = slot >= 0 ? 1.f : sum[i] == 0.f ? 0.f : 1.f / sum[i];   // 0: sees no key (a NaN sum is no such row's)
+      for (int i = 0; i < 8; ++i) {
+        if (slot >= 0) {
+          const float m = -(i & 1 ? neg_m[i / 2].y : neg_m[i / 2].x);
+          const float m_new = sum[i] == 0.f ? m : m + (float)((int)(__float_as_uint(sum[i]) >> 23) - 127);
+          inv[i] = ex2_approx(m - m_new);   // (as far as m could be raised: it may be a large number)
+          sum[i] *= inv[i];
+          (i & 1 ? neg_m[i / 2].y : neg_m[i / 2].x) = -m_new;
+        } else {
+          inv[i] = sum[i] == 0.f ? 0.f : 1.f / sum[i];   // 0: sees no key (a NaN sum is no such row's)
+        }
+      }
       const long long wrap = p.o_rs - (long long)(p.group - 1) * p.o_hs;   // from a token's last head to the next token's first
 #pragma unroll 1
       for (int b = 0; b < C::BLOCKS; ++b) {
