@@ -170,8 +170,8 @@ int launch_dependent(void (*kernel)(Params...), dim3 grid, dim3 block, size_t sm
   return launch_dependent_clusters(kernel, 1, grid, block, smem, stream, args...);
 }
 
-// launch_dependent, by the name under which the 8-bit cache and shared prefixes
-// use it (their sources are looked at for read-only loads by that name).
+// launch_dependent, by the name that the 8-bit cache and shared prefixes use.  (The
+// sources of all three launchers are looked at for read-only loads.)
 template <class... Params, class... Args>
 int launch_chained(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, const Args&... args) {
   return launch_dependent(kernel, grid, block, smem, stream, args...);
