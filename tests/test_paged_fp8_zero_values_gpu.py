@@ -33,7 +33,7 @@ def slots_of(p, b):
     return (p.table[b, j // p.page].long() * p.page + j % p.page).to(torch.int32)
 
 
-def check(p, o, lse, scale=None, window_right=0):
+def check(p, o, lse, scale=None, window_left=-1, window_right=0, prefix_len=0, sink_len=0):
     group = p.hq // p.hkv
     scale = 1.0 / p.d ** 0.5 if scale is None else scale
     u, least = torch.finfo(o.dtype).eps / 2, 2.0 ** LIMITS[o.dtype][0]
@@ -43,7 +43,7 @@ def check(p, o, lse, scale=None, window_right=0):
         (kc, ke), (vc, ve) = p.keys(b, 0), p.keys(b, 1)
         k, v, vc, ve = (x.repeat_interleave(group, 0) for x in (
             kc * torch.exp2(ke)[..., None], vc * torch.exp2(ve)[..., None], vc, ve))
-        hidden = ~seen_mask(n, n_k, -1, window_right, 0)
+        hidden = ~seen_mask(n, n_k, window_left, window_right, prefix_len, sink_len)
         q = p.q[row:row + n].double().transpose(0, 1)
         s = (scale * q @ k.transpose(1, 2)).masked_fill(hidden, -np.inf)
         ref_l = torch.logsumexp(s, -1)
@@ -112,6 +112,19 @@ def test_zero_values_among_the_others(first, dtype):
     o, lse = p.run(window_right=0)
     assert status() == fa2.FA2_OK
     check(p, o, lse)
+
+
+@pytest.mark.parametrize("mask", [dict(window_left=90, window_right=0, sink_len=4),
+                                  dict(window_left=300, window_right=2, prefix_len=5),
+                                  dict(window_left=700, window_right=0, sink_len=130)])
+@pytest.mark.parametrize("lens_q,lens_k,group", [([1, 3], [2000, 600], 4), ([40, 1], [900, 1500], 3), ([2], [9000], 16)])
+def test_zero_sinks_beside_a_window(lens_q, lens_k, group, mask):
+    """The first keys, seen past the window's edge, hold most of the weight and zeros."""
+    p = Problem(lens_q, lens_k, 2 * group, 2, 128, "bf16", 16, seed=11)
+    fill(p, 0.02, 0.9, [0, 1, 2, 3], "bf16", seed=12)
+    o, lse = p.run(**mask)
+    assert status() == fa2.FA2_OK
+    check(p, o, lse, **mask)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
