@@ -148,8 +148,13 @@ constexpr float kFp8ZeroInv = 309485009821345068724781056.f;   // 2^88
 // A key with an exponent below -20 adds its part of l by itself, 2^(s - m), not by
 // way of P.  m is at least 4 below the largest s + ev and exponents end at 60: any
 // other key that leaves l because its 2^(s + ev - m) is no fp32 number weighs less
-// than 2^-50 of one that stays, 2^-19 over 2^31 of them.
+// than 2^-50 of one that stays, 2^-19 over 2^31 of them.  (A branch of each thread:
+// 8 chunks of 512 tokens over 4096 keys 1012 us, without it 1009, by a warp's vote
+// 1016, its operands kept from before S(g) 1090.)
 constexpr float kFp8LowInv = 1048576.f;   // 2^20
+// Sums from 2^-40 to 2^40 go to the merge as they are (their bits): what leaves the
+// merge with 2^(m - max m), past 2^-126, then weighs less than 2^-46 of another part.
+constexpr unsigned kFp8NearLow = (127u - 40) << 23, kFp8NearHigh = (127u + 40) << 23;
 constexpr float kFp8NoMax = -FLT_MAX;   // m before a row's first key: the lowest finite score, so that -inf - m is no NaN
 
 // 2^e; 0 below fp32's normal range.
@@ -641,8 +646,8 @@ __device__ __forceinline__ void pg8_softmax(const Paged8Ctx<C>& t, const PagedFp
       if (!wait(P8_VOTE + rg, g, kSiteSoftmaxO)) return;
       if (*reinterpret_cast<volatile uint32_t*>(t.smem + C::OFF_VOTE + rg * 8 + 4 * (g & 1)) != 0) {
         // a value row of zeros (exponent 0) must not set the others' scale
-        const bool asks = value_inv == 1.f && over() > kFp8RaiseLog2;
-        if (__any_sync(0xffffffffu, asks)) {
+        if (__any_sync(0xffffffffu, value_inv == 1.f)) {
+          const bool asks = value_inv == 1.f && over() > kFp8RaiseLog2;
           const int s = g % C::VSTAGES;
           if (!wait(C::B_VFULL + s, g / C::VSTAGES, kSiteMmaV)) return;
           if (asks && pg8_zero_row<C>(pg8_v_row(t, s, tid))) {
@@ -664,7 +669,7 @@ __device__ __forceinline__ void pg8_softmax(const Paged8Ctx<C>& t, const PagedFp
           alpha[i] = 1.f;
           if (top + neg > kFp8RaiseLog2) {
             const float neg_new = kFp8TopLog2 - top;
-            const float half = ex2_approx(0.5f * (neg_new - neg));   // (l can be 2^88 and more where alpha is too small a number)
+            const float half = ex2_approx(0.5f * (neg_new - neg));   // (l may be far above 1 where alpha is no fp32 number)
             alpha[i] = half * half;
             sum = sum * half * half;
             neg = neg_new;
@@ -691,15 +696,14 @@ __device__ __forceinline__ void pg8_softmax(const Paged8Ctx<C>& t, const PagedFp
           tmem_st_wait();
         }
       }
-      const bool low = value_inv > kFp8LowInv;
-      if (__any_sync(0xffffffffu, low)) {   // their part of l by itself
-        const float shift = low ? (float)((int)(__float_as_uint(value_inv) >> 23) - 127) : -INFINITY;
+      if (value_inv > kFp8LowInv) {   // this key's part of l by itself
+        const float shift = (float)((int)(__float_as_uint(value_inv) >> 23) - 127);   // -ev
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float2 y = __fadd2_rn(__fadd2_rn(x[i], neg_m[i]), make_float2(shift, shift));
           l[i] = __fadd2_rn(l[i], make_float2(ex2_approx(y.x), ex2_approx(y.y)));
         }
-        value_inv = low ? 0.f : value_inv;
+        value_inv = 0.f;
       }
       uint32_t c[4][3];   // parts of two rows
 #pragma unroll
@@ -766,19 +770,22 @@ __device__ __forceinline__ void pg8_softmax(const Paged8Ctx<C>& t, const PagedFp
     const int rows = f->rows - r0, slot = f->slot;   // of these eight
     if (rows > 0) {
       const bool has_d = C::ROW == 128 || lane < 16;   // (64 rows of O^T lie in 16 lanes of each warp)
-      // A partial goes out with its sum in [1, 2) and m raised by the rest: m + log2 l is
-      // the row's weight among the partials, whatever its keys' exponents.
       float inv[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (slot >= 0) {
-          const float m = -(i & 1 ? neg_m[i / 2].y : neg_m[i / 2].x);
-          const float m_new = sum[i] == 0.f ? m : m + (float)((int)(__float_as_uint(sum[i]) >> 23) - 127);
-          inv[i] = ex2_approx(m - m_new);   // (as far as m could be raised: it may be a large number)
+      for (int i = 0; i < 8; ++i) inv[i] = slot >= 0 ? 1.f : sum[i] == 0.f ? 0.f : 1.f / sum[i];   // 0: sees no key (a NaN sum is no such row's)
+      // A partial's weight is l 2^m.  Where l is far from 1, by its keys' exponents, m is
+      // raised by l's power of two, so that the merge's 2^(m - max m) says the weight.
+      bool far = false;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) far |= __float_as_uint(sum[i]) - kFp8NearLow > kFp8NearHigh - kFp8NearLow;
+      if (slot >= 0 && far) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float& neg = i & 1 ? neg_m[i / 2].y : neg_m[i / 2].x;
+          const float n = sum[i] == 0.f ? neg : neg - (float)((int)(__float_as_uint(sum[i]) >> 23) - 127);
+          inv[i] = ex2_approx(n - neg);   // (as far as m could be raised: it may be a large number)
           sum[i] *= inv[i];
-          (i & 1 ? neg_m[i / 2].y : neg_m[i / 2].x) = -m_new;
-        } else {
-          inv[i] = sum[i] == 0.f ? 0.f : 1.f / sum[i];   // 0: sees no key (a NaN sum is no such row's)
+          neg = n;
         }
       }
       const long long wrap = p.o_rs - (long long)(p.group - 1) * p.o_hs;   // from a token's last head to the next token's first
