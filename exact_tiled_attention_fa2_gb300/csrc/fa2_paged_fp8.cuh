@@ -31,19 +31,19 @@
 // Schedule, fragments and merging of cut pairs are the 16-bit kernel's
 // (fa2_paged.cuh); a step here is two of its 64-key tiles, and pairs always lie on
 // the line: with one CTA an SM nothing would overlap a pair's start and end (8
-// chunks of 512 tokens over 4096 keys, d = 128: 1104 us, a CTA a pair 1489).  One CTA: four softmax
-// warps for every eight rows of a tile (a thread has one key and eight rows), the
-// MMA thread, the TMA warp (keys, values, exponents), and the planner, which
-// walks the fragments and prepares their q parts.  What runs seldom is rolled or
+// chunks of 512 tokens over 4096 keys, d = 128, as first built: 1104 us, a CTA a pair
+// 1489; now 942).  One CTA: four softmax warps for every eight rows of a tile (a
+// thread has one key and eight rows), the MMA thread, the TMA warp (keys, values,
+// exponents), and the planner, which walks the fragments and prepares their q parts.  What runs seldom is rolled or
 // shared: a call's code comes to each SM once, and with one thread for 32 rows,
 // four times the code, a call began 50 us later.
 //
 // Bounds.  Decoding: HBM (64 requests of 1000 .. 32000 keys, 8 K/V heads of 128:
 // 331 us, 6.6 TB/s); below some thousand keys a CTA the start (6 us) and the merge
-// (4 us).  With 32 rows a tile the softmax warps' instructions: 340 a step and
-// warp, 57 % of the issue slots (128 requests x heads of 8192 keys, d = 128: 82 us
-// at 32 rows, 75 at 16, 70 at 4; a chunk of 2048 tokens over 16384 keys 1712 us,
-// 341 TFLOP/s).
+// (4 us).  With 32 rows a tile the softmax warps' instructions: some 330 a step and
+// warp, 62 % of the issue slots (128 requests x heads of 8192 keys, d = 128, from an
+// empty L2 cache: 84 us at 32 rows, 74 at 16, 71 at 4; a chunk of 2048 tokens over
+// 16384 keys 1720 us, 340 TFLOP/s).
 #pragma once
 
 #include <cuda_fp8.h>
@@ -149,8 +149,8 @@ constexpr float kFp8ZeroInv = 309485009821345068724781056.f;   // 2^88
 // way of P.  m is at least 4 below the largest s + ev and exponents end at 60: any
 // other key that leaves l because its 2^(s + ev - m) is no fp32 number weighs less
 // than 2^-50 of one that stays, 2^-19 over 2^31 of them.  (A branch of each thread:
-// 8 chunks of 512 tokens over 4096 keys 1012 us, without it 1009, by a warp's vote
-// 1016, its operands kept from before S(g) 1090.)
+// 8 chunks of 512 tokens over 4096 keys, calls in a row, 1012 us, without it 1009, by
+// a warp's vote 1016, its operands kept from before S(g) 1090.)
 constexpr float kFp8LowInv = 1048576.f;   // 2^20
 // Sums from 2^-40 to 2^40 go to the merge as they are (their bits): what leaves the
 // merge with 2^(m - max m), past 2^-126, then weighs less than 2^-46 of another part.

@@ -165,7 +165,7 @@ int fp8_shape(const fa2_paged_fp8_params& a, Fp8Shape& s) {
   // One wave of the resident CTAs of a GB300's 152 SMs, fixed (see paged_ctas): two
   // an SM with up to eight rows (32 requests of 1 .. 8192 keys: 70 us, with one CTA
   // and deeper rings 88, from an empty L2 cache), one with more (16 requests of 8192
-  // keys, 16 rows: 80 us, with two CTAs 90)
+  // keys, 16 rows, as then built: 80 us, with two CTAs 90; now 74)
   s.ctas = c.head_dim == 256 || s.many || s.slot_rows > 8 ? 152 : 304;
   const size_t rows = 2 * (size_t)s.ctas * (size_t)s.slot_rows;
   s.ws_o_bytes = align256(rows * (size_t)c.head_dim * 4);

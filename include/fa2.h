@@ -618,7 +618,9 @@ int fa2_paged_read_fp8(const fa2_paged_read_fp8_params* params, void* stream);
  * query tile is 32 rows at most, where fa2_paged_fwd's has 128: from chunks of
  * some 32 to 100 tokens on, fa2_paged_read_fp8 and fa2_paged_fwd are faster where
  * there is room for the rows in 16 bits (8 requests of 64 tokens over 4096 keys, 4
- * heads of 128 to a K/V head: 140 and 88 us; of 8 tokens 42 and 71).
+ * heads of 128 to a K/V head: 141 and 89 us; of 8 tokens 41 and 71).  More than 32
+ * query heads to a K/V head are cut into equal parts, each of which reads the keys:
+ * two of 17 heads for 34, but 37 of one head for 37.
  */
 typedef struct fa2_paged_fp8_params {
   fa2_paged_cache_fp8 cache;
